@@ -263,6 +263,78 @@ int moe_forward_noalloc(const moe_config* cfg, int32_t num_tokens, const void* x
                         const int32_t* perm, const moe_expert_weights* weights, float* y,
                         void* y_act, void* stream);
 
+/* The whole layer for a few tokens, num_tokens <= MOE_FEW_TOKENS: moe_route,
+ * moe_dispatch and moe_forward in one call of two launches, for decode steps and
+ * single draft blocks, where launches and the pauses between them cost as much as
+ * the weights.  Routing (selection, top-p trim, budget, masked and NaN logits,
+ * statistics) and y are those of the three calls, every weight dtype and every
+ * option of cfg included, with one difference: with FP8 and MXFP4 weights the
+ * activations are not quantised (the weights are decoded, w = decode(q) * s), so y
+ * lies closer to the unquantised layer than moe_forward's; and h is kept to 16
+ * significant bits (float32 with F32 weights).  y is bit-reproducible.
+ *   topk_ids     (device) out [T, K] int32 or NULL, as moe_route writes it
+ *   topk_weights (device) out [T, K] float32 or NULL
+ *   shared_gate  (device) out [T] float32 or NULL; ignored when S = 0
+ *   route_stats  (device) out int32[4] or NULL
+ *   y            (device) out [T, H] float32 or NULL
+ *   y_act        (device) out [T, H] act_dtype or NULL; y and y_act not both NULL
+ * A slot of weight 0 is not computed.  x, w_router, w_shared_gate and the weights
+ * must be 16-byte aligned (with F32 weights 4-byte), scales, y, y_act and the other
+ * outputs to their element size, the workspace to 16 bytes (MOE_ERR_UNSUPPORTED
+ * otherwise, and for more than MOE_FEW_TOKENS tokens).  The workspace is not that
+ * of moe_workspace_size; moe_layer_few_workspace_size gives its bytes for any
+ * T <= max_tokens <= MOE_FEW_TOKENS.  It needs no initial contents; calls that
+ * overlap in time (other streams, graphs replayed side by side) need one each. */
+#define MOE_FEW_TOKENS 16
+int moe_layer_few_workspace_size(const moe_config* cfg, int32_t max_tokens, size_t* bytes);
+int moe_layer_few(const moe_config* cfg, int32_t num_tokens, const void* x, const void* w_router,
+                  const void* w_shared_gate, const float* logit_bias,
+                  const moe_expert_weights* weights /* (host) struct of (device) pointers */,
+                  int32_t* topk_ids, float* topk_weights, float* shared_gate, int32_t* route_stats,
+                  float* y, void* y_act, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Activations of moe_linear's epilogue. */
+typedef enum moe_activation {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_GELU = 2,      /* v/2 (1 + erf(v / sqrt 2))                                */
+  MOE_ACT_GELU_TANH = 3, /* v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3)))            */
+  MOE_ACT_SILU = 4       /* v / (1 + exp(-v))                                        */
+} moe_activation;
+
+#define MOE_LINEAR_MAX_FEATURES (1 << 20)
+#define MOE_LINEAR_MAX_ROWS (1 << 21)
+
+typedef struct moe_linear_config {
+  int32_t in_features;   /* length of a row of x and of w, 1..MOE_LINEAR_MAX_FEATURES  */
+  int32_t out_features;  /* rows of w, length of a row of y, 1..MOE_LINEAR_MAX_FEATURES */
+  int32_t in_dtype;      /* moe_dtype of x, w and bias: F32 or BF16                    */
+  int32_t out_dtype;     /* moe_dtype of y and residual: F32, or BF16 with BF16 inputs */
+  int32_t activation;    /* moe_activation                                             */
+} moe_linear_config;
+
+/* Dense matrix product with its epilogue, for the projections around the layer:
+ *   y[m,n] = act(sum_k x[m,k] w[n,k] + bias[n]) + residual[m,n]
+ * The sum is taken in float32 and everything after it is applied to it in float32;
+ * y is rounded once, to nearest even.  y is bit-reproducible for given sizes and alignments.
+ *   x        (device) [num_rows, in_features], rows ldx elements apart
+ *   w        (device) [out_features, in_features], rows ldw elements apart
+ *   bias     (device) [out_features] or NULL
+ *   residual (device) [num_rows, out_features] or NULL, rows ldr elements apart; may
+ *            be y itself (then ldr = ldy), otherwise y must overlap no input
+ *   y        (device) out [num_rows, out_features], rows ldy elements apart;
+ *            elements between the rows are left as they were
+ * Strides are in elements, at least the row's length (MOE_ERR_BAD_SHAPE otherwise)
+ * and at most 2^40.  Pointers need only be aligned to their element size; rows that
+ * start on 16-byte boundaries are the fast case.  num_rows = 0 returns MOE_OK and
+ * reads nothing but cfg; num_rows <= MOE_LINEAR_MAX_ROWS.  The workspace (16-byte
+ * aligned, moe_linear_workspace_size bytes for any num_rows <= max_rows) needs no
+ * initial contents; calls that overlap in time need one each. */
+int moe_linear_workspace_size(const moe_linear_config* cfg, int32_t max_rows, size_t* bytes);
+int moe_linear(const moe_linear_config* cfg, int32_t num_rows, const void* x, int64_t ldx, const void* w,
+               int64_t ldw, const void* bias, const void* residual, int64_t ldr, void* y, int64_t ldy,
+               void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* moe_status_string(int status);
 

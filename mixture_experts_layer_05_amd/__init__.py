@@ -26,8 +26,12 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe_mi355x.h")
 
 DTYPES = {"f32": 0, "bf16": 1, "fp8_e4m3_g128": 2, "mxfp4": 3}
 ENTRY_POINTS = ("moe_workspace_size", "moe_route", "moe_dispatch", "moe_forward",
-                "moe_forward_gate_up", "moe_forward_down", "moe_forward_noalloc", "moe_status_string",
+                "moe_forward_gate_up", "moe_forward_down", "moe_forward_noalloc", "moe_layer_few",
+                "moe_layer_few_workspace_size", "moe_linear", "moe_linear_workspace_size", "moe_status_string",
                 "moe_version")
+# Most tokens of a moe_layer_few call, and moe_linear's activations, as the header states them.
+FEW_TOKENS = 16
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 # Static scratch of moe_forward_noalloc (bytes), as the header states it.
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -51,6 +55,10 @@ class _Weights(ctypes.Structure):
         "ws_gate", "ws_up", "ws_down", "ss_gate", "ss_up", "ss_down")]
 
 
+class _LinearConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("in_features", "out_features", "in_dtype", "out_dtype", "activation")]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -71,8 +79,16 @@ def lib() -> ctypes.CDLL:
             getattr(L, name).argtypes = fwd
         L.moe_forward_noalloc.argtypes = [cfgp, i32, vp, vp, vp, vp, vp, vp, ctypes.POINTER(_Weights), vp, vp,
                                           vp]
+        i64, lincfgp = ctypes.c_int64, ctypes.POINTER(_LinearConfig)
+        L.moe_layer_few_workspace_size.argtypes = [cfgp, i32, ctypes.POINTER(sz)]
+        L.moe_layer_few.argtypes = [cfgp, i32, vp, vp, vp, vp, ctypes.POINTER(_Weights), vp, vp, vp, vp, vp, vp,
+                                    vp, sz, vp]
+        L.moe_linear_workspace_size.argtypes = [lincfgp, i32, ctypes.POINTER(sz)]
+        L.moe_linear.argtypes = [lincfgp, i32, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, sz, vp]
         for name in ("moe_workspace_size", "moe_route", "moe_dispatch", "moe_forward",
-                     "moe_forward_gate_up", "moe_forward_down", "moe_forward_noalloc", "moe_version"):
+                     "moe_forward_gate_up", "moe_forward_down", "moe_forward_noalloc", "moe_version",
+                     "moe_layer_few", "moe_layer_few_workspace_size", "moe_linear",
+                     "moe_linear_workspace_size"):
             getattr(L, name).restype = ctypes.c_int
         L.moe_status_string.argtypes = [ctypes.c_int]
         L.moe_status_string.restype = ctypes.c_char_p
@@ -250,16 +266,135 @@ def forward_noalloc(cfg, x, topk_weights, shared_gate, counts, offsets, perm, we
                                      _ptr(y_act), _stream(stream)), "moe_forward_noalloc")
 
 
+def layer_few_workspace_size(cfg: MoEConfig, max_tokens: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_layer_few_workspace_size(ctypes.byref(cfg.c()), int(max_tokens), ctypes.byref(n)),
+           "moe_layer_few_workspace_size")
+    return n.value
+
+
+def layer_few(cfg: MoEConfig, x, w_router, w_shared_gate, logit_bias, weights: _Weights, y, workspace,
+              topk_ids=None, topk_weights=None, shared_gate=None, route_stats=None, y_act=None,
+              stream=None) -> None:
+    """The whole layer for at most FEW_TOKENS tokens in two launches (moe_layer_few).
+    The routing outputs are optional; y may be None if y_act is given."""
+    T, E, K, H = x.shape[0], cfg.n_routed_experts, cfg.num_experts_per_tok, cfg.hidden_size
+    act = cfg.act_torch_dtype
+    _expect(x, (T, H), act, "x")
+    _expect(w_router, (E, H), act, "w_router")
+    _expect(w_shared_gate, (H,), act, "w_shared_gate")
+    _expect(logit_bias, (T, E), torch.float32, "logit_bias")
+    _expect(topk_ids, (T, K), torch.int32, "topk_ids")
+    _expect(topk_weights, (T, K), torch.float32, "topk_weights")
+    _expect(shared_gate, (T,), torch.float32, "shared_gate")
+    _expect(route_stats, (4,), torch.int32, "route_stats")
+    _expect(y, (T, H), torch.float32, "y")
+    _expect(y_act, (T, H), act, "y_act")
+    _check(lib().moe_layer_few(ctypes.byref(cfg.c()), T, _ptr(x), _ptr(w_router), _ptr(w_shared_gate),
+                               _ptr(logit_bias), ctypes.byref(weights), _ptr(topk_ids), _ptr(topk_weights),
+                               _ptr(shared_gate), _ptr(route_stats), _ptr(y), _ptr(y_act), _ptr(workspace),
+                               workspace.numel(), _stream(stream)), "moe_layer_few")
+
+
+_TORCH_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def _rows(t: Optional[torch.Tensor], shape, dtype, name: str):
+    """(address, row stride) of a matrix whose rows are contiguous, on the GPU."""
+    if t is None:
+        return None, 0
+    if tuple(t.shape) != shape or t.dtype != dtype:
+        raise ValueError(f"{name}: expected {shape} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError("tensors passed to the MoE library must live on the GPU")
+    ld, step = t.stride()
+    if shape[0] <= 1:
+        ld = shape[1]                 # a single row's stride means nothing
+    if step != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.data_ptr(), ld
+
+
+def linear_workspace_size(in_features: int, out_features: int, max_rows: int, in_dtype: str = "bf16",
+                          out_dtype: Optional[str] = None) -> int:
+    c = _LinearConfig(in_features, out_features, DTYPES[in_dtype], DTYPES[out_dtype or in_dtype], 0)
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_linear_workspace_size(ctypes.byref(c), int(max_rows), ctypes.byref(n)),
+           "moe_linear_workspace_size")
+    return n.value
+
+
+def linear(x, weight, bias, residual, y, workspace, activation: str = "none", stream=None) -> None:
+    """y = activation(x weight^T + bias) + residual (moe_linear).  x [M, K], weight
+    [N, K] and bias [N] share a dtype, residual and y [M, N] another; matrices may be
+    views with rows further apart than they are long.  bias and residual may be None;
+    residual may be y."""
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation: expected one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    (M, K), N = x.shape, weight.shape[0]
+    cx, cy = _dtype_code(x, "x"), _dtype_code(y, "y")
+    xp, ldx = _rows(x, (M, K), x.dtype, "x")
+    wp, ldw = _rows(weight, (N, K), x.dtype, "weight")
+    rp, ldr = _rows(residual, (M, N), y.dtype, "residual")
+    yp, ldy = _rows(y, (M, N), y.dtype, "y")
+    _expect(bias, (N,), x.dtype, "bias")
+    _check(lib().moe_linear(ctypes.byref(_LinearConfig(K, N, cx, cy, ACTIVATIONS[activation])), M, xp, ldx, wp,
+                            ldw, _ptr(bias), rp, ldr, yp, ldy, _ptr(workspace), workspace.numel(),
+                            _stream(stream)), "moe_linear")
+
+
+def _dtype_code(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return DTYPES["bf16"]
+    if t.dtype == torch.float32:
+        return DTYPES["f32"]
+    raise ValueError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+
+
+class Linear:
+    """A dense projection y = activation(x weight^T + bias) + residual.  Owns the
+    output and the workspace for up to `max_rows` rows and runs on the current
+    stream; `out_dtype` ("f32" / "bf16") is that of y and of the residual, by default
+    the weight's.  A call returns its rows of `y`, or `out` if that is given."""
+
+    def __init__(self, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, activation: str = "none",
+                 out_dtype: Optional[str] = None, max_rows: int = 1):
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"activation: expected one of {sorted(ACTIVATIONS)}, got {activation!r}")
+        self.weight, self.bias, self.activation, self.max_rows = weight, bias, activation, max_rows
+        self.N, self.K = weight.shape
+        in_dtype = "f32" if _dtype_code(weight, "weight") == DTYPES["f32"] else "bf16"
+        _expect(bias, (self.N,), weight.dtype, "bias")
+        self.out_dtype = _TORCH_DTYPES[out_dtype or in_dtype]
+        dev = weight.device
+        self.workspace = torch.empty(linear_workspace_size(self.K, self.N, max_rows, in_dtype, out_dtype),
+                                     dtype=torch.uint8, device=dev)
+        self.y = torch.empty(max_rows, self.N, dtype=self.out_dtype, device=dev)
+
+    def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        if x.shape[0] > self.max_rows:
+            raise ValueError("more rows than the projection was sized for")
+        y = self.y[:x.shape[0]] if out is None else out
+        _expect(y, (x.shape[0], self.N), self.out_dtype, "out")
+        linear(x, self.weight, self.bias, residual, y, self.workspace, self.activation, stream)
+        return y
+
+
 class MoELayer:
     """Owns the outputs and the workspace for up to `max_tokens` tokens and runs
     route -> dispatch -> forward on the current stream.  With `stats=True` each
-    route also fills `route_stats` (int32[4], as moe_route documents it)."""
+    route also fills `route_stats` (int32[4], as moe_route documents it).  With
+    `few=True` a call of at most FEW_TOKENS tokens runs as one moe_layer_few (two
+    launches; it fills the routing outputs but not counts, offsets and perm)."""
 
     def __init__(self, cfg: MoEConfig, weights: Dict[str, torch.Tensor], w_router: torch.Tensor,
                  w_shared_gate: Optional[torch.Tensor] = None,
                  shared: Optional[Dict[str, torch.Tensor]] = None, max_tokens: int = 1,
-                 device: str = "cuda", act_output: bool = False, stats: bool = False):
+                 device: str = "cuda", act_output: bool = False, stats: bool = False,
+                 few: bool = False):
         self.cfg = cfg
+        self.few = few
         self.weights_dict, self.shared_dict = weights, shared
         self.weights = expert_weights_struct(cfg, weights, shared)
         self.w_router, self.w_shared_gate = w_router, w_shared_gate
@@ -267,6 +402,8 @@ class MoELayer:
         E, K = cfg.n_routed_experts, cfg.num_experts_per_tok
         dev = torch.device(device)
         self.workspace = torch.empty(workspace_size(cfg, max_tokens), dtype=torch.uint8, device=dev)
+        self.few_workspace = torch.empty(layer_few_workspace_size(cfg, min(max_tokens, FEW_TOKENS)),
+                                         dtype=torch.uint8, device=dev) if few else None
         self.topk_ids = torch.empty(max_tokens, K, dtype=torch.int32, device=dev)
         self.topk_weights = torch.empty(max_tokens, K, dtype=torch.float32, device=dev)
         self.shared_gate = torch.empty(max_tokens, dtype=torch.float32, device=dev)
@@ -307,6 +444,13 @@ class MoELayer:
     def __call__(self, x, logit_bias=None, stream=None) -> torch.Tensor:
         if x.shape[0] > self.max_tokens:
             raise ValueError("more tokens than the layer was sized for")
+        if self.few and x.shape[0] <= FEW_TOKENS:
+            v = self.views(x.shape[0])
+            layer_few(self.cfg, x, self.w_router, self.w_shared_gate, logit_bias, self.weights, v["y"],
+                      self.few_workspace, v["topk_ids"], v["topk_weights"],
+                      v["shared_gate"] if self.cfg.shared_expert_intermediate_size > 0 else None,
+                      self.route_stats, v["y_act"], stream)
+            return v["y"]
         self.route(x, logit_bias, stream)
         self.dispatch(x.shape[0], stream)
         self.forward(x, stream)

@@ -1,0 +1,320 @@
+"""moe_layer_few: the whole layer for a few tokens, against the float64 oracle.
+
+Tolerances.  Routing weights: the harness's W_TOL.  y, relative L2 over the call and
+per token: h is kept to 16 significant bits (each bf16 plane is off by at most half a
+step, 2^-9 of h and then 2^-9 of the remainder: 2^-18), the float32 sums are short
+(at most 7168 / 128 / 8 blocks per wave and the 8 waves' partial sums, each step
+2^-24) and expf is good to 2^-22, so the errors, independent from element to element,
+stay below 2^-17 of y; 2^-16 is asserted.  F32 layers: float32 sums only, 1e-5."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_05_amd as moe
+import workloads as W
+from oracle import moe as O
+from tests import harness as Hn
+
+OK, NULL_PTR, BAD_SHAPE, BAD_DTYPE, UNSUPPORTED, WS_SMALL = 0, -1, -2, -3, -4, -5
+FAKE = 0x1000
+Y_TOL = {"f32": 1e-5, "bf16": 2.0 ** -16, "fp8_e4m3_g128": 2.0 ** -16, "mxfp4": 2.0 ** -16}
+
+
+# ----------------------------------------------------------------------------- refusals (no GPU)
+
+def _cfg(**kw):
+    base = dict(hidden_size=512, n_routed_experts=16, moe_intermediate_size=256, num_experts_per_tok=2,
+                shared_expert_intermediate_size=128, weight_dtype="bf16", act_dtype="bf16")
+    base.update(kw)
+    return moe.MoEConfig(**base)
+
+
+def _call(cfg, T=4, ws_bytes=1 << 30, weights=None, **kw):
+    p = dict(x=FAKE, w_router=FAKE, w_shared_gate=FAKE, bias=None, ids=None, w=None, sg=None, stats=None, y=FAKE,
+             y_act=None, ws=FAKE)
+    p.update(kw)
+    ew = moe._Weights(*[FAKE] * 12) if weights is None else weights
+    return moe.lib().moe_layer_few(ctypes.byref(cfg.c()), T, p["x"], p["w_router"], p["w_shared_gate"], p["bias"],
+                                   ctypes.byref(ew), p["ids"], p["w"], p["sg"], p["stats"], p["y"], p["y_act"],
+                                   p["ws"], ws_bytes, None)
+
+
+def _without(name):
+    w = moe._Weights(*[FAKE] * 12)
+    setattr(w, name, None)
+    return w
+
+
+def _shifted(name, by):
+    w = moe._Weights(*[FAKE] * 12)
+    setattr(w, name, FAKE + by)
+    return w
+
+
+def test_refusals():
+    cfg = _cfg()
+    assert _call(cfg, T=0, x=None, w_router=None, y=None, ws=None) == OK
+    assert _call(cfg, T=17) == UNSUPPORTED
+    assert _call(cfg, T=-1) == BAD_SHAPE
+    assert _call(_cfg(hidden_size=500)) == UNSUPPORTED
+    assert _call(_cfg(act_dtype="f32")) == BAD_DTYPE
+    for name in ("x", "w_router", "w_shared_gate", "y", "ws"):
+        assert _call(cfg, **{name: None}) == NULL_PTR, name
+    assert _call(cfg, ws_bytes=64) == WS_SMALL
+    for name in ("w_gate", "w_up", "w_down", "ws_gate", "ws_up", "ws_down"):
+        assert _call(cfg, weights=_without(name)) == NULL_PTR, name
+        assert _call(cfg, weights=_shifted(name, 8)) == UNSUPPORTED, name
+    fp8 = _cfg(weight_dtype="fp8_e4m3_g128")
+    for name in ("s_gate", "s_up", "s_down", "ss_gate", "ss_up", "ss_down"):
+        assert _call(fp8, weights=_without(name)) == NULL_PTR, name
+        assert _call(fp8, weights=_shifted(name, 2)) == UNSUPPORTED, name
+    for name, by in (("x", 8), ("w_router", 2), ("w_shared_gate", 4), ("ws", 8), ("y", 2), ("y_act", 1), ("ids", 2),
+                     ("w", 2), ("sg", 1), ("stats", 2), ("bias", 2)):
+        assert _call(cfg, **{name: FAKE + by}) == UNSUPPORTED, name
+
+
+def test_workspace_size():
+    sizes = [moe.layer_few_workspace_size(_cfg(), t) for t in (0, 1, 7, 16)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+    n = ctypes.c_size_t(0)
+    size = moe.lib().moe_layer_few_workspace_size
+    assert size(None, 4, ctypes.byref(n)) == NULL_PTR
+    assert size(ctypes.byref(_cfg().c()), 4, None) == NULL_PTR
+    assert size(ctypes.byref(_cfg().c()), 17, ctypes.byref(n)) == UNSUPPORTED
+    assert size(ctypes.byref(_cfg().c()), -1, ctypes.byref(n)) == BAD_SHAPE
+
+
+# ----------------------------------------------------------------------------- GPU
+
+def _layer(case, **kw):
+    wg = case.inp.w_shared_gate
+    return moe.MoELayer(Hn.config(case.shape), case.weights, case.inp.w_router.cuda(),
+                        None if wg is None else wg.cuda(), case.shared, max_tokens=max(case.T, 1), few=True, **kw)
+
+
+def _oracle(case):
+    s = case.shape
+    r = O.route(case.inp.x, case.inp.w_router, case.inp.w_shared_gate, case.inp.logit_bias, s.num_experts_per_tok,
+                bool(s.norm_topk_prob), s.expert_budget, s.top_p)
+    name = "plain" if s.weight_dtype in ("fp8_e4m3_g128", "mxfp4") else "model"
+    r["y"] = O.moe_combine(case.inp.x, r["ids"], r["w"], r["shared_gate"], case.expert_cpu, case.shared_cpu(),
+                           s.weight_dtype, None, [name])[name]
+    return r
+
+
+def _check(case, layer, ora, rows=None):
+    s, v = case.shape, layer.views(case.T)
+    rows = np.arange(case.T) if rows is None else np.asarray(rows)
+    assert np.array_equal(v["topk_ids"].cpu().numpy()[rows], ora["ids"][rows])
+    assert np.abs(v["topk_weights"].cpu().numpy()[rows] - ora["w"][rows]).max() <= Hn.W_TOL
+    if s.shared_expert_intermediate_size:
+        assert np.abs(v["shared_gate"].cpu().numpy()[rows] - ora["shared_gate"][rows]).max() <= 1e-5
+    y, ref = v["y"].cpu().numpy().astype(np.float64)[rows], ora["y"][rows]
+    tok = Hn.token_rel_l2(y, ref)
+    print(f"[case] y rel L2 {Hn.rel_l2(y, ref):.2e}, worst token {tok.max() if tok.size else 0:.2e}", flush=True)
+    assert Hn.rel_l2(y, ref) <= Y_TOL[s.weight_dtype]
+    assert tok.size == 0 or tok.max() <= Y_TOL[s.weight_dtype]
+    assert (y[np.linalg.norm(ref, axis=1) == 0] == 0).all()
+
+
+def _bias(case):
+    return None if case.inp.logit_bias is None else case.inp.logit_bias.cuda()
+
+
+SHAPES = [
+    (W.TINY, (1, 16)),
+    (W.LayerShape("odd_f32", 101, 5, 30, 3, 14, "f32", "f32"), (1, 5, 16)),
+    (W.LayerShape("vec_f32", 100, 5, 28, 3, 12, "f32", "f32"), (3,)),
+    (W.LayerShape("least_f32", 1, 1, 1, 1, 0, "f32", "f32"), (1, 2)),
+    (W.LayerShape("least_bf16", 128, 1, 128, 1, 0, "bf16", "bf16"), (1, 16)),
+    (W.LayerShape("slots_bf16", 256, 512, 128, 16, 128, "bf16", "bf16"), (1, 16)),
+    (W.LayerShape("all_bf16", 384, 16, 128, 16, 0, "bf16", "bf16"), (16,)),
+    (W.LayerShape("plain_softmax", 512, 40, 256, 4, 256, "bf16", "bf16", norm_topk_prob=0), (9,)),
+    (W.LayerShape("least_fp8", 128, 3, 128, 2, 128, W.DT_FP8, "bf16"), (1, 15)),
+    (W.LayerShape("small_fp8", 1152, 24, 384, 4, 640, W.DT_FP8, "bf16"), (13,)),
+    (W.LayerShape("least_mx", 256, 3, 256, 2, 256, W.DT_MXFP4, "bf16"), (1, 16)),
+    (W.LayerShape("small_mx", 1280, 24, 512, 4, 768, W.DT_MXFP4, "bf16"), (11,)),
+    (W.LayerShape("top_p", 512, 64, 128, 8, 128, "bf16", "bf16", top_p=0.6), (16,)),
+    (W.LayerShape("budget", 512, 64, 128, 6, 128, "bf16", "bf16", expert_budget=9), (16,)),
+    (W.LayerShape("budget_tight", 512, 64, 128, 6, 0, "bf16", "bf16", expert_budget=1), (16,)),
+    (W.LayerShape("budget_top_p", 512, 64, 128, 6, 0, W.DT_FP8, "bf16", expert_budget=7, top_p=0.7,
+                  norm_topk_prob=0), (12,)),
+    (W.DRAFTER, (1, 7, 16)),
+    (W.DRAFTER_FP8, (7,)),
+    (W.DRAFTER_MX4, (7,)),
+    (W.NARROW, (7,)),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape,T", [pytest.param(s, t, id=f"{s.name}-{t}") for s, ts in SHAPES for t in ts])
+def test_layer(shape, T):
+    print(f"\n[case] few {shape.name} T={T}", flush=True)
+    case = Hn.make_case(shape, T, 41 + T)
+    layer = _layer(case, stats=True)
+    layer.few_workspace.fill_(0xFF)                      # no initial contents are needed
+    layer.route_stats.fill_(-7)
+    layer.y.fill_(float("nan"))
+    layer(case.inp.x.cuda(), _bias(case))
+    torch.cuda.synchronize()
+    ora = _oracle(case)
+    _check(case, layer, ora)
+    if shape.expert_budget:
+        assert np.array_equal(layer.route_stats.cpu().numpy(), ora["stats"])
+    else:
+        n = len(set(ora["ids"].ravel().tolist()) - {-1})
+        assert layer.route_stats.tolist() == [n, n, 0, 0]
+
+
+@pytest.mark.gpu
+def test_agrees_with_the_three_calls():
+    case = Hn.make_case(W.DRAFTER, 7, 5)
+    few = _layer(case, act_output=True)
+    x, b = case.inp.x.cuda(), _bias(case)
+    few(x, b)
+    three = _layer(case, act_output=True)
+    three.few = False
+    three(x, b)
+    torch.cuda.synchronize()
+    assert torch.equal(few.topk_ids, three.topk_ids)
+    assert (few.topk_weights - three.topk_weights).abs().max() <= Hn.W_TOL
+    # The three calls keep h in bf16: half a step of 2^-8, uniform, is 2^-9 / sqrt(3) = 1.1e-3 of y.
+    assert Hn.rel_l2(few.y.cpu().double().numpy(), three.y.cpu().double().numpy()) <= 2e-3
+    assert torch.equal(few.y_act, few.y.bfloat16())
+
+
+@pytest.mark.gpu
+def test_masked_and_nan_logits():
+    """Masked experts are picked last with weight 0; a NaN counts as masked; a token
+    with nothing left gets NaN weights and no other token sees it."""
+    shape = W.LayerShape("mask", 256, 8, 128, 4, 0, "bf16", "bf16")
+    case = Hn.make_case(shape, 6, 77)
+    b = torch.zeros(6, 8)
+    b[1, 2:] = float("-inf")
+    b[2, :] = float("-inf")
+    b[3, 5] = float("nan")
+    b[4, 1:] = torch.finfo(torch.float32).min
+    case.inp.logit_bias = b
+    layer = _layer(case)
+    layer(case.inp.x.cuda(), b.cuda())
+    torch.cuda.synchronize()
+    ora = _oracle(case)
+    assert np.array_equal(layer.topk_ids.cpu().numpy()[[0, 1, 3, 5]], ora["ids"][[0, 1, 3, 5]])
+    assert layer.topk_ids[2].tolist() == [0, 1, 2, 3]
+    assert torch.isnan(layer.topk_weights[2]).all() and torch.isnan(layer.y[2]).all()
+    assert layer.topk_ids[4, 0] == 0 and layer.topk_weights[4].tolist() == [1, 0, 0, 0]
+    _check(case, layer, ora, [0, 1, 3, 5])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_one_experts_infinities_stay_with_its_tokens(bad):
+    shape = W.LayerShape("inf", 256, 8, 128, 2, 128, "bf16", "bf16")
+    case = Hn.make_case(shape, 8, 78)
+    ora = _oracle(case)
+    e = int(ora["ids"][0, 0])
+    case.weights["down"][e, 3, 5] = bad
+    case.weights["gate"][e, 7, 9] = bad
+    layer = _layer(case)
+    layer(case.inp.x.cuda())
+    torch.cuda.synchronize()
+    users = (ora["ids"] == e).any(axis=1)
+    assert users.any() and not users.all()
+    assert not torch.isfinite(layer.y[torch.from_numpy(np.nonzero(users)[0]).cuda()]).all()
+    _check(case, layer, ora, np.nonzero(~users)[0])
+
+
+@pytest.mark.gpu
+def test_mxfp4_scales_at_the_ends_of_their_range():
+    """E8M0 codes from 2^-126 on, met by activations that bring the product back to one."""
+    shape = W.LayerShape("mx_ends", 256, 2, 256, 1, 0, W.DT_MXFP4, "bf16")
+    case = Hn.make_case(shape, 4, 79, condition=False)
+    case.inp.w_router[0] = 0
+    case.inp.w_router[1] = 0                              # ties: expert 0
+    for name in ("gate", "up"):
+        case.weights[name + "_s"].copy_(torch.randint(1, 4, case.weights[name + "_s"].shape, dtype=torch.uint8))
+    case.inp.x = (torch.randint(-8, 9, (4, 256)).float() * 2.0 ** 116).bfloat16()
+    layer = _layer(case)
+    layer(case.inp.x.cuda())
+    torch.cuda.synchronize()
+    _check(case, layer, _oracle(case))
+
+
+@pytest.mark.gpu
+def test_outputs_are_optional():
+    case = Hn.make_case(W.LayerShape("opt", 256, 8, 128, 2, 128, "bf16", "bf16"), 5, 80)
+    layer = _layer(case, act_output=True)
+    x = case.inp.x.cuda()
+    layer(x)
+    y, act = layer.y.clone(), layer.y_act.clone()
+    layer.y_act.fill_(0)
+    moe.layer_few(layer.cfg, x, layer.w_router, layer.w_shared_gate, None, layer.weights, None, layer.few_workspace,
+                  y_act=layer.y_act)
+    y2 = torch.empty_like(y)
+    moe.layer_few(layer.cfg, x, layer.w_router, layer.w_shared_gate, None, layer.weights, y2, layer.few_workspace)
+    torch.cuda.synchronize()
+    assert torch.equal(layer.y_act, act) and torch.equal(y2, y)
+
+
+@pytest.mark.gpu
+def test_more_tokens_take_the_three_calls():
+    case = Hn.make_case(W.LayerShape("many", 256, 8, 128, 2, 128, "bf16", "bf16"), 17, 81)
+    layer = _layer(case)
+    y = layer(case.inp.x.cuda()).clone()
+    layer.few = False
+    assert torch.equal(layer(case.inp.x.cuda()), y)
+    layer.few = True
+    layer.y.fill_(-3.0)
+    layer(case.inp.x.cuda()[:7].contiguous())
+    torch.cuda.synchronize()
+    assert (layer.y[7:] == -3.0).all()                    # rows behind the last token
+
+
+@pytest.mark.gpu
+def test_captured_and_replayed():
+    """A captured call sees the inputs of its replay, alternating with eager calls of
+    other sizes on the same buffers."""
+    case = Hn.make_case(W.DRAFTER, 7, 6)
+    layer = _layer(case)
+    x, b = case.inp.x.cuda(), _bias(case)
+    xs = [x.clone(), x.flip(0).contiguous(), x.roll(1, 0).contiguous()]
+    want = []
+    for v in xs:
+        layer(v, b)
+        want.append(layer.y.clone())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer(x, b)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer(x, b)
+    for i in (1, 2, 0, 1, 1):
+        x.copy_(xs[i])
+        layer.y.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(layer.y, want[i]), i
+        layer(xs[2][:3].contiguous(), b[:3].contiguous())
+    torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """Two layers, a workspace each, on two streams without any order between them."""
+    cases = [Hn.make_case(W.DRAFTER, 7, 8), Hn.make_case(W.DRAFTER_MX4, 16, 9)]
+    layers = [_layer(c) for c in cases]
+    xs, bs = [c.inp.x.cuda() for c in cases], [_bias(c) for c in cases]
+    want = [layer(x, b).clone() for layer, x, b in zip(layers, xs, bs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for layer, x, b, s in zip(layers, xs, bs, streams):
+            with torch.cuda.stream(s):
+                layer(x, b)
+    torch.cuda.synchronize()
+    for layer, w in zip(layers, want):
+        assert torch.equal(layer.y, w)
