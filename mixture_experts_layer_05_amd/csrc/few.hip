@@ -10,27 +10,29 @@
 //                      It also clears the counters of the second kernel.
 //   few_second_kernel  every workgroup works the routing out from the logits by
 //                      itself (16 tokens: a few microseconds, no grid-wide step),
-//                      then takes work items from a counter: first the gate/up
-//                      items of the touched experts, then the down items, which
-//                      contract over all touched experts and the shared expert at
+//                      runs its share of the touched experts' gate/up tiles, waits
+//                      for the others', and runs its share of the down half, which
+//                      contracts over all touched experts and the shared expert at
 //                      once, so that y leaves the kernel finished.
 //
 // All tokens are the 16 rows of one MFMA tile, whatever expert they go to; a row
 // that an expert does not serve is zero there and its result is not used.  That
 // spares the gather and the permutation, and costs nothing: the matrix cores idle.
 //
-// Waiting.  A down item needs every gate/up item's h.  Items are handed out by an
-// atomic counter in order, gate/up items first, so when a workgroup holds a down
-// item every gate/up item has been taken by a workgroup that is running, and
-// gate/up items wait for nothing: the wait ends whatever part of the grid is
-// resident, also when other kernels share the GPU.
+// Waiting.  The down half needs every gate/up tile.  The tiles are handed out from
+// eight queues (one for each XCD; a workgroup whose own is empty takes from the
+// others), so a tile that has been taken is held by a workgroup that is running, and
+// that finishes it without waiting for anything.  A workgroup waits only when it has
+// seen all queues empty: the wait ends, whatever part of the grid is resident, also
+// when other kernels hold part of the GPU.
 //
-// y is the same from run to run: every sum has a fixed order (the counters only say
-// when something is complete).
+// y is the same from run to run: every sum has a fixed order (queues and
+// counters say who works and when something is complete, not in which order it is
+// added).
 //
-// h leaves the gate/up half as two bf16 planes, h = hi + lo (16 significant bits;
-// f32 layers keep one f32 plane): the second plane costs an L2 read and a second
-// MFMA, both idle here, and takes the rounding of h out of y.
+// h leaves the gate/up half as three bf16 planes whose sum is its float32 value (f32
+// layers keep one f32 plane).  With one plane its rounding would be the largest
+// error in y by far; the others cost L2 reads and MFMAs that are idle here.
 #include <algorithm>
 
 #include "moe_mi355x.h"
@@ -39,13 +41,16 @@
 namespace moe {
 namespace {
 
-constexpr int kFewThreads = 512;
+// Two workgroups of four waves on each of 256 CUs, 256 registers per lane: while one
+// workgroup adds a tile up the other one's loads keep the CU's memory path busy.
+constexpr int kFewThreads = 256;
 constexpr int kFewWaves = kFewThreads / kWave;
+constexpr int kFewGrid = 512;
 constexpr int kFewTokens = MOE_FEW_TOKENS;
 static_assert(kFewTokens == kSkinnyRows, "one MFMA tile of tokens");
 constexpr int kFewSlots = kFewTokens * kMaxTopK;
-constexpr int kFewGrid = 512;              // two workgroups of eight waves on each of 256 CUs
 constexpr int kFewRouterParts = 8;         // contraction parts of the router, at most
+constexpr int kQueues = 8;
 
 struct FewArgs {
   const void *x, *w_router, *w_gcol;
@@ -59,12 +64,13 @@ struct FewArgs {
   float* y;
   void* y_act;
   int act_bf16;
-  int* ctl;                // counters: next item, finished gate/up items
+  int* ctl;                // counters of the second kernel, see Ctl
   float* z;                // [parts, 16, ldz] partial logits
-  void *h, *h_lo;          // [T*K, I] routed then [T, S] shared
+  void* h[3];              // planes of [T*K, I] routed then [T, S] shared rows
+  float* part;             // [2 * kMaxRanges, 256] partial down tiles
   int T, H, E, I, K, S, ncols, ldz, parts, norm, budget;
   float top_p;
-  int rvec, hvec, ivec, svec;   // f32: rows of that length can be read in 16-byte pieces
+  int hvec, ivec, svec;   // f32: rows of that length can be read in 16-byte pieces
 };
 
 // ---------------------------------------------------------------- pieces of both kernels
@@ -86,28 +92,37 @@ __device__ __forceinline__ f32x4 red_sum(const Red& r, int lane) {
   return s;
 }
 
+// Blocks a wave loads at a time, within its 256 registers.
+template <int FMT>
+struct FewBatch {
+  static constexpr int kGateUp = FMT == kDtypeMxfp4 ? 4 : FMT == kDtypeFp8 ? 6 : 10;
+  static constexpr int kDown = FMT == kDtypeMxfp4 ? 1 : FMT == kDtypeFp8 ? 3 : 5;
+};
+
 template <int FMT>
 struct GuBlk {
   WBlk<FMT> w;
-  XBlk<FMT> x;
+  XBlk<FMT> x[1];
 };
 
-// This wave's eighth of x W^T over the contraction [b0, b1), in blocks, of one
+// This wave's quarter of x W^T over the contraction [b0, b1), in blocks, of one
 // 16-row weight tile.
 template <int FMT>
 __device__ __forceinline__ f32x4 wave_tile(const WRow& row, const void* xrow, bool live, int b0, int b1, int kdim,
-                                           bool vec, int wave, int g) {
+                                           bool vec, int wave, int lane) {
   const int n = b1 - b0;
   const int lo = b0 + wave * n / kFewWaves, hi = b0 + (wave + 1) * n / kFewWaves;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  two_ahead<GuBlk<FMT>>(
+  Acc acc{};
+  int at = lo;
+  batches<FewBatch<FMT>::kGateUp, GuBlk<FMT>>(
       hi - lo,
-      [&](int i, GuBlk<FMT>& k) {
-        load_w<FMT>(k.w, row, lo + i, g, kdim, vec);
-        load_x<FMT>(k.x, xrow, lo + i, g, kdim, vec, live);
+      [&](GuBlk<FMT>& k) __attribute__((always_inline)) {
+        load_w<FMT>(k.w, row, at, lane, kdim, vec);
+        load_x<FMT>(k.x[0], xrow, at, lane, kdim, vec, live);
+        ++at;
       },
-      [&](int, GuBlk<FMT>& k) { mma_block<FMT>(k.x, k.w, acc); });
-  return acc;
+      [&](GuBlk<FMT>& k) __attribute__((always_inline)) { mma_block<FMT>(k.x, k.w, acc); });
+  return tile_sums(acc, lane);
 }
 
 template <int FMT>
@@ -122,20 +137,38 @@ __device__ __forceinline__ size_t scale_bytes(int k) {
        : FMT == kDtypeMxfp4 ? static_cast<size_t>(k) / kMxBlock : 0;
 }
 template <int FMT>
-__device__ __forceinline__ WRow weight_row(const void* w, const void* s, size_t row, int k) {
-  return WRow{static_cast<const uint8_t*>(w) + row * row_bytes<FMT>(k),
-              static_cast<const uint8_t*>(s) + row * scale_bytes<FMT>(k)};
+__device__ __forceinline__ void set_row(WRow& r, int h, const void* w, const void* s, size_t row, int k) {
+  r.p[h] = static_cast<const uint8_t*>(w) + row * row_bytes<FMT>(k);
+  r.s[h] = static_cast<const uint8_t*>(s) + row * scale_bytes<FMT>(k);
 }
 
-// Columns [n0, n0 + 8) of a gate/up half: weight rows 0..7 of the tile are gate
-// rows, 8..15 the up rows of the same columns (past the width: the last row again,
-// not stored).
+// Columns [n0, n0 + 8) of a gate/up half: the tile's first 8 rows are gate rows, the
+// others the up rows of the same columns (past the width: the last row again, not
+// stored).
 template <int FMT>
 __device__ __forceinline__ WRow gate_up_row(const void* wg, const void* wu, const void* sg, const void* su,
-                                            size_t first, int n0, int width, int H, int r) {
-  const size_t row = first + min(n0 + (r & 7), width - 1);
-  return r < 8 ? weight_row<FMT>(wg, sg, row, H) : weight_row<FMT>(wu, su, row, H);
+                                            size_t first, int n0, int width, int H, int lane) {
+  const size_t row = first + min(n0 + (lane & 7), width - 1);
+  WRow r;
+  set_row<FMT>(r, 0, wg, sg, row, H);
+  set_row<FMT>(r, 1, wu, su, row, H);
+  return r;
 }
+
+// A store that other workgroups of the running kernel may read: written through to
+// the memory that the eight L2 caches share, so that making it visible needs no
+// write-back of a whole cache.
+template <class V>
+__device__ __forceinline__ void st_shared(V* p, V v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// A load of what st_shared stored, from the same memory.
+template <class V>
+__device__ __forceinline__ V ld_shared(const V* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// This wave's stores have reached that memory.
+__device__ __forceinline__ void stores_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // SwiGLU of a summed gate/up tile, written to h.  Lane l of a tile holds weight row
 // l % 16 of tokens 4 (l / 16) + i; at(token) is the token's row of h, or -1.
@@ -147,44 +180,69 @@ __device__ __forceinline__ void store_h(const FewArgs& a, const f32x4& s, size_t
   for (int i = 0; i < 4; ++i) {
     const float up = __shfl_xor(s[i], 8, kWave);
     const int row = at(4 * g + i);
-    if (r < 8 && n0 + r < width && row >= 0) {
-      const float h = s[i] / (1.0f + expf(-s[i])) * up;
-      const size_t o = base + static_cast<size_t>(row) * width + n0 + r;
-      if constexpr (FMT == kDtypeF32) {
-        static_cast<float*>(a.h)[o] = h;
-      } else {
-        const uint16_t hi = f32_to_bf16_bits(h);
-        const float back = bf16_bits_to_f32(hi);
-        static_cast<uint16_t*>(a.h)[o] = hi;
-        // An infinite hi has no remainder (inf - inf would turn it into NaN).
-        static_cast<uint16_t*>(a.h_lo)[o] = fabsf(back) < INFINITY ? f32_to_bf16_bits(h - back) : 0;
+    const float h = s[i] / (1.0f + expf(-s[i])) * up;
+    const size_t o = base + static_cast<size_t>(max(row, 0)) * width + n0 + r;
+    if constexpr (FMT == kDtypeF32) {
+      if (r < 8 && n0 + r < width && row >= 0) st_shared(static_cast<float*>(a.h[0]) + o, h);
+    } else {
+      // What a plane leaves over goes to the next; an infinite plane leaves nothing
+      // (inf - inf would turn it into NaN).  Widths are even, lanes store in pairs.
+      float rest = h;
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        const uint32_t b = f32_to_bf16_bits(rest);
+        const float v = bf16_bits_to_f32(static_cast<uint16_t>(b));
+        rest = fabsf(v) < INFINITY ? rest - v : 0.f;
+        const uint32_t pair = b | (__shfl_xor(b, 1, kWave) << 16);
+        if (r < 8 && !(r & 1) && row >= 0) st_shared(reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.h[p]) + o), pair);
       }
     }
   }
 }
 
+// Counters in the workspace, cleared by the first kernel; each on a line of its own
+// (atomics on one line take about 10 ns each, whoever sends them).
+struct Ctl {
+  static constexpr int kLine = 32;                          // ints
+  static constexpr int kQueue = 0;                          // next gate/up tile of each queue
+  static constexpr int kDone = kQueue + kQueues * kLine;    // finished tiles, in 16 counters
+  static constexpr int kGroups = 16;
+  static constexpr int kGo = kDone + kGroups * kLine;       // all tiles finished, one flag for each group
+  static constexpr int kRange = kGo + kGroups * kLine;      // next down range
+  static constexpr int kTile = kRange + kLine;              // finished parts of each down tile
+};
+__host__ __device__ inline int ctl_ints(int H) { return Ctl::kTile + (H + 15) / 16; }
+
+__device__ __forceinline__ int ctl_add(int* p, int v) {
+  return __hip_atomic_fetch_add(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // ---------------------------------------------------------------- first kernel
 
 template <int FMT>
-__global__ void __launch_bounds__(kFewThreads) few_first_kernel(FewArgs a) {
+__global__ void __launch_bounds__(kFewThreads, 2) few_first_kernel(FewArgs a) {
   constexpr int AFMT = FMT == kDtypeF32 ? kDtypeF32 : kDtypeBf16;   // the router's type
   __shared__ Red red;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
-  if (blockIdx.x == 0 && tid < 2) a.ctl[tid] = 0;
+  for (int i = blockIdx.x * kFewThreads + tid; i < ctl_ints(a.H); i += gridDim.x * kFewThreads) a.ctl[i] = 0;
 
   const size_t xrow_bytes = static_cast<size_t>(a.H) * (AFMT == kDtypeF32 ? 4 : 2);
   const void* xrow = static_cast<const uint8_t*>(a.x) + static_cast<size_t>(min(r, a.T - 1)) * xrow_bytes;
   const bool live = r < a.T;
   const int router = static_cast<int>(ceil_div(a.ncols, 16)) * a.parts;
-  int item = blockIdx.x;
+  const int item = blockIdx.x;
   if (item < router) {
     const int part = item % a.parts, c0 = item / a.parts * 16;
     const int nb = static_cast<int>(ceil_div(a.H, SkinnyFmt<AFMT>::kBlk));
-    const int c = min(c0 + r, a.ncols - 1);
-    const WRow row = c < a.E ? weight_row<AFMT>(a.w_router, nullptr, c, a.H) : WRow{static_cast<const uint8_t*>(a.w_gcol), nullptr};
+    WRow row;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = min(c0 + 8 * h + (lane & 7), a.ncols - 1);
+      set_row<AFMT>(row, h, c < a.E ? a.w_router : a.w_gcol, nullptr, c < a.E ? c : 0, a.H);
+    }
     red.v[wave][lane] = wave_tile<AFMT>(row, xrow, live, part * nb / a.parts, (part + 1) * nb / a.parts, a.H,
-                                        a.rvec, wave, g);
+                                        a.hvec, wave, lane);
     __syncthreads();
     if (wave == 0 && c0 + r < a.ncols) {
       const f32x4 s = red_sum(red, lane);
@@ -195,9 +253,9 @@ __global__ void __launch_bounds__(kFewThreads) few_first_kernel(FewArgs a) {
     return;
   }
   const int n0 = (item - router) * 8;
-  const WRow row = gate_up_row<FMT>(a.ws_gate, a.ws_up, a.ss_gate, a.ss_up, 0, n0, a.S, a.H, r);
+  const WRow row = gate_up_row<FMT>(a.ws_gate, a.ws_up, a.ss_gate, a.ss_up, 0, n0, a.S, a.H, lane);
   red.v[wave][lane] = wave_tile<FMT>(row, xrow, live, 0, static_cast<int>(ceil_div(a.H, SkinnyFmt<FMT>::kBlk)), a.H,
-                                     a.hvec, wave, g);
+                                     a.hvec, wave, lane);
   __syncthreads();
   if (wave == 0) {
     const f32x4 s = red_sum(red, lane);
@@ -247,6 +305,7 @@ struct Routing {
   float seg_w[kFewSlots + 1][kFewTokens];        // its weight, 0 if not served
 };
 struct RouteScratch {
+  float z[kFewTokens][kMaxExperts + 1];   // logits, the shared gate's last
   unsigned long long agg[kMaxExperts];
   int seg_of[kMaxExperts];
   int nu, dropped, empty;
@@ -258,22 +317,29 @@ __device__ void route_tokens(const FewArgs& a, Routing& R, RouteScratch& C, bool
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const size_t plane = static_cast<size_t>(kFewTokens) * a.ldz;
   constexpr int NJ = kMaxExperts / kWave;
+  // The planes added in order; all loads of a thread are in flight together.
+  for (int i = tid; i < a.T * a.ncols; i += kFewThreads) {
+    const int t = i / a.ncols, c = i - t * a.ncols;
+    const float* zr = a.z + static_cast<size_t>(t) * a.ldz + c;
+    float v[kFewRouterParts];
+#pragma unroll
+    for (int p = 0; p < kFewRouterParts; ++p) v[p] = p < a.parts ? zr[p * plane] : 0.f;
+    const float b = (a.bias && c < a.E) ? a.bias[static_cast<size_t>(t) * a.E + c] : 0.f;
+    float s = v[0];
+#pragma unroll
+    for (int p = 1; p < kFewRouterParts; ++p) s += v[p];
+    C.z[t][c] = s + b;
+  }
+  __syncthreads();
   for (int t = wave; t < a.T; t += kFewWaves) {
-    const float* zr = a.z + static_cast<size_t>(t) * a.ldz;
-    auto logit = [&](int c) {
-      float s = zr[c];
-      for (int p = 1; p < a.parts; ++p) s += zr[p * plane + c];
-      return s;
-    };
-    const float gate_logit = (a.S > 0 && lane == 0) ? logit(a.E) : 0.f;
+    const float gate_logit = (a.S > 0 && lane == 0) ? C.z[t][a.E] : 0.f;
     uint32_t key[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
       const int e = lane + kWave * j;
       key[j] = 0;
       if (e < a.E) {
-        float v = logit(e);
-        if (a.bias) v += a.bias[static_cast<size_t>(t) * a.E + e];
+        const float v = C.z[t][e];
         key[j] = order_key(v == v ? v : -INFINITY);
       }
     }
@@ -397,10 +463,6 @@ __device__ void route_tokens(const FewArgs& a, Routing& R, RouteScratch& C, bool
 
   // Segments: the touched experts in ascending order.  A slot of weight 0 is not run.
   for (int e = tid; e < kMaxExperts; e += kFewThreads) C.seg_of[e] = 0;
-  for (int i = tid; i < (kFewSlots + 1) * kFewTokens; i += kFewThreads) {
-    (&R.seg_slot[0][0])[i] = -1;
-    (&R.seg_w[0][0])[i] = 0.f;
-  }
   __syncthreads();
   for (int i = tid; i < slots; i += kFewThreads)
     if (R.ids[i] >= 0 && R.w[i] != 0.f) C.seg_of[R.ids[i]] = 1;
@@ -419,6 +481,11 @@ __device__ void route_tokens(const FewArgs& a, Routing& R, RouteScratch& C, bool
       n += __popcll(m);
     }
     if (lane == 0) R.n = n;
+  }
+  __syncthreads();
+  for (int i = tid; i < (R.n + 1) * kFewTokens; i += kFewThreads) {
+    (&R.seg_slot[0][0])[i] = -1;
+    (&R.seg_w[0][0])[i] = 0.f;
   }
   __syncthreads();
   for (int i = tid; i < slots; i += kFewThreads)
@@ -444,126 +511,252 @@ __device__ void route_tokens(const FewArgs& a, Routing& R, RouteScratch& C, bool
 
 // ---------------------------------------------------------------- second kernel
 
+// A block of the down half: weights and the planes of h that meet them.
 template <int FMT>
 struct DownBlk {
+  static constexpr int kPlanes = FMT == kDtypeF32 ? 1 : 3;
   WBlk<FMT> w;
-  XBlk<FMT> hi, lo;
+  XBlk<FMT> h[kPlanes];
+};
+
+// The next gate/up tile, or -1 when all queues are empty (called by one thread; q:
+// the queue it is at, all queues from `home` on are tried).  Queue q holds the q-th
+// eighth of the tiles.
+__device__ __forceinline__ int take_tile(int* ctl, int items, int home, int& tried) {
+  for (; tried < kQueues; ++tried) {
+    const int q = (home + tried) % kQueues;
+    const int lo = q * items / kQueues, n = (q + 1) * items / kQueues - lo;
+    int* c = ctl + Ctl::kQueue + q * Ctl::kLine;
+    // Other queues are looked at before they are written to.
+    if (tried > 0 && ld_shared(c) >= n) continue;
+    const int i = ctl_add(c, 1);
+    if (i < n) return lo + i;
+  }
+  return -1;
+}
+
+// The down half: the H / 16 output tiles, each contracted over the blocks of all
+// touched experts and the shared expert, are one line of tiles * nblk blocks that is
+// cut into equal ranges, so that every workgroup reads the same number of weights.
+// A tile that a cut goes through is added up from its parts, in their order, by the
+// workgroup that finishes its part last.  Up to one range for each workgroup, then
+// up to four of them, handed out as they are finished, while a range stays longer
+// than kLongRange blocks.
+constexpr int kMaxRanges = 4 * kFewGrid;
+constexpr int kShortRange = 2 * kFewWaves;   // blocks: two for each wave
+constexpr int kLongRange = 16 * kFewWaves;
+struct DownCut {
+  int tiles, nblk, ranges, q, rem;   // the first rem ranges hold q + 1 blocks, the others q
+  __device__ DownCut(int tiles_, int nblk_) : tiles(tiles_), nblk(nblk_) {
+    const int all = tiles * nblk;
+    ranges = max(1, min(kFewGrid, all / kShortRange));
+    if (all / kLongRange > kFewGrid) ranges = min(kMaxRanges, all / kLongRange);
+    q = all / ranges;
+    rem = all - q * ranges;
+  }
+  __device__ int start(int b) const { return b * q + min(b, rem); }
+  __device__ int owner(int f) const {          // the range that holds block f
+    const int wide = rem * (q + 1);
+    return f < wide ? f / (q + 1) : rem + (f - wide) / q;
+  }
 };
 
 template <int FMT>
-__global__ void __launch_bounds__(kFewThreads, 4) few_second_kernel(FewArgs a) {
+__global__ void __launch_bounds__(kFewThreads, 2) few_second_kernel(FewArgs a) {
   using F = SkinnyFmt<FMT>;
   __shared__ Red red;
   __shared__ Routing R;
   __shared__ RouteScratch C;
-  __shared__ int s_item;
+  __shared__ int s_next;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
   route_tokens(a, R, C, blockIdx.x == 0);
 
+  // ---- gate/up tiles.  The next tile is taken while one is running.
   const int n = R.n;
-  const int hb = static_cast<int>(ceil_div(a.H, F::kBlk)), ib = static_cast<int>(ceil_div(a.I, F::kBlk)),
-            sb = static_cast<int>(ceil_div(a.S, F::kBlk));
-  const int gu_tiles = static_cast<int>(ceil_div(a.I, 8));
-  const int gu_items = n * gu_tiles;
-  const int total = gu_items + static_cast<int>(ceil_div(a.H, 16));
-  const size_t h_shared = static_cast<size_t>(a.T) * a.K * a.I;
-  bool ready = false;
-
-  for (;;) {
-    __syncthreads();                 // the previous item's red and s_item have been read
-    if (tid == 0) s_item = __hip_atomic_fetch_add(&a.ctl[0], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const int gu_tiles = static_cast<int>(ceil_div(a.I, 8)), items = n * gu_tiles;
+  const int hb = static_cast<int>(ceil_div(a.H, F::kBlk));
+  const void* xrow = static_cast<const uint8_t*>(a.x) + static_cast<size_t>(min(r, a.T - 1)) * a.H * (F::kF32 ? 4 : 2);
+  int tried = 0, finished = 0;
+  if (tid == 0) s_next = take_tile(a.ctl, items, blockIdx.x % kQueues, tried);
+  __syncthreads();
+  int item = __builtin_amdgcn_readfirstlane(s_next);
+  while (item >= 0) {
+    const int seg = item / gu_tiles, n0 = item % gu_tiles * 8;
+    const int e = __builtin_amdgcn_readfirstlane(R.seg_expert[seg]);
+    const WRow row = gate_up_row<FMT>(a.w_gate, a.w_up, a.s_gate, a.s_up, static_cast<size_t>(e) * a.I, n0, a.I, a.H, lane);
+    int next = -1;
+    __syncthreads();                 // s_next has been read, the previous tile added up
+    if (tid == 0) next = take_tile(a.ctl, items, blockIdx.x % kQueues, tried);
+    red.v[wave][lane] = wave_tile<FMT>(row, xrow, R.seg_slot[seg][r] >= 0, 0, hb, a.H, a.hvec, wave, lane);
+    if (tid == 0) s_next = next;
     __syncthreads();
-    const int item = __builtin_amdgcn_readfirstlane(s_item);
-    if (item >= total) break;
-    if (item < gu_items) {
-      const int seg = item / gu_tiles, n0 = item % gu_tiles * 8;
-      const int e = __builtin_amdgcn_readfirstlane(R.seg_expert[seg]);
-      const WRow row = gate_up_row<FMT>(a.w_gate, a.w_up, a.s_gate, a.s_up, static_cast<size_t>(e) * a.I, n0, a.I,
-                                        a.H, r);
-      const void* xrow = static_cast<const uint8_t*>(a.x) + static_cast<size_t>(min(r, a.T - 1)) * a.H * (F::kF32 ? 4 : 2);
-      red.v[wave][lane] = wave_tile<FMT>(row, xrow, R.seg_slot[seg][r] >= 0, 0, hb, a.H, a.hvec, wave, g);
-      __syncthreads();
-      if (wave == 0) {
-        const f32x4 s = red_sum(red, lane);
-        store_h<FMT>(a, s, 0, n0, a.I, lane, [&](int t) { return static_cast<int>(R.seg_slot[seg][t]); });
-        // One wave wrote the item's h, so its release covers all of it.
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-        if (lane == 0) __hip_atomic_fetch_add(&a.ctl[1], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
-      continue;
-    }
-    if (!ready) {                    // uniform across the workgroup
-      if (tid == 0)
-        while (__hip_atomic_load(&a.ctl[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < gu_items)
-          __builtin_amdgcn_s_sleep(1);
-      __syncthreads();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-      ready = true;
-    }
-    const int n0 = (item - gu_items) * 16;
-    const int orow = min(n0 + r, a.H - 1);
-    const int nblk = n * ib + (a.S > 0 ? sb : 0);
-    const int lo = static_cast<int>(static_cast<int64_t>(wave) * nblk / kFewWaves);
-    const int hi = static_cast<int>(static_cast<int64_t>(wave + 1) * nblk / kFewWaves);
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    auto seg_of = [&](int b) { return min(b / ib, n); };
-    two_ahead<DownBlk<FMT>>(
-        hi - lo,
-        [&](int i, DownBlk<FMT>& k) {
-          const int b = lo + i, seg = seg_of(b), kb = b - seg * ib;
-          const bool shared = seg == n;
-          const int width = shared ? a.S : a.I;
-          const size_t wrow = shared ? orow : static_cast<size_t>(R.seg_expert[seg]) * a.H + orow;
-          const WRow row = weight_row<FMT>(shared ? a.ws_down : a.w_down, shared ? a.ss_down : a.s_down, wrow, width);
-          const bool vec = shared ? a.svec : a.ivec;
-          load_w<FMT>(k.w, row, kb, g, width, vec);
-          const int slot = R.seg_slot[seg][r];
-          const size_t ho = (shared ? h_shared : 0) + static_cast<size_t>(max(slot, 0)) * width;
-          if constexpr (F::kF32) {
-            load_x<FMT>(k.hi, static_cast<const float*>(a.h) + ho, kb, g, width, vec, slot >= 0);
-          } else {
-            load_x<FMT>(k.hi, static_cast<const uint16_t*>(a.h) + ho, kb, g, width, vec, slot >= 0);
-            load_x<FMT>(k.lo, static_cast<const uint16_t*>(a.h_lo) + ho, kb, g, width, vec, slot >= 0);
-          }
-        },
-        [&](int i, DownBlk<FMT>& k) {
-          const int seg = seg_of(lo + i);
-          f32x4 t = mma_raw<FMT>(k.hi, k.w, f32x4{0.f, 0.f, 0.f, 0.f});
-          if constexpr (!F::kF32) t = mma_raw<FMT>(k.lo, k.w, t);
-          const float4 w = *reinterpret_cast<const float4*>(&R.seg_w[seg][4 * g]);
-          const float ws[4] = {w.x, w.y, w.z, w.w};
-          // A token that the expert does not serve takes nothing, not 0 * inf either.
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float v = FMT == kDtypeFp8 ? t[q] * k.w.s : t[q];
-            acc[q] = ws[q] != 0.f ? fmaf(ws[q], v, acc[q]) : acc[q];
-          }
-        });
-    red.v[wave][lane] = acc;
-    __syncthreads();
-    if (wave == 0 && n0 + r < a.H) {
+    item = __builtin_amdgcn_readfirstlane(s_next);
+    if (wave == 0) {
       const f32x4 s = red_sum(red, lane);
+      store_h<FMT>(a, s, 0, n0, a.I, lane, [&](int t) { return static_cast<int>(R.seg_slot[seg][t]); });
+    }
+    ++finished;
+  }
+  // Every h of this workgroup was stored by wave 0.  The last one to count sees all
+  // counts, and says so to the others.
+  int* go = a.ctl + Ctl::kGo;
+  auto all_counted = [&]() {
+    int c = lane < Ctl::kGroups ? ld_shared(a.ctl + Ctl::kDone + lane * Ctl::kLine) : 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 4 * g + i;
-        if (t < a.T) {
-          const size_t o = static_cast<size_t>(t) * a.H + n0 + r;
-          if (a.y) a.y[o] = s[i];
-          if (a.y_act) {
-            if (a.act_bf16) static_cast<uint16_t*>(a.y_act)[o] = f32_to_bf16_bits(s[i]);
-            else static_cast<float*>(a.y_act)[o] = s[i];
+    for (int o = 8; o > 0; o >>= 1) c += __shfl_xor(c, o, 16);
+    return __builtin_amdgcn_readfirstlane(c) >= items;
+  };
+  const int group = blockIdx.x % Ctl::kGroups;
+  if (wave == 0 && finished > 0) {
+    stores_done();
+    if (lane == 0) ctl_add(a.ctl + Ctl::kDone + group * Ctl::kLine, finished);
+    stores_done();
+    if (all_counted() && lane < Ctl::kGroups) st_shared(go + lane * Ctl::kLine, 1);
+  }
+
+  // ---- the down half
+  const int ib = static_cast<int>(ceil_div(a.I, F::kBlk)), sb = static_cast<int>(ceil_div(a.S, F::kBlk));
+  const int nblk = n * ib + sb;
+  if (nblk == 0) {                   // no expert at all: y is zero
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kFewThreads + tid; i < static_cast<int64_t>(a.T) * a.H;
+         i += kFewGrid * kFewThreads) {
+      if (a.y) a.y[i] = 0.f;
+      if (a.y_act) {
+        if (a.act_bf16) static_cast<uint16_t*>(a.y_act)[i] = 0;
+        else static_cast<float*>(a.y_act)[i] = 0.f;
+      }
+    }
+    return;
+  }
+  const DownCut cut(static_cast<int>(ceil_div(a.H, 16)), nblk);
+  if (blockIdx.x >= cut.ranges) return;
+  if (wave == 0 && items > 0) {
+    // The flag is one line for 32 workgroups; now and then the counts themselves.
+    for (int i = 1; ld_shared(go + group * Ctl::kLine) == 0; ++i) {
+      if (i % 16 == 0 && all_counted()) break;
+      __builtin_amdgcn_s_sleep(8);
+    }
+  }
+  __syncthreads();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+
+  const size_t h_shared = static_cast<size_t>(a.T) * a.K * a.I;
+  int b = blockIdx.x;
+  while (b < cut.ranges) {
+    const int f0 = cut.start(b), f1 = cut.start(b + 1);
+    const int tile0 = f0 / nblk, tile1 = (f1 - 1) / nblk;
+    int next = cut.ranges;
+    if (tid == 0 && cut.ranges > kFewGrid) next = kFewGrid + ctl_add(a.ctl + Ctl::kRange, 1);
+    for (int tile = tile0; tile <= tile1; ++tile) {
+      const int base = tile * nblk;
+      const int k0 = max(f0 - base, 0), k1 = min(f1 - base, nblk);
+      const int lo = k0 + wave * (k1 - k0) / kFewWaves, hi = k0 + (wave + 1) * (k1 - k0) / kFewWaves;
+      // Positions of the loads and of their use: segment and block in it.
+      int lseg = min(lo / ib, n), lkb = lo - lseg * ib, useg = lseg, ukb = lkb;
+      WRow row{};
+      size_t hoff = 0;
+      bool live = false;
+      auto enter = [&]() __attribute__((always_inline)) {
+        const bool shared = lseg == n;
+        const int width = shared ? a.S : a.I;
+        const size_t first = shared ? 0 : static_cast<size_t>(__builtin_amdgcn_readfirstlane(R.seg_expert[lseg])) * a.H;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          set_row<FMT>(row, h, shared ? a.ws_down : a.w_down, shared ? a.ss_down : a.s_down,
+                       first + min(tile * 16 + 8 * h + (lane & 7), a.H - 1), width);
+        const int slot = R.seg_slot[lseg][r];
+        live = slot >= 0;
+        hoff = ((shared ? h_shared : 0) + static_cast<size_t>(max(slot, 0)) * width) * (F::kF32 ? 4 : 2);
+      };
+      if (lo < hi) enter();
+      Acc acc{};
+      batches<FewBatch<FMT>::kDown, DownBlk<FMT>>(
+          hi - lo,
+          [&](DownBlk<FMT>& k) __attribute__((always_inline)) {
+            if (lseg < n && lkb == ib) {
+              ++lseg;
+              lkb = 0;
+              enter();
+            }
+            const bool shared = lseg == n;
+            const int width = shared ? a.S : a.I, vec = shared ? a.svec : a.ivec;
+            load_w<FMT>(k.w, row, lkb, lane, width, vec);
+#pragma unroll
+            for (int p = 0; p < DownBlk<FMT>::kPlanes; ++p)
+              load_x<FMT>(k.h[p], static_cast<const uint8_t*>(a.h[p]) + hoff, lkb, lane, width, vec, live);
+            ++lkb;
+          },
+          [&](DownBlk<FMT>& k) __attribute__((always_inline)) {
+            if (useg < n && ukb == ib) {
+              ++useg;
+              ukb = 0;
+            }
+            ++ukb;
+            Acc t{};
+            mma_planes<FMT, DownBlk<FMT>::kPlanes>(k.h, k.w, t);
+            const float4 wt = *reinterpret_cast<const float4*>(&R.seg_w[useg][4 * g]);
+            const float ws[4] = {wt.x, wt.y, wt.z, wt.w};
+            // A token that the expert does not serve takes nothing, not 0 * inf either.
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const float v = FMT == kDtypeFp8 ? t.v[h][half][q] * k.w.s[h] : t.v[h][half][q];
+                  const float s = acc.v[h][half][q];
+                  acc.v[h][half][q] = ws[q] != 0.f ? fmaf(ws[q], v, s) : s;
+                }
+          });
+      const f32x4 mine = tile_sums(acc, lane);
+      __syncthreads();               // the previous tile has been added up
+      red.v[wave][lane] = mine;
+      if (tid == 0) s_next = next;
+      __syncthreads();
+      if (wave != 0) continue;
+      f32x4 s = red_sum(red, lane);
+      if (k0 > 0 || k1 < nblk) {     // a part: the last one to arrive adds them up
+        const int b0 = cut.owner(base), b1 = cut.owner(base + nblk - 1);
+        float* part = a.part + (static_cast<size_t>(b) * 2 + (tile == tile0 ? 0 : 1)) * 256;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st_shared(part + 64 * i + lane, s[i]);
+        stores_done();
+        int before = 0;
+        if (lane == 0) before = ctl_add(a.ctl + Ctl::kTile + tile, 1);
+        if (__builtin_amdgcn_readfirstlane(before) != b1 - b0) continue;
+        s = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int o = b0; o <= b1; ++o) {
+          // The tile is range o's first one, unless the range began in an earlier tile.
+          const float* p = a.part + (static_cast<size_t>(o) * 2 + (cut.start(o) / nblk == tile ? 0 : 1)) * 256;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[i] += ld_shared(p + 64 * i + lane);
+        }
+      }
+      const int col = tile * 16 + r;
+      if (col < a.H) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = 4 * g + i;
+          if (t < a.T) {
+            const size_t o = static_cast<size_t>(t) * a.H + col;
+            if (a.y) a.y[o] = s[i];
+            if (a.y_act) {
+              if (a.act_bf16) static_cast<uint16_t*>(a.y_act)[o] = f32_to_bf16_bits(s[i]);
+              else static_cast<float*>(a.y_act)[o] = s[i];
+            }
           }
         }
       }
     }
+    b = __builtin_amdgcn_readfirstlane(s_next);
   }
 }
 
 // ---------------------------------------------------------------- host
 
 struct FewLayout {
-  size_t ctl, z, h, h_lo, total;
+  size_t ctl, z, h[3], part, total;
   int ldz, parts;
 };
 
@@ -577,17 +770,25 @@ FewLayout few_layout(const moe_config& c, int64_t T) {
   };
   const bool f32 = c.weight_dtype == MOE_DTYPE_F32;
   L.ldz = static_cast<int>(align_up(c.n_routed_experts + 1, 16));
-  // At least one block of contraction for each wave of a part.
-  const int blocks = static_cast<int>(ceil_div(c.hidden_size, f32 ? 32 : 128));
-  L.parts = std::max(1, std::min(kFewRouterParts, blocks / kFewWaves));
-  L.ctl = take(2 * sizeof(int));
+  // At least two blocks of contraction for each wave of a part.
+  const int blocks = static_cast<int>(ceil_div(c.hidden_size, f32 ? 32 : 64));
+  L.parts = std::max(1, std::min(kFewRouterParts, blocks / (2 * kFewWaves)));
+  L.ctl = take(ctl_ints(c.hidden_size) * sizeof(int));
   L.z = take(static_cast<size_t>(L.parts) * kFewTokens * L.ldz * sizeof(float));
   const size_t elems = static_cast<size_t>(T) * c.num_experts_per_tok * c.moe_intermediate_size +
                        static_cast<size_t>(T) * c.shared_expert_intermediate_size;
-  L.h = take(elems * (f32 ? 4 : 2));
-  L.h_lo = take(f32 ? 0 : elems * 2);
+  for (int p = 0; p < 3; ++p) L.h[p] = take(f32 ? (p ? 0 : elems * 4) : elems * 2);
+  L.part = take(static_cast<size_t>(kMaxRanges) * 2 * 256 * sizeof(float));
   L.total = off;
   return L;
+}
+
+// The second kernel numbers its gate/up tiles and its down blocks in 32 bits.
+bool few_countable(const moe_config& c) {
+  const int64_t experts = std::min<int64_t>(c.n_routed_experts, kFewSlots);
+  const int64_t tiles = ceil_div(c.hidden_size, 16);
+  const int64_t nblk = experts * ceil_div(c.moe_intermediate_size, 32) + ceil_div(c.shared_expert_intermediate_size, 32);
+  return experts * ceil_div(c.moe_intermediate_size, 8) * kQueues < (int64_t{1} << 31) && tiles * nblk < (int64_t{1} << 31);
 }
 
 bool misaligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
@@ -612,7 +813,7 @@ int moe_layer_few_workspace_size(const moe_config* cfg, int32_t max_tokens, size
   size_t n = 0;
   const int st = moe_workspace_size(cfg, max_tokens, bytes ? &n : nullptr);   // the layer's checks
   if (st) return st;
-  if (max_tokens > kFewTokens) return MOE_ERR_UNSUPPORTED;
+  if (max_tokens > kFewTokens || !few_countable(*cfg)) return MOE_ERR_UNSUPPORTED;
   *bytes = few_layout(*cfg, max_tokens).total;
   return MOE_OK;
 }
@@ -675,8 +876,8 @@ int moe_layer_few(const moe_config* cfg, int32_t T, const void* x, const void* w
   a.act_bf16 = f32 ? 0 : 1;
   a.ctl = reinterpret_cast<int*>(ws + L.ctl);
   a.z = reinterpret_cast<float*>(ws + L.z);
-  a.h = ws + L.h;
-  a.h_lo = ws + L.h_lo;
+  for (int p = 0; p < 3; ++p) a.h[p] = ws + L.h[p];
+  a.part = reinterpret_cast<float*>(ws + L.part);
   a.T = T;
   a.H = cfg->hidden_size;
   a.E = cfg->n_routed_experts;
@@ -689,7 +890,7 @@ int moe_layer_few(const moe_config* cfg, int32_t T, const void* x, const void* w
   a.norm = cfg->norm_topk_prob;
   a.budget = cfg->expert_budget;
   a.top_p = (cfg->top_p > 0.f && cfg->top_p < 1.f) ? cfg->top_p : 0.f;
-  a.rvec = a.hvec = wide && a.H % 4 == 0;
+  a.hvec = wide && a.H % 4 == 0;
   // h rows: the workspace is aligned, the shared rows start at T*K*I.
   a.ivec = wide && a.I % 4 == 0;
   a.svec = wide && a.S % 4 == 0 && (static_cast<int64_t>(T) * a.K * a.I) % 4 == 0;
