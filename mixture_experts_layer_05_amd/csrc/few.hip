@@ -49,7 +49,7 @@ constexpr int kFewGrid = 512;
 constexpr int kFewTokens = MOE_FEW_TOKENS;
 static_assert(kFewTokens == kSkinnyRows, "one MFMA tile of tokens");
 constexpr int kFewSlots = kFewTokens * kMaxTopK;
-constexpr int kFewRouterParts = 8;         // contraction parts of the router, at most
+constexpr int kFewRouterParts = 4;         // contraction parts of the router, at most
 constexpr int kQueues = 8;
 
 struct FewArgs {
@@ -67,7 +67,7 @@ struct FewArgs {
   int* ctl;                // counters of the second kernel, see Ctl
   float* z;                // [parts, 16, ldz] partial logits
   void* h[3];              // planes of [T*K, I] routed then [T, S] shared rows
-  float* part;             // [2 * kMaxRanges, 256] partial down tiles
+  float* part;             // [2 * kMaxRanges, sets, 256] partial down tiles
   int T, H, E, I, K, S, ncols, ldz, parts, norm, budget;
   float top_p;
   int hvec, ivec, svec;   // f32: rows of that length can be read in 16-byte pieces
@@ -92,12 +92,16 @@ __device__ __forceinline__ f32x4 red_sum(const Red& r, int lane) {
   return s;
 }
 
-// Blocks a wave loads at a time, within its 256 registers.
+// Blocks a wave loads at a time, within its 256 registers.  In the down half, where
+// a block of weights meets three planes of h, a wave runs kSets tiles side by side on
+// one block of h.
 template <int FMT>
 struct FewBatch {
   static constexpr int kGateUp = FMT == kDtypeMxfp4 ? 4 : FMT == kDtypeFp8 ? 6 : 10;
-  static constexpr int kDown = FMT == kDtypeMxfp4 ? 1 : FMT == kDtypeFp8 ? 3 : 5;
+  static constexpr int kDown = FMT == kDtypeMxfp4 ? 1 : FMT == kDtypeFp8 ? 2 : 4;
+  static constexpr int kSets = FMT == kDtypeF32 ? 1 : FMT == kDtypeBf16 ? 2 : 4;
 };
+constexpr int kMaxSets = 4;
 
 template <int FMT>
 struct GuBlk {
@@ -108,50 +112,39 @@ struct GuBlk {
 // This wave's quarter of x W^T over the contraction [b0, b1), in blocks, of one
 // 16-row weight tile.
 template <int FMT>
-__device__ __forceinline__ f32x4 wave_tile(const WRow& row, const void* xrow, bool live, int b0, int b1, int kdim,
-                                           bool vec, int wave, int lane) {
+__device__ __forceinline__ f32x4 wave_tile(const Matrices& m, const WRow& row, const void* x, uint32_t xoff, bool live,
+                                           int b0, int b1, int kdim, bool vec, int wave, int lane) {
   const int n = b1 - b0;
   const int lo = b0 + wave * n / kFewWaves, hi = b0 + (wave + 1) * n / kFewWaves;
-  Acc acc{};
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   int at = lo;
   batches<FewBatch<FMT>::kGateUp, GuBlk<FMT>>(
       hi - lo,
       [&](GuBlk<FMT>& k) __attribute__((always_inline)) {
-        load_w<FMT>(k.w, row, at, lane, kdim, vec);
-        load_x<FMT>(k.x[0], xrow, at, lane, kdim, vec, live);
+        load_w<FMT>(k.w, m, row, at, lane, kdim, vec);
+        load_x<FMT>(k.x[0], x, xoff, at, lane, kdim, vec, live);
         ++at;
       },
-      [&](GuBlk<FMT>& k) __attribute__((always_inline)) { mma_block<FMT>(k.x, k.w, acc); });
-  return tile_sums(acc, lane);
+      [&](GuBlk<FMT>& k) __attribute__((always_inline)) { acc = mma_planes<FMT, 1>(k.x, k.w, lane, acc); });
+  return acc;
 }
 
+// A gate/up tile: the first 8 rows lie in the gate matrix of an expert, the others in
+// its up matrix.
 template <int FMT>
-__device__ __forceinline__ size_t row_bytes(int k) {
-  return FMT == kDtypeF32 ? static_cast<size_t>(k) * 4
-       : FMT == kDtypeBf16 ? static_cast<size_t>(k) * 2
-       : FMT == kDtypeFp8 ? static_cast<size_t>(k) : static_cast<size_t>(k) / 2;
+__device__ __forceinline__ Matrices gate_up(const void* wg, const void* wu, const void* sg, const void* su, int expert,
+                                            int width, int H) {
+  const size_t w = static_cast<size_t>(expert) * width * row_bytes<FMT>(H);
+  const size_t s = static_cast<size_t>(expert) * width * scale_bytes<FMT>(H);
+  return Matrices{{static_cast<const uint8_t*>(wg) + w, static_cast<const uint8_t*>(wu) + w},
+                  {static_cast<const uint8_t*>(sg) + s, static_cast<const uint8_t*>(su) + s}};
 }
+// Its columns [n0, n0 + 8) (past the width: the last row again, not stored).
 template <int FMT>
-__device__ __forceinline__ size_t scale_bytes(int k) {
-  return FMT == kDtypeFp8 ? static_cast<size_t>(k) / kGroup * 4
-       : FMT == kDtypeMxfp4 ? static_cast<size_t>(k) / kMxBlock : 0;
-}
-template <int FMT>
-__device__ __forceinline__ void set_row(WRow& r, int h, const void* w, const void* s, size_t row, int k) {
-  r.p[h] = static_cast<const uint8_t*>(w) + row * row_bytes<FMT>(k);
-  r.s[h] = static_cast<const uint8_t*>(s) + row * scale_bytes<FMT>(k);
-}
-
-// Columns [n0, n0 + 8) of a gate/up half: the tile's first 8 rows are gate rows, the
-// others the up rows of the same columns (past the width: the last row again, not
-// stored).
-template <int FMT>
-__device__ __forceinline__ WRow gate_up_row(const void* wg, const void* wu, const void* sg, const void* su,
-                                            size_t first, int n0, int width, int H, int lane) {
-  const size_t row = first + min(n0 + (lane & 7), width - 1);
+__device__ __forceinline__ WRow gate_up_row(int n0, int width, int H, int lane) {
   WRow r;
-  set_row<FMT>(r, 0, wg, sg, row, H);
-  set_row<FMT>(r, 1, wu, su, row, H);
+  set_row<FMT>(r, 0, min(n0 + (lane & 7), width - 1), H, lane);
+  set_row<FMT>(r, 1, min(n0 + (lane & 7), width - 1), H, lane);
   return r;
 }
 
@@ -211,13 +204,15 @@ struct Ctl {
   static constexpr int kRange = kGo + kGroups * kLine;      // next down range
   static constexpr int kTile = kRange + kLine;              // finished parts of each down tile
 };
-__host__ __device__ inline int ctl_ints(int H) { return Ctl::kTile + (H + 15) / 16; }
+__host__ __device__ inline int ctl_ints(int H) { return Ctl::kTile + (H + 15) / 16; }   // enough for any kSets
 
 __device__ __forceinline__ int ctl_add(int* p, int v) {
   return __hip_atomic_fetch_add(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // ---------------------------------------------------------------- first kernel
+
+__host__ __device__ inline int router_tiles(int E, int S) { return (E + 15) / 16 + (S > 0 ? 1 : 0); }
 
 template <int FMT>
 __global__ void __launch_bounds__(kFewThreads, 2) few_first_kernel(FewArgs a) {
@@ -227,24 +222,25 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_first_kernel(FewArgs a) {
   const int r = lane & 15, g = lane >> 4;
   for (int i = blockIdx.x * kFewThreads + tid; i < ctl_ints(a.H); i += gridDim.x * kFewThreads) a.ctl[i] = 0;
 
-  const size_t xrow_bytes = static_cast<size_t>(a.H) * (AFMT == kDtypeF32 ? 4 : 2);
-  const void* xrow = static_cast<const uint8_t*>(a.x) + static_cast<size_t>(min(r, a.T - 1)) * xrow_bytes;
+  const uint32_t xoff = static_cast<uint32_t>(min(r, a.T - 1)) * static_cast<uint32_t>(row_bytes<AFMT>(a.H));
   const bool live = r < a.T;
-  const int router = static_cast<int>(ceil_div(a.ncols, 16)) * a.parts;
+  const int router = router_tiles(a.E, a.S) * a.parts;
   const int item = blockIdx.x;
   if (item < router) {
-    const int part = item % a.parts, c0 = item / a.parts * 16;
+    // 16 logits; the last tile is the shared gate's, alone in a matrix of one row.
+    const int part = item % a.parts, tile = item / a.parts;
     const int nb = static_cast<int>(ceil_div(a.H, SkinnyFmt<AFMT>::kBlk));
+    const bool gate = tile * 16 >= a.E;
+    const int c0 = gate ? a.E : tile * 16, cols = gate ? 1 : min(16, a.E - c0);
+    const void* w = gate ? a.w_gcol : a.w_router;
     WRow row;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = min(c0 + 8 * h + (lane & 7), a.ncols - 1);
-      set_row<AFMT>(row, h, c < a.E ? a.w_router : a.w_gcol, nullptr, c < a.E ? c : 0, a.H);
-    }
-    red.v[wave][lane] = wave_tile<AFMT>(row, xrow, live, part * nb / a.parts, (part + 1) * nb / a.parts, a.H,
-                                        a.hvec, wave, lane);
+    for (int h = 0; h < 2; ++h)
+      set_row<AFMT>(row, h, (gate ? 0 : c0) + min(8 * h + (lane & 7), cols - 1), a.H, lane);
+    red.v[wave][lane] = wave_tile<AFMT>(Matrices{{w, w}, {nullptr, nullptr}}, row, a.x, xoff, live,
+                                        part * nb / a.parts, (part + 1) * nb / a.parts, a.H, a.hvec, wave, lane);
     __syncthreads();
-    if (wave == 0 && c0 + r < a.ncols) {
+    if (wave == 0 && r < cols) {
       const f32x4 s = red_sum(red, lane);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -253,9 +249,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_first_kernel(FewArgs a) {
     return;
   }
   const int n0 = (item - router) * 8;
-  const WRow row = gate_up_row<FMT>(a.ws_gate, a.ws_up, a.ss_gate, a.ss_up, 0, n0, a.S, a.H, lane);
-  red.v[wave][lane] = wave_tile<FMT>(row, xrow, live, 0, static_cast<int>(ceil_div(a.H, SkinnyFmt<FMT>::kBlk)), a.H,
-                                     a.hvec, wave, lane);
+  red.v[wave][lane] = wave_tile<FMT>(gate_up<FMT>(a.ws_gate, a.ws_up, a.ss_gate, a.ss_up, 0, a.S, a.H),
+                                     gate_up_row<FMT>(n0, a.S, a.H, lane), a.x, xoff, live, 0,
+                                     static_cast<int>(ceil_div(a.H, SkinnyFmt<FMT>::kBlk)), a.H, a.hvec, wave, lane);
   __syncthreads();
   if (wave == 0) {
     const f32x4 s = red_sum(red, lane);
@@ -275,21 +271,20 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 
+// Maximum over the wave: rotations within the rows of 16 lanes, then the four rows.
 template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
-  const uint32_t o = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
-      static_cast<int>(v), static_cast<int>(v), CTRL, 0xf, 0xf, false));
-  return max(v, o);
+__device__ __forceinline__ uint32_t ror_max(uint32_t v) {
+  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xf, 0xf, true)));
 }
-// Maximum over the wave, in every lane.
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-  v = dpp_max<0x111>(v);      // row_shr 1, 2, 4, 8: lane 15 of each row of 16
-  v = dpp_max<0x112>(v);
-  v = dpp_max<0x114>(v);
-  v = dpp_max<0x118>(v);
-  v = dpp_max<0x142>(v);      // row_bcast 15, 31: lane 63
-  v = dpp_max<0x143>(v);
-  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+  v = ror_max<0x121>(v);
+  v = ror_max<0x122>(v);
+  v = ror_max<0x124>(v);
+  v = ror_max<0x128>(v);
+  const int i = static_cast<int>(v);
+  const uint32_t a = static_cast<uint32_t>(__builtin_amdgcn_readlane(i, 0)), b = static_cast<uint32_t>(__builtin_amdgcn_readlane(i, 16)),
+                 c = static_cast<uint32_t>(__builtin_amdgcn_readlane(i, 32)), d = static_cast<uint32_t>(__builtin_amdgcn_readlane(i, 48));
+  return max(max(a, b), max(c, d));
 }
 
 constexpr double kFewFixed = 8589934592.0;   // 2^33: budget aggregates in fixed point, as in moe_route
@@ -312,86 +307,123 @@ struct RouteScratch {
   int list[kFewSlots];
 };
 
-// Same selection, trim and budget as moe_route.
+// Top-k of one token by one wave (same selection and trim as moe_route).  A lane holds
+// the keys of experts lane, lane + 64, ... in descending order (the lower id first
+// among equals); each round takes the largest head of the lanes.
+template <int NJ>
+__device__ __forceinline__ void route_token(const FewArgs& a, Routing& R, const float* z, int t, int lane) {
+  const float gate_logit = (a.S > 0 && lane == 0) ? z[a.E] : 0.f;
+  uint32_t key[NJ];
+  int id[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int e = lane + kWave * j;
+    const float v = e < a.E ? z[e] : 0.f;
+    key[j] = e < a.E ? order_key(v == v ? v : -INFINITY) : 0;
+    id[j] = e;
+  }
+  // Odd-even merge sort of at most 8: (0 1)(2 3)(4 5)(6 7) (0 2)(1 3)(4 6)(5 7) (1 2)(5 6)
+  // (0 4)(1 5)(2 6)(3 7) (2 4)(3 5) (1 2)(3 4)(5 6), as far as NJ goes.
+  auto order = [&](int i, int j) __attribute__((always_inline)) {
+    if (j >= NJ) return;
+    const bool swap = key[j] > key[i] || (key[j] == key[i] && id[j] < id[i]);
+    const uint32_t k = swap ? key[j] : key[i];
+    key[j] = swap ? key[i] : key[j];
+    key[i] = k;
+    const int e = swap ? id[j] : id[i];
+    id[j] = swap ? id[i] : id[j];
+    id[i] = e;
+  };
+  if constexpr (NJ > 1) { order(0, 1); order(2, 3); order(4, 5); order(6, 7); }
+  if constexpr (NJ > 2) { order(0, 2); order(1, 3); order(4, 6); order(5, 7); order(1, 2); order(5, 6); }
+  if constexpr (NJ > 4) { order(0, 4); order(1, 5); order(2, 6); order(3, 7); order(2, 4); order(3, 5); order(1, 2);
+                          order(3, 4); order(5, 6); }
+  const float zmax = key_value(wave_max_u32(key[0]));
+  // Softmax denominator over all experts (only without renormalisation).
+  float denom_all = 0.f;
+  if (!a.norm) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      if (key[j] != 0) denom_all += expf(key_value(key[j]) - zmax);
+    denom_all = wave_sum(denom_all);
+  }
+  int my_id = -1;
+  float my_z = 0.f;
+  for (int k = 0; k < a.K; ++k) {
+    const uint32_t m = wave_max_u32(key[0]);
+    unsigned long long has = __ballot(key[0] == m);
+    int owner = __builtin_ctzll(has), e = __builtin_amdgcn_readlane(id[0], owner);
+    for (has &= has - 1; has; has &= has - 1) {        // ties: the lowest id
+      const int o = __builtin_ctzll(has), f = __builtin_amdgcn_readlane(id[0], o);
+      if (f < e) { e = f; owner = o; }
+    }
+    const bool pop = lane == owner;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      key[j] = pop ? (j + 1 < NJ ? key[j + 1 < NJ ? j + 1 : j] : 0) : key[j];
+      id[j] = pop ? id[j + 1 < NJ ? j + 1 : j] : id[j];
+    }
+    if (lane == k) { my_id = e; my_z = key_value(m); }
+  }
+  const float p = lane < a.K ? expf(my_z - zmax) : 0.f;
+  bool kept = lane < a.K;
+  if (a.top_p > 0.f) {
+    float before = 0.f, all = 0.f;
+    for (int k = 0; k < a.K; ++k) {
+      const float pk = __shfl(p, k, kWave);
+      if (k < lane) before += pk;
+      all += pk;
+    }
+    kept = kept && (lane == 0 || before < a.top_p * all);
+  }
+  const float pk = kept ? p : 0.f;
+  const float denom = a.norm ? wave_sum(pk) : denom_all;
+  if (lane < a.K) {
+    R.ids[t * a.K + lane] = kept ? my_id : -1;
+    R.w[t * a.K + lane] = pk / denom;
+  }
+  if (lane == 0) R.sg[t] = a.S > 0 ? 1.0f / (1.0f + expf(-gate_logit)) : 0.f;
+}
+
+// Same routing as moe_route, budget included.
 __device__ void route_tokens(const FewArgs& a, Routing& R, RouteScratch& C, bool report) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const size_t plane = static_cast<size_t>(kFewTokens) * a.ldz;
-  constexpr int NJ = kMaxExperts / kWave;
-  // The planes added in order; all loads of a thread are in flight together.
-  for (int i = tid; i < a.T * a.ncols; i += kFewThreads) {
-    const int t = i / a.ncols, c = i - t * a.ncols;
-    const float* zr = a.z + static_cast<size_t>(t) * a.ldz + c;
-    float v[kFewRouterParts];
+  // The planes added in order, four columns to a load (rows of z are multiples of 16
+  // long), kAhead loads of a thread in flight together.
+  constexpr int kAhead = 4;
+  const int quads = static_cast<int>(ceil_div(a.ncols, 4)), all = a.T * quads;
+  for (int i0 = tid; i0 < all; i0 += kFewThreads * kAhead) {
+    f32x4 v[kAhead][kFewRouterParts];
 #pragma unroll
-    for (int p = 0; p < kFewRouterParts; ++p) v[p] = p < a.parts ? zr[p * plane] : 0.f;
-    const float b = (a.bias && c < a.E) ? a.bias[static_cast<size_t>(t) * a.E + c] : 0.f;
-    float s = v[0];
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = min(i0 + k * kFewThreads, all - 1);
+      const float* zr = a.z + static_cast<size_t>(i / quads) * a.ldz + 4 * (i % quads);
 #pragma unroll
-    for (int p = 1; p < kFewRouterParts; ++p) s += v[p];
-    C.z[t][c] = s + b;
+      for (int p = 0; p < kFewRouterParts; ++p)
+        v[k][p] = p < a.parts ? *reinterpret_cast<const f32x4*>(zr + p * plane) : f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + k * kFewThreads;
+      if (i >= all) break;
+      const int t = i / quads, c0 = 4 * (i % quads);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float s = v[k][0][q];
+#pragma unroll
+        for (int p = 1; p < kFewRouterParts; ++p) s += v[k][p][q];
+        const int c = c0 + q;
+        if (c < a.ncols) C.z[t][c] = s + (a.bias && c < a.E ? a.bias[static_cast<size_t>(t) * a.E + c] : 0.f);
+      }
+    }
   }
   __syncthreads();
   for (int t = wave; t < a.T; t += kFewWaves) {
-    const float gate_logit = (a.S > 0 && lane == 0) ? C.z[t][a.E] : 0.f;
-    uint32_t key[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int e = lane + kWave * j;
-      key[j] = 0;
-      if (e < a.E) {
-        const float v = C.z[t][e];
-        key[j] = order_key(v == v ? v : -INFINITY);
-      }
-    }
-    // Softmax denominator over all experts (only without renormalisation).
-    float denom_all = 0.f;
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) top = max(top, key[j]);
-    const float zmax = key_value(wave_max_u32(top));
-    if (!a.norm) {
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        if (lane + kWave * j < a.E) denom_all += expf(key_value(key[j]) - zmax);
-      denom_all = wave_sum(denom_all);
-    }
-    int my_id = -1;
-    float my_z = 0.f;
-    for (int k = 0; k < a.K; ++k) {
-      uint32_t best = 0;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) best = max(best, key[j]);
-      const uint32_t m = wave_max_u32(best);
-      // The lowest id that holds it: ids grow with j, then with the lane.
-      int id = 0x7fffffff;
-#pragma unroll
-      for (int j = NJ - 1; j >= 0; --j) {
-        const unsigned long long has = __ballot(key[j] == m);
-        if (has) id = kWave * j + __builtin_ctzll(has);
-      }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        if (lane + kWave * j == id) key[j] = 0;
-      if (lane == k) { my_id = id; my_z = key_value(m); }
-    }
-    const float p = lane < a.K ? expf(my_z - zmax) : 0.f;
-    bool kept = lane < a.K;
-    if (a.top_p > 0.f) {
-      float before = 0.f, all = 0.f;
-      for (int k = 0; k < a.K; ++k) {
-        const float pk = __shfl(p, k, kWave);
-        if (k < lane) before += pk;
-        all += pk;
-      }
-      kept = kept && (lane == 0 || before < a.top_p * all);
-    }
-    const float pk = kept ? p : 0.f;
-    const float denom = a.norm ? wave_sum(pk) : denom_all;
-    if (lane < a.K) {
-      R.ids[t * a.K + lane] = kept ? my_id : -1;
-      R.w[t * a.K + lane] = pk / denom;
-    }
-    if (lane == 0) R.sg[t] = a.S > 0 ? 1.0f / (1.0f + expf(-gate_logit)) : 0.f;
+    if (a.E <= kWave) route_token<1>(a, R, C.z[t], t, lane);
+    else if (a.E <= 2 * kWave) route_token<2>(a, R, C.z[t], t, lane);
+    else if (a.E <= 4 * kWave) route_token<4>(a, R, C.z[t], t, lane);
+    else route_token<8>(a, R, C.z[t], t, lane);
   }
   const int slots = a.T * a.K;
   for (int e = tid; e < kMaxExperts; e += kFewThreads) { C.agg[e] = 0ull; C.seg_of[e] = 0; }
@@ -515,7 +547,7 @@ __device__ void route_tokens(const FewArgs& a, Routing& R, RouteScratch& C, bool
 template <int FMT>
 struct DownBlk {
   static constexpr int kPlanes = FMT == kDtypeF32 ? 1 : 3;
-  WBlk<FMT> w;
+  WBlk<FMT> w[FewBatch<FMT>::kSets];
   XBlk<FMT> h[kPlanes];
 };
 
@@ -535,16 +567,16 @@ __device__ __forceinline__ int take_tile(int* ctl, int items, int home, int& tri
   return -1;
 }
 
-// The down half: the H / 16 output tiles, each contracted over the blocks of all
+// The down half: the output tiles (16 kSets columns), each contracted over the blocks of all
 // touched experts and the shared expert, are one line of tiles * nblk blocks that is
 // cut into equal ranges, so that every workgroup reads the same number of weights.
 // A tile that a cut goes through is added up from its parts, in their order, by the
 // workgroup that finishes its part last.  Up to one range for each workgroup, then
-// up to four of them, handed out as they are finished, while a range stays longer
+// up to eight of them, handed out as they are finished, while a range stays longer
 // than kLongRange blocks.
-constexpr int kMaxRanges = 4 * kFewGrid;
+constexpr int kMaxRanges = 8 * kFewGrid;
 constexpr int kShortRange = 2 * kFewWaves;   // blocks: two for each wave
-constexpr int kLongRange = 16 * kFewWaves;
+constexpr int kLongRange = 4 * kFewWaves;
 struct DownCut {
   int tiles, nblk, ranges, q, rem;   // the first rem ranges hold q + 1 blocks, the others q
   __device__ DownCut(int tiles_, int nblk_) : tiles(tiles_), nblk(nblk_) {
@@ -564,19 +596,24 @@ struct DownCut {
 template <int FMT>
 __global__ void __launch_bounds__(kFewThreads, 2) few_second_kernel(FewArgs a) {
   using F = SkinnyFmt<FMT>;
-  __shared__ Red red;
+  constexpr int NS = FewBatch<FMT>::kSets;
+  // The routing's scratch is done with when the first tile is added up.
+  __shared__ union {
+    RouteScratch scratch;
+    Red red[NS];
+  } U;
   __shared__ Routing R;
-  __shared__ RouteScratch C;
+  Red(&red)[NS] = U.red;
   __shared__ int s_next;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
-  route_tokens(a, R, C, blockIdx.x == 0);
+  route_tokens(a, R, U.scratch, blockIdx.x == 0);
 
   // ---- gate/up tiles.  The next tile is taken while one is running.
   const int n = R.n;
   const int gu_tiles = static_cast<int>(ceil_div(a.I, 8)), items = n * gu_tiles;
   const int hb = static_cast<int>(ceil_div(a.H, F::kBlk));
-  const void* xrow = static_cast<const uint8_t*>(a.x) + static_cast<size_t>(min(r, a.T - 1)) * a.H * (F::kF32 ? 4 : 2);
+  const uint32_t xoff = static_cast<uint32_t>(min(r, a.T - 1)) * static_cast<uint32_t>(a.H) * (F::kF32 ? 4 : 2);
   int tried = 0, finished = 0;
   if (tid == 0) s_next = take_tile(a.ctl, items, blockIdx.x % kQueues, tried);
   __syncthreads();
@@ -584,16 +621,17 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_second_kernel(FewArgs a) {
   while (item >= 0) {
     const int seg = item / gu_tiles, n0 = item % gu_tiles * 8;
     const int e = __builtin_amdgcn_readfirstlane(R.seg_expert[seg]);
-    const WRow row = gate_up_row<FMT>(a.w_gate, a.w_up, a.s_gate, a.s_up, static_cast<size_t>(e) * a.I, n0, a.I, a.H, lane);
+    const Matrices m = gate_up<FMT>(a.w_gate, a.w_up, a.s_gate, a.s_up, e, a.I, a.H);
+    const WRow row = gate_up_row<FMT>(n0, a.I, a.H, lane);
     int next = -1;
     __syncthreads();                 // s_next has been read, the previous tile added up
     if (tid == 0) next = take_tile(a.ctl, items, blockIdx.x % kQueues, tried);
-    red.v[wave][lane] = wave_tile<FMT>(row, xrow, R.seg_slot[seg][r] >= 0, 0, hb, a.H, a.hvec, wave, lane);
+    red[0].v[wave][lane] = wave_tile<FMT>(m, row, a.x, xoff, R.seg_slot[seg][r] >= 0, 0, hb, a.H, a.hvec, wave, lane);
     if (tid == 0) s_next = next;
     __syncthreads();
     item = __builtin_amdgcn_readfirstlane(s_next);
     if (wave == 0) {
-      const f32x4 s = red_sum(red, lane);
+      const f32x4 s = red_sum(red[0], lane);
       store_h<FMT>(a, s, 0, n0, a.I, lane, [&](int t) { return static_cast<int>(R.seg_slot[seg][t]); });
     }
     ++finished;
@@ -629,7 +667,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_second_kernel(FewArgs a) {
     }
     return;
   }
-  const DownCut cut(static_cast<int>(ceil_div(a.H, 16)), nblk);
+  const DownCut cut(static_cast<int>(ceil_div(a.H, 16 * NS)), nblk);
   if (blockIdx.x >= cut.ranges) return;
   if (wave == 0 && items > 0) {
     // The flag is one line for 32 workgroups; now and then the counts themselves.
@@ -654,23 +692,31 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_second_kernel(FewArgs a) {
       const int lo = k0 + wave * (k1 - k0) / kFewWaves, hi = k0 + (wave + 1) * (k1 - k0) / kFewWaves;
       // Positions of the loads and of their use: segment and block in it.
       int lseg = min(lo / ib, n), lkb = lo - lseg * ib, useg = lseg, ukb = lkb;
-      WRow row{};
-      size_t hoff = 0;
+      Matrices m{};
+      WRow row[NS];
+      uint32_t hoff = 0;
+      size_t hbase = 0;
       bool live = false;
       auto enter = [&]() __attribute__((always_inline)) {
         const bool shared = lseg == n;
         const int width = shared ? a.S : a.I;
         const size_t first = shared ? 0 : static_cast<size_t>(__builtin_amdgcn_readfirstlane(R.seg_expert[lseg])) * a.H;
+        m.w[0] = m.w[1] = static_cast<const uint8_t*>(shared ? a.ws_down : a.w_down) + first * row_bytes<FMT>(width);
+        m.s[0] = m.s[1] = static_cast<const uint8_t*>(shared ? a.ss_down : a.s_down) + first * scale_bytes<FMT>(width);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          set_row<FMT>(row, h, shared ? a.ws_down : a.w_down, shared ? a.ss_down : a.s_down,
-                       first + min(tile * 16 + 8 * h + (lane & 7), a.H - 1), width);
+        for (int j = 0; j < NS; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            set_row<FMT>(row[j], h, min((tile * NS + j) * 16 + 8 * h + (lane & 7), a.H - 1), width, lane);
         const int slot = R.seg_slot[lseg][r];
         live = slot >= 0;
-        hoff = ((shared ? h_shared : 0) + static_cast<size_t>(max(slot, 0)) * width) * (F::kF32 ? 4 : 2);
+        hbase = (shared ? h_shared : 0) * (F::kF32 ? 4 : 2);
+        hoff = static_cast<uint32_t>(max(slot, 0)) * static_cast<uint32_t>(width) * (F::kF32 ? 4 : 2);
       };
       if (lo < hi) enter();
-      Acc acc{};
+      f32x4 acc[NS];
+#pragma unroll
+      for (int j = 0; j < NS; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
       batches<FewBatch<FMT>::kDown, DownBlk<FMT>>(
           hi - lo,
           [&](DownBlk<FMT>& k) __attribute__((always_inline)) {
@@ -681,10 +727,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_second_kernel(FewArgs a) {
             }
             const bool shared = lseg == n;
             const int width = shared ? a.S : a.I, vec = shared ? a.svec : a.ivec;
-            load_w<FMT>(k.w, row, lkb, lane, width, vec);
+#pragma unroll
+            for (int j = 0; j < NS; ++j) load_w<FMT>(k.w[j], m, row[j], lkb, lane, width, vec);
 #pragma unroll
             for (int p = 0; p < DownBlk<FMT>::kPlanes; ++p)
-              load_x<FMT>(k.h[p], static_cast<const uint8_t*>(a.h[p]) + hoff, lkb, lane, width, vec, live);
+              load_x<FMT>(k.h[p], static_cast<const uint8_t*>(a.h[p]) + hbase, hoff, lkb, lane, width, vec, live);
             ++lkb;
           },
           [&](DownBlk<FMT>& k) __attribute__((always_inline)) {
@@ -693,57 +740,60 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_second_kernel(FewArgs a) {
               ukb = 0;
             }
             ++ukb;
-            Acc t{};
-            mma_planes<FMT, DownBlk<FMT>::kPlanes>(k.h, k.w, t);
             const float4 wt = *reinterpret_cast<const float4*>(&R.seg_w[useg][4 * g]);
             const float ws[4] = {wt.x, wt.y, wt.z, wt.w};
-            // A token that the expert does not serve takes nothing, not 0 * inf either.
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int j = 0; j < NS; ++j) {
+              const f32x4 t = mma_planes<FMT, DownBlk<FMT>::kPlanes>(k.h, k.w[j], lane, f32x4{0.f, 0.f, 0.f, 0.f});
+              // A token that the expert does not serve takes nothing, not 0 * inf either.
 #pragma unroll
-              for (int half = 0; half < 2; ++half)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const float v = FMT == kDtypeFp8 ? t.v[h][half][q] * k.w.s[h] : t.v[h][half][q];
-                  const float s = acc.v[h][half][q];
-                  acc.v[h][half][q] = ws[q] != 0.f ? fmaf(ws[q], v, s) : s;
-                }
+              for (int q = 0; q < 4; ++q) acc[j][q] = ws[q] != 0.f ? fmaf(ws[q], t[q], acc[j][q]) : acc[j][q];
+            }
           });
-      const f32x4 mine = tile_sums(acc, lane);
       __syncthreads();               // the previous tile has been added up
-      red.v[wave][lane] = mine;
+#pragma unroll
+      for (int j = 0; j < NS; ++j) red[j].v[wave][lane] = acc[j];
       if (tid == 0) s_next = next;
       __syncthreads();
       if (wave != 0) continue;
-      f32x4 s = red_sum(red, lane);
+      f32x4 s[NS];
+#pragma unroll
+      for (int j = 0; j < NS; ++j) s[j] = red_sum(red[j], lane);
       if (k0 > 0 || k1 < nblk) {     // a part: the last one to arrive adds them up
         const int b0 = cut.owner(base), b1 = cut.owner(base + nblk - 1);
-        float* part = a.part + (static_cast<size_t>(b) * 2 + (tile == tile0 ? 0 : 1)) * 256;
+        float* part = a.part + (static_cast<size_t>(b) * 2 + (tile == tile0 ? 0 : 1)) * (256 * NS);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) st_shared(part + 64 * i + lane, s[i]);
+        for (int j = 0; j < NS; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st_shared(part + 256 * j + 64 * i + lane, s[j][i]);
         stores_done();
         int before = 0;
         if (lane == 0) before = ctl_add(a.ctl + Ctl::kTile + tile, 1);
         if (__builtin_amdgcn_readfirstlane(before) != b1 - b0) continue;
-        s = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < NS; ++j) s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
         for (int o = b0; o <= b1; ++o) {
           // The tile is range o's first one, unless the range began in an earlier tile.
-          const float* p = a.part + (static_cast<size_t>(o) * 2 + (cut.start(o) / nblk == tile ? 0 : 1)) * 256;
+          const float* p = a.part + (static_cast<size_t>(o) * 2 + (cut.start(o) / nblk == tile ? 0 : 1)) * (256 * NS);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[i] += ld_shared(p + 64 * i + lane);
+          for (int j = 0; j < NS; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[j][i] += ld_shared(p + 256 * j + 64 * i + lane);
         }
       }
-      const int col = tile * 16 + r;
-      if (col < a.H) {
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        const int col = (tile * NS + j) * 16 + r;
+        if (col >= a.H) continue;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int t = 4 * g + i;
           if (t < a.T) {
             const size_t o = static_cast<size_t>(t) * a.H + col;
-            if (a.y) a.y[o] = s[i];
+            if (a.y) a.y[o] = s[j][i];
             if (a.y_act) {
-              if (a.act_bf16) static_cast<uint16_t*>(a.y_act)[o] = f32_to_bf16_bits(s[i]);
-              else static_cast<float*>(a.y_act)[o] = s[i];
+              if (a.act_bf16) static_cast<uint16_t*>(a.y_act)[o] = f32_to_bf16_bits(s[j][i]);
+              else static_cast<float*>(a.y_act)[o] = s[j][i];
             }
           }
         }
@@ -770,32 +820,36 @@ FewLayout few_layout(const moe_config& c, int64_t T) {
   };
   const bool f32 = c.weight_dtype == MOE_DTYPE_F32;
   L.ldz = static_cast<int>(align_up(c.n_routed_experts + 1, 16));
-  // At least two blocks of contraction for each wave of a part.
+  // Parts of one batch of each wave.
   const int blocks = static_cast<int>(ceil_div(c.hidden_size, f32 ? 32 : 64));
-  L.parts = std::max(1, std::min(kFewRouterParts, blocks / (2 * kFewWaves)));
+  L.parts = static_cast<int>(std::min<int64_t>(kFewRouterParts, ceil_div(blocks, 10 * kFewWaves)));
   L.ctl = take(ctl_ints(c.hidden_size) * sizeof(int));
   L.z = take(static_cast<size_t>(L.parts) * kFewTokens * L.ldz * sizeof(float));
   const size_t elems = static_cast<size_t>(T) * c.num_experts_per_tok * c.moe_intermediate_size +
                        static_cast<size_t>(T) * c.shared_expert_intermediate_size;
   for (int p = 0; p < 3; ++p) L.h[p] = take(f32 ? (p ? 0 : elems * 4) : elems * 2);
-  L.part = take(static_cast<size_t>(kMaxRanges) * 2 * 256 * sizeof(float));
+  L.part = take(static_cast<size_t>(kMaxRanges) * 2 * kMaxSets * 256 * sizeof(float));
   L.total = off;
   return L;
 }
 
-// The second kernel numbers its gate/up tiles and its down blocks in 32 bits.
+// The second kernel numbers its gate/up tiles and its down blocks in 32 bits; offsets
+// within one expert's matrix and within a plane of h are 32-bit byte offsets.
 bool few_countable(const moe_config& c) {
   const int64_t experts = std::min<int64_t>(c.n_routed_experts, kFewSlots);
-  const int64_t tiles = ceil_div(c.hidden_size, 16);
-  const int64_t nblk = experts * ceil_div(c.moe_intermediate_size, 32) + ceil_div(c.shared_expert_intermediate_size, 32);
-  return experts * ceil_div(c.moe_intermediate_size, 8) * kQueues < (int64_t{1} << 31) && tiles * nblk < (int64_t{1} << 31);
+  const int64_t H = c.hidden_size, I = c.moe_intermediate_size, S = c.shared_expert_intermediate_size;
+  const int64_t nblk = experts * ceil_div(I, 32) + ceil_div(S, 32), lim = int64_t{1} << 31;
+  const int64_t size = c.weight_dtype == MOE_DTYPE_F32 ? 4 : 2;
+  return experts * ceil_div(I, 8) * kQueues < lim && ceil_div(H, 16) * nblk < lim && H * I * size < 2 * lim &&
+         H * S * size < 2 * lim && H * c.n_routed_experts * size < 2 * lim &&
+         (kFewSlots * I + kFewTokens * S) * size < 2 * lim;
 }
 
 bool misaligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
 template <int FMT>
 int few_launch(const FewArgs& a, hipStream_t s) {
-  const int first = static_cast<int>(ceil_div(a.ncols, 16)) * a.parts + static_cast<int>(ceil_div(a.S, 8));
+  const int first = router_tiles(a.E, a.S) * a.parts + static_cast<int>(ceil_div(a.S, 8));
   few_first_kernel<FMT><<<first, kFewThreads, 0, s>>>(a);
   if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
   few_second_kernel<FMT><<<kFewGrid, kFewThreads, 0, s>>>(a);

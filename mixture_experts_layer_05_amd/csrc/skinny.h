@@ -8,11 +8,9 @@
 // A load instruction takes 128 bytes from each of 8 weight rows.  The plain operand
 // layout (16 rows, 64 bytes each) reads at three quarters of that rate: 5.2 against
 // 6.9 TB/s over 336 MB, 4.3 against 5.1 over 42 MB.  Lane l, with column c = l % 16 and
-// lane group g = l / 16, loads row c % 8, 16-byte piece 4 (c / 8) + g.  To the MFMA the
-// columns c < 8 are then the 8 rows over the first half of the 128 bytes and the
-// columns c >= 8 the same rows over the second half, so each register meets the
-// activations of both halves, in two accumulators of which half the columns count.
-// That doubles the MFMAs, which are idle otherwise.
+// lane group g = l / 16, loads row c % 8, 16-byte piece 4 (c / 8) + g, of the first 8
+// rows and of the second 8.  Lanes c and c ^ 8 then exchange one register each, which
+// gives both the operands of row c: its first and its second 64 bytes.
 //
 // A block is 128 bytes of each weight row: 64 bf16, 128 fp8 (one scale group), 256
 // MXFP4 or 32 f32 elements.  The activations are taken in the order in which the lanes
@@ -38,11 +36,11 @@ struct SkinnyFmt {
 };
 constexpr int kBlkBytes = 128;   // of a weight row
 
-// A lane's view of its two weight rows: rows c % 8 of the first and of the second 8
-// of the tile, and their scales.
+// A lane's view of its two weight rows of a tile, c % 8 of the first and of the second
+// 8: offsets of its piece of block 0, and of its scale, from a base that the whole
+// wave shares.
 struct WRow {
-  const uint8_t* p[2];
-  const void* s[2];
+  uint32_t w[2], s[2];
 };
 
 // One block of a tile, as loaded.
@@ -55,59 +53,91 @@ template <int FMT>
 struct XBlk {
   uint4 v[2][SkinnyFmt<FMT>::kX];   // the two halves of the block
 };
-// Sums of a tile's two row sets over the two halves.
-struct Acc {
-  f32x4 v[2][2];
-};
 
-// Four floats at element k of a row of `kdim`, zeros past its end.
-__device__ __forceinline__ uint4 ld_f32x4(const float* row, int k, int kdim, bool vec) {
-  if (vec) return k < kdim ? ld16(row + k) : uint4{0, 0, 0, 0};
-  uint4 r;
-  r.x = k + 0 < kdim ? __float_as_uint(row[k + 0]) : 0;
-  r.y = k + 1 < kdim ? __float_as_uint(row[k + 1]) : 0;
-  r.z = k + 2 < kdim ? __float_as_uint(row[k + 2]) : 0;
-  r.w = k + 3 < kdim ? __float_as_uint(row[k + 3]) : 0;
+template <int FMT>
+__host__ __device__ constexpr size_t row_bytes(int k) {
+  return FMT == kDtypeF32 ? static_cast<size_t>(k) * 4
+       : FMT == kDtypeBf16 ? static_cast<size_t>(k) * 2
+       : FMT == kDtypeFp8 ? static_cast<size_t>(k) : static_cast<size_t>(k) / 2;
+}
+template <int FMT>
+__host__ __device__ constexpr size_t scale_bytes(int k) {
+  return FMT == kDtypeFp8 ? static_cast<size_t>(k) / kGroup * 4
+       : FMT == kDtypeMxfp4 ? static_cast<size_t>(k) / kMxBlock : 0;
+}
+
+// A lane's 16-byte piece of its block.
+__device__ __forceinline__ int lane_piece(int lane) { return ((lane >> 1) & 4) + (lane >> 4); }
+
+// The h-th row of the lane is row `row` of a matrix of rows of k elements.  A matrix
+// starts at the base that load_w is given and is smaller than 4 GiB.
+template <int FMT>
+__device__ __forceinline__ void set_row(WRow& r, int h, int row, int k, int lane) {
+  r.w[h] = static_cast<uint32_t>(row) * static_cast<uint32_t>(row_bytes<FMT>(k)) + 16 * lane_piece(lane);
+  r.s[h] = static_cast<uint32_t>(row) * static_cast<uint32_t>(scale_bytes<FMT>(k)) +
+           (FMT == kDtypeMxfp4 ? lane_piece(lane) : 0);
+}
+
+// Four floats, of which the row holds the first n (vec: 16-byte aligned, all or none).
+__device__ __forceinline__ uint4 ld_f32x4(const uint8_t* p, int n, bool vec) {
+  uint4 r = {0, 0, 0, 0};
+  if (vec) {
+    if (n > 0) r = ld16(p);
+    return r;
+  }
+  const uint32_t* f = reinterpret_cast<const uint32_t*>(p);
+  if (n > 0) r.x = f[0];
+  if (n > 1) r.y = f[1];
+  if (n > 2) r.z = f[2];
+  if (n > 3) r.w = f[3];
   return r;
 }
 
-// Block b of a tile's weight rows.  kdim and vec matter to f32 only: the other types
-// come in whole blocks, 16-byte aligned.
+// Block b of a tile's weight rows, the first 8 from the matrix at w[0], the others from
+// the one at w[1] (scales at s).  kdim and vec matter to f32 only: the other types come
+// in whole blocks, 16-byte aligned.
+struct Matrices {
+  const void *w[2], *s[2];
+};
 template <int FMT>
-__device__ __forceinline__ void load_w(WBlk<FMT>& w, const WRow& r, int b, int lane, int kdim, bool vec) {
-  const int piece = ((lane >> 1) & 4) + (lane >> 4);
+__device__ __forceinline__ void load_w(WBlk<FMT>& k, const Matrices& m, const WRow& r, int b, int lane, int kdim,
+                                       bool vec) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
+    const uint8_t* wb = static_cast<const uint8_t*>(m.w[h]) + static_cast<size_t>(b) * kBlkBytes;
+    const uint8_t* sb = static_cast<const uint8_t*>(m.s[h]);
     if constexpr (FMT == kDtypeF32) {
-      w.v[h] = ld_f32x4(reinterpret_cast<const float*>(r.p[h]), 32 * b + 4 * piece, kdim, vec);
+      k.v[h] = ld_f32x4(wb + r.w[h], kdim - 32 * b - 4 * lane_piece(lane), vec);
     } else {
-      w.v[h] = ld16_stream(r.p[h] + static_cast<size_t>(b) * kBlkBytes + 16 * piece);
-      if constexpr (FMT == kDtypeFp8) w.s[h] = static_cast<const float*>(r.s[h])[b];
+      k.v[h] = ld16_stream(wb + r.w[h]);
+      if constexpr (FMT == kDtypeFp8) k.s[h] = *reinterpret_cast<const float*>(sb + 4 * b + r.s[h]);
       if constexpr (FMT == kDtypeMxfp4)
-        w.s[h] = __uint_as_float(static_cast<uint32_t>(static_cast<const uint8_t*>(r.s[h])[8 * b + piece]) << 23);
+        k.s[h] = __uint_as_float(static_cast<uint32_t>(*(sb + 8 * b + r.s[h])) << 23);
     }
   }
 }
 
-// The activations that meet block b; zeros for a row that is not `live`.
+// The activations that meet block b, of the row at byte `off` from x; zeros for a row
+// that is not `live`.
 template <int FMT>
-__device__ __forceinline__ void load_x(XBlk<FMT>& x, const void* row, int b, int lane, int kdim, bool vec, bool live) {
+__device__ __forceinline__ void load_x(XBlk<FMT>& k, const void* x, uint32_t off, int b, int lane, int kdim, bool vec,
+                                       bool live) {
   using F = SkinnyFmt<FMT>;
   const int g = lane >> 4;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int q = 0; q < F::kX; ++q) x.v[h][q] = uint4{0, 0, 0, 0};
+    for (int q = 0; q < F::kX; ++q) k.v[h][q] = uint4{0, 0, 0, 0};
   if (!live) return;
+  const uint8_t* xb = static_cast<const uint8_t*>(x) + static_cast<size_t>(b) * F::kBlk * (F::kF32 ? 4 : 2);
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int q = 0; q < F::kX; ++q) {
       if constexpr (FMT == kDtypeF32)
-        x.v[h][q] = ld_f32x4(static_cast<const float*>(row), 32 * b + 16 * h + 4 * g, kdim, vec);
+        k.v[h][q] = ld_f32x4(xb + off + 4 * (16 * h + 4 * g), kdim - 32 * b - 16 * h - 4 * g, vec);
       else
-        x.v[h][q] = ld16(static_cast<const uint8_t*>(row) +
-                         2 * (static_cast<size_t>(b) * F::kBlk + h * (F::kBlk / 2) + g * (F::kBlk / 8) + 8 * q));
+        k.v[h][q] = ld16(xb + off + 2 * (h * (F::kBlk / 2) + g * (F::kBlk / 8) + 8 * q));
     }
 }
 
@@ -134,64 +164,57 @@ __device__ __forceinline__ uint4 decode_w(const uint4& v, float s, int q) {
   }
 }
 
-// acc += (the sum of N activation planes) * w over one block, without fp8 scales.
+// (a, b) of lanes c < 8 and (a', b') of lanes c + 8 become (a, a') and (b, b').
+__device__ __forceinline__ void trade(uint32_t& a, uint32_t& b, bool upper) {
+  const uint32_t give = upper ? a : b;
+  const uint32_t got = static_cast<uint32_t>(
+      __builtin_amdgcn_update_dpp(0, static_cast<int>(give), 0x128, 0xf, 0xf, true));   // row_ror:8, lane ^ 8
+  a = upper ? got : a;
+  b = upper ? b : got;
+}
+
+// acc += (the sum of N activation planes) * w over one block; element i of lane l is
+// weight row l % 16 of the tile and activation row 4 (l / 16) + i.
 template <int FMT, int N>
-__device__ __forceinline__ void mma_planes(const XBlk<FMT> (&x)[N], const WBlk<FMT>& w, Acc& acc) {
+__device__ __forceinline__ f32x4 mma_planes(const XBlk<FMT> (&x)[N], WBlk<FMT> w, int lane, f32x4 acc) {
+  const bool upper = lane & 8;
+  trade(w.v[0].x, w.v[1].x, upper);
+  trade(w.v[0].y, w.v[1].y, upper);
+  trade(w.v[0].z, w.v[1].z, upper);
+  trade(w.v[0].w, w.v[1].w, upper);
+  if constexpr (FMT == kDtypeF32) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if constexpr (FMT == kDtypeF32) {
-      const float wv[4] = {__uint_as_float(w.v[h].x), __uint_as_float(w.v[h].y), __uint_as_float(w.v[h].z),
-                           __uint_as_float(w.v[h].w)};
+    for (int h = 0; h < 2; ++h) {
+      const uint4 xv = x[0].v[h][0], wv = w.v[h];
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(xv.x), __uint_as_float(wv.x), acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(xv.y), __uint_as_float(wv.y), acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(xv.z), __uint_as_float(wv.z), acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(xv.w), __uint_as_float(wv.w), acc, 0, 0, 0);
+    }
+    return acc;
+  } else {
+    if constexpr (FMT == kDtypeMxfp4) {
+      uint32_t s0 = __float_as_uint(w.s[0]), s1 = __float_as_uint(w.s[1]);
+      trade(s0, s1, upper);
+      w.s[0] = __uint_as_float(s0);
+      w.s[1] = __uint_as_float(s1);
+    }
+    f32x4 t = FMT == kDtypeFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint4 xv = x[0].v[k][0];
-        const float xs[4] = {__uint_as_float(xv.x), __uint_as_float(xv.y), __uint_as_float(xv.z), __uint_as_float(xv.w)};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc.v[h][k] = __builtin_amdgcn_mfma_f32_16x16x4f32(xs[i], wv[i], acc.v[h][k], 0, 0, 0);
-      }
-    } else {
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int q = 0; q < SkinnyFmt<FMT>::kX; ++q) {
         const uint4 wq = decode_w<FMT>(w.v[h], w.s[h], q);
 #pragma unroll
-        for (int p = N - 1; p >= 0; --p)      // the smallest plane first
-#pragma unroll
-          for (int k = 0; k < 2; ++k) acc.v[h][k] = mfma_bf16_16x16x32(x[p].v[k][q], wq, acc.v[h][k]);
+        for (int p = N - 1; p >= 0; --p) t = mfma_bf16_16x16x32(x[p].v[h][q], wq, t);   // the smallest plane first
       }
+    if constexpr (FMT == kDtypeFp8) {
+      const float s = upper ? w.s[1] : w.s[0];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] = fmaf(t[i], s, acc[i]);
     }
+    return t;
   }
-}
-
-// acc += x * w over one block.
-template <int FMT>
-__device__ __forceinline__ void mma_block(const XBlk<FMT> (&x)[1], const WBlk<FMT>& w, Acc& acc) {
-  if constexpr (FMT == kDtypeFp8) {
-    Acc t{};
-    mma_planes<FMT, 1>(x, w, t);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc.v[h][k][i] = fmaf(t.v[h][k][i], w.s[h], acc.v[h][k][i]);
-  } else {
-    mma_planes<FMT, 1>(x, w, acc);
-  }
-}
-
-// The tile's sums, the two halves added: element i of lane l is weight row l % 16 of
-// the tile and activation row 4 (l / 16) + i.
-__device__ __forceinline__ f32x4 tile_sums(const Acc& acc, int lane) {
-  const bool upper = lane & 8;       // row set 1, and the columns that hold second halves
-  f32x4 s;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float give = upper ? acc.v[0][1][i] : acc.v[1][0][i];
-    const float own = upper ? acc.v[1][1][i] : acc.v[0][0][i];
-    s[i] = own + __shfl_xor(give, 8, kWave);
-  }
-  return s;
 }
 
 // Runs n blocks in batches of D: the loads of a batch are issued together, then its
