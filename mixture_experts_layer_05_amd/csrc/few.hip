@@ -92,41 +92,54 @@ __device__ __forceinline__ f32x4 red_sum(const Red& r, int lane) {
   return s;
 }
 
-// Blocks a wave loads at a time, within its 256 registers.  In the down half, where
-// a block of weights meets three planes of h, a wave runs kSets tiles side by side on
-// one block of h.
+// Blocks of weights that a wave loads at a time, within its 256 registers.  Where an
+// activation block is large next to a weight block, several tiles run side by side on
+// one: kWide in the gate/up half when there are enough tiles (kWideTiles for each
+// workgroup), kSets in the down half, whose weights meet three planes of h.  With one
+// tile at a time the activations' loads took a fifth to a third of the gate/up time of
+// the quantised types.
 template <int FMT>
 struct FewBatch {
+  static constexpr int kWide = FMT == kDtypeMxfp4 ? 4 : FMT == kDtypeF32 ? 1 : 2;
   static constexpr int kGateUp = FMT == kDtypeMxfp4 ? 4 : FMT == kDtypeFp8 ? 6 : 10;
-  static constexpr int kDown = FMT == kDtypeMxfp4 ? 1 : FMT == kDtypeFp8 ? 2 : 4;
+  static constexpr int kGateUpWide = FMT == kDtypeMxfp4 ? 2 : FMT == kDtypeFp8 ? 4 : 5;
+  static constexpr int kDown = FMT == kDtypeMxfp4 || FMT == kDtypeFp8 ? 1 : 4;
   static constexpr int kSets = FMT == kDtypeF32 ? 1 : FMT == kDtypeBf16 ? 2 : 4;
 };
+constexpr int kWideTiles = 16;
 constexpr int kMaxSets = 4;
 
-template <int FMT>
+// NS gate/up tiles side by side on one block of x.
+template <int FMT, int NS>
 struct GuBlk {
-  WBlk<FMT> w;
+  WBlk<FMT> w[NS];
   XBlk<FMT> x[1];
 };
 
-// This wave's quarter of x W^T over the contraction [b0, b1), in blocks, of one
-// 16-row weight tile.
-template <int FMT>
-__device__ __forceinline__ f32x4 wave_tile(const Matrices& m, const WRow& row, const void* x, uint32_t xoff, bool live,
-                                           int b0, int b1, int kdim, bool vec, int wave, int lane) {
+// This wave's quarter of x W^T over the contraction [b0, b1), in blocks, of NS 16-row
+// weight tiles.  first() is called when the loads of the first batch are on their way.
+template <int FMT, int NS, class First>
+__device__ __forceinline__ void wave_tiles(const Matrices& m, const WRow (&row)[NS], const void* x, uint32_t xoff,
+                                           bool live, int b0, int b1, int kdim, bool vec, int wave, int lane,
+                                           f32x4 (&acc)[NS], First first) {
   const int n = b1 - b0;
   const int lo = b0 + wave * n / kFewWaves, hi = b0 + (wave + 1) * n / kFewWaves;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < NS; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
   int at = lo;
-  batches<FewBatch<FMT>::kGateUp, GuBlk<FMT>>(
+  batches<NS == 1 ? FewBatch<FMT>::kGateUp : FewBatch<FMT>::kGateUpWide, GuBlk<FMT, NS>>(
       hi - lo,
-      [&](GuBlk<FMT>& k) __attribute__((always_inline)) {
-        load_w<FMT>(k.w, m, row, at, lane, kdim, vec);
+      [&](GuBlk<FMT, NS>& k) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < NS; ++j) load_w<FMT>(k.w[j], m, row[j], at, lane, kdim, vec);
         load_x<FMT>(k.x[0], x, xoff, at, lane, kdim, vec, live);
         ++at;
       },
-      [&](GuBlk<FMT>& k) __attribute__((always_inline)) { acc = mma_planes<FMT, 1>(k.x, k.w, lane, acc); });
-  return acc;
+      [&](GuBlk<FMT, NS>& k) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < NS; ++j) acc[j] = mma_planes<FMT, 1>(k.x, k.w[j], lane, acc[j]);
+      },
+      first);
 }
 
 // A gate/up tile: the first 8 rows lie in the gate matrix of an expert, the others in
@@ -141,11 +154,9 @@ __device__ __forceinline__ Matrices gate_up(const void* wg, const void* wu, cons
 }
 // Its columns [n0, n0 + 8) (past the width: the last row again, not stored).
 template <int FMT>
-__device__ __forceinline__ WRow gate_up_row(int n0, int width, int H, int lane) {
-  WRow r;
-  set_row<FMT>(r, 0, min(n0 + (lane & 7), width - 1), H, lane);
-  set_row<FMT>(r, 1, min(n0 + (lane & 7), width - 1), H, lane);
-  return r;
+__device__ __forceinline__ WRow gate_up_row(const Matrices& m, int n0, int width, int H, int lane) {
+  const int row = min(n0 + (lane & 7), width - 1);
+  return weight_rows<FMT>(m, row, row, H, lane);
 }
 
 // A store that other workgroups of the running kernel may read: written through to
@@ -232,13 +243,14 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_first_kernel(FewArgs a) {
     const int nb = static_cast<int>(ceil_div(a.H, SkinnyFmt<AFMT>::kBlk));
     const bool gate = tile * 16 >= a.E;
     const int c0 = gate ? a.E : tile * 16, cols = gate ? 1 : min(16, a.E - c0);
-    const void* w = gate ? a.w_gcol : a.w_router;
-    WRow row;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      set_row<AFMT>(row, h, (gate ? 0 : c0) + min(8 * h + (lane & 7), cols - 1), a.H, lane);
-    red.v[wave][lane] = wave_tile<AFMT>(Matrices{{w, w}, {nullptr, nullptr}}, row, a.x, xoff, live,
-                                        part * nb / a.parts, (part + 1) * nb / a.parts, a.H, a.hvec, wave, lane);
+    const void* w = (gate ? a.w_gcol : a.w_router);
+    const Matrices m{{w, w}, {nullptr, nullptr}};
+    const int row0 = (gate ? 0 : c0) + min(lane & 7, cols - 1), row1 = (gate ? 0 : c0) + min(8 + (lane & 7), cols - 1);
+    const WRow row[1] = {weight_rows<AFMT>(m, row0, row1, a.H, lane)};
+    f32x4 acc[1];
+    wave_tiles<AFMT, 1>(m, row, a.x, xoff, live, part * nb / a.parts, (part + 1) * nb / a.parts, a.H, a.hvec, wave,
+                        lane, acc, [] {});
+    red.v[wave][lane] = acc[0];
     __syncthreads();
     if (wave == 0 && r < cols) {
       const f32x4 s = red_sum(red, lane);
@@ -249,9 +261,12 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_first_kernel(FewArgs a) {
     return;
   }
   const int n0 = (item - router) * 8;
-  red.v[wave][lane] = wave_tile<FMT>(gate_up<FMT>(a.ws_gate, a.ws_up, a.ss_gate, a.ss_up, 0, a.S, a.H),
-                                     gate_up_row<FMT>(n0, a.S, a.H, lane), a.x, xoff, live, 0,
-                                     static_cast<int>(ceil_div(a.H, SkinnyFmt<FMT>::kBlk)), a.H, a.hvec, wave, lane);
+  const Matrices m = gate_up<FMT>(a.ws_gate, a.ws_up, a.ss_gate, a.ss_up, 0, a.S, a.H);
+  const WRow row[1] = {gate_up_row<FMT>(m, n0, a.S, a.H, lane)};
+  f32x4 acc[1];
+  wave_tiles<FMT, 1>(m, row, a.x, xoff, live, 0, static_cast<int>(ceil_div(a.H, SkinnyFmt<FMT>::kBlk)), a.H, a.hvec,
+                     wave, lane, acc, [] {});
+  red.v[wave][lane] = acc[0];
   __syncthreads();
   if (wave == 0) {
     const f32x4 s = red_sum(red, lane);
@@ -300,130 +315,170 @@ struct Routing {
   float seg_w[kFewSlots + 1][kFewTokens];        // its weight, 0 if not served
 };
 struct RouteScratch {
-  float z[kFewTokens][kMaxExperts + 1];   // logits, the shared gate's last
   unsigned long long agg[kMaxExperts];
   int seg_of[kMaxExperts];
   int nu, dropped, empty;
-  int list[kFewSlots];
+  struct {
+    unsigned long long mass;
+    int id;
+  } list[kFewSlots];               // the experts in use
 };
 
-// Top-k of one token by one wave (same selection and trim as moe_route).  A lane holds
-// the keys of experts lane, lane + 64, ... in descending order (the lower id first
-// among equals); each round takes the largest head of the lanes.
-template <int NJ>
-__device__ __forceinline__ void route_token(const FewArgs& a, Routing& R, const float* z, int t, int lane) {
-  const float gate_logit = (a.S > 0 && lane == 0) ? z[a.E] : 0.f;
-  uint32_t key[NJ];
-  int id[NJ];
+// Top-k of TN tokens t0, t0 + 4, ... by one wave (same selection and trim as moe_route).
+// A lane holds the keys of experts 4 lane .. + 4 (and 256 further on), sorted; each
+// round takes the largest head of the lanes.  The rounds are chains of dependent
+// steps, so several tokens go through them together.
+template <int NQ, int TN>
+__device__ __forceinline__ void route_some(const FewArgs& a, Routing& R, int t0, int lane) {
+  constexpr int NJ = 4 * NQ;
+  const size_t plane = static_cast<size_t>(kFewTokens) * a.ldz;
+  uint32_t key[TN][NJ];
+  int id[NJ][TN];
+  float gate[TN];
+  // All loads first.  Rows of z are multiples of 16 long; a lane takes 4 columns at a time.
+  f32x4 v[TN][NQ][kFewRouterParts];
+  float gv[TN][kFewRouterParts];
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int e = lane + kWave * j;
-    const float v = e < a.E ? z[e] : 0.f;
-    key[j] = e < a.E ? order_key(v == v ? v : -INFINITY) : 0;
-    id[j] = e;
+  for (int i = 0; i < TN; ++i) {
+    const float* zr = a.z + static_cast<size_t>(min(t0 + i * kFewWaves, a.T - 1)) * a.ldz;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+      for (int p = 0; p < kFewRouterParts; ++p)
+        v[i][q][p] = p < a.parts && 4 * (lane + kWave * q) < a.E ? *reinterpret_cast<const f32x4*>(zr + p * plane + 4 * (lane + kWave * q))
+                                                                 : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int p = 0; p < kFewRouterParts; ++p) gv[i][p] = p < a.parts && a.S > 0 ? zr[p * plane + a.E] : 0.f;
   }
-  // Odd-even merge sort of at most 8: (0 1)(2 3)(4 5)(6 7) (0 2)(1 3)(4 6)(5 7) (1 2)(5 6)
-  // (0 4)(1 5)(2 6)(3 7) (2 4)(3 5) (1 2)(3 4)(5 6), as far as NJ goes.
-  auto order = [&](int i, int j) __attribute__((always_inline)) {
-    if (j >= NJ) return;
-    const bool swap = key[j] > key[i] || (key[j] == key[i] && id[j] < id[i]);
-    const uint32_t k = swap ? key[j] : key[i];
-    key[j] = swap ? key[i] : key[j];
-    key[i] = k;
-    const int e = swap ? id[j] : id[i];
-    id[j] = swap ? id[i] : id[j];
-    id[i] = e;
+#pragma unroll
+  for (int i = 0; i < TN; ++i) {
+    const float* bias = a.bias ? a.bias + static_cast<size_t>(min(t0 + i * kFewWaves, a.T - 1)) * a.E : nullptr;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int e = 4 * (lane + kWave * q) + c;
+        float z = v[i][q][0][c];
+#pragma unroll
+        for (int p = 1; p < kFewRouterParts; ++p) z += v[i][q][p][c];
+        if (bias && e < a.E) z += bias[e];
+        key[i][4 * q + c] = e < a.E ? order_key(z == z ? z : -INFINITY) : 0;
+        id[4 * q + c][i] = e;
+      }
+    gate[i] = gv[i][0];
+#pragma unroll
+    for (int p = 1; p < kFewRouterParts; ++p) gate[i] += gv[i][p];
+  }
+  // Odd-even merge sort of 4 or 8: descending, the lower id first among equals.
+  auto order = [&](int x, int y) __attribute__((always_inline)) {
+    if (y >= NJ) return;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      const bool swap = key[i][y] > key[i][x] || (key[i][y] == key[i][x] && id[y][i] < id[x][i]);
+      const uint32_t k = swap ? key[i][y] : key[i][x];
+      key[i][y] = swap ? key[i][x] : key[i][y];
+      key[i][x] = k;
+      const int e = swap ? id[y][i] : id[x][i];
+      id[y][i] = swap ? id[x][i] : id[y][i];
+      id[x][i] = e;
+    }
   };
-  if constexpr (NJ > 1) { order(0, 1); order(2, 3); order(4, 5); order(6, 7); }
-  if constexpr (NJ > 2) { order(0, 2); order(1, 3); order(4, 6); order(5, 7); order(1, 2); order(5, 6); }
-  if constexpr (NJ > 4) { order(0, 4); order(1, 5); order(2, 6); order(3, 7); order(2, 4); order(3, 5); order(1, 2);
-                          order(3, 4); order(5, 6); }
-  const float zmax = key_value(wave_max_u32(key[0]));
+  order(0, 1); order(2, 3); order(0, 2); order(1, 3); order(1, 2);
+  if constexpr (NJ > 4) {
+    order(4, 5); order(6, 7); order(4, 6); order(5, 7); order(5, 6);
+    order(0, 4); order(1, 5); order(2, 6); order(3, 7); order(2, 4); order(3, 5); order(1, 2); order(3, 4); order(5, 6);
+  }
+  float zmax[TN], denom_all[TN], my_z[TN];
+  int my_id[TN];
+#pragma unroll
+  for (int i = 0; i < TN; ++i) {
+    zmax[i] = key_value(wave_max_u32(key[i][0]));
+    denom_all[i] = 0.f;
+    my_z[i] = 0.f;
+    my_id[i] = -1;
+  }
   // Softmax denominator over all experts (only without renormalisation).
-  float denom_all = 0.f;
   if (!a.norm) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
-      if (key[j] != 0) denom_all += expf(key_value(key[j]) - zmax);
-    denom_all = wave_sum(denom_all);
-  }
-  int my_id = -1;
-  float my_z = 0.f;
-  for (int k = 0; k < a.K; ++k) {
-    const uint32_t m = wave_max_u32(key[0]);
-    unsigned long long has = __ballot(key[0] == m);
-    int owner = __builtin_ctzll(has), e = __builtin_amdgcn_readlane(id[0], owner);
-    for (has &= has - 1; has; has &= has - 1) {        // ties: the lowest id
-      const int o = __builtin_ctzll(has), f = __builtin_amdgcn_readlane(id[0], o);
-      if (f < e) { e = f; owner = o; }
-    }
-    const bool pop = lane == owner;
+    for (int i = 0; i < TN; ++i) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      key[j] = pop ? (j + 1 < NJ ? key[j + 1 < NJ ? j + 1 : j] : 0) : key[j];
-      id[j] = pop ? id[j + 1 < NJ ? j + 1 : j] : id[j];
+      for (int j = 0; j < NJ; ++j)
+        if (key[i][j] != 0) denom_all[i] += expf(key_value(key[i][j]) - zmax[i]);
+      denom_all[i] = wave_sum(denom_all[i]);
     }
-    if (lane == k) { my_id = e; my_z = key_value(m); }
   }
-  const float p = lane < a.K ? expf(my_z - zmax) : 0.f;
-  bool kept = lane < a.K;
-  if (a.top_p > 0.f) {
-    float before = 0.f, all = 0.f;
-    for (int k = 0; k < a.K; ++k) {
-      const float pk = __shfl(p, k, kWave);
-      if (k < lane) before += pk;
-      all += pk;
+  for (int k = 0; k < a.K; ++k) {
+    uint32_t m[TN];
+    unsigned long long has[TN], more = 0;
+#pragma unroll
+    for (int i = 0; i < TN; ++i) m[i] = wave_max_u32(key[i][0]);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      has[i] = __ballot(key[i][0] == m[i]);
+      more |= has[i] & (has[i] - 1);
     }
-    kept = kept && (lane == 0 || before < a.top_p * all);
+    int owner[TN], e[TN];
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      owner[i] = __builtin_ctzll(has[i]);
+      e[i] = __builtin_amdgcn_readlane(id[0][i], owner[i]);
+    }
+    if (more) {                        // ties: the lowest id
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+        for (unsigned long long h = has[i] & (has[i] - 1); h; h &= h - 1) {
+          const int o = __builtin_ctzll(h), f = __builtin_amdgcn_readlane(id[0][i], o);
+          if (f < e[i]) { e[i] = f; owner[i] = o; }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      const bool pop = lane == owner[i];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        key[i][j] = pop ? (j + 1 < NJ ? key[i][j + 1 < NJ ? j + 1 : j] : 0) : key[i][j];
+        id[j][i] = pop ? id[j + 1 < NJ ? j + 1 : j][i] : id[j][i];
+      }
+      if (lane == k) { my_id[i] = e[i]; my_z[i] = key_value(m[i]); }
+    }
   }
-  const float pk = kept ? p : 0.f;
-  const float denom = a.norm ? wave_sum(pk) : denom_all;
-  if (lane < a.K) {
-    R.ids[t * a.K + lane] = kept ? my_id : -1;
-    R.w[t * a.K + lane] = pk / denom;
+#pragma unroll
+  for (int i = 0; i < TN; ++i) {
+    const int t = t0 + i * kFewWaves;
+    const float p = lane < a.K ? expf(my_z[i] - zmax[i]) : 0.f;
+    bool kept = lane < a.K;
+    if (a.top_p > 0.f) {
+      float before = 0.f, all = 0.f;
+      for (int k = 0; k < a.K; ++k) {
+        const float pk = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(p), k));
+        if (k < lane) before += pk;
+        all += pk;
+      }
+      kept = kept && (lane == 0 || before < a.top_p * all);
+    }
+    const float pk = kept ? p : 0.f;
+    const float denom = a.norm ? wave_sum(pk) : denom_all[i];
+    if (t < a.T) {
+      if (lane < a.K) {
+        R.ids[t * a.K + lane] = kept ? my_id[i] : -1;
+        R.w[t * a.K + lane] = pk / denom;
+      }
+      if (lane == 0) R.sg[t] = a.S > 0 ? 1.0f / (1.0f + expf(-gate[i])) : 0.f;
+    }
   }
-  if (lane == 0) R.sg[t] = a.S > 0 ? 1.0f / (1.0f + expf(-gate_logit)) : 0.f;
 }
 
 // Same routing as moe_route, budget included.
-__device__ void route_tokens(const FewArgs& a, Routing& R, RouteScratch& C, bool report) {
+__device__ __forceinline__ void route_tokens(const FewArgs& a, Routing& R, RouteScratch& C, bool report) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const size_t plane = static_cast<size_t>(kFewTokens) * a.ldz;
-  // The planes added in order, four columns to a load (rows of z are multiples of 16
-  // long), kAhead loads of a thread in flight together.
-  constexpr int kAhead = 4;
-  const int quads = static_cast<int>(ceil_div(a.ncols, 4)), all = a.T * quads;
-  for (int i0 = tid; i0 < all; i0 += kFewThreads * kAhead) {
-    f32x4 v[kAhead][kFewRouterParts];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int i = min(i0 + k * kFewThreads, all - 1);
-      const float* zr = a.z + static_cast<size_t>(i / quads) * a.ldz + 4 * (i % quads);
-#pragma unroll
-      for (int p = 0; p < kFewRouterParts; ++p)
-        v[k][p] = p < a.parts ? *reinterpret_cast<const f32x4*>(zr + p * plane) : f32x4{0.f, 0.f, 0.f, 0.f};
+  if (a.T <= kFewWaves) {
+    if (wave < a.T) {
+      if (a.E <= 256) route_some<1, 1>(a, R, wave, lane);
+      else route_some<2, 1>(a, R, wave, lane);
     }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int i = i0 + k * kFewThreads;
-      if (i >= all) break;
-      const int t = i / quads, c0 = 4 * (i % quads);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float s = v[k][0][q];
-#pragma unroll
-        for (int p = 1; p < kFewRouterParts; ++p) s += v[k][p][q];
-        const int c = c0 + q;
-        if (c < a.ncols) C.z[t][c] = s + (a.bias && c < a.E ? a.bias[static_cast<size_t>(t) * a.E + c] : 0.f);
-      }
-    }
-  }
-  __syncthreads();
-  for (int t = wave; t < a.T; t += kFewWaves) {
-    if (a.E <= kWave) route_token<1>(a, R, C.z[t], t, lane);
-    else if (a.E <= 2 * kWave) route_token<2>(a, R, C.z[t], t, lane);
-    else if (a.E <= 4 * kWave) route_token<4>(a, R, C.z[t], t, lane);
-    else route_token<8>(a, R, C.z[t], t, lane);
+  } else {
+    if (a.E <= 256) route_some<1, 4>(a, R, wave, lane);
+    else route_some<2, 4>(a, R, wave, lane);
   }
   const int slots = a.T * a.K;
   for (int e = tid; e < kMaxExperts; e += kFewThreads) { C.agg[e] = 0ull; C.seg_of[e] = 0; }
@@ -437,7 +492,7 @@ __device__ void route_tokens(const FewArgs& a, Routing& R, RouteScratch& C, bool
       if (e >= 0) {
         const float w = R.w[i];
         if (w == w) atomicAdd(&C.agg[e], static_cast<unsigned long long>(llrint(static_cast<double>(w) * kFewFixed)));
-        if (atomicExch(&C.seg_of[e], 1) == 0) C.list[atomicAdd(&C.nu, 1)] = e;
+        if (atomicExch(&C.seg_of[e], 1) == 0) C.list[atomicAdd(&C.nu, 1)].id = e;
       }
     }
     __syncthreads();
@@ -445,14 +500,16 @@ __device__ void route_tokens(const FewArgs& a, Routing& R, RouteScratch& C, bool
     const bool active = a.budget > 0 && nu > a.budget;
     if (active) {
       int e = -1, rank = 0;
+      unsigned long long mass = 0;
       if (tid < nu) {
-        e = C.list[tid];
-        const unsigned long long v = C.agg[e];
-        for (int o = 0; o < nu; ++o) {
-          const int f = C.list[o];
-          const unsigned long long u = C.agg[f];
-          rank += (u > v || (u == v && f < e)) ? 1 : 0;
-        }
+        e = C.list[tid].id;
+        mass = C.list[tid].mass = C.agg[e];
+      }
+      __syncthreads();
+#pragma unroll 8
+      for (int o = 0; o < nu; ++o) {
+        const unsigned long long other = C.list[o].mass;
+        rank += (other > mass || (other == mass && C.list[o].id < e)) ? 1 : 0;
       }
       __syncthreads();
       if (e >= 0) C.seg_of[e] = rank < a.budget ? 1 : 0;
@@ -571,71 +628,110 @@ __device__ __forceinline__ int take_tile(int* ctl, int items, int home, int& tri
 // touched experts and the shared expert, are one line of tiles * nblk blocks that is
 // cut into equal ranges, so that every workgroup reads the same number of weights.
 // A tile that a cut goes through is added up from its parts, in their order, by the
-// workgroup that finishes its part last.  Up to one range for each workgroup, then
-// up to eight of them, handed out as they are finished, while a range stays longer
-// than kLongRange blocks.
-constexpr int kMaxRanges = 8 * kFewGrid;
+// workgroup that finishes its part last.
+// Short lines are cut into one range for each workgroup (or fewer).  Long ones are cut
+// into a range of half that length for each, then as many of a quarter, then twice as
+// many of an eighth, which are handed out as ranges are finished: few parts, and a
+// short last one.
+constexpr int kMaxRanges = 4 * kFewGrid;
 constexpr int kShortRange = 2 * kFewWaves;   // blocks: two for each wave
-constexpr int kLongRange = 4 * kFewWaves;
+constexpr int kLongRange = 16 * kFewWaves;
 struct DownCut {
-  int tiles, nblk, ranges, q, rem;   // the first rem ranges hold q + 1 blocks, the others q
-  __device__ DownCut(int tiles_, int nblk_) : tiles(tiles_), nblk(nblk_) {
+  int tiles, nblk, ranges, q, rem;
+  bool graded;
+  __device__ __forceinline__ DownCut(int tiles_, int nblk_) : tiles(tiles_), nblk(nblk_) {
     const int all = tiles * nblk;
-    ranges = max(1, min(kFewGrid, all / kShortRange));
-    if (all / kLongRange > kFewGrid) ranges = min(kMaxRanges, all / kLongRange);
-    q = all / ranges;
-    rem = all - q * ranges;
+    graded = all >= kLongRange * kFewGrid;
+    // In units of q blocks: ungraded ranges are one unit, the graded ones 4, 2 and 1.
+    const int units = graded ? 8 * kFewGrid : max(1, min(kFewGrid, all / kShortRange));
+    ranges = graded ? kMaxRanges : units;
+    q = all / units;
+    rem = all - q * units;                     // the first rem units are one block longer
   }
-  __device__ int start(int b) const { return b * q + min(b, rem); }
-  __device__ int owner(int f) const {          // the range that holds block f
-    const int wide = rem * (q + 1);
-    return f < wide ? f / (q + 1) : rem + (f - wide) / q;
+  __device__ __forceinline__ int unit_start(int u) const { return u * q + min(u, rem); }
+  __device__ __forceinline__ int start(int b) const {
+    if (!graded) return unit_start(b);
+    return unit_start(b <= kFewGrid ? 4 * b : b <= 2 * kFewGrid ? 2 * (b + kFewGrid) : b + 4 * kFewGrid);
+  }
+  __device__ __forceinline__ int owner(int f) const {          // the range that holds block f
+    const int longer = rem * (q + 1);
+    const int u = f < longer ? f / (q + 1) : rem + (f - longer) / q;
+    if (!graded) return u;
+    return u < 4 * kFewGrid ? u / 4 : u < 6 * kFewGrid ? u / 2 - kFewGrid : u - 4 * kFewGrid;
   }
 };
 
-template <int FMT>
-__global__ void __launch_bounds__(kFewThreads, 2) few_second_kernel(FewArgs a) {
+// This workgroup's gate/up items (NS tiles each, `tiles` items for each expert); returns
+// how many it ran.  The next item is taken while one is running, but not before the
+// first loads are on their way: a workgroup that comes early must not take the only
+// item of one that comes late.
+template <int FMT, int NS>
+__device__ __forceinline__ int gate_up_half(const FewArgs& a, const Routing& R, Red* red, int& s_next, int items,
+                                            int tiles, int wave, int lane) {
   using F = SkinnyFmt<FMT>;
-  constexpr int NS = FewBatch<FMT>::kSets;
-  // The routing's scratch is done with when the first tile is added up.
-  __shared__ union {
-    RouteScratch scratch;
-    Red red[NS];
-  } U;
-  __shared__ Routing R;
-  Red(&red)[NS] = U.red;
-  __shared__ int s_next;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int r = lane & 15, g = lane >> 4;
-  route_tokens(a, R, U.scratch, blockIdx.x == 0);
-
-  // ---- gate/up tiles.  The next tile is taken while one is running.
-  const int n = R.n;
-  const int gu_tiles = static_cast<int>(ceil_div(a.I, 8)), items = n * gu_tiles;
+  const int tid = threadIdx.x, r = lane & 15;
   const int hb = static_cast<int>(ceil_div(a.H, F::kBlk));
   const uint32_t xoff = static_cast<uint32_t>(min(r, a.T - 1)) * static_cast<uint32_t>(a.H) * (F::kF32 ? 4 : 2);
+  const int home = blockIdx.x % kQueues;
   int tried = 0, finished = 0;
-  if (tid == 0) s_next = take_tile(a.ctl, items, blockIdx.x % kQueues, tried);
+  if (tid == 0) s_next = take_tile(a.ctl, items, home, tried);
   __syncthreads();
   int item = __builtin_amdgcn_readfirstlane(s_next);
   while (item >= 0) {
-    const int seg = item / gu_tiles, n0 = item % gu_tiles * 8;
-    const int e = __builtin_amdgcn_readfirstlane(R.seg_expert[seg]);
-    const Matrices m = gate_up<FMT>(a.w_gate, a.w_up, a.s_gate, a.s_up, e, a.I, a.H);
-    const WRow row = gate_up_row<FMT>(n0, a.I, a.H, lane);
+    const int seg = item / tiles, n0 = item % tiles * (8 * NS);
+    const Matrices m = gate_up<FMT>(a.w_gate, a.w_up, a.s_gate, a.s_up, __builtin_amdgcn_readfirstlane(R.seg_expert[seg]), a.I, a.H);
+    WRow row[NS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j) row[j] = gate_up_row<FMT>(m, n0 + 8 * j, a.I, a.H, lane);
     int next = -1;
-    __syncthreads();                 // s_next has been read, the previous tile added up
-    if (tid == 0) next = take_tile(a.ctl, items, blockIdx.x % kQueues, tried);
-    red[0].v[wave][lane] = wave_tile<FMT>(m, row, a.x, xoff, R.seg_slot[seg][r] >= 0, 0, hb, a.H, a.hvec, wave, lane);
+    f32x4 acc[NS];
+    wave_tiles<FMT, NS>(m, row, a.x, xoff, R.seg_slot[seg][r] >= 0, 0, hb, a.H, a.hvec, wave, lane, acc,
+                        [&]() __attribute__((always_inline)) {
+                          if (tid == 0) next = take_tile(a.ctl, items, home, tried);
+                        });
+    __syncthreads();                 // s_next has been read, the previous tiles added up
+#pragma unroll
+    for (int j = 0; j < NS; ++j) red[j].v[wave][lane] = acc[j];
     if (tid == 0) s_next = next;
     __syncthreads();
     item = __builtin_amdgcn_readfirstlane(s_next);
     if (wave == 0) {
-      const f32x4 s = red_sum(red[0], lane);
-      store_h<FMT>(a, s, 0, n0, a.I, lane, [&](int t) { return static_cast<int>(R.seg_slot[seg][t]); });
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        const f32x4 s = red_sum(red[j], lane);
+        store_h<FMT>(a, s, 0, n0 + 8 * j, a.I, lane, [&](int t) { return static_cast<int>(R.seg_slot[seg][t]); });
+      }
     }
     ++finished;
   }
+  return finished;
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kFewThreads, 2) few_second_kernel(FewArgs a) {
+  using F = SkinnyFmt<FMT>;
+  constexpr int NS = FewBatch<FMT>::kSets, kWide = FewBatch<FMT>::kWide;
+  // The routing's scratch is done with when the first tile is added up.
+  __shared__ union {
+    RouteScratch scratch;
+    Red red[kMaxSets];
+  } U;
+  __shared__ Routing R;
+  Red* const red = U.red;
+  __shared__ int s_next, s_ready;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  if (tid == 0) s_ready = 0;
+  route_tokens(a, R, U.scratch, blockIdx.x == 0);
+
+  // ---- gate/up tiles
+  const int n = R.n;
+  const int gu_tiles = static_cast<int>(ceil_div(a.I, 8)), wide_tiles = static_cast<int>(ceil_div(a.I, 8 * kWide));
+  const bool wide = kWide > 1 && n * gu_tiles >= kWideTiles * kFewGrid;
+  const int items = n * (wide ? wide_tiles : gu_tiles);
+  int finished = 0;
+  if (kWide > 1 && wide) finished = gate_up_half<FMT, kWide>(a, R, red, s_next, items, wide_tiles, wave, lane);
+  else finished = gate_up_half<FMT, 1>(a, R, red, s_next, items, gu_tiles, wave, lane);
   // Every h of this workgroup was stored by wave 0.  The last one to count sees all
   // counts, and says so to the others.
   int* go = a.ctl + Ctl::kGo;
@@ -669,16 +765,27 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_second_kernel(FewArgs a) {
   }
   const DownCut cut(static_cast<int>(ceil_div(a.H, 16 * NS)), nblk);
   if (blockIdx.x >= cut.ranges) return;
-  if (wave == 0 && items > 0) {
-    // The flag is one line for 32 workgroups; now and then the counts themselves.
-    for (int i = 1; ld_shared(go + group * Ctl::kLine) == 0; ++i) {
-      if (i % 16 == 0 && all_counted()) break;
-      __builtin_amdgcn_s_sleep(8);
+  // Waits until every h is there: wave 0 for the grid, the others for wave 0.  Only
+  // wave 0 invalidates the caches (for the whole CU and its L2); when all waves did,
+  // that took 10 us.
+  bool ready = false;
+  auto wait_for_h = [&]() __attribute__((always_inline)) {
+    if (ready) return;
+    ready = true;
+    if (wave == 0) {
+      // The flag is one line for 32 workgroups; now and then the counts themselves.
+      if (items > 0)
+        for (int i = 1; ld_shared(go + group * Ctl::kLine) == 0; ++i) {
+          if (i % 16 == 0 && all_counted()) break;
+          __builtin_amdgcn_s_sleep(8);
+        }
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+      __hip_atomic_store(&s_ready, 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
+    } else {
+      while (__hip_atomic_load(&s_ready, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) == 0) __builtin_amdgcn_s_sleep(4);
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
     }
-  }
-  __syncthreads();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-
+  };
   const size_t h_shared = static_cast<size_t>(a.T) * a.K * a.I;
   int b = blockIdx.x;
   while (b < cut.ranges) {
@@ -690,66 +797,94 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_second_kernel(FewArgs a) {
       const int base = tile * nblk;
       const int k0 = max(f0 - base, 0), k1 = min(f1 - base, nblk);
       const int lo = k0 + wave * (k1 - k0) / kFewWaves, hi = k0 + (wave + 1) * (k1 - k0) / kFewWaves;
-      // Positions of the loads and of their use: segment and block in it.
-      int lseg = min(lo / ib, n), lkb = lo - lseg * ib, useg = lseg, ukb = lkb;
+      // Positions of the weights' loads, of h's loads and of their use: expert segment
+      // and block in it.
+      struct Pos {
+        int seg, kb;
+      };
+      const int seg0 = min(lo / ib, n);
+      Pos lw{seg0, lo - seg0 * ib}, lh = lw, u = lw;
+      // Whether a new segment begins.
+      auto step = [&](Pos& p) __attribute__((always_inline)) {
+        if (p.seg == n || ++p.kb < ib) {
+          p.kb += p.seg == n;
+          return false;
+        }
+        ++p.seg;
+        p.kb = 0;
+        return true;
+      };
       Matrices m{};
       WRow row[NS];
+      auto enter_w = [&]() __attribute__((always_inline)) {
+        const bool shared = lw.seg == n;
+        const int width = (shared ? a.S : a.I);
+        const size_t first = shared ? 0 : static_cast<size_t>(__builtin_amdgcn_readfirstlane(R.seg_expert[lw.seg])) * a.H;
+        m.w[0] = m.w[1] = static_cast<const uint8_t*>((shared ? a.ws_down : a.w_down)) + first * row_bytes<FMT>(width);
+        m.s[0] = m.s[1] = static_cast<const uint8_t*>((shared ? a.ss_down : a.s_down)) + first * scale_bytes<FMT>(width);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          const int row0 = (tile * NS + j) * 16 + (lane & 7);
+          row[j] = weight_rows<FMT>(m, min(row0, a.H - 1), min(row0 + 8, a.H - 1), width, lane);
+        }
+      };
       uint32_t hoff = 0;
       size_t hbase = 0;
       bool live = false;
-      auto enter = [&]() __attribute__((always_inline)) {
-        const bool shared = lseg == n;
-        const int width = shared ? a.S : a.I;
-        const size_t first = shared ? 0 : static_cast<size_t>(__builtin_amdgcn_readfirstlane(R.seg_expert[lseg])) * a.H;
-        m.w[0] = m.w[1] = static_cast<const uint8_t*>(shared ? a.ws_down : a.w_down) + first * row_bytes<FMT>(width);
-        m.s[0] = m.s[1] = static_cast<const uint8_t*>(shared ? a.ss_down : a.s_down) + first * scale_bytes<FMT>(width);
-#pragma unroll
-        for (int j = 0; j < NS; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            set_row<FMT>(row[j], h, min((tile * NS + j) * 16 + 8 * h + (lane & 7), a.H - 1), width, lane);
-        const int slot = R.seg_slot[lseg][r];
+      auto enter_h = [&]() __attribute__((always_inline)) {
+        const bool shared = lh.seg == n;
+        const int slot = R.seg_slot[lh.seg][r];
         live = slot >= 0;
         hbase = (shared ? h_shared : 0) * (F::kF32 ? 4 : 2);
-        hoff = static_cast<uint32_t>(max(slot, 0)) * static_cast<uint32_t>(width) * (F::kF32 ? 4 : 2);
+        hoff = static_cast<uint32_t>(max(slot, 0)) * static_cast<uint32_t>((shared ? a.S : a.I)) * (F::kF32 ? 4 : 2);
       };
-      if (lo < hi) enter();
+      if (lo < hi) {
+        enter_w();
+        enter_h();
+      }
       f32x4 acc[NS];
 #pragma unroll
       for (int j = 0; j < NS; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-      batches<FewBatch<FMT>::kDown, DownBlk<FMT>>(
-          hi - lo,
-          [&](DownBlk<FMT>& k) __attribute__((always_inline)) {
-            if (lseg < n && lkb == ib) {
-              ++lseg;
-              lkb = 0;
-              enter();
-            }
-            const bool shared = lseg == n;
-            const int width = shared ? a.S : a.I, vec = shared ? a.svec : a.ivec;
+      constexpr int D = FewBatch<FMT>::kDown;
+      for (int c = lo; c < hi; c += D) {
+        DownBlk<FMT> k[D];
 #pragma unroll
-            for (int j = 0; j < NS; ++j) load_w<FMT>(k.w[j], m, row[j], lkb, lane, width, vec);
+        for (int d = 0; d < D; ++d)
+          if (c + d < hi) {
+            const bool shared = lw.seg == n;
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+              load_w<FMT>(k[d].w[j], m, row[j], lw.kb, lane, (shared ? a.S : a.I), (shared ? a.svec : a.ivec));
+            if (step(lw) && c + d + 1 < hi) enter_w();
+          }
+        // The weights do not depend on h: the first ones are on their way during the wait.
+        wait_for_h();
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+          if (c + d < hi) {
+            const bool shared = lh.seg == n;
 #pragma unroll
             for (int p = 0; p < DownBlk<FMT>::kPlanes; ++p)
-              load_x<FMT>(k.h[p], static_cast<const uint8_t*>(a.h[p]) + hbase, hoff, lkb, lane, width, vec, live);
-            ++lkb;
-          },
-          [&](DownBlk<FMT>& k) __attribute__((always_inline)) {
-            if (useg < n && ukb == ib) {
-              ++useg;
-              ukb = 0;
-            }
-            ++ukb;
-            const float4 wt = *reinterpret_cast<const float4*>(&R.seg_w[useg][4 * g]);
+              load_x<FMT>(k[d].h[p], static_cast<const uint8_t*>(a.h[p]) + hbase, hoff, lh.kb, lane,
+                          (shared ? a.S : a.I), (shared ? a.svec : a.ivec), live);
+            if (step(lh) && c + d + 1 < hi) enter_h();
+          }
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+          if (c + d < hi) {
+            const float4 wt = *reinterpret_cast<const float4*>(&R.seg_w[u.seg][4 * g]);
             const float ws[4] = {wt.x, wt.y, wt.z, wt.w};
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
-              const f32x4 t = mma_planes<FMT, DownBlk<FMT>::kPlanes>(k.h, k.w[j], lane, f32x4{0.f, 0.f, 0.f, 0.f});
+              const f32x4 t = mma_planes<FMT, DownBlk<FMT>::kPlanes>(k[d].h, k[d].w[j], lane, f32x4{0.f, 0.f, 0.f, 0.f});
               // A token that the expert does not serve takes nothing, not 0 * inf either.
 #pragma unroll
               for (int q = 0; q < 4; ++q) acc[j][q] = ws[q] != 0.f ? fmaf(ws[q], t[q], acc[j][q]) : acc[j][q];
             }
-          });
+            step(u);
+          }
+      }
+      wait_for_h();                  // a wave without a block
       __syncthreads();               // the previous tile has been added up
 #pragma unroll
       for (int j = 0; j < NS; ++j) red[j].v[wave][lane] = acc[j];

@@ -36,18 +36,23 @@ struct SkinnyFmt {
 };
 constexpr int kBlkBytes = 128;   // of a weight row
 
-// A lane's view of its two weight rows of a tile, c % 8 of the first and of the second
-// 8: offsets of its piece of block 0, and of its scale, from a base that the whole
-// wave shares.
+// The matrices of a tile's first and second 8 rows, and their scales.
+struct Matrices {
+  const void *w[2], *s[2];
+};
+// A lane's view of a tile: offsets of its piece of block 0 in rows c % 8 of the first
+// and of the second 8, and the scales of the tile's row c (the row whose operands the
+// lane holds after the trade).
 struct WRow {
-  uint32_t w[2], s[2];
+  uint32_t w[2];
+  const uint8_t* s;
 };
 
 // One block of a tile, as loaded.
 template <int FMT>
 struct WBlk {
   uint4 v[2];
-  float s[2];     // fp8 group scale, or 2^(e - 127) of the lane's MXFP4 block
+  uint2 s;        // fp8: the row's group scale; MXFP4: its 8 E8M0 codes
 };
 template <int FMT>
 struct XBlk {
@@ -69,13 +74,17 @@ __host__ __device__ constexpr size_t scale_bytes(int k) {
 // A lane's 16-byte piece of its block.
 __device__ __forceinline__ int lane_piece(int lane) { return ((lane >> 1) & 4) + (lane >> 4); }
 
-// The h-th row of the lane is row `row` of a matrix of rows of k elements.  A matrix
-// starts at the base that load_w is given and is smaller than 4 GiB.
+// Rows row0 and row1, of k elements, of the first and the second matrix are the lane's
+// rows c % 8.  A matrix is smaller than 4 GiB.
 template <int FMT>
-__device__ __forceinline__ void set_row(WRow& r, int h, int row, int k, int lane) {
-  r.w[h] = static_cast<uint32_t>(row) * static_cast<uint32_t>(row_bytes<FMT>(k)) + 16 * lane_piece(lane);
-  r.s[h] = static_cast<uint32_t>(row) * static_cast<uint32_t>(scale_bytes<FMT>(k)) +
-           (FMT == kDtypeMxfp4 ? lane_piece(lane) : 0);
+__device__ __forceinline__ WRow weight_rows(const Matrices& m, int row0, int row1, int k, int lane) {
+  WRow r;
+  const uint32_t bytes = static_cast<uint32_t>(row_bytes<FMT>(k));
+  r.w[0] = static_cast<uint32_t>(row0) * bytes + 16 * lane_piece(lane);
+  r.w[1] = static_cast<uint32_t>(row1) * bytes + 16 * lane_piece(lane);
+  r.s = static_cast<const uint8_t*>((lane & 8) ? m.s[1] : m.s[0]) +
+        static_cast<size_t>((lane & 8) ? row1 : row0) * scale_bytes<FMT>(k);
+  return r;
 }
 
 // Four floats, of which the row holds the first n (vec: 16-byte aligned, all or none).
@@ -93,27 +102,22 @@ __device__ __forceinline__ uint4 ld_f32x4(const uint8_t* p, int n, bool vec) {
   return r;
 }
 
-// Block b of a tile's weight rows, the first 8 from the matrix at w[0], the others from
-// the one at w[1] (scales at s).  kdim and vec matter to f32 only: the other types come
-// in whole blocks, 16-byte aligned.
-struct Matrices {
-  const void *w[2], *s[2];
-};
+// Block b of a tile's weight rows.  kdim and vec matter to f32 only: the other types
+// come in whole blocks, 16-byte aligned.
 template <int FMT>
 __device__ __forceinline__ void load_w(WBlk<FMT>& k, const Matrices& m, const WRow& r, int b, int lane, int kdim,
                                        bool vec) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint8_t* wb = static_cast<const uint8_t*>(m.w[h]) + static_cast<size_t>(b) * kBlkBytes;
-    const uint8_t* sb = static_cast<const uint8_t*>(m.s[h]);
-    if constexpr (FMT == kDtypeF32) {
-      k.v[h] = ld_f32x4(wb + r.w[h], kdim - 32 * b - 4 * lane_piece(lane), vec);
-    } else {
-      k.v[h] = ld16_stream(wb + r.w[h]);
-      if constexpr (FMT == kDtypeFp8) k.s[h] = *reinterpret_cast<const float*>(sb + 4 * b + r.s[h]);
-      if constexpr (FMT == kDtypeMxfp4)
-        k.s[h] = __uint_as_float(static_cast<uint32_t>(*(sb + 8 * b + r.s[h])) << 23);
-    }
+    if constexpr (FMT == kDtypeF32) k.v[h] = ld_f32x4(wb + r.w[h], kdim - 32 * b - 4 * lane_piece(lane), vec);
+    else k.v[h] = ld16_stream(wb + r.w[h]);
+  }
+  if constexpr (FMT == kDtypeFp8) k.s.x = *reinterpret_cast<const uint32_t*>(r.s + 4 * b);
+  if constexpr (FMT == kDtypeMxfp4) {
+    typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+    const u32x2_any v = *reinterpret_cast<const u32x2_any*>(r.s + 8 * b);
+    k.s = uint2{v.x, v.y};
   }
 }
 
@@ -193,23 +197,24 @@ __device__ __forceinline__ f32x4 mma_planes(const XBlk<FMT> (&x)[N], WBlk<FMT> w
     }
     return acc;
   } else {
+    // 2^(e - 127) of the lane's E8M0 blocks, code g of either half.
+    float e8[2] = {0.f, 0.f};
     if constexpr (FMT == kDtypeMxfp4) {
-      uint32_t s0 = __float_as_uint(w.s[0]), s1 = __float_as_uint(w.s[1]);
-      trade(s0, s1, upper);
-      w.s[0] = __uint_as_float(s0);
-      w.s[1] = __uint_as_float(s1);
+      const int at = 8 * (lane >> 4);
+      e8[0] = __uint_as_float(((w.s.x >> at) & 0xffu) << 23);
+      e8[1] = __uint_as_float(((w.s.y >> at) & 0xffu) << 23);
     }
     f32x4 t = FMT == kDtypeFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int q = 0; q < SkinnyFmt<FMT>::kX; ++q) {
-        const uint4 wq = decode_w<FMT>(w.v[h], w.s[h], q);
+        const uint4 wq = decode_w<FMT>(w.v[h], e8[h], q);
 #pragma unroll
         for (int p = N - 1; p >= 0; --p) t = mfma_bf16_16x16x32(x[p].v[h][q], wq, t);   // the smallest plane first
       }
     if constexpr (FMT == kDtypeFp8) {
-      const float s = upper ? w.s[1] : w.s[0];
+      const float s = __uint_as_float(w.s.x);
 #pragma unroll
       for (int i = 0; i < 4; ++i) t[i] = fmaf(t[i], s, acc[i]);
     }
@@ -219,19 +224,21 @@ __device__ __forceinline__ f32x4 mma_planes(const XBlk<FMT> (&x)[N], WBlk<FMT> w
 
 // Runs n blocks in batches of D: the loads of a batch are issued together, then its
 // blocks are used.  A wave waits for a whole batch; its neighbours on the CU fill that
-// time (a ring that keeps loads in flight across batches needed more registers, which
-// halved the waves, and ran slower).  issue and use step their own position.
-template <int D, class B, class Issue, class Use>
-__device__ __forceinline__ void batches(int n, Issue issue, Use use) {
+// time.  issue and use step their own position; first() runs once, when the first
+// batch's loads have been issued.
+template <int D, class B, class Issue, class Use, class First>
+__device__ __forceinline__ void batches(int n, Issue issue, Use use, First first) {
   for (int c = 0; c < n; c += D) {
     B b[D];
 #pragma unroll
     for (int s = 0; s < D; ++s)
       if (c + s < n) issue(b[s]);
+    if (c == 0) first();
 #pragma unroll
     for (int s = 0; s < D; ++s)
       if (c + s < n) use(b[s]);
   }
+  if (n <= 0) first();
 }
 
 }  // namespace
