@@ -5,15 +5,14 @@
 // is lost between kernels, where the memory stands idle while one grid drains and
 // the next fills, so the layer runs as two grids:
 //
-//   few_first_kernel   what does not depend on the routing: the router logits, split
-//                      over the contraction, and the shared expert's gate/up half.
-//                      It also clears the counters of the second kernel.
-//   few_second_kernel  every workgroup works the routing out from the logits by
-//                      itself (16 tokens: a few microseconds, no grid-wide step),
-//                      runs its share of the touched experts' gate/up tiles, waits
-//                      for the others', and runs its share of the down half, which
-//                      contracts over all touched experts and the shared expert at
-//                      once, so that y leaves the kernel finished.
+//   few_first_kernel   the router logits, split over the contraction; it also clears
+//                      the counters of the second kernel.
+//   few_second_kernel  a few workgroups work the routing out from the logits and
+//                      publish it; meanwhile the others run the shared expert's
+//                      gate/up tiles, which do not depend on it.  Then the touched
+//                      experts' gate/up tiles, and the down half, which contracts over
+//                      all touched experts and the shared expert at once, so that y
+//                      leaves the kernel finished.
 //
 // All tokens are the 16 rows of one MFMA tile, whatever expert they go to; a row
 // that an expert does not serve is zero there and its result is not used.  That
@@ -24,7 +23,8 @@
 // others), so a tile that has been taken is held by a workgroup that is running, and
 // that finishes it without waiting for anything.  A workgroup waits only when it has
 // seen all queues empty: the wait ends, whatever part of the grid is resident, also
-// when other kernels hold part of the GPU.
+// when other kernels hold part of the GPU.  The wait for the published routing is
+// bounded: a workgroup that does not find it in time works it out by itself.
 //
 // y is the same from run to run: every sum has a fixed order (queues and
 // counters say who works and when something is complete, not in which order it is
@@ -47,6 +47,7 @@ constexpr int kFewThreads = 256;
 constexpr int kFewWaves = kFewThreads / kWave;
 constexpr int kFewGrid = 512;
 constexpr int kFewTokens = MOE_FEW_TOKENS;
+static_assert(kFewTokens * kMaxTopK <= kFewThreads, "a thread for each slot");
 static_assert(kFewTokens == kSkinnyRows, "one MFMA tile of tokens");
 constexpr int kFewSlots = kFewTokens * kMaxTopK;
 constexpr int kFewRouterParts = 4;         // contraction parts of the router, at most
@@ -67,6 +68,7 @@ struct FewArgs {
   int* ctl;                // counters of the second kernel, see Ctl
   float* z;                // [parts, 16, ldz] partial logits
   void* h[3];              // planes of [T*K, I] routed then [T, S] shared rows
+  int* routed;             // published routing: ids and weights [T, K], shared gates [T]
   float* part;             // [2 * kMaxRanges, sets, 256] partial down tiles
   int T, H, E, I, K, S, ncols, ldz, parts, norm, budget;
   float top_p;
@@ -208,12 +210,14 @@ __device__ __forceinline__ void store_h(const FewArgs& a, const f32x4& s, size_t
 // (atomics on one line take about 10 ns each, whoever sends them).
 struct Ctl {
   static constexpr int kLine = 32;                          // ints
-  static constexpr int kQueue = 0;                          // next gate/up tile of each queue
-  static constexpr int kDone = kQueue + kQueues * kLine;    // finished tiles, in 16 counters
+  static constexpr int kQueue = 0;                          // next gate/up item of each queue
+  static constexpr int kSharedQueue = kQueue + kQueues * kLine;   // the same for the shared expert
+  static constexpr int kDone = kSharedQueue + kQueues * kLine;    // finished tiles, in 16 counters
   static constexpr int kGroups = 16;
   static constexpr int kGo = kDone + kGroups * kLine;       // all tiles finished, one flag for each group
   static constexpr int kRange = kGo + kGroups * kLine;      // next down range
-  static constexpr int kTile = kRange + kLine;              // finished parts of each down tile
+  static constexpr int kRouted = kRange + kLine;            // routing published, one flag for four tokens
+  static constexpr int kTile = kRouted + 4 * kLine;         // finished parts of each down tile
 };
 __host__ __device__ inline int ctl_ints(int H) { return Ctl::kTile + (H + 15) / 16; }   // enough for any kSets
 
@@ -225,53 +229,34 @@ __device__ __forceinline__ int ctl_add(int* p, int v) {
 
 __host__ __device__ inline int router_tiles(int E, int S) { return (E + 15) / 16 + (S > 0 ? 1 : 0); }
 
-template <int FMT>
+// AFMT: the type of x and of the router.
+template <int AFMT>
 __global__ void __launch_bounds__(kFewThreads, 2) few_first_kernel(FewArgs a) {
-  constexpr int AFMT = FMT == kDtypeF32 ? kDtypeF32 : kDtypeBf16;   // the router's type
   __shared__ Red red;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
   for (int i = blockIdx.x * kFewThreads + tid; i < ctl_ints(a.H); i += gridDim.x * kFewThreads) a.ctl[i] = 0;
 
   const uint32_t xoff = static_cast<uint32_t>(min(r, a.T - 1)) * static_cast<uint32_t>(row_bytes<AFMT>(a.H));
-  const bool live = r < a.T;
-  const int router = router_tiles(a.E, a.S) * a.parts;
-  const int item = blockIdx.x;
-  if (item < router) {
-    // 16 logits; the last tile is the shared gate's, alone in a matrix of one row.
-    const int part = item % a.parts, tile = item / a.parts;
-    const int nb = static_cast<int>(ceil_div(a.H, SkinnyFmt<AFMT>::kBlk));
-    const bool gate = tile * 16 >= a.E;
-    const int c0 = gate ? a.E : tile * 16, cols = gate ? 1 : min(16, a.E - c0);
-    const void* w = (gate ? a.w_gcol : a.w_router);
-    const Matrices m{{w, w}, {nullptr, nullptr}};
-    const int row0 = (gate ? 0 : c0) + min(lane & 7, cols - 1), row1 = (gate ? 0 : c0) + min(8 + (lane & 7), cols - 1);
-    const WRow row[1] = {weight_rows<AFMT>(m, row0, row1, a.H, lane)};
-    f32x4 acc[1];
-    wave_tiles<AFMT, 1>(m, row, a.x, xoff, live, part * nb / a.parts, (part + 1) * nb / a.parts, a.H, a.hvec, wave,
-                        lane, acc, [] {});
-    red.v[wave][lane] = acc[0];
-    __syncthreads();
-    if (wave == 0 && r < cols) {
-      const f32x4 s = red_sum(red, lane);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        a.z[(static_cast<size_t>(part) * kFewTokens + 4 * g + i) * a.ldz + c0 + r] = s[i];
-    }
-    return;
-  }
-  const int n0 = (item - router) * 8;
-  const Matrices m = gate_up<FMT>(a.ws_gate, a.ws_up, a.ss_gate, a.ss_up, 0, a.S, a.H);
-  const WRow row[1] = {gate_up_row<FMT>(m, n0, a.S, a.H, lane)};
+  // 16 logits; the last tile is the shared gate's, alone in a matrix of one row.
+  const int part = blockIdx.x % a.parts, tile = blockIdx.x / a.parts;
+  const int nb = static_cast<int>(ceil_div(a.H, SkinnyFmt<AFMT>::kBlk));
+  const bool gate = tile * 16 >= a.E;
+  const int c0 = gate ? a.E : tile * 16, cols = gate ? 1 : min(16, a.E - c0);
+  const void* w = gate ? a.w_gcol : a.w_router;
+  const Matrices m{{w, w}, {nullptr, nullptr}};
+  const int row0 = (gate ? 0 : c0) + min(lane & 7, cols - 1), row1 = (gate ? 0 : c0) + min(8 + (lane & 7), cols - 1);
+  const WRow row[1] = {weight_rows<AFMT>(m, row0, row1, a.H, lane)};
   f32x4 acc[1];
-  wave_tiles<FMT, 1>(m, row, a.x, xoff, live, 0, static_cast<int>(ceil_div(a.H, SkinnyFmt<FMT>::kBlk)), a.H, a.hvec,
-                     wave, lane, acc, [] {});
+  wave_tiles<AFMT, 1>(m, row, a.x, xoff, r < a.T, part * nb / a.parts, (part + 1) * nb / a.parts, a.H, a.hvec, wave,
+                      lane, acc, [] {});
   red.v[wave][lane] = acc[0];
   __syncthreads();
-  if (wave == 0) {
+  if (wave == 0 && r < cols) {
     const f32x4 s = red_sum(red, lane);
-    store_h<FMT>(a, s, static_cast<size_t>(a.T) * a.K * a.I, n0, a.S, lane,
-                 [&](int t) { return t < a.T ? t : -1; });
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      a.z[(static_cast<size_t>(part) * kFewTokens + 4 * g + i) * a.ldz + c0 + r] = s[i];
   }
 }
 
@@ -302,6 +287,9 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   return max(max(a, b), max(c, d));
 }
 
+// Looks at a routing flag before a workgroup does the routing itself (about 0.4 us each).
+constexpr int kRouteTries = 64;
+
 constexpr double kFewFixed = 8589934592.0;   // 2^33: budget aggregates in fixed point, as in moe_route
 
 // What every workgroup knows of the call's routing.
@@ -318,168 +306,162 @@ struct RouteScratch {
   unsigned long long agg[kMaxExperts];
   int seg_of[kMaxExperts];
   int nu, dropped, empty;
-  struct {
+  struct alignas(16) {
     unsigned long long mass;
     int id;
   } list[kFewSlots];               // the experts in use
 };
 
-// Top-k of TN tokens t0, t0 + 4, ... by one wave (same selection and trim as moe_route).
-// A lane holds the keys of experts 4 lane .. + 4 (and 256 further on), sorted; each
-// round takes the largest head of the lanes.  The rounds are chains of dependent
-// steps, so several tokens go through them together.
-template <int NQ, int TN>
-__device__ __forceinline__ void route_some(const FewArgs& a, Routing& R, int t0, int lane) {
+// Top-k of token t by one wave (same selection and trim as moe_route).  A lane holds
+// the keys of experts 4 lane .. + 4 (and 256 further on), sorted; each round takes the
+// largest head of the lanes.
+template <int NQ>
+__device__ __forceinline__ void route_token(const FewArgs& a, Routing& R, int t, int lane) {
   constexpr int NJ = 4 * NQ;
   const size_t plane = static_cast<size_t>(kFewTokens) * a.ldz;
-  uint32_t key[TN][NJ];
-  int id[NJ][TN];
-  float gate[TN];
+  const float* zr = a.z + static_cast<size_t>(t) * a.ldz;
+  const float* bias = a.bias ? a.bias + static_cast<size_t>(t) * a.E : nullptr;
+  uint32_t key[NJ];
+  int id[NJ];
   // All loads first.  Rows of z are multiples of 16 long; a lane takes 4 columns at a time.
-  f32x4 v[TN][NQ][kFewRouterParts];
-  float gv[TN][kFewRouterParts];
+  f32x4 v[NQ][kFewRouterParts];
+  float b[NJ], gv[kFewRouterParts];
 #pragma unroll
-  for (int i = 0; i < TN; ++i) {
-    const float* zr = a.z + static_cast<size_t>(min(t0 + i * kFewWaves, a.T - 1)) * a.ldz;
+  for (int q = 0; q < NQ; ++q) {
+    const int e = 4 * (lane + kWave * q);
 #pragma unroll
-    for (int q = 0; q < NQ; ++q)
+    for (int p = 0; p < kFewRouterParts; ++p)
+      v[q][p] = p < a.parts && e < a.E ? *reinterpret_cast<const f32x4*>(zr + p * plane + e) : f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int p = 0; p < kFewRouterParts; ++p)
-        v[i][q][p] = p < a.parts && 4 * (lane + kWave * q) < a.E ? *reinterpret_cast<const f32x4*>(zr + p * plane + 4 * (lane + kWave * q))
-                                                                 : f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int p = 0; p < kFewRouterParts; ++p) gv[i][p] = p < a.parts && a.S > 0 ? zr[p * plane + a.E] : 0.f;
+    for (int c = 0; c < 4; ++c) b[4 * q + c] = bias && e + c < a.E ? bias[e + c] : 0.f;
   }
 #pragma unroll
-  for (int i = 0; i < TN; ++i) {
-    const float* bias = a.bias ? a.bias + static_cast<size_t>(min(t0 + i * kFewWaves, a.T - 1)) * a.E : nullptr;
+  for (int p = 0; p < kFewRouterParts; ++p) gv[p] = p < a.parts && a.S > 0 ? zr[p * plane + a.E] : 0.f;
 #pragma unroll
-    for (int q = 0; q < NQ; ++q)
+  for (int j = 0; j < NJ; ++j) {
+    const int e = 4 * (lane + kWave * (j / 4)) + j % 4;
+    float z = v[j / 4][0][j % 4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int e = 4 * (lane + kWave * q) + c;
-        float z = v[i][q][0][c];
-#pragma unroll
-        for (int p = 1; p < kFewRouterParts; ++p) z += v[i][q][p][c];
-        if (bias && e < a.E) z += bias[e];
-        key[i][4 * q + c] = e < a.E ? order_key(z == z ? z : -INFINITY) : 0;
-        id[4 * q + c][i] = e;
-      }
-    gate[i] = gv[i][0];
-#pragma unroll
-    for (int p = 1; p < kFewRouterParts; ++p) gate[i] += gv[i][p];
+    for (int p = 1; p < kFewRouterParts; ++p) z += v[j / 4][p][j % 4];
+    z += b[j];
+    key[j] = e < a.E ? order_key(z == z ? z : -INFINITY) : 0;
+    id[j] = e;
   }
+  float gate = gv[0];
+#pragma unroll
+  for (int p = 1; p < kFewRouterParts; ++p) gate += gv[p];
   // Odd-even merge sort of 4 or 8: descending, the lower id first among equals.
   auto order = [&](int x, int y) __attribute__((always_inline)) {
-    if (y >= NJ) return;
-#pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      const bool swap = key[i][y] > key[i][x] || (key[i][y] == key[i][x] && id[y][i] < id[x][i]);
-      const uint32_t k = swap ? key[i][y] : key[i][x];
-      key[i][y] = swap ? key[i][x] : key[i][y];
-      key[i][x] = k;
-      const int e = swap ? id[y][i] : id[x][i];
-      id[y][i] = swap ? id[x][i] : id[y][i];
-      id[x][i] = e;
-    }
+    const bool swap = key[y] > key[x] || (key[y] == key[x] && id[y] < id[x]);
+    const uint32_t k = swap ? key[y] : key[x];
+    key[y] = swap ? key[x] : key[y];
+    key[x] = k;
+    const int e = swap ? id[y] : id[x];
+    id[y] = swap ? id[x] : id[y];
+    id[x] = e;
   };
   order(0, 1); order(2, 3); order(0, 2); order(1, 3); order(1, 2);
   if constexpr (NJ > 4) {
     order(4, 5); order(6, 7); order(4, 6); order(5, 7); order(5, 6);
     order(0, 4); order(1, 5); order(2, 6); order(3, 7); order(2, 4); order(3, 5); order(1, 2); order(3, 4); order(5, 6);
   }
-  float zmax[TN], denom_all[TN], my_z[TN];
-  int my_id[TN];
-#pragma unroll
-  for (int i = 0; i < TN; ++i) {
-    zmax[i] = key_value(wave_max_u32(key[i][0]));
-    denom_all[i] = 0.f;
-    my_z[i] = 0.f;
-    my_id[i] = -1;
-  }
+  const float zmax = key_value(wave_max_u32(key[0]));
   // Softmax denominator over all experts (only without renormalisation).
+  float denom_all = 0.f;
   if (!a.norm) {
 #pragma unroll
-    for (int i = 0; i < TN; ++i) {
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        if (key[i][j] != 0) denom_all[i] += expf(key_value(key[i][j]) - zmax[i]);
-      denom_all[i] = wave_sum(denom_all[i]);
-    }
+    for (int j = 0; j < NJ; ++j)
+      if (key[j] != 0) denom_all += expf(key_value(key[j]) - zmax);
+    denom_all = wave_sum(denom_all);
   }
+  int my_id = -1;
+  float my_z = 0.f;
   for (int k = 0; k < a.K; ++k) {
-    uint32_t m[TN];
-    unsigned long long has[TN], more = 0;
-#pragma unroll
-    for (int i = 0; i < TN; ++i) m[i] = wave_max_u32(key[i][0]);
-#pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      has[i] = __ballot(key[i][0] == m[i]);
-      more |= has[i] & (has[i] - 1);
+    const uint32_t m = wave_max_u32(key[0]);
+    unsigned long long has = __ballot(key[0] == m);
+    int owner = __builtin_ctzll(has), e = __builtin_amdgcn_readlane(id[0], owner);
+    for (has &= has - 1; has; has &= has - 1) {        // ties: the lowest id
+      const int o = __builtin_ctzll(has), f = __builtin_amdgcn_readlane(id[0], o);
+      if (f < e) { e = f; owner = o; }
     }
-    int owner[TN], e[TN];
+    const bool pop = lane == owner;
 #pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      owner[i] = __builtin_ctzll(has[i]);
-      e[i] = __builtin_amdgcn_readlane(id[0][i], owner[i]);
+    for (int j = 0; j < NJ; ++j) {
+      key[j] = pop ? (j + 1 < NJ ? key[j + 1 < NJ ? j + 1 : j] : 0) : key[j];
+      id[j] = pop ? id[j + 1 < NJ ? j + 1 : j] : id[j];
     }
-    if (more) {                        // ties: the lowest id
-#pragma unroll
-      for (int i = 0; i < TN; ++i)
-        for (unsigned long long h = has[i] & (has[i] - 1); h; h &= h - 1) {
-          const int o = __builtin_ctzll(h), f = __builtin_amdgcn_readlane(id[0][i], o);
-          if (f < e[i]) { e[i] = f; owner[i] = o; }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      const bool pop = lane == owner[i];
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        key[i][j] = pop ? (j + 1 < NJ ? key[i][j + 1 < NJ ? j + 1 : j] : 0) : key[i][j];
-        id[j][i] = pop ? id[j + 1 < NJ ? j + 1 : j][i] : id[j][i];
-      }
-      if (lane == k) { my_id[i] = e[i]; my_z[i] = key_value(m[i]); }
-    }
+    if (lane == k) { my_id = e; my_z = key_value(m); }
   }
-#pragma unroll
-  for (int i = 0; i < TN; ++i) {
-    const int t = t0 + i * kFewWaves;
-    const float p = lane < a.K ? expf(my_z[i] - zmax[i]) : 0.f;
-    bool kept = lane < a.K;
-    if (a.top_p > 0.f) {
-      float before = 0.f, all = 0.f;
-      for (int k = 0; k < a.K; ++k) {
-        const float pk = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(p), k));
-        if (k < lane) before += pk;
-        all += pk;
-      }
-      kept = kept && (lane == 0 || before < a.top_p * all);
+  const float p = lane < a.K ? expf(my_z - zmax) : 0.f;
+  bool kept = lane < a.K;
+  if (a.top_p > 0.f) {
+    float before = 0.f, all = 0.f;
+    for (int k = 0; k < a.K; ++k) {
+      const float pk = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(p), k));
+      if (k < lane) before += pk;
+      all += pk;
     }
-    const float pk = kept ? p : 0.f;
-    const float denom = a.norm ? wave_sum(pk) : denom_all[i];
-    if (t < a.T) {
-      if (lane < a.K) {
-        R.ids[t * a.K + lane] = kept ? my_id[i] : -1;
-        R.w[t * a.K + lane] = pk / denom;
-      }
-      if (lane == 0) R.sg[t] = a.S > 0 ? 1.0f / (1.0f + expf(-gate[i])) : 0.f;
-    }
+    kept = kept && (lane == 0 || before < a.top_p * all);
   }
+  const float pk = kept ? p : 0.f;
+  const float denom = a.norm ? wave_sum(pk) : denom_all;
+  if (lane < a.K) {
+    R.ids[t * a.K + lane] = kept ? my_id : -1;
+    R.w[t * a.K + lane] = pk / denom;
+  }
+  if (lane == 0) R.sg[t] = a.S > 0 ? 1.0f / (1.0f + expf(-gate)) : 0.f;
 }
 
-// Same routing as moe_route, budget included.
-__device__ __forceinline__ void route_tokens(const FewArgs& a, Routing& R, RouteScratch& C, bool report) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  if (a.T <= kFewWaves) {
-    if (wave < a.T) {
-      if (a.E <= 256) route_some<1, 1>(a, R, wave, lane);
-      else route_some<2, 1>(a, R, wave, lane);
-    }
-  } else {
-    if (a.E <= 256) route_some<1, 4>(a, R, wave, lane);
-    else route_some<2, 4>(a, R, wave, lane);
+// Routes and publishes tokens 4 j to 4 j + 3 (j: the workgroup).
+__device__ __forceinline__ void publish_routing(const FewArgs& a, Routing& R, int j, int wave, int lane) {
+  const int tid = threadIdx.x, t = j * kFewWaves + wave;
+  if (t < a.T) {
+    if (a.E <= 256) route_token<1>(a, R, t, lane);
+    else route_token<2>(a, R, t, lane);
   }
+  __syncthreads();
+  const int first = j * kFewWaves * a.K, n = min(kFewWaves * a.K, a.T * a.K - first);
+  if (tid < n) {
+    st_shared(a.routed + first + tid, R.ids[first + tid]);
+    st_shared(a.routed + kFewSlots + first + tid, __float_as_int(R.w[first + tid]));
+  }
+  if (tid < kFewWaves && j * kFewWaves + tid < a.T)
+    st_shared(a.routed + 2 * kFewSlots + j * kFewWaves + tid, __float_as_int(R.sg[j * kFewWaves + tid]));
+  stores_done();
+  __syncthreads();
+  if (tid == 0) st_shared(a.ctl + Ctl::kRouted + j * Ctl::kLine, 1);
+}
+
+// All tokens' routing: as published, or if that does not come in time, worked out here.
+__device__ __forceinline__ void fetch_routing(const FewArgs& a, Routing& R, RouteScratch& C, int wave, int lane) {
+  const int tid = threadIdx.x, groups = (a.T + kFewWaves - 1) / kFewWaves;
+  if (wave == 0) {
+    bool there = false;
+    for (int i = 0; i < kRouteTries && !there; ++i) {
+      if (i > 0) __builtin_amdgcn_s_sleep(4);
+      there = __all(lane >= groups || ld_shared(a.ctl + Ctl::kRouted + min(lane, groups - 1) * Ctl::kLine) != 0);
+    }
+    if (lane == 0) C.nu = there;
+  }
+  __syncthreads();
+  if (C.nu) {
+    if (tid < a.T * a.K) {
+      R.ids[tid] = ld_shared(a.routed + tid);
+      R.w[tid] = __int_as_float(ld_shared(a.routed + kFewSlots + tid));
+    }
+    if (tid < a.T) R.sg[tid] = __int_as_float(ld_shared(a.routed + 2 * kFewSlots + tid));
+  } else {
+    for (int t = wave; t < a.T; t += kFewWaves) {
+      if (a.E <= 256) route_token<1>(a, R, t, lane);
+      else route_token<2>(a, R, t, lane);
+    }
+  }
+  __syncthreads();
+}
+
+// The budget over all tokens, as in moe_route, then the touched experts' segments.
+__device__ __forceinline__ void finish_routing(const FewArgs& a, Routing& R, RouteScratch& C, bool report) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int slots = a.T * a.K;
   for (int e = tid; e < kMaxExperts; e += kFewThreads) { C.agg[e] = 0ull; C.seg_of[e] = 0; }
   if (tid == 0) { C.nu = 0; C.dropped = 0; C.empty = 0; }
@@ -506,38 +488,34 @@ __device__ __forceinline__ void route_tokens(const FewArgs& a, Routing& R, Route
         mass = C.list[tid].mass = C.agg[e];
       }
       __syncthreads();
-#pragma unroll 8
+#pragma unroll 4
       for (int o = 0; o < nu; ++o) {
-        const unsigned long long other = C.list[o].mass;
-        rank += (other > mass || (other == mass && C.list[o].id < e)) ? 1 : 0;
+        const auto other = C.list[o];
+        rank += static_cast<int>(other.mass > mass) | (static_cast<int>(other.mass == mass) & static_cast<int>(other.id < e));
       }
       __syncthreads();
       if (e >= 0) C.seg_of[e] = rank < a.budget ? 1 : 0;
       __syncthreads();
-      if (tid < a.T) {
-        int* ir = R.ids + tid * a.K;
-        float* wr = R.w + tid * a.K;
-        int nk = 0, nd = 0;
-        float sum = 0.f;
-        for (int k = 0; k < a.K; ++k) {
-          if (ir[k] < 0) continue;
-          if (C.seg_of[ir[k]]) { sum += wr[k]; ++nk; } else { ++nd; }
-        }
-        if (nd) {
-          int j = 0;
-          for (int k = 0; k < a.K; ++k) {
-            const int e2 = ir[k];
-            if (e2 >= 0 && C.seg_of[e2]) {
-              const float v = wr[k];
-              ir[j] = e2;
-              wr[j] = a.norm ? v / sum : v;
-              ++j;
-            }
+      // Kept slots to the front, a wave for each token.
+      for (int t = wave; t < a.T; t += kFewWaves) {
+        int* ir = R.ids + t * a.K;
+        float* wr = R.w + t * a.K;
+        const int id = lane < a.K ? ir[lane] : -1;
+        const float w = lane < a.K ? wr[lane] : 0.f;
+        const bool keep = id >= 0 && C.seg_of[id] != 0;
+        const unsigned long long kept = __ballot(keep), dropped = __ballot(id >= 0 && !keep);
+        const int nk = __popcll(kept);
+        if (dropped) {
+          const float sum = wave_sum(keep ? w : 0.f);
+          if (lane < a.K && lane >= nk) { ir[lane] = -1; wr[lane] = 0.f; }
+          if (keep) {
+            const int at = __popcll(kept & ((1ull << lane) - 1));
+            ir[at] = id;
+            wr[at] = a.norm ? w / sum : w;
           }
-          for (; j < a.K; ++j) { ir[j] = -1; wr[j] = 0.f; }
-          atomicAdd(&C.dropped, nd);
+          if (lane == 0) atomicAdd(&C.dropped, __popcll(dropped));
         }
-        if (nk == 0) atomicAdd(&C.empty, 1);
+        if (nk == 0 && lane == 0) atomicAdd(&C.empty, 1);
       }
       __syncthreads();
     }
@@ -608,14 +586,14 @@ struct DownBlk {
   XBlk<FMT> h[kPlanes];
 };
 
-// The next gate/up tile, or -1 when all queues are empty (called by one thread; q:
-// the queue it is at, all queues from `home` on are tried).  Queue q holds the q-th
+// The next gate/up item, or -1 when all queues are empty (called by one thread; all
+// queues from `home` on are tried, `tried` of them have been found empty).  Queue q holds the q-th
 // eighth of the tiles.
-__device__ __forceinline__ int take_tile(int* ctl, int items, int home, int& tried) {
+__device__ __forceinline__ int take_tile(int* queues, int items, int home, int& tried) {
   for (; tried < kQueues; ++tried) {
     const int q = (home + tried) % kQueues;
     const int lo = q * items / kQueues, n = (q + 1) * items / kQueues - lo;
-    int* c = ctl + Ctl::kQueue + q * Ctl::kLine;
+    int* c = queues + q * Ctl::kLine;
     // Other queues are looked at before they are written to.
     if (tried > 0 && ld_shared(c) >= n) continue;
     const int i = ctl_add(c, 1);
@@ -636,6 +614,7 @@ __device__ __forceinline__ int take_tile(int* ctl, int items, int home, int& tri
 constexpr int kMaxRanges = 4 * kFewGrid;
 constexpr int kShortRange = 2 * kFewWaves;   // blocks: two for each wave
 constexpr int kLongRange = 16 * kFewWaves;
+constexpr int kPartsAhead = 4;               // parts of a tile read at a time
 struct DownCut {
   int tiles, nblk, ranges, q, rem;
   bool graded;
@@ -661,33 +640,41 @@ struct DownCut {
   }
 };
 
-// This workgroup's gate/up items (NS tiles each, `tiles` items for each expert); returns
-// how many it ran.  The next item is taken while one is running, but not before the
-// first loads are on their way: a workgroup that comes early must not take the only
-// item of one that comes late.
-template <int FMT, int NS>
+// This workgroup's gate/up items (NS tiles each, `tiles` items for each expert) of the
+// touched experts, or of the shared expert; returns how many it ran.  The next item is
+// taken while one is running, but not before the first loads are on their way: a
+// workgroup that comes early must not take the only item of one that comes late.
+template <int FMT, int NS, bool SHARED>
 __device__ __forceinline__ int gate_up_half(const FewArgs& a, const Routing& R, Red* red, int& s_next, int items,
                                             int tiles, int wave, int lane) {
   using F = SkinnyFmt<FMT>;
   const int tid = threadIdx.x, r = lane & 15;
-  const int hb = static_cast<int>(ceil_div(a.H, F::kBlk));
+  const int hb = static_cast<int>(ceil_div(a.H, F::kBlk)), width = SHARED ? a.S : a.I;
   const uint32_t xoff = static_cast<uint32_t>(min(r, a.T - 1)) * static_cast<uint32_t>(a.H) * (F::kF32 ? 4 : 2);
+  const size_t hbase = SHARED ? static_cast<size_t>(a.T) * a.K * a.I : 0;
   const int home = blockIdx.x % kQueues;
+  int* queues = a.ctl + (SHARED ? Ctl::kSharedQueue : Ctl::kQueue);
   int tried = 0, finished = 0;
-  if (tid == 0) s_next = take_tile(a.ctl, items, home, tried);
+  // Workgroups 0 to 255 lie on different CUs.  If there is no more than one item for
+  // each CU the others come two microseconds later, so that no CU runs two.
+  if (items <= kFewGrid / 2 && blockIdx.x >= kFewGrid / 2) __builtin_amdgcn_s_sleep(64);
+  if (tid == 0) s_next = take_tile(queues, items, home, tried);
   __syncthreads();
   int item = __builtin_amdgcn_readfirstlane(s_next);
   while (item >= 0) {
-    const int seg = item / tiles, n0 = item % tiles * (8 * NS);
-    const Matrices m = gate_up<FMT>(a.w_gate, a.w_up, a.s_gate, a.s_up, __builtin_amdgcn_readfirstlane(R.seg_expert[seg]), a.I, a.H);
+    const int seg = SHARED ? 0 : item / tiles, n0 = (item - seg * tiles) * (8 * NS);
+    const Matrices m = SHARED ? gate_up<FMT>(a.ws_gate, a.ws_up, a.ss_gate, a.ss_up, 0, width, a.H)
+                              : gate_up<FMT>(a.w_gate, a.w_up, a.s_gate, a.s_up,
+                                             __builtin_amdgcn_readfirstlane(R.seg_expert[seg]), width, a.H);
     WRow row[NS];
 #pragma unroll
-    for (int j = 0; j < NS; ++j) row[j] = gate_up_row<FMT>(m, n0 + 8 * j, a.I, a.H, lane);
+    for (int j = 0; j < NS; ++j) row[j] = gate_up_row<FMT>(m, n0 + 8 * j, width, a.H, lane);
     int next = -1;
     f32x4 acc[NS];
-    wave_tiles<FMT, NS>(m, row, a.x, xoff, R.seg_slot[seg][r] >= 0, 0, hb, a.H, a.hvec, wave, lane, acc,
+    const bool live = SHARED ? r < a.T : R.seg_slot[seg][r] >= 0;
+    wave_tiles<FMT, NS>(m, row, a.x, xoff, live, 0, hb, a.H, a.hvec, wave, lane, acc,
                         [&]() __attribute__((always_inline)) {
-                          if (tid == 0) next = take_tile(a.ctl, items, home, tried);
+                          if (tid == 0) next = take_tile(queues, items, home, tried);
                         });
     __syncthreads();                 // s_next has been read, the previous tiles added up
 #pragma unroll
@@ -699,11 +686,14 @@ __device__ __forceinline__ int gate_up_half(const FewArgs& a, const Routing& R, 
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
         const f32x4 s = red_sum(red[j], lane);
-        store_h<FMT>(a, s, 0, n0 + 8 * j, a.I, lane, [&](int t) { return static_cast<int>(R.seg_slot[seg][t]); });
+        store_h<FMT>(a, s, hbase, n0 + 8 * j, width, lane, [&](int t) {
+          return SHARED ? (t < a.T ? t : -1) : static_cast<int>(R.seg_slot[seg][t]);
+        });
       }
     }
     ++finished;
   }
+  __syncthreads();                   // red and s_next are free
   return finished;
 }
 
@@ -722,16 +712,20 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_second_kernel(FewArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
   if (tid == 0) s_ready = 0;
-  route_tokens(a, R, U.scratch, blockIdx.x == 0);
+  if (static_cast<int>(blockIdx.x) * kFewWaves < a.T) publish_routing(a, R, blockIdx.x, wave, lane);
+  const int shared_items = static_cast<int>(ceil_div(a.S, 8));
+  int finished = 0;
+  if (a.S > 0) finished = gate_up_half<FMT, 1, true>(a, R, red, s_next, shared_items, shared_items, wave, lane);
+  fetch_routing(a, R, U.scratch, wave, lane);
+  finish_routing(a, R, U.scratch, blockIdx.x == 0);
 
-  // ---- gate/up tiles
   const int n = R.n;
   const int gu_tiles = static_cast<int>(ceil_div(a.I, 8)), wide_tiles = static_cast<int>(ceil_div(a.I, 8 * kWide));
   const bool wide = kWide > 1 && n * gu_tiles >= kWideTiles * kFewGrid;
-  const int items = n * (wide ? wide_tiles : gu_tiles);
-  int finished = 0;
-  if (kWide > 1 && wide) finished = gate_up_half<FMT, kWide>(a, R, red, s_next, items, wide_tiles, wave, lane);
-  else finished = gate_up_half<FMT, 1>(a, R, red, s_next, items, gu_tiles, wave, lane);
+  const int routed_items = n * (wide ? wide_tiles : gu_tiles);
+  if (kWide > 1 && wide) finished += gate_up_half<FMT, kWide, false>(a, R, red, s_next, routed_items, wide_tiles, wave, lane);
+  else finished += gate_up_half<FMT, 1, false>(a, R, red, s_next, routed_items, gu_tiles, wave, lane);
+  const int items = routed_items + shared_items;
   // Every h of this workgroup was stored by wave 0.  The last one to count sees all
   // counts, and says so to the others.
   int* go = a.ctl + Ctl::kGo;
@@ -907,13 +901,25 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_second_kernel(FewArgs a) {
         if (__builtin_amdgcn_readfirstlane(before) != b1 - b0) continue;
 #pragma unroll
         for (int j = 0; j < NS; ++j) s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (int o = b0; o <= b1; ++o) {
-          // The tile is range o's first one, unless the range began in an earlier tile.
-          const float* p = a.part + (static_cast<size_t>(o) * 2 + (cut.start(o) / nblk == tile ? 0 : 1)) * (256 * NS);
+        for (int o = b0; o <= b1; o += kPartsAhead) {
+          float v[kPartsAhead][NS][4];
 #pragma unroll
-          for (int j = 0; j < NS; ++j)
+          for (int d = 0; d < kPartsAhead; ++d) {
+            // The tile is range o's first one, unless the range began in an earlier tile.
+            const int at = min(o + d, b1);
+            const float* p = a.part + (static_cast<size_t>(at) * 2 + (cut.start(at) / nblk == tile ? 0 : 1)) * (256 * NS);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[j][i] += ld_shared(p + 256 * j + 64 * i + lane);
+            for (int j = 0; j < NS; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[d][j][i] = ld_shared(p + 256 * j + 64 * i + lane);
+          }
+#pragma unroll
+          for (int d = 0; d < kPartsAhead; ++d)
+            if (o + d <= b1)
+#pragma unroll
+              for (int j = 0; j < NS; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[j][i] += v[d][j][i];
         }
       }
 #pragma unroll
@@ -941,7 +947,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_second_kernel(FewArgs a) {
 // ---------------------------------------------------------------- host
 
 struct FewLayout {
-  size_t ctl, z, h[3], part, total;
+  size_t ctl, z, h[3], routed, part, total;
   int ldz, parts;
 };
 
@@ -963,6 +969,7 @@ FewLayout few_layout(const moe_config& c, int64_t T) {
   const size_t elems = static_cast<size_t>(T) * c.num_experts_per_tok * c.moe_intermediate_size +
                        static_cast<size_t>(T) * c.shared_expert_intermediate_size;
   for (int p = 0; p < 3; ++p) L.h[p] = take(f32 ? (p ? 0 : elems * 4) : elems * 2);
+  L.routed = take((2 * kFewSlots + kFewTokens) * sizeof(int));
   L.part = take(static_cast<size_t>(kMaxRanges) * 2 * kMaxSets * 256 * sizeof(float));
   L.total = off;
   return L;
@@ -975,7 +982,7 @@ bool few_countable(const moe_config& c) {
   const int64_t H = c.hidden_size, I = c.moe_intermediate_size, S = c.shared_expert_intermediate_size;
   const int64_t nblk = experts * ceil_div(I, 32) + ceil_div(S, 32), lim = int64_t{1} << 31;
   const int64_t size = c.weight_dtype == MOE_DTYPE_F32 ? 4 : 2;
-  return experts * ceil_div(I, 8) * kQueues < lim && ceil_div(H, 16) * nblk < lim && H * I * size < 2 * lim &&
+  return std::max(experts * ceil_div(I, 8), ceil_div(S, 8)) * kQueues < lim && ceil_div(H, 16) * nblk < lim && H * I * size < 2 * lim &&
          H * S * size < 2 * lim && H * c.n_routed_experts * size < 2 * lim &&
          (kFewSlots * I + kFewTokens * S) * size < 2 * lim;
 }
@@ -984,8 +991,8 @@ bool misaligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>
 
 template <int FMT>
 int few_launch(const FewArgs& a, hipStream_t s) {
-  const int first = router_tiles(a.E, a.S) * a.parts + static_cast<int>(ceil_div(a.S, 8));
-  few_first_kernel<FMT><<<first, kFewThreads, 0, s>>>(a);
+  constexpr int AFMT = FMT == kDtypeF32 ? kDtypeF32 : kDtypeBf16;
+  few_first_kernel<AFMT><<<router_tiles(a.E, a.S) * a.parts, kFewThreads, 0, s>>>(a);
   if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
   few_second_kernel<FMT><<<kFewGrid, kFewThreads, 0, s>>>(a);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH_FAILED;
@@ -1066,6 +1073,7 @@ int moe_layer_few(const moe_config* cfg, int32_t T, const void* x, const void* w
   a.ctl = reinterpret_cast<int*>(ws + L.ctl);
   a.z = reinterpret_cast<float*>(ws + L.z);
   for (int p = 0; p < 3; ++p) a.h[p] = ws + L.h[p];
+  a.routed = reinterpret_cast<int*>(ws + L.routed);
   a.part = reinterpret_cast<float*>(ws + L.part);
   a.T = T;
   a.H = cfg->hidden_size;
