@@ -287,7 +287,8 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   return max(max(a, b), max(c, d));
 }
 
-// Looks at a routing flag before a workgroup does the routing itself (about 0.4 us each).
+// Looks at the routing flags before a workgroup does the routing itself (0.4 us each or
+// more).
 constexpr int kRouteTries = 64;
 
 constexpr double kFewFixed = 8589934592.0;   // 2^33: budget aggregates in fixed point, as in moe_route
@@ -412,13 +413,15 @@ __device__ __forceinline__ void route_token(const FewArgs& a, Routing& R, int t,
   if (lane == 0) R.sg[t] = a.S > 0 ? 1.0f / (1.0f + expf(-gate)) : 0.f;
 }
 
+__device__ __forceinline__ void route_token_any(const FewArgs& a, Routing& R, int t, int lane) {
+  if (a.E <= 256) route_token<1>(a, R, t, lane);
+  else route_token<2>(a, R, t, lane);
+}
+
 // Routes and publishes tokens 4 j to 4 j + 3 (j: the workgroup).
 __device__ __forceinline__ void publish_routing(const FewArgs& a, Routing& R, int j, int wave, int lane) {
   const int tid = threadIdx.x, t = j * kFewWaves + wave;
-  if (t < a.T) {
-    if (a.E <= 256) route_token<1>(a, R, t, lane);
-    else route_token<2>(a, R, t, lane);
-  }
+  if (t < a.T) route_token_any(a, R, t, lane);
   __syncthreads();
   const int first = j * kFewWaves * a.K, n = min(kFewWaves * a.K, a.T * a.K - first);
   if (tid < n) {
@@ -432,12 +435,13 @@ __device__ __forceinline__ void publish_routing(const FewArgs& a, Routing& R, in
   if (tid == 0) st_shared(a.ctl + Ctl::kRouted + j * Ctl::kLine, 1);
 }
 
-// All tokens' routing: as published, or if that does not come in time, worked out here.
+// All tokens' routing.  Up to a token for each wave, worked out here; more, as published,
+// or if that does not come in time, here too.
 __device__ __forceinline__ void fetch_routing(const FewArgs& a, Routing& R, RouteScratch& C, int wave, int lane) {
   const int tid = threadIdx.x, groups = (a.T + kFewWaves - 1) / kFewWaves;
   if (wave == 0) {
     bool there = false;
-    for (int i = 0; i < kRouteTries && !there; ++i) {
+    for (int i = 0; i < kRouteTries && !there && groups > 1; ++i) {
       if (i > 0) __builtin_amdgcn_s_sleep(4);
       there = __all(lane >= groups || ld_shared(a.ctl + Ctl::kRouted + min(lane, groups - 1) * Ctl::kLine) != 0);
     }
@@ -451,10 +455,7 @@ __device__ __forceinline__ void fetch_routing(const FewArgs& a, Routing& R, Rout
     }
     if (tid < a.T) R.sg[tid] = __int_as_float(ld_shared(a.routed + 2 * kFewSlots + tid));
   } else {
-    for (int t = wave; t < a.T; t += kFewWaves) {
-      if (a.E <= 256) route_token<1>(a, R, t, lane);
-      else route_token<2>(a, R, t, lane);
-    }
+    for (int t = wave; t < a.T; t += kFewWaves) route_token_any(a, R, t, lane);
   }
   __syncthreads();
 }
@@ -587,9 +588,9 @@ struct DownBlk {
 };
 
 // The next gate/up item, or -1 when all queues are empty (called by one thread; all
-// queues from `home` on are tried, `tried` of them have been found empty).  Queue q holds the q-th
-// eighth of the tiles.
-__device__ __forceinline__ int take_tile(int* queues, int items, int home, int& tried) {
+// queues from `home` on are tried, `tried` of them have been found empty).  Queue q
+// holds the q-th eighth of the items.
+__device__ __forceinline__ int take_item(int* queues, int items, int home, int& tried) {
   for (; tried < kQueues; ++tried) {
     const int q = (home + tried) % kQueues;
     const int lo = q * items / kQueues, n = (q + 1) * items / kQueues - lo;
@@ -640,41 +641,41 @@ struct DownCut {
   }
 };
 
-// This workgroup's gate/up items (NS tiles each, `tiles` items for each expert) of the
-// touched experts, or of the shared expert; returns how many it ran.  The next item is
-// taken while one is running, but not before the first loads are on their way: a
-// workgroup that comes early must not take the only item of one that comes late.
-template <int FMT, int NS, bool SHARED>
-__device__ __forceinline__ int gate_up_half(const FewArgs& a, const Routing& R, Red* red, int& s_next, int items,
-                                            int tiles, int wave, int lane) {
+// This workgroup's gate/up items of NS tiles each: `shared_items` of the shared expert
+// first, then `tiles` for each touched expert, handed out from the queues; returns how
+// many it ran.  The next item is taken while one is running, but not before the first
+// loads are on their way: a workgroup that comes early must not take the only item of
+// one that comes late.
+enum class Items { Shared, Routed, Both };
+template <int FMT, int NS, Items KIND>
+__device__ __forceinline__ int gate_up_half(const FewArgs& a, const Routing& R, Red* red, int& s_next, int* queues,
+                                            int shared_items, int items, int tiles, int wave, int lane) {
   using F = SkinnyFmt<FMT>;
-  const int tid = threadIdx.x, r = lane & 15;
-  const int hb = static_cast<int>(ceil_div(a.H, F::kBlk)), width = SHARED ? a.S : a.I;
+  const int r = lane & 15, hb = static_cast<int>(ceil_div(a.H, F::kBlk));
   const uint32_t xoff = static_cast<uint32_t>(min(r, a.T - 1)) * static_cast<uint32_t>(a.H) * (F::kF32 ? 4 : 2);
-  const size_t hbase = SHARED ? static_cast<size_t>(a.T) * a.K * a.I : 0;
-  const int home = blockIdx.x % kQueues;
-  int* queues = a.ctl + (SHARED ? Ctl::kSharedQueue : Ctl::kQueue);
+  const int tid = threadIdx.x, home = blockIdx.x % kQueues;
   int tried = 0, finished = 0;
   // Workgroups 0 to 255 lie on different CUs.  If there is no more than one item for
   // each CU the others come two microseconds later, so that no CU runs two.
   if (items <= kFewGrid / 2 && blockIdx.x >= kFewGrid / 2) __builtin_amdgcn_s_sleep(64);
-  if (tid == 0) s_next = take_tile(queues, items, home, tried);
+  if (tid == 0) s_next = take_item(queues, items, home, tried);
   __syncthreads();
   int item = __builtin_amdgcn_readfirstlane(s_next);
   while (item >= 0) {
-    const int seg = SHARED ? 0 : item / tiles, n0 = (item - seg * tiles) * (8 * NS);
-    const Matrices m = SHARED ? gate_up<FMT>(a.ws_gate, a.ws_up, a.ss_gate, a.ss_up, 0, width, a.H)
-                              : gate_up<FMT>(a.w_gate, a.w_up, a.s_gate, a.s_up,
-                                             __builtin_amdgcn_readfirstlane(R.seg_expert[seg]), width, a.H);
+    const bool shared = KIND == Items::Shared || (KIND == Items::Both && item < shared_items);
+    const int routed = KIND == Items::Routed ? item : item - shared_items, seg = shared ? 0 : routed / tiles;
+    const int n0 = (shared ? item : routed - seg * tiles) * (8 * NS), width = shared ? a.S : a.I;
+    const int e = shared ? 0 : __builtin_amdgcn_readfirstlane(R.seg_expert[seg]);
+    const Matrices m = gate_up<FMT>(shared ? a.ws_gate : a.w_gate, shared ? a.ws_up : a.w_up,
+                                    shared ? a.ss_gate : a.s_gate, shared ? a.ss_up : a.s_up, e, width, a.H);
     WRow row[NS];
 #pragma unroll
     for (int j = 0; j < NS; ++j) row[j] = gate_up_row<FMT>(m, n0 + 8 * j, width, a.H, lane);
     int next = -1;
     f32x4 acc[NS];
-    const bool live = SHARED ? r < a.T : R.seg_slot[seg][r] >= 0;
-    wave_tiles<FMT, NS>(m, row, a.x, xoff, live, 0, hb, a.H, a.hvec, wave, lane, acc,
-                        [&]() __attribute__((always_inline)) {
-                          if (tid == 0) next = take_tile(queues, items, home, tried);
+    wave_tiles<FMT, NS>(m, row, a.x, xoff, shared ? r < a.T : R.seg_slot[seg][r] >= 0, 0, hb, a.H, a.hvec, wave, lane,
+                        acc, [&]() __attribute__((always_inline)) {
+                          if (tid == 0) next = take_item(queues, items, home, tried);
                         });
     __syncthreads();                 // s_next has been read, the previous tiles added up
 #pragma unroll
@@ -683,13 +684,12 @@ __device__ __forceinline__ int gate_up_half(const FewArgs& a, const Routing& R, 
     __syncthreads();
     item = __builtin_amdgcn_readfirstlane(s_next);
     if (wave == 0) {
+      const size_t base = shared ? static_cast<size_t>(a.T) * a.K * a.I : 0;
 #pragma unroll
-      for (int j = 0; j < NS; ++j) {
-        const f32x4 s = red_sum(red[j], lane);
-        store_h<FMT>(a, s, hbase, n0 + 8 * j, width, lane, [&](int t) {
-          return SHARED ? (t < a.T ? t : -1) : static_cast<int>(R.seg_slot[seg][t]);
+      for (int j = 0; j < NS; ++j)
+        store_h<FMT>(a, red_sum(red[j], lane), base, n0 + 8 * j, width, lane, [&](int t) __attribute__((always_inline)) {
+          return shared ? (t < a.T ? t : -1) : static_cast<int>(R.seg_slot[seg][t]);
         });
-      }
     }
     ++finished;
   }
@@ -712,22 +712,35 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_second_kernel(FewArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
   if (tid == 0) s_ready = 0;
-  if (static_cast<int>(blockIdx.x) * kFewWaves < a.T) publish_routing(a, R, blockIdx.x, wave, lane);
+  // ---- the gate/up half.  Up to four tokens are routed by every workgroup at once,
+  // before the memory is busy, and all items are handed out together.  More tokens are
+  // routed by a few workgroups while the others run the shared expert's items.
+  const bool few = a.T <= kFewWaves;
   const int shared_items = static_cast<int>(ceil_div(a.S, 8));
   int finished = 0;
-  if (a.S > 0) finished = gate_up_half<FMT, 1, true>(a, R, red, s_next, shared_items, shared_items, wave, lane);
+  if (!few) {
+    if (static_cast<int>(blockIdx.x) * kFewWaves < a.T) publish_routing(a, R, blockIdx.x, wave, lane);
+    if (a.S > 0)
+      finished = gate_up_half<FMT, 1, Items::Shared>(a, R, red, s_next, a.ctl + Ctl::kSharedQueue, shared_items,
+                                                     shared_items, 1, wave, lane);
+  }
   fetch_routing(a, R, U.scratch, wave, lane);
   finish_routing(a, R, U.scratch, blockIdx.x == 0);
-
   const int n = R.n;
-  const int gu_tiles = static_cast<int>(ceil_div(a.I, 8)), wide_tiles = static_cast<int>(ceil_div(a.I, 8 * kWide));
-  const bool wide = kWide > 1 && n * gu_tiles >= kWideTiles * kFewGrid;
-  const int routed_items = n * (wide ? wide_tiles : gu_tiles);
-  if (kWide > 1 && wide) finished += gate_up_half<FMT, kWide, false>(a, R, red, s_next, routed_items, wide_tiles, wave, lane);
-  else finished += gate_up_half<FMT, 1, false>(a, R, red, s_next, routed_items, gu_tiles, wave, lane);
-  const int items = routed_items + shared_items;
+  int tiles = static_cast<int>(ceil_div(a.I, 8));
+  if (kWide > 1 && !few && n * tiles >= kWideTiles * kFewGrid) {
+    tiles = static_cast<int>(ceil_div(a.I, 8 * kWide));
+    finished += gate_up_half<FMT, kWide, Items::Routed>(a, R, red, s_next, a.ctl + Ctl::kQueue, 0, n * tiles, tiles,
+                                                        wave, lane);
+  } else {
+    const int first = few ? shared_items : 0;
+    finished += gate_up_half<FMT, 1, Items::Both>(a, R, red, s_next, a.ctl + Ctl::kQueue, first, first + n * tiles,
+                                                  tiles, wave, lane);
+  }
+  const int items = shared_items + n * tiles;
   // Every h of this workgroup was stored by wave 0.  The last one to count sees all
-  // counts, and says so to the others.
+  // counts, and says so to the others: polling the counters themselves slowed those
+  // who still had to count.
   int* go = a.ctl + Ctl::kGo;
   auto all_counted = [&]() {
     int c = lane < Ctl::kGroups ? ld_shared(a.ctl + Ctl::kDone + lane * Ctl::kLine) : 0;
@@ -982,7 +995,7 @@ bool few_countable(const moe_config& c) {
   const int64_t H = c.hidden_size, I = c.moe_intermediate_size, S = c.shared_expert_intermediate_size;
   const int64_t nblk = experts * ceil_div(I, 32) + ceil_div(S, 32), lim = int64_t{1} << 31;
   const int64_t size = c.weight_dtype == MOE_DTYPE_F32 ? 4 : 2;
-  return std::max(experts * ceil_div(I, 8), ceil_div(S, 8)) * kQueues < lim && ceil_div(H, 16) * nblk < lim && H * I * size < 2 * lim &&
+  return (experts * ceil_div(I, 8) + ceil_div(S, 8)) * kQueues < lim && ceil_div(H, 16) * nblk < lim && H * I * size < 2 * lim &&
          H * S * size < 2 * lim && H * c.n_routed_experts * size < 2 * lim &&
          (kFewSlots * I + kFewTokens * S) * size < 2 * lim;
 }
