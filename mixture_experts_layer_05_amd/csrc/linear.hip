@@ -1,11 +1,18 @@
 // Dense matrix product with its epilogue: y = act(x W^T + bias) + residual.
 //
 // Sums run in float32 over the whole contraction; bias, activation and residual are
-// applied to the float32 sum, which is rounded once, to y's type.
+// applied to the float32 sum, which is rounded once, to y's type.  Three kernels:
+//
+//   linear_skinny_kernel  at most 16 rows of x: streams W, see skinny.h;
+//   linear_tile_kernel    more rows: tiles through LDS, any alignment;
+//   linear_any_kernel     strides too large for the others' offsets.
+//
+// When their tiles do not fill the GPU the first two cut the contraction into parts,
+// whose sums a second launch adds in order and finishes.
 #include <algorithm>
 
 #include "moe_mi355x.h"
-#include "schedule.h"
+#include "skinny.h"
 
 namespace moe {
 namespace {
@@ -51,7 +58,291 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int m, int n, float 
   else static_cast<uint16_t*>(a.y)[o] = f32_to_bf16_bits(v);
 }
 
-// ---------------------------------------------------------------- any size and alignment
+// Eight bf16 of a row, of which it holds the first n more (ANY: 2-byte aligned).
+template <bool ANY>
+__device__ __forceinline__ uint4 ld8_bf16(const uint16_t* p, int n) {
+  if (n >= 8) {
+    if constexpr (ANY) {
+      typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+      const u32x4_any v = *reinterpret_cast<const u32x4_any*>(p);
+      return uint4{v.x, v.y, v.z, v.w};
+    }
+    return ld16(p);
+  }
+  uint32_t v[4] = {0, 0, 0, 0};
+  if constexpr (ANY) {               // aligned rows are multiples of 8 long
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) v[k >> 1] |= static_cast<uint32_t>(p[k]) << (16 * (k & 1));
+  }
+  return uint4{v[0], v[1], v[2], v[3]};
+}
+// 16 bytes of a row from element k on, zeros past its end.
+template <bool F32, bool ANY>
+__device__ __forceinline__ uint4 ld_piece(const void* row, int k, int kdim) {
+  if constexpr (F32) return ld_f32x4(static_cast<const uint8_t*>(row) + 4 * static_cast<size_t>(k), kdim - k, !ANY);
+  else return ld8_bf16<ANY>(static_cast<const uint16_t*>(row) + k, kdim - k);
+}
+
+// ---------------------------------------------------------------- at most 16 rows
+//
+// A workgroup of four waves computes 8 SETS columns over one part of the contraction,
+// a quarter for each wave.  With 8 columns the weights of a block are one register,
+// and the two halves of the block are multiplied apart (each over all 16 columns of
+// the MFMA, of which 8 are its own).
+constexpr int kSkinnyWaves = 4;
+
+template <bool F32, bool OUT32, bool ANY, int SETS>
+__global__ void __launch_bounds__(kSkinnyWaves * kWave, 2) linear_skinny_kernel(LinearArgs a, int parts, float* part) {
+  constexpr int FMT = F32 ? kDtypeF32 : kDtypeBf16;
+  constexpr int kBlk = SkinnyFmt<FMT>::kBlk, kPiece = F32 ? 4 : 8, kSize = F32 ? 4 : 2;
+  constexpr int D = SETS == 1 ? 12 : 10;
+  __shared__ f32x4 red[kSkinnyWaves][kWave];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.x * (8 * SETS), p = blockIdx.y;
+  const int nb = static_cast<int>(ceil_div(a.K, kBlk));
+  const int b0 = static_cast<int>(static_cast<int64_t>(p) * nb / parts), b1 = static_cast<int>(static_cast<int64_t>(p + 1) * nb / parts);
+  const int lo = b0 + wave * (b1 - b0) / kSkinnyWaves, hi = b0 + (wave + 1) * (b1 - b0) / kSkinnyWaves;
+  // Rows within the first one's 4 GiB (the host checks the strides).
+  const uint8_t* wbase = static_cast<const uint8_t*>(a.w) + static_cast<size_t>(n0) * a.ldw * kSize;
+  const uint8_t* xbase = static_cast<const uint8_t*>(a.x);
+  uint32_t woff[SETS];
+#pragma unroll
+  for (int h = 0; h < SETS; ++h)
+    woff[h] = static_cast<uint32_t>(min(8 * h + (lane & 7), a.N - 1 - n0)) * static_cast<uint32_t>(a.ldw) * kSize +
+              16 * lane_piece(lane);
+  const uint32_t xoff = static_cast<uint32_t>(min(r, a.M - 1)) * static_cast<uint32_t>(a.ldx) * kSize + 16 * g;
+  const bool live = r < a.M;
+  const bool tail = a.K % kBlk != 0;
+
+  struct Blk {
+    uint4 w[SETS], x[2];
+  };
+  f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  int at = lo;
+  batches<D, Blk>(
+      hi - lo,
+      [&](Blk& k) __attribute__((always_inline)) {
+        const uint8_t* wb = wbase + static_cast<size_t>(at) * kBlkBytes;
+        const uint8_t* xb = xbase + static_cast<size_t>(at) * kBlkBytes;
+        // Elements of the row from this block on; only the last block can be cut.
+        const int left = a.K - at * kBlk;
+        k.x[0] = k.x[1] = uint4{0, 0, 0, 0};
+        if (!ANY && !tail) {
+#pragma unroll
+          for (int h = 0; h < SETS; ++h) k.w[h] = ld16_stream(wb + woff[h]);
+          if (live) {
+            k.x[0] = ld16(xb + xoff);
+            k.x[1] = ld16(xb + xoff + 64);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < SETS; ++h) k.w[h] = ld_piece<F32, ANY>(wb + woff[h], 0, left - kPiece * lane_piece(lane));
+          if (live) {
+            k.x[0] = ld_piece<F32, ANY>(xb + xoff, 0, left - kPiece * g);
+            k.x[1] = ld_piece<F32, ANY>(xb + xoff + 64, 0, left - kPiece * (g + 4));
+          }
+        }
+        ++at;
+      },
+      [&](Blk& k) __attribute__((always_inline)) {
+        if constexpr (SETS == 2) {
+          WBlk<FMT> w;
+          w.v[0] = k.w[0];
+          w.v[1] = k.w[1];
+          XBlk<FMT> x[1];
+          x[0].v[0][0] = k.x[0];
+          x[0].v[1][0] = k.x[1];
+          acc[0] = mma_planes<FMT, 1>(x, w, lane, acc[0]);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if constexpr (F32) {
+              acc[h] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k.x[h].x), __uint_as_float(k.w[0].x), acc[h], 0, 0, 0);
+              acc[h] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k.x[h].y), __uint_as_float(k.w[0].y), acc[h], 0, 0, 0);
+              acc[h] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k.x[h].z), __uint_as_float(k.w[0].z), acc[h], 0, 0, 0);
+              acc[h] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(k.x[h].w), __uint_as_float(k.w[0].w), acc[h], 0, 0, 0);
+            } else {
+              acc[h] = mfma_bf16_16x16x32(k.x[h], k.w[0], acc[h]);
+            }
+          }
+        }
+      },
+      [] {});
+  f32x4 s = acc[0];
+  if constexpr (SETS == 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v = (lane & 8) ? acc[1][i] : acc[0][i];
+      s[i] = v + __shfl_xor(v, 8, kWave);
+    }
+  }
+  red[wave][lane] = s;
+  __syncthreads();
+  // Wave w finishes elements i = w: rows 4 g + w.
+  float v = red[0][lane][wave];
+#pragma unroll
+  for (int o = 1; o < kSkinnyWaves; ++o) v += red[o][lane][wave];
+  const int m = 4 * g + wave, n = n0 + r;
+  if (m < a.M && n < a.N && r < 8 * SETS) {
+    if (parts > 1) part[(static_cast<size_t>(p) * a.M + m) * a.N + n] = v;
+    else finish<F32, OUT32>(a, m, n, v);
+  }
+}
+
+// ---------------------------------------------------------------- LDS tiles
+//
+// BM x BN outputs per workgroup of 2 x 2 waves, from 32x32 MFMAs.  A stage is 128 bytes
+// of each row (64 bf16 or 32 f32), double-buffered in LDS; its loads go to registers
+// two stages ahead, which takes any alignment and fills the row ends with zeros.  Rows
+// are stored unpadded with their 16-byte pieces permuted by (row / 2) mod 8, so that a
+// fragment read touches each bank group once per 16 rows.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// Tiles that share rows of W are neighbours on one XCD (workgroup b runs on XCD b % 8).
+__device__ __forceinline__ int xcd_tile(int b, int total) {
+  const int per = (total + 7) / 8;
+  return b / 8 < per && (b % 8) * per + b / 8 < total ? (b % 8) * per + b / 8 : -1;
+}
+
+template <bool F32, bool OUT32, bool ANY, int BM, int BN>
+__global__ void __launch_bounds__(256, 2) linear_tile_kernel(LinearArgs a, int parts, float* part) {
+  constexpr int kElems = F32 ? 32 : 64, kPiece = F32 ? 4 : 8, kSize = F32 ? 4 : 2;
+  constexpr int RA = BM / 32, RB = BN / 32, NI = BM / 64, NJ = BN / 64;
+  constexpr int kStage = (BM + BN) * 128;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1, r32 = lane & 31, hi = lane >> 5;
+  const int mt = static_cast<int>(ceil_div(a.M, BM)), nt = static_cast<int>(ceil_div(a.N, BN));
+  const int item = xcd_tile(blockIdx.x, mt * nt * parts);
+  if (item < 0) return;
+  const int p = item % parts, m0 = (item / parts) % mt * BM, n0 = (item / parts) / mt * BN;
+  const int stages = static_cast<int>(ceil_div(a.K, kElems));
+  const int s0 = static_cast<int>(static_cast<int64_t>(p) * stages / parts), s1 = static_cast<int>(static_cast<int64_t>(p + 1) * stages / parts);
+
+  // Thread t loads piece t % 8 of rows t / 8 + 32 q; rows past the end repeat the last.
+  const int row = tid >> 3, piece = tid & 7;
+  const uint8_t* xbase = static_cast<const uint8_t*>(a.x) + static_cast<size_t>(m0) * a.ldx * kSize;
+  const uint8_t* wbase = static_cast<const uint8_t*>(a.w) + static_cast<size_t>(n0) * a.ldw * kSize;
+  uint32_t xoff[RA], woff[RB];
+#pragma unroll
+  for (int q = 0; q < RA; ++q)
+    xoff[q] = static_cast<uint32_t>(min(row + 32 * q, a.M - 1 - m0)) * static_cast<uint32_t>(a.ldx) * kSize + 16 * piece;
+#pragma unroll
+  for (int q = 0; q < RB; ++q)
+    woff[q] = static_cast<uint32_t>(min(row + 32 * q, a.N - 1 - n0)) * static_cast<uint32_t>(a.ldw) * kSize + 16 * piece;
+  struct Regs {
+    uint4 x[RA], w[RB];
+  };
+  auto load = [&](Regs& R, int s) __attribute__((always_inline)) {
+    const int st = min(s, s1 - 1), left = a.K - st * kElems - piece * kPiece;
+    const uint8_t* xb = xbase + static_cast<size_t>(st) * 128;
+    const uint8_t* wb = wbase + static_cast<size_t>(st) * 128;
+#pragma unroll
+    for (int q = 0; q < RA; ++q) R.x[q] = ld_piece<F32, ANY>(xb + xoff[q], 0, left);
+#pragma unroll
+    for (int q = 0; q < RB; ++q) R.w[q] = ld_piece<F32, ANY>(wb + woff[q], 0, left);
+  };
+  const uint32_t lds = static_cast<uint32_t>(row * 128 + ((piece ^ ((row >> 1) & 7)) * 16));
+  auto store = [&](const Regs& R, int buf) __attribute__((always_inline)) {
+    uint8_t* d = smem + buf * kStage + lds;
+#pragma unroll
+    for (int q = 0; q < RA; ++q) *reinterpret_cast<uint4*>(d + 32 * q * 128) = R.x[q];
+#pragma unroll
+    for (int q = 0; q < RB; ++q) *reinterpret_cast<uint4*>(d + BM * 128 + 32 * q * 128) = R.w[q];
+  };
+  f32x16 acc[NI][NJ];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+  const uint32_t swz = static_cast<uint32_t>(hi ^ ((r32 >> 1) & 7));
+  auto compute = [&](int buf) __attribute__((always_inline)) {
+    const uint8_t* As = smem + buf * kStage + (wm * (BM / 2) + r32) * 128;
+    const uint8_t* Bs = smem + buf * kStage + (BM + wn * (BN / 2) + r32) * 128;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      const uint32_t pc = ((2 * kk) ^ swz) * 16;
+      uint4 xf[NI], wf[NJ];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) xf[i] = *reinterpret_cast<const uint4*>(As + i * 32 * 128 + pc);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) wf[j] = *reinterpret_cast<const uint4*>(Bs + j * 32 * 128 + pc);
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          if constexpr (F32) {
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(xf[i].x), __uint_as_float(wf[j].x), acc[i][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(xf[i].y), __uint_as_float(wf[j].y), acc[i][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(xf[i].z), __uint_as_float(wf[j].z), acc[i][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(xf[i].w), __uint_as_float(wf[j].w), acc[i][j], 0, 0, 0);
+          } else {
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, xf[i]), __builtin_bit_cast(bf16x8, wf[j]), acc[i][j], 0, 0, 0);
+          }
+        }
+    }
+  };
+
+  // Iteration s: barrier; write stage s + 1 from registers, start loading s + 3 into
+  // them (past the end the last stage again), multiply stage s.
+  Regs R0, R1;
+  load(R0, s0);
+  load(R1, s0 + 1);
+  store(R0, 0);
+  load(R0, s0 + 2);
+  for (int s = s0; s < s1; s += 2) {
+    __syncthreads();
+    store(R1, 1);
+    load(R1, s + 3);
+    compute(0);
+    if (s + 1 == s1) break;
+    __syncthreads();
+    store(R0, 0);
+    load(R0, s + 4);
+    compute(1);
+  }
+
+  // Lane l, element v: row 8 (v / 4) + 4 (l / 32) + v % 4, column l % 32 of a block.
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int m = m0 + wm * (BM / 2) + 32 * i + 8 * (v >> 2) + 4 * hi + (v & 3);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int n = n0 + wn * (BN / 2) + 32 * j + r32;
+        if (m < a.M && n < a.N) {
+          if (parts > 1) part[(static_cast<size_t>(p) * a.M + m) * a.N + n] = acc[i][j][v];
+          else finish<F32, OUT32>(a, m, n, acc[i][j][v]);
+        }
+      }
+    }
+}
+
+// ---------------------------------------------------------------- parts added up
+
+template <bool F32, bool OUT32>
+__global__ void __launch_bounds__(256) linear_finish_kernel(LinearArgs a, int parts, const float* part) {
+  const int64_t plane = static_cast<int64_t>(a.M) * a.N;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= plane) return;
+  float v = part[i];
+  int p = 1;
+  for (; p + 4 <= parts; p += 4) {   // four loads in flight
+    const float b = part[i + plane * p], c = part[i + plane * (p + 1)], d = part[i + plane * (p + 2)],
+                e = part[i + plane * (p + 3)];
+    v += b; v += c; v += d; v += e;
+  }
+  for (; p < parts; ++p) v += part[i + plane * p];
+  const int m = static_cast<int>(i / a.N);
+  finish<F32, OUT32>(a, m, static_cast<int>(i - static_cast<int64_t>(m) * a.N), v);
+}
+
+// ---------------------------------------------------------------- any stride
 //
 // 64 x 64 outputs per workgroup of 4 waves, stages of 32 contraction elements read
 // element by element.
@@ -115,15 +406,88 @@ int check_linear(const moe_linear_config* c, int32_t rows) {
   return MOE_OK;
 }
 
-size_t linear_workspace(const moe_linear_config&, int32_t) { return 256; }
+// How a product runs: which tiles, and in how many parts of the contraction.
+struct LinearPlan {
+  int rows, cols;    // of a tile (rows 16: the skinny kernel)
+  int64_t tiles;
+  int parts;
+};
+constexpr int kFillGroups = 512;        // two workgroups on each CU
+
+LinearPlan linear_plan(const moe_linear_config& c, int64_t M) {
+  const int64_t N = c.out_features, K = c.in_features, size = c.in_dtype == MOE_DTYPE_F32 ? 4 : 2;
+  LinearPlan p{};
+  if (M <= kSkinnyRows) {
+    // 16 columns while that gives two workgroups for each CU, else 8; below one workgroup
+    // for each CU parts of at least 16 blocks.
+    p.rows = kSkinnyRows;
+    p.cols = ceil_div(N, 16) >= kFillGroups ? 16 : 8;
+    p.tiles = ceil_div(N, p.cols);
+    const int64_t blocks = ceil_div(K * size, kBlkBytes);
+    p.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kFillGroups / 2 / p.tiles, blocks / 16, 16})));
+    return p;
+  }
+  p.rows = M <= 64 ? 64 : 128;
+  p.cols = 128;
+  p.tiles = ceil_div(M, p.rows) * ceil_div(N, p.cols);
+  // Parts of at least 8 stages, as many as fill the GPU once with two workgroups on a CU.
+  const int64_t stages = ceil_div(K * size, 128);
+  p.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kFillGroups / p.tiles, stages / 8, 16})));
+  return p;
+}
+
+// Bytes of partial sums of any call of at most M rows.
+size_t linear_workspace(const moe_linear_config& c, int64_t M) {
+  size_t most = 256;
+  auto take = [&](int64_t rows) {
+    const LinearPlan p = linear_plan(c, rows);
+    if (p.parts > 1) most = std::max(most, static_cast<size_t>(p.parts) * rows * c.out_features * sizeof(float));
+  };
+  // The number of parts depends on the number of tile rows only and shrinks with it.
+  take(std::min<int64_t>(M, kSkinnyRows));
+  if (M > kSkinnyRows) take(std::min<int64_t>(M, 64));
+  for (int64_t rows = 128; M > 64; rows += 128) {
+    take(std::min(rows, M));
+    if (rows >= M || linear_plan(c, rows).parts == 1) break;
+  }
+  return most;
+}
 
 bool off(const void* p, int dtype) { return reinterpret_cast<uintptr_t>(p) % (dtype == MOE_DTYPE_F32 ? 4 : 2) != 0; }
 
+template <bool F32, bool OUT32, bool ANY>
+int linear_launch(const LinearArgs& a, const LinearPlan& p, float* part, hipStream_t s) {
+  if (p.rows == kSkinnyRows) {
+    const dim3 grid(static_cast<unsigned>(p.tiles), static_cast<unsigned>(p.parts));
+    if (p.cols == 16) linear_skinny_kernel<F32, OUT32, ANY, 2><<<grid, 256, 0, s>>>(a, p.parts, part);
+    else linear_skinny_kernel<F32, OUT32, ANY, 1><<<grid, 256, 0, s>>>(a, p.parts, part);
+  } else {
+    const unsigned grid = static_cast<unsigned>(ceil_div(p.tiles * p.parts, 8) * 8);
+    if (p.rows == 64) linear_tile_kernel<F32, OUT32, ANY, 64, 128><<<grid, 256, 0, s>>>(a, p.parts, part);
+    else linear_tile_kernel<F32, OUT32, ANY, 128, 128><<<grid, 256, 0, s>>>(a, p.parts, part);
+  }
+  if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
+  if (p.parts > 1) {
+    linear_finish_kernel<F32, OUT32><<<static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.M) * a.N, 256)), 256, 0, s>>>(
+        a, p.parts, part);
+    if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
+  }
+  return MOE_OK;
+}
+
 template <bool F32, bool OUT32>
-int linear_launch(const LinearArgs& a, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(ceil_div(a.N, kAnyTile)), static_cast<unsigned>(ceil_div(a.M, kAnyTile)));
-  linear_any_kernel<F32, OUT32><<<grid, 256, 0, s>>>(a);
-  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH_FAILED;
+int linear_dispatch(const LinearArgs& a, const moe_linear_config& c, float* part, hipStream_t s) {
+  // Offsets within a tile's rows are 32-bit byte offsets.
+  if (std::max(a.ldx, a.ldw) >= (int64_t{1} << 23)) {
+    const dim3 grid(static_cast<unsigned>(ceil_div(a.N, kAnyTile)), static_cast<unsigned>(ceil_div(a.M, kAnyTile)));
+    linear_any_kernel<F32, OUT32><<<grid, 256, 0, s>>>(a);
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH_FAILED;
+  }
+  const int64_t unit = F32 ? 4 : 8;        // elements of 16 bytes
+  const bool aligned = a.ldx % unit == 0 && a.ldw % unit == 0 && a.K % unit == 0 &&
+                       reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && reinterpret_cast<uintptr_t>(a.w) % 16 == 0;
+  const LinearPlan p = linear_plan(c, a.M);
+  return aligned ? linear_launch<F32, OUT32, false>(a, p, part, s) : linear_launch<F32, OUT32, true>(a, p, part, s);
 }
 
 }  // namespace
@@ -172,8 +536,10 @@ int moe_linear(const moe_linear_config* cfg, int32_t M, const void* x, int64_t l
   a.K = static_cast<int>(K);
   a.act = cfg->activation;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (cfg->in_dtype == MOE_DTYPE_F32) return linear_launch<true, true>(a, s);
-  return cfg->out_dtype == MOE_DTYPE_F32 ? linear_launch<false, true>(a, s) : linear_launch<false, false>(a, s);
+  float* part = static_cast<float*>(workspace);
+  if (cfg->in_dtype == MOE_DTYPE_F32) return linear_dispatch<true, true>(a, *cfg, part, s);
+  return cfg->out_dtype == MOE_DTYPE_F32 ? linear_dispatch<false, true>(a, *cfg, part, s)
+                                         : linear_dispatch<false, false>(a, *cfg, part, s);
 }
 
 }  // extern "C"
