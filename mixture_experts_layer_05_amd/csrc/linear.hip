@@ -86,17 +86,19 @@ __device__ __forceinline__ uint4 ld_piece(const void* row, int k, int kdim) {
 
 // ---------------------------------------------------------------- at most 16 rows
 //
-// A workgroup of four waves computes 8 SETS columns over one part of the contraction,
-// a quarter for each wave.  With 8 columns the weights of a block are one register,
+// A workgroup of eight waves computes 8 SETS columns over one part of the contraction,
+// an eighth for each wave.  Short batches and many waves (three workgroups on a CU with
+// 8 columns, two with 16): four waves with batches three times as long took twice the
+// time on 1 x 5120 x 5120.  With 8 columns the weights of a block are one register,
 // and the two halves of the block are multiplied apart (each over all 16 columns of
 // the MFMA, of which 8 are its own).
-constexpr int kSkinnyWaves = 4;
+constexpr int kSkinnyWaves = 8;
 
 template <bool F32, bool OUT32, bool ANY, int SETS>
-__global__ void __launch_bounds__(kSkinnyWaves * kWave, 2) linear_skinny_kernel(LinearArgs a, int parts, float* part) {
+__global__ void __launch_bounds__(kSkinnyWaves * kWave, SETS == 1 ? 6 : 4) linear_skinny_kernel(LinearArgs a, int parts, float* part) {
   constexpr int FMT = F32 ? kDtypeF32 : kDtypeBf16;
   constexpr int kBlk = SkinnyFmt<FMT>::kBlk, kPiece = F32 ? 4 : 8, kSize = F32 ? 4 : 2;
-  constexpr int D = SETS == 1 ? 12 : 10;
+  constexpr int D = SETS == 1 ? 4 : 5;
   __shared__ f32x4 red[kSkinnyWaves][kWave];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
@@ -180,7 +182,8 @@ __global__ void __launch_bounds__(kSkinnyWaves * kWave, 2) linear_skinny_kernel(
   }
   red[wave][lane] = s;
   __syncthreads();
-  // Wave w finishes elements i = w: rows 4 g + w.
+  // Wave w < 4 finishes elements i = w: rows 4 g + w.
+  if (wave >= 4) return;
   float v = red[0][lane][wave];
 #pragma unroll
   for (int o = 1; o < kSkinnyWaves; ++o) v += red[o][lane][wave];
@@ -459,8 +462,8 @@ template <bool F32, bool OUT32, bool ANY>
 int linear_launch(const LinearArgs& a, const LinearPlan& p, float* part, hipStream_t s) {
   if (p.rows == kSkinnyRows) {
     const dim3 grid(static_cast<unsigned>(p.tiles), static_cast<unsigned>(p.parts));
-    if (p.cols == 16) linear_skinny_kernel<F32, OUT32, ANY, 2><<<grid, 256, 0, s>>>(a, p.parts, part);
-    else linear_skinny_kernel<F32, OUT32, ANY, 1><<<grid, 256, 0, s>>>(a, p.parts, part);
+    if (p.cols == 16) linear_skinny_kernel<F32, OUT32, ANY, 2><<<grid, kSkinnyWaves * kWave, 0, s>>>(a, p.parts, part);
+    else linear_skinny_kernel<F32, OUT32, ANY, 1><<<grid, kSkinnyWaves * kWave, 0, s>>>(a, p.parts, part);
   } else {
     const unsigned grid = static_cast<unsigned>(ceil_div(p.tiles * p.parts, 8) * 8);
     if (p.rows == 64) linear_tile_kernel<F32, OUT32, ANY, 64, 128><<<grid, 256, 0, s>>>(a, p.parts, part);
