@@ -280,30 +280,42 @@ def layer_few(cfg: MoEConfig, x, w_router, w_shared_gate, logit_bias, weights: _
     The routing outputs are optional; y may be None if y_act is given."""
     T, E, K, H = x.shape[0], cfg.n_routed_experts, cfg.num_experts_per_tok, cfg.hidden_size
     act = cfg.act_torch_dtype
-    _expect(x, (T, H), act, "x")
     _expect(w_router, (E, H), act, "w_router")
     _expect(w_shared_gate, (H,), act, "w_shared_gate")
-    _expect(logit_bias, (T, E), torch.float32, "logit_bias")
     _expect(topk_ids, (T, K), torch.int32, "topk_ids")
     _expect(topk_weights, (T, K), torch.float32, "topk_weights")
     _expect(shared_gate, (T,), torch.float32, "shared_gate")
     _expect(route_stats, (4,), torch.int32, "route_stats")
     _expect(y, (T, H), torch.float32, "y")
     _expect(y_act, (T, H), act, "y_act")
-    _check(lib().moe_layer_few(ctypes.byref(cfg.c()), T, _ptr(x), _ptr(w_router), _ptr(w_shared_gate),
-                               _ptr(logit_bias), ctypes.byref(weights), _ptr(topk_ids), _ptr(topk_weights),
-                               _ptr(shared_gate), _ptr(route_stats), _ptr(y), _ptr(y_act), _ptr(workspace),
-                               workspace.numel(), _stream(stream)), "moe_layer_few")
+    _layer_few_call(ctypes.byref(cfg.c()), cfg, x, logit_bias,
+                    (_ptr(w_router), _ptr(w_shared_gate), ctypes.byref(weights)),
+                    (_ptr(topk_ids), _ptr(topk_weights), _ptr(shared_gate), _ptr(route_stats), _ptr(y), _ptr(y_act),
+                     _ptr(workspace), workspace.numel()), stream)
+
+
+def _layer_few_call(c, cfg, x, logit_bias, weights, outputs, stream) -> None:
+    """moe_layer_few with the addresses of the weights and of the outputs; checks what a
+    caller brings to each call."""
+    T = x.shape[0]
+    _expect(x, (T, cfg.hidden_size), cfg.act_torch_dtype, "x")
+    bp = None
+    if logit_bias is not None:
+        _expect(logit_bias, (T, cfg.n_routed_experts), torch.float32, "logit_bias")
+        bp = _ptr(logit_bias)
+    xp, (wr, wg, w) = _ptr(x), weights
+    with _on(x.device):
+        status = lib().moe_layer_few(c, T, xp, wr, wg, bp, w, *outputs, _stream_of(x.device, stream))
+    if status != 0:
+        raise MoEError(status, "moe_layer_few")
 
 
 _TORCH_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
 
 
-def _rows(t: Optional[torch.Tensor], shape, dtype, name: str):
+def _rows(t: torch.Tensor, shape, dtype, name: str):
     """(address, row stride) of a matrix whose rows are contiguous, on the GPU."""
-    if t is None:
-        return None, 0
-    if tuple(t.shape) != shape or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name}: expected {shape} {dtype}, got {tuple(t.shape)} {t.dtype}")
     if not t.is_cuda:
         raise ValueError("tensors passed to the MoE library must live on the GPU")
@@ -332,15 +344,45 @@ def linear(x, weight, bias, residual, y, workspace, activation: str = "none", st
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation: expected one of {sorted(ACTIVATIONS)}, got {activation!r}")
     (M, K), N = x.shape, weight.shape[0]
-    cx, cy = _dtype_code(x, "x"), _dtype_code(y, "y")
-    xp, ldx = _rows(x, (M, K), x.dtype, "x")
+    cfg = _LinearConfig(K, N, _dtype_code(x, "x"), _dtype_code(y, "y"), ACTIVATIONS[activation])
     wp, ldw = _rows(weight, (N, K), x.dtype, "weight")
-    rp, ldr = _rows(residual, (M, N), y.dtype, "residual")
-    yp, ldy = _rows(y, (M, N), y.dtype, "y")
     _expect(bias, (N,), x.dtype, "bias")
-    _check(lib().moe_linear(ctypes.byref(_LinearConfig(K, N, cx, cy, ACTIVATIONS[activation])), M, xp, ldx, wp,
-                            ldw, _ptr(bias), rp, ldr, yp, ldy, _ptr(workspace), workspace.numel(),
-                            _stream(stream)), "moe_linear")
+    _linear_call(ctypes.byref(cfg), M, N, K, x, wp, ldw, _ptr(bias), residual, y, _ptr(workspace), workspace.numel(),
+                 x.dtype, y.dtype, stream)
+
+
+def _linear_call(cfg, M, N, K, x, wp, ldw, bp, residual, y, ws, ws_bytes, in_dtype, out_dtype, stream) -> None:
+    xp, ldx = _rows(x, (M, K), in_dtype, "x")
+    rp, ldr = (None, 0) if residual is None else _rows(residual, (M, N), out_dtype, "residual")
+    yp, ldy = _rows(y, (M, N), out_dtype, "y")
+    with _on(x.device):
+        status = lib().moe_linear(cfg, M, xp, ldx, wp, ldw, bp, rp, ldr, yp, ldy, ws, ws_bytes,
+                                  _stream_of(x.device, stream))
+    if status != 0:
+        raise MoEError(status, "moe_linear")
+
+
+class _Here:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE_CTX = _Here()
+
+
+def _on(device: torch.device):
+    """A context in which `device` is current (kernels are launched on the current one)."""
+    return _HERE_CTX if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+
+
+def _stream_of(device: torch.device, stream) -> int:
+    """The stream's handle, by default that of the device's current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return _stream(stream)
 
 
 def _dtype_code(t: torch.Tensor, name: str) -> int:
@@ -370,14 +412,20 @@ class Linear:
         self.workspace = torch.empty(linear_workspace_size(self.K, self.N, max_rows, in_dtype, out_dtype),
                                      dtype=torch.uint8, device=dev)
         self.y = torch.empty(max_rows, self.N, dtype=self.out_dtype, device=dev)
+        self._cfg = _LinearConfig(self.K, self.N, DTYPES[in_dtype], DTYPES[out_dtype or in_dtype],
+                                  ACTIVATIONS[activation])
 
     def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         if x.shape[0] > self.max_rows:
             raise ValueError("more rows than the projection was sized for")
-        y = self.y[:x.shape[0]] if out is None else out
-        _expect(y, (x.shape[0], self.N), self.out_dtype, "out")
-        linear(x, self.weight, self.bias, residual, y, self.workspace, self.activation, stream)
+        M = x.shape[0]
+        y = out if out is not None else self.y if M == self.max_rows else self.y[:M]
+        self._cfg.activation = ACTIVATIONS[self.activation]
+        wp, ldw = _rows(self.weight, (self.N, self.K), self.weight.dtype, "weight")
+        _linear_call(ctypes.byref(self._cfg), M, self.N, self.K, x, wp, ldw,
+                     None if self.bias is None else _ptr(self.bias), residual, y, self.workspace.data_ptr(),
+                     self.workspace.numel(), self.weight.dtype, self.out_dtype, stream)
         return y
 
 
@@ -404,6 +452,8 @@ class MoELayer:
         self.workspace = torch.empty(workspace_size(cfg, max_tokens), dtype=torch.uint8, device=dev)
         self.few_workspace = torch.empty(layer_few_workspace_size(cfg, min(max_tokens, FEW_TOKENS)),
                                          dtype=torch.uint8, device=dev) if few else None
+        # For a call of T tokens: the layer's buffers, its rows of y, and the addresses.
+        self._few_calls = {}
         self.topk_ids = torch.empty(max_tokens, K, dtype=torch.int32, device=dev)
         self.topk_weights = torch.empty(max_tokens, K, dtype=torch.float32, device=dev)
         self.shared_gate = torch.empty(max_tokens, dtype=torch.float32, device=dev)
@@ -445,13 +495,26 @@ class MoELayer:
         if x.shape[0] > self.max_tokens:
             raise ValueError("more tokens than the layer was sized for")
         if self.few and x.shape[0] <= FEW_TOKENS:
-            v = self.views(x.shape[0])
-            layer_few(self.cfg, x, self.w_router, self.w_shared_gate, logit_bias, self.weights, v["y"],
-                      self.few_workspace, v["topk_ids"], v["topk_weights"],
-                      v["shared_gate"] if self.cfg.shared_expert_intermediate_size > 0 else None,
-                      self.route_stats, v["y_act"], stream)
-            return v["y"]
+            return self._call_few(x, logit_bias, stream)
         self.route(x, logit_bias, stream)
         self.dispatch(x.shape[0], stream)
         self.forward(x, stream)
         return self.views(x.shape[0])["y"]
+
+    def _call_few(self, x, logit_bias, stream) -> torch.Tensor:
+        T = x.shape[0]
+        buffers = (self.topk_ids, self.topk_weights, self.shared_gate, self.route_stats, self.y, self.y_act,
+                   self.few_workspace)
+        call = self._few_calls.get(T)
+        if call is None or any(a is not b for a, b in zip(call[0], buffers)):
+            v = self.views(T)
+            shared = v["shared_gate"] if self.cfg.shared_expert_intermediate_size > 0 else None
+            call = self._few_calls[T] = (
+                buffers, v["y"],
+                (_ptr(v["topk_ids"]), _ptr(v["topk_weights"]), _ptr(shared), _ptr(self.route_stats), _ptr(v["y"]),
+                 _ptr(v["y_act"]), _ptr(self.few_workspace), self.few_workspace.numel()))
+        _expect(self.w_router, (self.cfg.n_routed_experts, self.cfg.hidden_size), self.cfg.act_torch_dtype, "w_router")
+        _expect(self.w_shared_gate, (self.cfg.hidden_size,), self.cfg.act_torch_dtype, "w_shared_gate")
+        weights = (_ptr(self.w_router), _ptr(self.w_shared_gate), ctypes.byref(self.weights))
+        _layer_few_call(ctypes.byref(self.cfg.c()), self.cfg, x, logit_bias, weights, call[2], stream)
+        return call[1]

@@ -1,10 +1,12 @@
 // Dense matrix product with its epilogue: y = act(x W^T + bias) + residual.
 //
 // Sums run in float32 over the whole contraction; bias, activation and residual are
-// applied to the float32 sum, which is rounded once, to y's type.  Three kernels:
+// applied to the float32 sum, which is rounded once, to y's type.  Four kernels:
 //
 //   linear_skinny_kernel  at most 16 rows of x: streams W, see skinny.h;
 //   linear_tile_kernel    more rows: tiles through LDS, any alignment;
+//   linear_wide_kernel    enough rows and columns to fill the GPU with 256 x 256 tiles
+//                         (aligned bf16): the matrix cores' rate;
 //   linear_any_kernel     strides too large for the others' offsets.
 //
 // When their tiles do not fill the GPU the first two cut the contraction into parts,
@@ -12,6 +14,7 @@
 #include <algorithm>
 
 #include "moe_mi355x.h"
+#include "dma.h"
 #include "skinny.h"
 
 namespace moe {
@@ -201,8 +204,6 @@ __global__ void __launch_bounds__(kSkinnyWaves * kWave, SETS == 1 ? 6 : 4) linea
 // two stages ahead, which takes any alignment and fills the row ends with zeros.  Rows
 // are stored unpadded with their 16-byte pieces permuted by (row / 2) mod 8, so that a
 // fragment read touches each bank group once per 16 rows.
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
 // Tiles that share rows of W are neighbours on one XCD (workgroup b runs on XCD b % 8).
 __device__ __forceinline__ int xcd_tile(int b, int total) {
   const int per = (total + 7) / 8;
@@ -326,6 +327,195 @@ __global__ void __launch_bounds__(256, 2) linear_tile_kernel(LinearArgs a, int p
     }
 }
 
+// ---------------------------------------------------------------- 256 x 256 tiles
+//
+// 256 x 256 outputs per workgroup of 8 waves, two per SIMD; wave w computes rows
+// [128 (w / 4), +128) x columns [64 (w % 4), +64) as 4 x 2 blocks of 32x32x16 MFMAs (128
+// accumulators), so that one wave's fragment reads and waits overlap the other's MFMAs.
+// A stage is 64 elements, 128 bytes of each row, double-buffered in LDS: the rows of x
+// go there by DMA one stage ahead, the rows of W through registers two stages ahead,
+// which keeps two stages of the HBM stream in flight within the LDS.  Tiles are walked
+// in bands of 8 row blocks, so that the 32 tiles that run on an XCD at a time share 8
+// row blocks and 4 column blocks in its L2.
+constexpr int kWideTile = 256, kWideThreads = 512;
+constexpr int kWideRow = 128;
+constexpr int kWideStage = 2 * kWideTile * kWideRow;
+constexpr int kWideBand = 8;
+
+template <bool OUT32>
+__global__ void __launch_bounds__(kWideThreads) linear_wide_kernel(LinearArgs a, bool vec) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kWideStage];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3, r32 = lane & 31, hi = lane >> 5;
+  const int mt = static_cast<int>(ceil_div(a.M, kWideTile)), nt = static_cast<int>(ceil_div(a.N, kWideTile));
+  const uint32_t xrow = static_cast<uint32_t>(a.ldx) * 2, wrow = static_cast<uint32_t>(a.ldw) * 2;
+  const int nk = a.K / 64;                   // even: the host sends multiples of 128
+
+  // DMA instruction q of this wave covers tile rows 8 (4 wave + q) + lane / 8; LDS piece
+  // lane % 8 holds global piece (lane % 8) ^ ((row / 2) mod 8).
+  const int drow = lane >> 3;
+  uint32_t dpiece[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) dpiece[h] = static_cast<uint32_t>(((lane & 7) ^ ((4 * h + (drow >> 1)) & 7)) * 16);
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_address(smem));
+  const uint32_t fswz = static_cast<uint32_t>(hi ^ ((r32 >> 1) & 7));
+  const uint32_t bldsoff = static_cast<uint32_t>((tid >> 3) * kWideRow + (((tid & 7) ^ ((tid >> 4) & 7)) * 16));
+
+  const XcdWalk walk(mt * nt);
+  for (int tile = walk.tile; tile < walk.end; tile += walk.step) {
+    const int band = tile / (kWideBand * nt), in_band = tile - band * kWideBand * nt;
+    const int bm = min(kWideBand, mt - band * kWideBand);
+    const int m0 = (band * kWideBand + in_band % bm) * kWideTile, n0 = in_band / bm * kWideTile;
+    // Rows past the end repeat the last one; their sums are not stored.  The descriptors
+    // cover the tile's rows, the host's bound on the strides keeps them below 4 GiB.
+    const int xr = min(kWideTile, a.M - m0) - 1, wr = min(kWideTile, a.N - n0) - 1;
+    const i32x4_t ra = dma_rsrc(static_cast<const uint8_t*>(a.x) + static_cast<size_t>(m0) * xrow,
+                                static_cast<uint32_t>(xr) * xrow + static_cast<uint32_t>(a.K) * 2);
+    const __amdgpu_buffer_rsrc_t rb = buf_rsrc(static_cast<const uint8_t*>(a.w) + static_cast<size_t>(n0) * wrow,
+                                               static_cast<uint32_t>(wr) * wrow + static_cast<uint32_t>(a.K) * 2);
+    uint32_t aoff[4], boff[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      aoff[q] = static_cast<uint32_t>(min(8 * (4 * wave + q) + drow, xr)) * xrow + dpiece[q & 1];
+      boff[q] = static_cast<uint32_t>(min((tid >> 3) + 64 * q, wr)) * wrow + (tid & 7) * 16;
+    }
+    auto issue_a = [&](int ks) __attribute__((always_inline)) {
+      dma4_rows(ra, aoff, static_cast<uint32_t>(ks) * kWideRow,
+                lds0 + static_cast<uint32_t>(ks & 1) * kWideStage + 4 * wave * 1024);
+    };
+    struct BRegs {
+      uint4 v[4];
+    };
+    auto load_b = [&](BRegs& R, int ks) __attribute__((always_inline)) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) R.v[q] = buf_ld16(rb, boff[q], static_cast<uint32_t>(ks) * kWideRow);
+    };
+    auto store_b = [&](const BRegs& R, int ks) __attribute__((always_inline)) {
+      uint8_t* dst = smem + (ks & 1) * kWideStage + kWideTile * kWideRow + bldsoff;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(dst + 64 * q * kWideRow) = R.v[q];
+    };
+    f32x16 acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+    auto compute = [&](int ks) __attribute__((always_inline)) {
+      const uint8_t* base = smem + (ks & 1) * kWideStage;
+      const uint8_t* As = base + (wm * 128 + r32) * kWideRow;
+      const uint8_t* Bs = base + (kWideTile + wn * 64 + r32) * kWideRow;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const uint32_t piece = ((2 * kk) ^ fswz) * 16;
+        uint4 af[4], bf[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) bf[j] = *reinterpret_cast<const uint4*>(Bs + 32 * j * kWideRow + piece);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) af[i] = *reinterpret_cast<const uint4*>(As + 32 * i * kWideRow + piece);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[i][j] = mfma_bf16_32x32x16(af[i], bf[j], acc[i][j]);
+      }
+    };
+    // Iteration ks: wait for x(ks); barrier; write W(ks + 1) from registers and start
+    // x(ks + 1) into the other buffer; refill those registers with W(ks + 3); multiply
+    // stage ks.  Past the end the last stage of W is read again, so that every iteration
+    // has the same number of loads in flight.
+    BRegs R0, R1;
+    load_b(R0, 0);
+    load_b(R1, 1);
+    __syncthreads();                 // the previous tile is done with both buffers
+    store_b(R0, 0);
+    issue_a(0);
+    load_b(R0, min(2, nk - 1));
+    for (int ks = 0; ks < nk; ks += 2) {
+      wait_vm<4>();
+      __syncthreads();
+      store_b(R1, ks + 1);
+      issue_a(ks + 1);
+      load_b(R1, min(ks + 3, nk - 1));
+      compute(ks);
+      wait_vm<4>();
+      __syncthreads();
+      if (ks + 2 < nk) {
+        store_b(R0, ks + 2);
+        issue_a(ks + 2);
+      }
+      load_b(R0, min(ks + 4, nk - 1));
+      compute(ks + 1);
+    }
+    wait_vm<0>();                    // no load may still be writing registers or LDS
+    __syncthreads();                 // every wave is done reading the stage buffers
+
+    // Out through LDS in four rounds of 64 rows (32 of each row half) x 256 columns, rows
+    // padded to 264 floats, so that bias, residual and y are taken in whole row segments:
+    // lane l holds columns 4 l .. + 4.
+    constexpr int kStride = 264;
+    float* stg = reinterpret_cast<float*>(smem);
+    const int n = n0 + 4 * lane;
+    float bias[4] = {0.f, 0.f, 0.f, 0.f};
+    if (a.bias) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (n + c < a.N) bias[c] = elem<false>(a.bias, n + c);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          stg[(wm * 32 + 8 * (v >> 2) + 4 * hi + (v & 3)) * kStride + wn * 64 + 32 * j + r32] = acc[i][j][v];
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int R = 8 * wave + k;
+        const int m = m0 + (R < 32 ? 32 * i + R : 128 + 32 * i + (R - 32));
+        if (m < a.M && n < a.N) {
+          const f32x4 s = *reinterpret_cast<const f32x4*>(stg + R * kStride + 4 * lane);
+          float v[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[c] = activate(s[c] + bias[c], a.act);
+          const size_t ro = static_cast<size_t>(m) * a.ldr + n, yo = static_cast<size_t>(m) * a.ldy + n;
+          if (vec) {                 // four columns at a time: aligned, N a multiple of 4
+            if constexpr (OUT32) {
+              f32x4 o = {v[0], v[1], v[2], v[3]};
+              if (a.residual) o += *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.residual) + ro);
+              *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + yo) = o;
+            } else {
+              if (a.residual) {
+                const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.residual) + ro);
+                v[0] += bf16_bits_to_f32(static_cast<uint16_t>(q.x));
+                v[1] += bf16_bits_to_f32(static_cast<uint16_t>(q.x >> 16));
+                v[2] += bf16_bits_to_f32(static_cast<uint16_t>(q.y));
+                v[3] += bf16_bits_to_f32(static_cast<uint16_t>(q.y >> 16));
+              }
+              uint2 o;
+              o.x = f32_to_bf16_bits(v[0]) | static_cast<uint32_t>(f32_to_bf16_bits(v[1])) << 16;
+              o.y = f32_to_bf16_bits(v[2]) | static_cast<uint32_t>(f32_to_bf16_bits(v[3])) << 16;
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + yo) = o;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (n + c < a.N) {
+                float o = v[c];
+                if (a.residual) o += elem<OUT32>(a.residual, ro + c);
+                if constexpr (OUT32) static_cast<float*>(a.y)[yo + c] = o;
+                else static_cast<uint16_t*>(a.y)[yo + c] = f32_to_bf16_bits(o);
+              }
+          }
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
 // ---------------------------------------------------------------- parts added up
 
 template <bool F32, bool OUT32>
@@ -439,6 +629,13 @@ LinearPlan linear_plan(const moe_linear_config& c, int64_t M) {
   return p;
 }
 
+// 256 x 256 tiles when they keep the CUs at least three quarters busy: the last round of
+// one tile for each CU may be short.
+bool wide_fills(int64_t M, int64_t N) {
+  const int64_t tiles = ceil_div(M, kWideTile) * ceil_div(N, kWideTile);
+  return M * N * 4 >= ceil_div(tiles, 256) * 256 * kWideTile * kWideTile * 3;
+}
+
 // Bytes of partial sums of any call of at most M rows.
 size_t linear_workspace(const moe_linear_config& c, int64_t M) {
   size_t most = 256;
@@ -490,6 +687,15 @@ int linear_dispatch(const LinearArgs& a, const moe_linear_config& c, float* part
   const bool aligned = a.ldx % unit == 0 && a.ldw % unit == 0 && a.K % unit == 0 &&
                        reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && reinterpret_cast<uintptr_t>(a.w) % 16 == 0;
   const LinearPlan p = linear_plan(c, a.M);
+  if constexpr (!F32) {
+    if (aligned && a.K % 128 == 0 && wide_fills(a.M, a.N)) {
+      const uintptr_t four = OUT32 ? 16 : 8;
+      const bool vec = a.N % 4 == 0 && a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % four == 0 &&
+                       (!a.residual || (a.ldr % 4 == 0 && reinterpret_cast<uintptr_t>(a.residual) % four == 0));
+      linear_wide_kernel<OUT32><<<256, kWideThreads, 0, s>>>(a, vec);
+      return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH_FAILED;
+    }
+  }
   return aligned ? linear_launch<F32, OUT32, false>(a, p, part, s) : linear_launch<F32, OUT32, true>(a, p, part, s);
 }
 

@@ -176,6 +176,17 @@ def test_largest(M, K, N):
     _run(M, K, N, "bf16", "bf16", "none", True, True, seed=6, rows=rows)
 
 
+# 256 x 256 tiles, cut at both edges; rows of x and W further apart than they are long, y and
+# the residual aligned to four elements or not.
+@pytest.mark.gpu
+@pytest.mark.parametrize("o", ["bf16", "f32"])
+@pytest.mark.parametrize("N,pads", [(3900, (8, 8, 4, 4)), (3900, (0, 0, 1, 3)), (3897, (64, 8, 3, 7))])
+def test_wide_tiles(N, pads, o):
+    M = 4001
+    rows = torch.cat([torch.arange(0, 300), torch.arange(M - 200, M)])
+    _run(M, 256, N, "bf16", o, "silu", True, True, seed=10, pads=pads, rows=rows)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 20, 200, 1500])
 def test_in_place_on_the_residual(M):
