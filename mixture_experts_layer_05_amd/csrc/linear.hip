@@ -28,6 +28,9 @@ struct LinearArgs {
   int act;
 };
 
+// Floats between rows of a plane of partial sums.
+__host__ __device__ inline int64_t part_stride(int64_t N) { return (N + 3) / 4 * 4; }
+
 // ---------------------------------------------------------------- epilogue
 
 // tanh(u) = 1 - 2 / (1 + e^(2u)): exact at both infinities, and near 0 within a few
@@ -59,6 +62,51 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int m, int n, float 
   const size_t o = static_cast<size_t>(m) * a.ldy + n;
   if constexpr (OUT32) static_cast<float*>(a.y)[o] = v;
   else static_cast<uint16_t*>(a.y)[o] = f32_to_bf16_bits(v);
+}
+
+// Four neighbouring elements.  The vector accesses need only the elements' alignment.
+template <bool F32, bool OUT32>
+__device__ __forceinline__ void finish4(const LinearArgs& a, int m, int n, f32x4 v) {
+  typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+  typedef uint16_t u16x4_any __attribute__((ext_vector_type(4), aligned(2)));
+  if (n + 4 > a.N) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (n + c < a.N) finish<F32, OUT32>(a, m, n + c, v[c]);
+    return;
+  }
+  if (a.bias) {
+    if constexpr (F32) {
+      const f32x4_any b = *reinterpret_cast<const f32x4_any*>(static_cast<const float*>(a.bias) + n);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] += b[c];
+    } else {
+      const u16x4_any b = *reinterpret_cast<const u16x4_any*>(static_cast<const uint16_t*>(a.bias) + n);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] += bf16_bits_to_f32(b[c]);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) v[c] = activate(v[c], a.act);
+  const size_t ro = static_cast<size_t>(m) * a.ldr + n, yo = static_cast<size_t>(m) * a.ldy + n;
+  if constexpr (OUT32) {
+    if (a.residual) {
+      const f32x4_any q = *reinterpret_cast<const f32x4_any*>(static_cast<const float*>(a.residual) + ro);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] += q[c];
+    }
+    *reinterpret_cast<f32x4_any*>(static_cast<float*>(a.y) + yo) = f32x4_any{v[0], v[1], v[2], v[3]};
+  } else {
+    if (a.residual) {
+      const u16x4_any q = *reinterpret_cast<const u16x4_any*>(static_cast<const uint16_t*>(a.residual) + ro);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] += bf16_bits_to_f32(q[c]);
+    }
+    u16x4_any o;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[c] = f32_to_bf16_bits(v[c]);
+    *reinterpret_cast<u16x4_any*>(static_cast<uint16_t*>(a.y) + yo) = o;
+  }
 }
 
 // Eight bf16 of a row, of which it holds the first n more (ANY: 2-byte aligned).
@@ -192,7 +240,7 @@ __global__ void __launch_bounds__(kSkinnyWaves * kWave, SETS == 1 ? 6 : 4) linea
   for (int o = 1; o < kSkinnyWaves; ++o) v += red[o][lane][wave];
   const int m = 4 * g + wave, n = n0 + r;
   if (m < a.M && n < a.N && r < 8 * SETS) {
-    if (parts > 1) part[(static_cast<size_t>(p) * a.M + m) * a.N + n] = v;
+    if (parts > 1) part[(static_cast<size_t>(p) * a.M + m) * part_stride(a.N) + n] = v;
     else finish<F32, OUT32>(a, m, n, v);
   }
 }
@@ -320,37 +368,38 @@ __global__ void __launch_bounds__(256, 2) linear_tile_kernel(LinearArgs a, int p
       for (int j = 0; j < NJ; ++j) {
         const int n = n0 + wn * (BN / 2) + 32 * j + r32;
         if (m < a.M && n < a.N) {
-          if (parts > 1) part[(static_cast<size_t>(p) * a.M + m) * a.N + n] = acc[i][j][v];
+          if (parts > 1) part[(static_cast<size_t>(p) * a.M + m) * part_stride(a.N) + n] = acc[i][j][v];
           else finish<F32, OUT32>(a, m, n, acc[i][j][v]);
         }
       }
     }
 }
 
-// ---------------------------------------------------------------- 256 x 256 tiles
+// ---------------------------------------------------------------- 256-row tiles
 //
-// 256 x 256 outputs per workgroup of 8 waves, two per SIMD; wave w computes rows
-// [128 (w / 4), +128) x columns [64 (w % 4), +64) as 4 x 2 blocks of 32x32x16 MFMAs (128
-// accumulators), so that one wave's fragment reads and waits overlap the other's MFMAs.
+// 256 x BN outputs per workgroup of 8 waves, two per SIMD, so that one wave's fragment
+// reads and waits overlap the other's MFMAs.  A wave computes 128 x 64 (BN = 256) or
+// 64 x 64 (BN = 128) outputs in blocks of 32x32x16 MFMAs.
 // A stage is 64 elements, 128 bytes of each row, double-buffered in LDS: the rows of x
 // go there by DMA one stage ahead, the rows of W through registers two stages ahead,
 // which keeps two stages of the HBM stream in flight within the LDS.  Tiles are walked
 // in bands of 8 row blocks, so that the 32 tiles that run on an XCD at a time share 8
 // row blocks and 4 column blocks in its L2.
-constexpr int kWideTile = 256, kWideThreads = 512;
+constexpr int kWideRows = 256, kWideThreads = 512;
 constexpr int kWideRow = 128;
-constexpr int kWideStage = 2 * kWideTile * kWideRow;
 constexpr int kWideBand = 8;
 
-template <bool OUT32>
-__global__ void __launch_bounds__(kWideThreads) linear_wide_kernel(LinearArgs a, bool vec) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kWideStage];
+template <bool OUT32, int BN>
+__global__ void __launch_bounds__(kWideThreads) linear_wide_kernel(LinearArgs a, int parts, float* part) {
+  constexpr int kStage = (kWideRows + BN) * kWideRow;
+  constexpr int WN = BN / 64, WM = 8 / WN, NI = kWideRows / WM / 32, NB = BN / 64;   // NB: W pieces per thread
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kStage];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 2, wn = wave & 3, r32 = lane & 31, hi = lane >> 5;
-  const int mt = static_cast<int>(ceil_div(a.M, kWideTile)), nt = static_cast<int>(ceil_div(a.N, kWideTile));
+  const int wm = wave / WN, wn = wave % WN, r32 = lane & 31, hi = lane >> 5;
+  const int mt = static_cast<int>(ceil_div(a.M, kWideRows)), nt = static_cast<int>(ceil_div(a.N, BN));
   const uint32_t xrow = static_cast<uint32_t>(a.ldx) * 2, wrow = static_cast<uint32_t>(a.ldw) * 2;
-  const int nk = a.K / 64;                   // even: the host sends multiples of 128
+  const int pairs = a.K / 128;               // of stages
 
   // DMA instruction q of this wave covers tile rows 8 (4 wave + q) + lane / 8; LDS piece
   // lane % 8 holds global piece (lane % 8) ^ ((row / 2) mod 8).
@@ -362,61 +411,65 @@ __global__ void __launch_bounds__(kWideThreads) linear_wide_kernel(LinearArgs a,
   const uint32_t fswz = static_cast<uint32_t>(hi ^ ((r32 >> 1) & 7));
   const uint32_t bldsoff = static_cast<uint32_t>((tid >> 3) * kWideRow + (((tid & 7) ^ ((tid >> 4) & 7)) * 16));
 
-  const XcdWalk walk(mt * nt);
-  for (int tile = walk.tile; tile < walk.end; tile += walk.step) {
+  const XcdWalk walk(mt * nt * parts);
+  for (int item = walk.tile; item < walk.end; item += walk.step) {
+    const int tile = item / parts, p = item - tile * parts;
+    // Stages [k0, nk), an even number of them (the host sends contractions of whole pairs).
+    const int k0 = 2 * (p * pairs / parts), nk = 2 * ((p + 1) * pairs / parts);
     const int band = tile / (kWideBand * nt), in_band = tile - band * kWideBand * nt;
     const int bm = min(kWideBand, mt - band * kWideBand);
-    const int m0 = (band * kWideBand + in_band % bm) * kWideTile, n0 = in_band / bm * kWideTile;
+    const int m0 = (band * kWideBand + in_band % bm) * kWideRows, n0 = in_band / bm * BN;
     // Rows past the end repeat the last one; their sums are not stored.  The descriptors
     // cover the tile's rows, the host's bound on the strides keeps them below 4 GiB.
-    const int xr = min(kWideTile, a.M - m0) - 1, wr = min(kWideTile, a.N - n0) - 1;
+    const int xr = min(kWideRows, a.M - m0) - 1, wr = min(BN, a.N - n0) - 1;
     const i32x4_t ra = dma_rsrc(static_cast<const uint8_t*>(a.x) + static_cast<size_t>(m0) * xrow,
                                 static_cast<uint32_t>(xr) * xrow + static_cast<uint32_t>(a.K) * 2);
     const __amdgpu_buffer_rsrc_t rb = buf_rsrc(static_cast<const uint8_t*>(a.w) + static_cast<size_t>(n0) * wrow,
                                                static_cast<uint32_t>(wr) * wrow + static_cast<uint32_t>(a.K) * 2);
-    uint32_t aoff[4], boff[4];
+    uint32_t aoff[4], boff[NB];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 4; ++q)
       aoff[q] = static_cast<uint32_t>(min(8 * (4 * wave + q) + drow, xr)) * xrow + dpiece[q & 1];
+#pragma unroll
+    for (int q = 0; q < NB; ++q)
       boff[q] = static_cast<uint32_t>(min((tid >> 3) + 64 * q, wr)) * wrow + (tid & 7) * 16;
-    }
     auto issue_a = [&](int ks) __attribute__((always_inline)) {
       dma4_rows(ra, aoff, static_cast<uint32_t>(ks) * kWideRow,
-                lds0 + static_cast<uint32_t>(ks & 1) * kWideStage + 4 * wave * 1024);
+                lds0 + static_cast<uint32_t>(ks & 1) * kStage + 4 * wave * 1024);
     };
     struct BRegs {
-      uint4 v[4];
+      uint4 v[NB];
     };
     auto load_b = [&](BRegs& R, int ks) __attribute__((always_inline)) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) R.v[q] = buf_ld16(rb, boff[q], static_cast<uint32_t>(ks) * kWideRow);
+      for (int q = 0; q < NB; ++q) R.v[q] = buf_ld16(rb, boff[q], static_cast<uint32_t>(ks) * kWideRow);
     };
     auto store_b = [&](const BRegs& R, int ks) __attribute__((always_inline)) {
-      uint8_t* dst = smem + (ks & 1) * kWideStage + kWideTile * kWideRow + bldsoff;
+      uint8_t* dst = smem + (ks & 1) * kStage + kWideRows * kWideRow + bldsoff;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(dst + 64 * q * kWideRow) = R.v[q];
+      for (int q = 0; q < NB; ++q) *reinterpret_cast<uint4*>(dst + 64 * q * kWideRow) = R.v[q];
     };
-    f32x16 acc[4][2];
+    f32x16 acc[NI][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
     auto compute = [&](int ks) __attribute__((always_inline)) {
-      const uint8_t* base = smem + (ks & 1) * kWideStage;
-      const uint8_t* As = base + (wm * 128 + r32) * kWideRow;
-      const uint8_t* Bs = base + (kWideTile + wn * 64 + r32) * kWideRow;
+      const uint8_t* base = smem + (ks & 1) * kStage;
+      const uint8_t* As = base + (wm * 32 * NI + r32) * kWideRow;
+      const uint8_t* Bs = base + (kWideRows + wn * 64 + r32) * kWideRow;
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         const uint32_t piece = ((2 * kk) ^ fswz) * 16;
-        uint4 af[4], bf[2];
+        uint4 af[NI], bf[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) bf[j] = *reinterpret_cast<const uint4*>(Bs + 32 * j * kWideRow + piece);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) af[i] = *reinterpret_cast<const uint4*>(As + 32 * i * kWideRow + piece);
+        for (int i = 0; i < NI; ++i) af[i] = *reinterpret_cast<const uint4*>(As + 32 * i * kWideRow + piece);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
           for (int j = 0; j < 2; ++j) acc[i][j] = mfma_bf16_32x32x16(af[i], bf[j], acc[i][j]);
       }
@@ -426,20 +479,20 @@ __global__ void __launch_bounds__(kWideThreads) linear_wide_kernel(LinearArgs a,
     // stage ks.  Past the end the last stage of W is read again, so that every iteration
     // has the same number of loads in flight.
     BRegs R0, R1;
-    load_b(R0, 0);
-    load_b(R1, 1);
+    load_b(R0, k0);
+    load_b(R1, k0 + 1);
     __syncthreads();                 // the previous tile is done with both buffers
-    store_b(R0, 0);
-    issue_a(0);
-    load_b(R0, min(2, nk - 1));
-    for (int ks = 0; ks < nk; ks += 2) {
-      wait_vm<4>();
+    store_b(R0, k0);
+    issue_a(k0);
+    load_b(R0, min(k0 + 2, nk - 1));
+    for (int ks = k0; ks < nk; ks += 2) {
+      wait_vm<NB>();
       __syncthreads();
       store_b(R1, ks + 1);
       issue_a(ks + 1);
       load_b(R1, min(ks + 3, nk - 1));
       compute(ks);
-      wait_vm<4>();
+      wait_vm<NB>();
       __syncthreads();
       if (ks + 2 < nk) {
         store_b(R0, ks + 2);
@@ -451,64 +504,29 @@ __global__ void __launch_bounds__(kWideThreads) linear_wide_kernel(LinearArgs a,
     wait_vm<0>();                    // no load may still be writing registers or LDS
     __syncthreads();                 // every wave is done reading the stage buffers
 
-    // Out through LDS in four rounds of 64 rows (32 of each row half) x 256 columns, rows
-    // padded to 264 floats, so that bias, residual and y are taken in whole row segments:
-    // lane l holds columns 4 l .. + 4.
-    constexpr int kStride = 264;
+    // Out through LDS, so that bias, residual and y (or the part's sums) are taken in
+    // whole row segments, four columns to a lane.  NI rounds of 32 rows of each wave row;
+    // rows padded by 8 floats.
+    constexpr int kStride = BN + 8, kLanes = BN / 4, kRows = 32 * WM;   // lanes and rows of a round
     float* stg = reinterpret_cast<float*>(smem);
-    const int n = n0 + 4 * lane;
-    float bias[4] = {0.f, 0.f, 0.f, 0.f};
-    if (a.bias) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (n + c < a.N) bias[c] = elem<false>(a.bias, n + c);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NI; ++i) {
 #pragma unroll
       for (int v = 0; v < 16; ++v)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           stg[(wm * 32 + 8 * (v >> 2) + 4 * hi + (v & 3)) * kStride + wn * 64 + 32 * j + r32] = acc[i][j][v];
       __syncthreads();
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int R = 8 * wave + k;
-        const int m = m0 + (R < 32 ? 32 * i + R : 128 + 32 * i + (R - 32));
+#pragma unroll 1
+      for (int k = 0; k < kRows * kLanes / kWideThreads; ++k) {   // not unrolled: the epilogue is long
+        const int at = tid + k * kWideThreads, R = at / kLanes, c = 4 * (at % kLanes);
+        const int m = m0 + (R / 32 * NI + i) * 32 + R % 32, n = n0 + c;
         if (m < a.M && n < a.N) {
-          const f32x4 s = *reinterpret_cast<const f32x4*>(stg + R * kStride + 4 * lane);
-          float v[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) v[c] = activate(s[c] + bias[c], a.act);
-          const size_t ro = static_cast<size_t>(m) * a.ldr + n, yo = static_cast<size_t>(m) * a.ldy + n;
-          if (vec) {                 // four columns at a time: aligned, N a multiple of 4
-            if constexpr (OUT32) {
-              f32x4 o = {v[0], v[1], v[2], v[3]};
-              if (a.residual) o += *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.residual) + ro);
-              *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + yo) = o;
-            } else {
-              if (a.residual) {
-                const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.residual) + ro);
-                v[0] += bf16_bits_to_f32(static_cast<uint16_t>(q.x));
-                v[1] += bf16_bits_to_f32(static_cast<uint16_t>(q.x >> 16));
-                v[2] += bf16_bits_to_f32(static_cast<uint16_t>(q.y));
-                v[3] += bf16_bits_to_f32(static_cast<uint16_t>(q.y >> 16));
-              }
-              uint2 o;
-              o.x = f32_to_bf16_bits(v[0]) | static_cast<uint32_t>(f32_to_bf16_bits(v[1])) << 16;
-              o.y = f32_to_bf16_bits(v[2]) | static_cast<uint32_t>(f32_to_bf16_bits(v[3])) << 16;
-              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + yo) = o;
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (n + c < a.N) {
-                float o = v[c];
-                if (a.residual) o += elem<OUT32>(a.residual, ro + c);
-                if constexpr (OUT32) static_cast<float*>(a.y)[yo + c] = o;
-                else static_cast<uint16_t*>(a.y)[yo + c] = f32_to_bf16_bits(o);
-              }
-          }
+          const f32x4 s = *reinterpret_cast<const f32x4*>(stg + R * kStride + c);
+          if (parts > 1)
+            *reinterpret_cast<f32x4*>(part + (static_cast<size_t>(p) * a.M + m) * part_stride(a.N) + n) = s;
+          else
+            finish4<false, OUT32>(a, m, n, s);
         }
       }
       __syncthreads();
@@ -518,21 +536,31 @@ __global__ void __launch_bounds__(kWideThreads) linear_wide_kernel(LinearArgs a,
 
 // ---------------------------------------------------------------- parts added up
 
+// A thread adds up four neighbouring sums, all parts' loads in flight together as far as
+// kPartsAhead goes.  Rows of a plane are padded to multiples of four.
+constexpr int kPartsAhead = 8;
+
 template <bool F32, bool OUT32>
 __global__ void __launch_bounds__(256) linear_finish_kernel(LinearArgs a, int parts, const float* part) {
-  const int64_t plane = static_cast<int64_t>(a.M) * a.N;
+  const int quads = static_cast<int>(part_stride(a.N) / 4);
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= plane) return;
-  float v = part[i];
-  int p = 1;
-  for (; p + 4 <= parts; p += 4) {   // four loads in flight
-    const float b = part[i + plane * p], c = part[i + plane * (p + 1)], d = part[i + plane * (p + 2)],
-                e = part[i + plane * (p + 3)];
-    v += b; v += c; v += d; v += e;
+  if (i >= static_cast<int64_t>(a.M) * quads) return;
+  const int64_t plane = static_cast<int64_t>(a.M) * quads;
+  const f32x4* v = reinterpret_cast<const f32x4*>(part) + i;
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < parts; p += kPartsAhead) {
+    f32x4 b[kPartsAhead];
+#pragma unroll
+    for (int k = 0; k < kPartsAhead; ++k)
+      if (p + k < parts) b[k] = v[plane * (p + k)];
+#pragma unroll
+    for (int k = 0; k < kPartsAhead; ++k)
+      if (p + k < parts)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[c] += b[k][c];
   }
-  for (; p < parts; ++p) v += part[i + plane * p];
-  const int m = static_cast<int>(i / a.N);
-  finish<F32, OUT32>(a, m, static_cast<int>(i - static_cast<int64_t>(m) * a.N), v);
+  const int m = static_cast<int>(i / quads);
+  finish4<F32, OUT32>(a, m, 4 * static_cast<int>(i - static_cast<int64_t>(m) * quads), s);
 }
 
 // ---------------------------------------------------------------- any stride
@@ -601,62 +629,68 @@ int check_linear(const moe_linear_config* c, int32_t rows) {
 
 // How a product runs: which tiles, and in how many parts of the contraction.
 struct LinearPlan {
-  int rows, cols;    // of a tile (rows 16: the skinny kernel)
+  int rows, cols;    // of a tile (rows 16: the skinny kernel; 256: the 256-row tiles)
   int64_t tiles;
   int parts;
 };
-constexpr int kFillGroups = 512;        // two workgroups on each CU
+constexpr int kCus = 256;
+constexpr int kMaxParts = 16;
+// Most bytes of partial sums: a plan with parts fills the GPU at most once, with two
+// 128 x 128 tiles or one 256 x 128 tile on each CU.
+constexpr size_t kMaxPartBytes = size_t{2} * kCus * 128 * 128 * sizeof(float);
 
-LinearPlan linear_plan(const moe_linear_config& c, int64_t M) {
-  const int64_t N = c.out_features, K = c.in_features, size = c.in_dtype == MOE_DTYPE_F32 ? 4 : 2;
+// The cheapest plan by an estimate in microseconds.  A CU takes about 36 KB of operands
+// in a microsecond in the 256-row kernel and 28 KB in the other (measured; what limits
+// both in bf16), multiplies about 0.5 MFLOP f32, and partial sums cross at 5 TB/s twice.
+LinearPlan linear_plan(const moe_linear_config& c, int64_t M, bool wide) {
+  const int64_t N = c.out_features, K = c.in_features;
+  const bool f32 = c.in_dtype == MOE_DTYPE_F32;
   LinearPlan p{};
   if (M <= kSkinnyRows) {
     // 16 columns while that gives two workgroups for each CU, else 8; below one workgroup
     // for each CU parts of at least 16 blocks.
     p.rows = kSkinnyRows;
-    p.cols = ceil_div(N, 16) >= kFillGroups ? 16 : 8;
+    p.cols = ceil_div(N, 16) >= 2 * kCus ? 16 : 8;
     p.tiles = ceil_div(N, p.cols);
-    const int64_t blocks = ceil_div(K * size, kBlkBytes);
-    p.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kFillGroups / 2 / p.tiles, blocks / 16, 16})));
+    const int64_t blocks = ceil_div(K * (f32 ? 4 : 2), kBlkBytes);
+    p.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kCus / p.tiles, blocks / 16, kMaxParts})));
     return p;
   }
-  p.rows = M <= 64 ? 64 : 128;
-  p.cols = 128;
-  p.tiles = ceil_div(M, p.rows) * ceil_div(N, p.cols);
-  // Parts of at least 8 stages, as many as fill the GPU once with two workgroups on a CU.
-  const int64_t stages = ceil_div(K * size, 128);
-  p.parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kFillGroups / p.tiles, stages / 8, 16})));
+  static const struct { int rows, cols, on_cu; } kTiles[] = {{64, 128, 2}, {128, 128, 2}, {256, 128, 1}, {256, 256, 1}};
+  const int64_t stages = ceil_div(K * (f32 ? 4 : 2), 128);
+  double best = 0;
+  for (const auto& t : kTiles) {
+    if (t.rows == kWideRows && !wide) continue;
+    const int64_t tiles = ceil_div(M, t.rows) * ceil_div(N, t.cols);
+    const int64_t slots = static_cast<int64_t>(t.on_cu) * kCus;
+    for (int parts = 1; parts <= kMaxParts; ++parts) {
+      if (parts > 1 && (tiles * parts > slots || stages / parts < 4 || (t.cols == 256))) break;
+      const int64_t items = tiles * parts, rounds = ceil_div(items, slots);
+      const double shared = items > kCus ? t.on_cu : 1;             // tiles that share a CU
+      const double deep = static_cast<double>(ceil_div(stages, parts));
+      const double load = (t.rows + t.cols) * 0.128 * deep / (t.rows == kWideRows ? 36 : shared > 1 ? 28 : 20);
+      const double mult = f32 ? t.rows * t.cols * 64 * deep / 0.5e6 : 0;
+      const double us = rounds * shared * std::max(load, mult) + 2 + 0.5 * rounds +
+                        (parts > 1 ? 4 + parts * static_cast<double>(M) * N * 8 / 5e6 : 0);
+      if (p.tiles == 0 || us < best) {
+        best = us;
+        p = LinearPlan{t.rows, t.cols, tiles, parts};
+      }
+    }
+  }
   return p;
-}
-
-// 256 x 256 tiles when they keep the CUs at least three quarters busy: the last round of
-// one tile for each CU may be short.
-bool wide_fills(int64_t M, int64_t N) {
-  const int64_t tiles = ceil_div(M, kWideTile) * ceil_div(N, kWideTile);
-  return M * N * 4 >= ceil_div(tiles, 256) * 256 * kWideTile * kWideTile * 3;
 }
 
 // Bytes of partial sums of any call of at most M rows.
 size_t linear_workspace(const moe_linear_config& c, int64_t M) {
-  size_t most = 256;
-  auto take = [&](int64_t rows) {
-    const LinearPlan p = linear_plan(c, rows);
-    if (p.parts > 1) most = std::max(most, static_cast<size_t>(p.parts) * rows * c.out_features * sizeof(float));
-  };
-  // The number of parts depends on the number of tile rows only and shrinks with it.
-  take(std::min<int64_t>(M, kSkinnyRows));
-  if (M > kSkinnyRows) take(std::min<int64_t>(M, 64));
-  for (int64_t rows = 128; M > 64; rows += 128) {
-    take(std::min(rows, M));
-    if (rows >= M || linear_plan(c, rows).parts == 1) break;
-  }
-  return most;
+  const double want = static_cast<double>(kMaxParts) * M * part_stride(c.out_features) * sizeof(float);
+  return want < static_cast<double>(kMaxPartBytes) ? std::max<size_t>(static_cast<size_t>(want), 256) : kMaxPartBytes;
 }
 
 bool off(const void* p, int dtype) { return reinterpret_cast<uintptr_t>(p) % (dtype == MOE_DTYPE_F32 ? 4 : 2) != 0; }
 
 template <bool F32, bool OUT32, bool ANY>
-int linear_launch(const LinearArgs& a, const LinearPlan& p, float* part, hipStream_t s) {
+void linear_launch(const LinearArgs& a, const LinearPlan& p, float* part, hipStream_t s) {
   if (p.rows == kSkinnyRows) {
     const dim3 grid(static_cast<unsigned>(p.tiles), static_cast<unsigned>(p.parts));
     if (p.cols == 16) linear_skinny_kernel<F32, OUT32, ANY, 2><<<grid, kSkinnyWaves * kWave, 0, s>>>(a, p.parts, part);
@@ -666,13 +700,6 @@ int linear_launch(const LinearArgs& a, const LinearPlan& p, float* part, hipStre
     if (p.rows == 64) linear_tile_kernel<F32, OUT32, ANY, 64, 128><<<grid, 256, 0, s>>>(a, p.parts, part);
     else linear_tile_kernel<F32, OUT32, ANY, 128, 128><<<grid, 256, 0, s>>>(a, p.parts, part);
   }
-  if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
-  if (p.parts > 1) {
-    linear_finish_kernel<F32, OUT32><<<static_cast<unsigned>(ceil_div(static_cast<int64_t>(a.M) * a.N, 256)), 256, 0, s>>>(
-        a, p.parts, part);
-    if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
-  }
-  return MOE_OK;
 }
 
 template <bool F32, bool OUT32>
@@ -686,17 +713,25 @@ int linear_dispatch(const LinearArgs& a, const moe_linear_config& c, float* part
   const int64_t unit = F32 ? 4 : 8;        // elements of 16 bytes
   const bool aligned = a.ldx % unit == 0 && a.ldw % unit == 0 && a.K % unit == 0 &&
                        reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && reinterpret_cast<uintptr_t>(a.w) % 16 == 0;
-  const LinearPlan p = linear_plan(c, a.M);
-  if constexpr (!F32) {
-    if (aligned && a.K % 128 == 0 && wide_fills(a.M, a.N)) {
-      const uintptr_t four = OUT32 ? 16 : 8;
-      const bool vec = a.N % 4 == 0 && a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % four == 0 &&
-                       (!a.residual || (a.ldr % 4 == 0 && reinterpret_cast<uintptr_t>(a.residual) % four == 0));
-      linear_wide_kernel<OUT32><<<256, kWideThreads, 0, s>>>(a, vec);
-      return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH_FAILED;
+  const LinearPlan p = linear_plan(c, a.M, !F32 && aligned && a.K % 128 == 0);
+  if (p.rows == kWideRows) {
+    if constexpr (!F32) {
+      const unsigned grid = static_cast<unsigned>(std::min<int64_t>(kCus, ceil_div(p.tiles * p.parts, 8) * 8));
+      if (p.cols == 256) linear_wide_kernel<OUT32, 256><<<grid, kWideThreads, 0, s>>>(a, p.parts, part);
+      else linear_wide_kernel<OUT32, 128><<<grid, kWideThreads, 0, s>>>(a, p.parts, part);
     }
+  } else if (aligned) {
+    linear_launch<F32, OUT32, false>(a, p, part, s);
+  } else {
+    linear_launch<F32, OUT32, true>(a, p, part, s);
   }
-  return aligned ? linear_launch<F32, OUT32, false>(a, p, part, s) : linear_launch<F32, OUT32, true>(a, p, part, s);
+  if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
+  if (p.parts > 1) {
+    linear_finish_kernel<F32, OUT32><<<static_cast<unsigned>(ceil_div(a.M * part_stride(a.N) / 4, 256)), 256, 0, s>>>(
+        a, p.parts, part);
+    if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
+  }
+  return MOE_OK;
 }
 
 }  // namespace
