@@ -33,17 +33,37 @@ __host__ __device__ inline int64_t part_stride(int64_t N) { return (N + 3) / 4 *
 
 // ---------------------------------------------------------------- epilogue
 
-// tanh(u) = 1 - 2 / (1 + e^(2u)): exact at both infinities, and near 0 within a few
-// 2^-24 of 1, which is what the 1 + tanh of the activation keeps of it.
-__device__ __forceinline__ float tanh_f32(float u) { return 1.0f - 2.0f / (1.0f + expf(2.0f * u)); }
+// v / (1 + e^-u): silu with u = v, and with u = 2 sqrt(2/pi) (v + 0.044715 v^3) the tanh
+// form of gelu, as (1 + tanh(u/2)) / 2 = 1 / (1 + e^-u); e^-u = inf gives 0.  QUICK: the
+// hardware's exponential and reciprocal, good to 2^-22 (1 + |u|), for results that are
+// rounded to bf16.
+template <bool QUICK>
+__device__ __forceinline__ float gated(float v, float u) {
+  if constexpr (QUICK) return v * __builtin_amdgcn_rcpf(1.0f + __expf(-u));
+  else return v / (1.0f + expf(-u));
+}
 
-__device__ __forceinline__ float activate(float v, int act) {
+template <bool QUICK, int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
   switch (act) {
-    case MOE_ACT_RELU: return v < 0.0f ? 0.0f : v;                              // NaN stays NaN
-    case MOE_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678f));
-    case MOE_ACT_GELU_TANH: return 0.5f * v * (1.0f + tanh_f32(0.79788456f * (v + 0.044715f * v * v * v)));
-    case MOE_ACT_SILU: return v / (1.0f + expf(-v));
-    default: return v;
+    case MOE_ACT_RELU:
+#pragma unroll
+      for (int c = 0; c < N; ++c) v[c] = v[c] < 0.0f ? 0.0f : v[c];             // NaN stays NaN
+      break;
+    case MOE_ACT_GELU:
+#pragma unroll
+      for (int c = 0; c < N; ++c) v[c] = 0.5f * v[c] * (1.0f + erff(v[c] * 0.70710678f));
+      break;
+    case MOE_ACT_GELU_TANH:
+#pragma unroll
+      for (int c = 0; c < N; ++c) v[c] = gated<QUICK>(v[c], 1.59576912f * (v[c] + 0.044715f * v[c] * v[c] * v[c]));
+      break;
+    case MOE_ACT_SILU:
+#pragma unroll
+      for (int c = 0; c < N; ++c) v[c] = gated<QUICK>(v[c], v[c]);
+      break;
+    default:
+      break;
   }
 }
 
@@ -56,8 +76,9 @@ __device__ __forceinline__ float elem(const void* p, size_t i) {
 // One output element from its float32 sum.
 template <bool F32, bool OUT32>
 __device__ __forceinline__ void finish(const LinearArgs& a, int m, int n, float v) {
-  if (a.bias) v += elem<F32>(a.bias, n);
-  v = activate(v, a.act);
+  float t[1] = {a.bias ? v + elem<F32>(a.bias, n) : v};
+  activate<!OUT32>(t, a.act);
+  v = t[0];
   if (a.residual) v += elem<OUT32>(a.residual, static_cast<size_t>(m) * a.ldr + n);
   const size_t o = static_cast<size_t>(m) * a.ldy + n;
   if constexpr (OUT32) static_cast<float*>(a.y)[o] = v;
@@ -66,15 +87,16 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int m, int n, float 
 
 // Four neighbouring elements.  The vector accesses need only the elements' alignment.
 template <bool F32, bool OUT32>
-__device__ __forceinline__ void finish4(const LinearArgs& a, int m, int n, f32x4 v) {
+__device__ __forceinline__ void finish4(const LinearArgs& a, int m, int n, f32x4 s) {
   typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
   typedef uint16_t u16x4_any __attribute__((ext_vector_type(4), aligned(2)));
   if (n + 4 > a.N) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      if (n + c < a.N) finish<F32, OUT32>(a, m, n + c, v[c]);
+      if (n + c < a.N) finish<F32, OUT32>(a, m, n + c, s[c]);
     return;
   }
+  float v[4] = {s[0], s[1], s[2], s[3]};
   if (a.bias) {
     if constexpr (F32) {
       const f32x4_any b = *reinterpret_cast<const f32x4_any*>(static_cast<const float*>(a.bias) + n);
@@ -86,8 +108,7 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, int m, int n, f32x4
       for (int c = 0; c < 4; ++c) v[c] += bf16_bits_to_f32(b[c]);
     }
   }
-#pragma unroll
-  for (int c = 0; c < 4; ++c) v[c] = activate(v[c], a.act);
+  activate<!OUT32>(v, a.act);
   const size_t ro = static_cast<size_t>(m) * a.ldr + n, yo = static_cast<size_t>(m) * a.ldy + n;
   if constexpr (OUT32) {
     if (a.residual) {
