@@ -85,48 +85,95 @@ __device__ __forceinline__ void finish(const LinearArgs& a, int m, int n, float 
   else static_cast<uint16_t*>(a.y)[o] = f32_to_bf16_bits(v);
 }
 
-// Four neighbouring elements.  The vector accesses need only the elements' alignment.
-template <bool F32, bool OUT32>
-__device__ __forceinline__ void finish4(const LinearArgs& a, int m, int n, f32x4 s) {
-  typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
-  typedef uint16_t u16x4_any __attribute__((ext_vector_type(4), aligned(2)));
-  if (n + 4 > a.N) {
+// Four neighbouring elements; these accesses need only the elements' alignment.
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint16_t u16x4_any __attribute__((ext_vector_type(4), aligned(2)));
+template <bool F32>
+__device__ __forceinline__ f32x4 load4(const void* p, size_t i) {
+  f32x4 v;
+  if constexpr (F32) {
+    const f32x4_any q = *reinterpret_cast<const f32x4_any*>(static_cast<const float*>(p) + i);
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (n + c < a.N) finish<F32, OUT32>(a, m, n + c, s[c]);
-    return;
-  }
-  float v[4] = {s[0], s[1], s[2], s[3]};
-  if (a.bias) {
-    if constexpr (F32) {
-      const f32x4_any b = *reinterpret_cast<const f32x4_any*>(static_cast<const float*>(a.bias) + n);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] += b[c];
-    } else {
-      const u16x4_any b = *reinterpret_cast<const u16x4_any*>(static_cast<const uint16_t*>(a.bias) + n);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] += bf16_bits_to_f32(b[c]);
-    }
-  }
-  activate<!OUT32>(v, a.act);
-  const size_t ro = static_cast<size_t>(m) * a.ldr + n, yo = static_cast<size_t>(m) * a.ldy + n;
-  if constexpr (OUT32) {
-    if (a.residual) {
-      const f32x4_any q = *reinterpret_cast<const f32x4_any*>(static_cast<const float*>(a.residual) + ro);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] += q[c];
-    }
-    *reinterpret_cast<f32x4_any*>(static_cast<float*>(a.y) + yo) = f32x4_any{v[0], v[1], v[2], v[3]};
+    for (int c = 0; c < 4; ++c) v[c] = q[c];
   } else {
-    if (a.residual) {
-      const u16x4_any q = *reinterpret_cast<const u16x4_any*>(static_cast<const uint16_t*>(a.residual) + ro);
+    const u16x4_any q = *reinterpret_cast<const u16x4_any*>(static_cast<const uint16_t*>(p) + i);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] += bf16_bits_to_f32(q[c]);
-    }
+    for (int c = 0; c < 4; ++c) v[c] = bf16_bits_to_f32(q[c]);
+  }
+  return v;
+}
+template <bool F32>
+__device__ __forceinline__ void store4(void* p, size_t i, const float* v) {
+  if constexpr (F32) {
+    *reinterpret_cast<f32x4_any*>(static_cast<float*>(p) + i) = f32x4_any{v[0], v[1], v[2], v[3]};
+  } else {
     u16x4_any o;
 #pragma unroll
     for (int c = 0; c < 4; ++c) o[c] = f32_to_bf16_bits(v[c]);
-    *reinterpret_cast<u16x4_any*>(static_cast<uint16_t*>(a.y) + yo) = o;
+    *reinterpret_cast<u16x4_any*>(static_cast<uint16_t*>(p) + i) = o;
+  }
+}
+
+// D rows of four neighbouring columns from n on (rows m[d], of which those past the end
+// are left out).  The residual's loads are in flight together.
+template <bool F32, bool OUT32, int D>
+__device__ __forceinline__ void finish_quads(const LinearArgs& a, const int (&m)[D], int n, const f32x4 (&s)[D]) {
+  if (n + 4 > a.N) {
+#pragma unroll 1
+    for (int d = 0; d < D; ++d)
+      for (int c = 0; c < 4; ++c)
+        if (m[d] < a.M && n + c < a.N) finish<F32, OUT32>(a, m[d], n + c, s[d][c]);
+    return;
+  }
+  f32x4 res[D];
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+    res[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (a.residual && m[d] < a.M) res[d] = load4<OUT32>(a.residual, static_cast<size_t>(m[d]) * a.ldr + n);
+  }
+  f32x4 bias = {0.f, 0.f, 0.f, 0.f};
+  if (a.bias) bias = load4<F32>(a.bias, n);
+  float v[4 * D];
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[4 * d + c] = s[d][c] + bias[c];
+  activate<!OUT32>(v, a.act);
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[4 * d + c] += res[d][c];
+    if (m[d] < a.M) store4<OUT32>(a.y, static_cast<size_t>(m[d]) * a.ldy + n, v + 4 * d);
+  }
+}
+
+// ROWS x BN sums in LDS, rows `stride` floats apart, as y or as part p's sums: row_of(R)
+// is the row of y behind row R.  Whole row segments, four columns to a thread.
+template <bool F32, bool OUT32, int BN, int ROWS, int THREADS, class RowOf>
+__device__ __forceinline__ void finish_rows(const LinearArgs& a, const float* stg, int stride, int n0, int parts, int p,
+                                            float* part, RowOf row_of) {
+  constexpr int kLanes = BN / 4, kIter = ROWS * kLanes / THREADS, D = 4;
+  static_assert(THREADS % kLanes == 0 && kIter % D == 0, "a thread keeps its columns");
+  const int tid = threadIdx.x, c = 4 * (tid % kLanes), n = n0 + c;
+  if (n >= a.N) return;
+#pragma unroll 1
+  for (int k = 0; k < kIter; k += D) {
+    int m[D];
+    f32x4 s[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int R = (tid + (k + d) * THREADS) / kLanes;
+      m[d] = row_of(R);
+      s[d] = *reinterpret_cast<const f32x4*>(stg + R * stride + c);
+    }
+    if (parts > 1) {
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+        if (m[d] < a.M)
+          *reinterpret_cast<f32x4*>(part + (static_cast<size_t>(p) * a.M + m[d]) * part_stride(a.N) + n) = s[d];
+    } else {
+      finish_quads<F32, OUT32, D>(a, m, n, s);
+    }
   }
 }
 
@@ -379,21 +426,25 @@ __global__ void __launch_bounds__(256, 2) linear_tile_kernel(LinearArgs a, int p
     compute(1);
   }
 
+  // Out through LDS, NI rounds of 32 rows of each wave row, rows padded by 8 floats.
   // Lane l, element v: row 8 (v / 4) + 4 (l / 32) + v % 4, column l % 32 of a block.
+  constexpr int kStride = BN + 8;
+  static_assert(64 * kStride * 4 <= 2 * kStage, "a round fits the stage buffers");
+  float* stg = reinterpret_cast<float*>(smem);
+  __syncthreads();                   // every wave is done reading the stage buffers
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
+  for (int i = 0; i < NI; ++i) {
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int m = m0 + wm * (BM / 2) + 32 * i + 8 * (v >> 2) + 4 * hi + (v & 3);
+    for (int v = 0; v < 16; ++v)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int n = n0 + wn * (BN / 2) + 32 * j + r32;
-        if (m < a.M && n < a.N) {
-          if (parts > 1) part[(static_cast<size_t>(p) * a.M + m) * part_stride(a.N) + n] = acc[i][j][v];
-          else finish<F32, OUT32>(a, m, n, acc[i][j][v]);
-        }
-      }
-    }
+      for (int j = 0; j < NJ; ++j)
+        stg[(wm * 32 + 8 * (v >> 2) + 4 * hi + (v & 3)) * kStride + wn * (BN / 2) + 32 * j + r32] = acc[i][j][v];
+    __syncthreads();
+    finish_rows<F32, OUT32, BN, 64, 256>(a, stg, kStride, n0, parts, p, part, [&](int R) {
+      return m0 + (R / 32) * (BM / 2) + 32 * i + R % 32;
+    });
+    __syncthreads();
+  }
 }
 
 // ---------------------------------------------------------------- 256-row tiles
@@ -528,7 +579,7 @@ __global__ void __launch_bounds__(kWideThreads) linear_wide_kernel(LinearArgs a,
     // Out through LDS, so that bias, residual and y (or the part's sums) are taken in
     // whole row segments, four columns to a lane.  NI rounds of 32 rows of each wave row;
     // rows padded by 8 floats.
-    constexpr int kStride = BN + 8, kLanes = BN / 4, kRows = 32 * WM;   // lanes and rows of a round
+    constexpr int kStride = BN + 8;
     float* stg = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -538,18 +589,9 @@ __global__ void __launch_bounds__(kWideThreads) linear_wide_kernel(LinearArgs a,
         for (int j = 0; j < 2; ++j)
           stg[(wm * 32 + 8 * (v >> 2) + 4 * hi + (v & 3)) * kStride + wn * 64 + 32 * j + r32] = acc[i][j][v];
       __syncthreads();
-#pragma unroll 1
-      for (int k = 0; k < kRows * kLanes / kWideThreads; ++k) {   // not unrolled: the epilogue is long
-        const int at = tid + k * kWideThreads, R = at / kLanes, c = 4 * (at % kLanes);
-        const int m = m0 + (R / 32 * NI + i) * 32 + R % 32, n = n0 + c;
-        if (m < a.M && n < a.N) {
-          const f32x4 s = *reinterpret_cast<const f32x4*>(stg + R * kStride + c);
-          if (parts > 1)
-            *reinterpret_cast<f32x4*>(part + (static_cast<size_t>(p) * a.M + m) * part_stride(a.N) + n) = s;
-          else
-            finish4<false, OUT32>(a, m, n, s);
-        }
-      }
+      finish_rows<false, OUT32, BN, 32 * WM, kWideThreads>(a, stg, kStride, n0, parts, p, part, [&](int R) {
+        return m0 + (R / 32 * NI + i) * 32 + R % 32;
+      });
       __syncthreads();
     }
   }
@@ -580,8 +622,9 @@ __global__ void __launch_bounds__(256) linear_finish_kernel(LinearArgs a, int pa
 #pragma unroll
         for (int c = 0; c < 4; ++c) s[c] += b[k][c];
   }
-  const int m = static_cast<int>(i / quads);
-  finish4<F32, OUT32>(a, m, 4 * static_cast<int>(i - static_cast<int64_t>(m) * quads), s);
+  const int m[1] = {static_cast<int>(i / quads)};
+  const f32x4 t[1] = {s};
+  finish_quads<F32, OUT32, 1>(a, m, 4 * static_cast<int>(i - static_cast<int64_t>(m[0]) * quads), t);
 }
 
 // ---------------------------------------------------------------- any stride
