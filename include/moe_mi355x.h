@@ -269,9 +269,9 @@ int moe_forward_noalloc(const moe_config* cfg, int32_t num_tokens, const void* x
  * the weights.  Routing (selection, top-p trim, budget, masked and NaN logits,
  * statistics) and y are those of the three calls, every weight dtype and every
  * option of cfg included, with one difference: with FP8 and MXFP4 weights the
- * activations are not quantised (the weights are decoded, w = decode(q) * s), so y
- * lies closer to the unquantised layer than moe_forward's; and h is kept to 16
- * significant bits (float32 with F32 weights).  y is bit-reproducible.
+ * activations are not quantised (the weights are decoded, w = decode(q) * s) and with
+ * BF16 weights h is not rounded to bf16, so y lies closer to the exact layer than
+ * moe_forward's.  y is bit-reproducible.
  *   topk_ids     (device) out [T, K] int32 or NULL, as moe_route writes it
  *   topk_weights (device) out [T, K] float32 or NULL
  *   shared_gate  (device) out [T] float32 or NULL; ignored when S = 0
@@ -281,7 +281,8 @@ int moe_forward_noalloc(const moe_config* cfg, int32_t num_tokens, const void* x
  * A slot of weight 0 is not computed.  x, w_router, w_shared_gate and the weights
  * must be 16-byte aligned (with F32 weights 4-byte), scales, y, y_act and the other
  * outputs to their element size, the workspace to 16 bytes (MOE_ERR_UNSUPPORTED
- * otherwise, and for more than MOE_FEW_TOKENS tokens).  The workspace is not that
+ * otherwise, and for more than MOE_FEW_TOKENS tokens or for an expert matrix, a router
+ * or intermediate activations of 4 GiB or more).  The workspace is not that
  * of moe_workspace_size; moe_layer_few_workspace_size gives its bytes for any
  * T <= max_tokens <= MOE_FEW_TOKENS.  It needs no initial contents; calls that
  * overlap in time (other streams, graphs replayed side by side) need one each. */

@@ -288,15 +288,16 @@ def layer_few(cfg: MoEConfig, x, w_router, w_shared_gate, logit_bias, weights: _
     _expect(route_stats, (4,), torch.int32, "route_stats")
     _expect(y, (T, H), torch.float32, "y")
     _expect(y_act, (T, H), act, "y_act")
+    _together(x.device, w_router, w_shared_gate, topk_ids, topk_weights, shared_gate, route_stats, y, y_act)
     _layer_few_call(ctypes.byref(cfg.c()), cfg, x, logit_bias,
                     (_ptr(w_router), _ptr(w_shared_gate), ctypes.byref(weights)),
                     (_ptr(topk_ids), _ptr(topk_weights), _ptr(shared_gate), _ptr(route_stats), _ptr(y), _ptr(y_act),
-                     _ptr(workspace), workspace.numel()), stream)
+                     _ptr(workspace), workspace.numel()), workspace, stream)
 
 
-def _layer_few_call(c, cfg, x, logit_bias, weights, outputs, stream) -> None:
+def _layer_few_call(c, cfg, x, logit_bias, weights, outputs, home, stream) -> None:
     """moe_layer_few with the addresses of the weights and of the outputs; checks what a
-    caller brings to each call."""
+    caller brings to each call (home: a tensor of the layer's, for its device)."""
     T = x.shape[0]
     _expect(x, (T, cfg.hidden_size), cfg.act_torch_dtype, "x")
     bp = None
@@ -304,6 +305,7 @@ def _layer_few_call(c, cfg, x, logit_bias, weights, outputs, stream) -> None:
         _expect(logit_bias, (T, cfg.n_routed_experts), torch.float32, "logit_bias")
         bp = _ptr(logit_bias)
     xp, (wr, wg, w) = _ptr(x), weights
+    _together(x.device, logit_bias, home)
     with _on(x.device):
         status = lib().moe_layer_few(c, T, xp, wr, wg, bp, w, *outputs, _stream_of(x.device, stream))
     if status != 0:
@@ -347,19 +349,27 @@ def linear(x, weight, bias, residual, y, workspace, activation: str = "none", st
     cfg = _LinearConfig(K, N, _dtype_code(x, "x"), _dtype_code(y, "y"), ACTIVATIONS[activation])
     wp, ldw = _rows(weight, (N, K), x.dtype, "weight")
     _expect(bias, (N,), x.dtype, "bias")
-    _linear_call(ctypes.byref(cfg), M, N, K, x, wp, ldw, _ptr(bias), residual, y, _ptr(workspace), workspace.numel(),
-                 x.dtype, y.dtype, stream)
+    _together(x.device, bias, workspace)
+    _linear_call(ctypes.byref(cfg), M, N, K, x, weight, wp, ldw, _ptr(bias), residual, y, _ptr(workspace),
+                 workspace.numel(), x.dtype, y.dtype, stream)
 
 
-def _linear_call(cfg, M, N, K, x, wp, ldw, bp, residual, y, ws, ws_bytes, in_dtype, out_dtype, stream) -> None:
+def _linear_call(cfg, M, N, K, x, weight, wp, ldw, bp, residual, y, ws, ws_bytes, in_dtype, out_dtype, stream) -> None:
     xp, ldx = _rows(x, (M, K), in_dtype, "x")
     rp, ldr = (None, 0) if residual is None else _rows(residual, (M, N), out_dtype, "residual")
     yp, ldy = _rows(y, (M, N), out_dtype, "y")
+    _together(x.device, weight, residual, y)
     with _on(x.device):
         status = lib().moe_linear(cfg, M, xp, ldx, wp, ldw, bp, rp, ldr, yp, ldy, ws, ws_bytes,
                                   _stream_of(x.device, stream))
     if status != 0:
         raise MoEError(status, "moe_linear")
+
+
+def _together(device: torch.device, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors passed to the MoE library must be on one GPU, got {device} and {t.device}")
 
 
 class _Here:
@@ -423,7 +433,7 @@ class Linear:
         y = out if out is not None else self.y if M == self.max_rows else self.y[:M]
         self._cfg.activation = ACTIVATIONS[self.activation]
         wp, ldw = _rows(self.weight, (self.N, self.K), self.weight.dtype, "weight")
-        _linear_call(ctypes.byref(self._cfg), M, self.N, self.K, x, wp, ldw,
+        _linear_call(ctypes.byref(self._cfg), M, self.N, self.K, x, self.weight, wp, ldw,
                      None if self.bias is None else _ptr(self.bias), residual, y, self.workspace.data_ptr(),
                      self.workspace.numel(), self.weight.dtype, self.out_dtype, stream)
         return y
@@ -516,5 +526,5 @@ class MoELayer:
         _expect(self.w_router, (self.cfg.n_routed_experts, self.cfg.hidden_size), self.cfg.act_torch_dtype, "w_router")
         _expect(self.w_shared_gate, (self.cfg.hidden_size,), self.cfg.act_torch_dtype, "w_shared_gate")
         weights = (_ptr(self.w_router), _ptr(self.w_shared_gate), ctypes.byref(self.weights))
-        _layer_few_call(ctypes.byref(self.cfg.c()), self.cfg, x, logit_bias, weights, call[2], stream)
+        _layer_few_call(ctypes.byref(self.cfg.c()), self.cfg, x, logit_bias, weights, call[2], self.w_router, stream)
         return call[1]

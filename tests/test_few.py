@@ -1,11 +1,9 @@
 """moe_layer_few: the whole layer for a few tokens, against the float64 oracle.
 
 Tolerances.  Routing weights: the harness's W_TOL.  y, relative L2 over the call and
-per token: h is kept to 16 significant bits (each bf16 plane is off by at most half a
-step, 2^-9 of h and then 2^-9 of the remainder: 2^-18), the float32 sums are short
-(at most 7168 / 128 / 8 blocks per wave and the 8 waves' partial sums, each step
-2^-24) and expf is good to 2^-22, so the errors, independent from element to element,
-stay below 2^-17 of y; 2^-16 is asserted.  F32 layers: float32 sums only, 1e-5."""
+per token: products are exact, the float32 sums are short (at most some hundred steps of
+2^-24, whose errors are independent) and expf is good to 2^-22, so the errors stay well
+below 2^-17 of y; 2^-16 is asserted.  F32 layers: float32 sums only, 1e-5."""
 import ctypes
 
 import numpy as np
