@@ -166,6 +166,41 @@ def test_layer(shape, T):
         assert layer.route_stats.tolist() == [n, n, 0, 0]
 
 
+# More work per workgroup: gate/up items of several tiles (touched experts x I / 8 at
+# least 8192) and down ranges of falling length (tiles x blocks at least 32768).
+MANY = [
+    (W.LayerShape("many_f32", 96, 512, 520, 16, 24, "f32", "f32"), 16),
+    (W.LayerShape("many_bf16", 384, 512, 512, 16, 128, "bf16", "bf16"), 16),
+    (W.LayerShape("many_fp8", 384, 512, 512, 16, 128, W.DT_FP8, "bf16"), 15),
+    (W.LayerShape("many_mx", 512, 512, 512, 16, 256, W.DT_MXFP4, "bf16"), 16),
+    (W.LayerShape("long_bf16", 1152, 256, 512, 16, 0, "bf16", "bf16"), 16),
+    (W.LayerShape("long_fp8", 2048, 256, 512, 16, 128, W.DT_FP8, "bf16"), 16),
+    (W.LayerShape("long_mx", 2560, 256, 1024, 16, 0, W.DT_MXFP4, "bf16"), 13),
+    (W.LayerShape("many_budget", 256, 512, 128, 16, 128, "bf16", "bf16", expert_budget=100), 16),
+    (W.LayerShape("many_budget_top_p", 256, 512, 256, 12, 0, W.DT_MXFP4, "bf16", expert_budget=40, top_p=0.8), 16),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape,T", [pytest.param(s, t, id=f"{s.name}-{t}") for s, t in MANY])
+def test_long_lines_of_work(shape, T):
+    print(f"\n[case] few {shape.name} T={T}", flush=True)
+    case = Hn.make_case(shape, T, 91)
+    layer = _layer(case, stats=True)
+    x, b = case.inp.x.cuda(), _bias(case)
+    layer(x, b)
+    y = layer.y.clone()
+    torch.cuda.synchronize()
+    ora = _oracle(case)
+    _check(case, layer, ora)
+    if shape.expert_budget:
+        assert np.array_equal(layer.route_stats.cpu().numpy(), ora["stats"])
+    for _ in range(3):                                   # whoever arrives last: the same bits
+        layer(x, b)
+        torch.cuda.synchronize()
+        assert torch.equal(layer.y, y)
+
+
 @pytest.mark.gpu
 def test_agrees_with_the_three_calls():
     case = Hn.make_case(W.DRAFTER, 7, 5)
