@@ -167,7 +167,7 @@ def test_layer(shape, T):
 
 
 # More work per workgroup: gate/up items of several tiles (touched experts x I / 8 at
-# least 8192) and down ranges of falling length (tiles x blocks at least 32768).
+# least 2048) and down ranges of falling length (tiles x blocks at least 32768).
 MANY = [
     (W.LayerShape("many_f32", 96, 512, 520, 16, 24, "f32", "f32"), 16),
     (W.LayerShape("many_bf16", 384, 512, 512, 16, 128, "bf16", "bf16"), 16),
