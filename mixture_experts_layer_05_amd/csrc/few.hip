@@ -106,6 +106,7 @@ struct FewBatch {
   static constexpr int kGateUp = FMT == kDtypeMxfp4 ? 4 : FMT == kDtypeFp8 ? 6 : 10;
   static constexpr int kGateUpWide = FMT == kDtypeMxfp4 ? 2 : FMT == kDtypeFp8 ? 4 : 5;
   static constexpr int kDown = FMT == kDtypeMxfp4 || FMT == kDtypeFp8 ? 1 : 4;
+  static constexpr int kDownScales = FMT == kDtypeMxfp4 ? 2 : 4;   // blocks whose scales are loaded together
   static constexpr int kSets = FMT == kDtypeF32 ? 1 : FMT == kDtypeBf16 ? 2 : 4;
 };
 // 512 experts, top-10, I 512, H 5120, 9 tokens: 143 us with 16 tiles for each workgroup,
@@ -127,24 +128,53 @@ template <int FMT, int NS, class First>
 __device__ __forceinline__ void wave_tiles(const Matrices& m, const WRow (&row)[NS], const void* x, uint32_t xoff,
                                            bool live, int b0, int b1, int kdim, bool vec, int wave, int lane,
                                            f32x4 (&acc)[NS], First first) {
+  constexpr int D = NS == 1 ? FewBatch<FMT>::kGateUp : FewBatch<FMT>::kGateUpWide;
   const int n = b1 - b0;
   const int lo = b0 + wave * n / kFewWaves, hi = b0 + (wave + 1) * n / kFewWaves;
 #pragma unroll
   for (int j = 0; j < NS; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  int at = lo;
-  batches<NS == 1 ? FewBatch<FMT>::kGateUp : FewBatch<FMT>::kGateUpWide, GuBlk<FMT, NS>>(
-      hi - lo,
-      [&](GuBlk<FMT, NS>& k) __attribute__((always_inline)) {
+  if constexpr (!Scales<FMT, 1>::kAny) {
+    int at = lo;
+    batches<D, GuBlk<FMT, NS>>(
+        hi - lo,
+        [&](GuBlk<FMT, NS>& k) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < NS; ++j) load_w<FMT>(k.w[j], m, row[j], at, lane, kdim, vec);
-        load_x<FMT>(k.x[0], x, xoff, at, lane, kdim, vec, live);
-        ++at;
-      },
-      [&](GuBlk<FMT, NS>& k) __attribute__((always_inline)) {
+          for (int j = 0; j < NS; ++j) load_w<FMT>(k.w[j], m, row[j], at, lane, kdim, vec);
+          load_x<FMT>(k.x[0], x, xoff, at, lane, kdim, vec, live);
+          ++at;
+        },
+        [&](GuBlk<FMT, NS>& k) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < NS; ++j) acc[j] = mma_planes<FMT, 1>(k.x, k.w[j], lane, acc[j]);
-      },
-      first);
+          for (int j = 0; j < NS; ++j) acc[j] = mma_planes<FMT, 1>(k.x, k.w[j], lane, acc[j]);
+        },
+        first);
+  } else {
+    const int blocks = kdim / SkinnyFmt<FMT>::kBlk;      // of a row
+    for (int c = lo; c < hi; c += D) {
+      GuBlk<FMT, NS> k[D];
+      Scales<FMT, D> sc[NS];
+#pragma unroll
+      for (int j = 0; j < NS; ++j) sc[j].load(row[j].s + blk_scale_bytes<FMT>() * c, blocks - c);
+#pragma unroll
+      for (int s = 0; s < D; ++s)
+        if (c + s < hi) {
+#pragma unroll
+          for (int j = 0; j < NS; ++j) load_w<FMT>(k[s].w[j], m, row[j], c + s, lane, kdim, vec);
+          load_x<FMT>(k[s].x[0], x, xoff, c + s, lane, kdim, vec, live);
+        }
+      if (c == lo) first();
+#pragma unroll
+      for (int s = 0; s < D; ++s)
+        if (c + s < hi) {
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            k[s].w[j].s = sc[j].block(s);
+            acc[j] = mma_planes<FMT, 1>(k[s].x, k[s].w[j], lane, acc[j]);
+          }
+        }
+    }
+    if (hi <= lo) first();
+  }
 }
 
 // A gate/up tile: the first 8 rows lie in the gate matrix of an expert, the others in
@@ -855,7 +885,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_second_kernel(FewArgs a) {
       f32x4 acc[NS];
 #pragma unroll
       for (int j = 0; j < NS; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-      constexpr int D = FewBatch<FMT>::kDown;
+      constexpr int D = FewBatch<FMT>::kDown, DS = FewBatch<FMT>::kDownScales;
+      Scales<FMT, DS> sc[NS];        // of the coming blocks, `scales` of them
+      int scales = 0;
       for (int c = lo; c < hi; c += D) {
         DownBlk<FMT> k[D];
 #pragma unroll
@@ -865,6 +897,16 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_second_kernel(FewArgs a) {
 #pragma unroll
             for (int j = 0; j < NS; ++j)
               load_w<FMT>(k[d].w[j], m, row[j], lw.kb, lane, (shared ? a.S : a.I), (shared ? a.svec : a.ivec));
+            if constexpr (Scales<FMT, 1>::kAny) {
+              static_assert(D == 1, "one block's scales at a time");
+              if (scales == 0) {
+                const int left = (shared ? sb : ib) - lw.kb;
+                scales = min(left, DS);
+#pragma unroll
+                for (int j = 0; j < NS; ++j) sc[j].load(row[j].s + blk_scale_bytes<FMT>() * lw.kb, left);
+              }
+              --scales;
+            }
             if (step(lw) && c + d + 1 < hi) enter_w();
           }
         // The weights do not depend on h: the first ones are on their way during the wait.
@@ -886,6 +928,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_second_kernel(FewArgs a) {
             const float ws[4] = {wt.x, wt.y, wt.z, wt.w};
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
+              k[d].w[j].s = sc[j].block(0);
+              sc[j].step();
               const f32x4 t = mma_planes<FMT, DownBlk<FMT>::kPlanes>(k[d].h, k[d].w[j], lane, f32x4{0.f, 0.f, 0.f, 0.f});
               // A token that the expert does not serve takes nothing, not 0 * inf either.
 #pragma unroll
