@@ -208,7 +208,9 @@ __device__ __forceinline__ uint4 ld_piece(const void* row, int k, int kdim) {
 // A workgroup of eight waves computes 8 SETS columns over one part of the contraction,
 // an eighth for each wave.  Short batches and many waves (three workgroups on a CU with
 // 8 columns, two with 16): four waves with batches three times as long took twice the
-// time on 1 x 5120 x 5120.  With 8 columns the weights of a block are one register,
+// time on 1 x 5120 x 5120, which now takes 13.6 us (52 MB: 3.9 TB/s; bound by the start
+// and the drain of one short grid); 7 x 5120 x 17408 takes 40.6 (178 MB: 4.4 TB/s, the
+// memory).  With 8 columns the weights of a block are one register,
 // and the two halves of the block are multiplied apart (each over all 16 columns of
 // the MFMA, of which 8 are its own).
 constexpr int kSkinnyWaves = 8;
@@ -320,6 +322,10 @@ __global__ void __launch_bounds__(kSkinnyWaves * kWave, SETS == 1 ? 6 : 4) linea
 // two stages ahead, which takes any alignment and fills the row ends with zeros.  Rows
 // are stored unpadded with their 16-byte pieces permuted by (row / 2) mod 8, so that a
 // fragment read touches each bank group once per 16 rows.
+// Bound by the bytes that a CU takes in, about 28 KB in a microsecond: 1001 x 1537 x 2049
+// bf16 with odd row strides 27 us and 9 for its parts' sum, 333 x 1023 x 515 f32 16 and 4.
+// The results leave through LDS as row segments with four residual loads in flight; with
+// one element at a time 715 x 64 x 15104 took 72 us instead of 28.
 // Tiles that share rows of W are neighbours on one XCD (workgroup b runs on XCD b % 8).
 __device__ __forceinline__ int xcd_tile(int b, int total) {
   const int per = (total + 7) / 8;
@@ -457,6 +463,10 @@ __global__ void __launch_bounds__(256, 2) linear_tile_kernel(LinearArgs a, int p
 // which keeps two stages of the HBM stream in flight within the LDS.  Tiles are walked
 // in bands of 8 row blocks, so that the 32 tiles that run on an XCD at a time share 8
 // row blocks and 4 column blocks in its L2.
+// 8192 x 7168 x 4096: 418 us, 1.15 PFLOP/s (the library's product alone 371 us), bound by
+// the matrix cores; 224 x 5120 x 5120 in 240 items of 6 parts: 20 us, bound by the bytes
+// that a CU takes in (36 KB in a microsecond), and 7 for its parts' sum (the library's
+// product alone 47).
 constexpr int kWideRows = 256, kWideThreads = 512;
 constexpr int kWideRow = 128;
 constexpr int kWideBand = 8;
