@@ -415,6 +415,7 @@ class Linear:
             raise ValueError(f"activation: expected one of {sorted(ACTIVATIONS)}, got {activation!r}")
         self.weight, self.bias, self.activation, self.max_rows = weight, bias, activation, max_rows
         self.N, self.K = weight.shape
+        self.in_dtype = weight.dtype
         in_dtype = "f32" if _dtype_code(weight, "weight") == DTYPES["f32"] else "bf16"
         _expect(bias, (self.N,), weight.dtype, "bias")
         self.out_dtype = _TORCH_DTYPES[out_dtype or in_dtype]
@@ -432,10 +433,12 @@ class Linear:
         M = x.shape[0]
         y = out if out is not None else self.y if M == self.max_rows else self.y[:M]
         self._cfg.activation = ACTIVATIONS[self.activation]
-        wp, ldw = _rows(self.weight, (self.N, self.K), self.weight.dtype, "weight")
-        _linear_call(ctypes.byref(self._cfg), M, self.N, self.K, x, self.weight, wp, ldw,
-                     None if self.bias is None else _ptr(self.bias), residual, y, self.workspace.data_ptr(),
-                     self.workspace.numel(), self.weight.dtype, self.out_dtype, stream)
+        wp, ldw = _rows(self.weight, (self.N, self.K), self.in_dtype, "weight")
+        if self.bias is not None:
+            _expect(self.bias, (self.N,), self.in_dtype, "bias")
+            _together(x.device, self.bias)
+        _linear_call(ctypes.byref(self._cfg), M, self.N, self.K, x, self.weight, wp, ldw, _ptr(self.bias), residual, y,
+                     self.workspace.data_ptr(), self.workspace.numel(), self.in_dtype, self.out_dtype, stream)
         return y
 
 

@@ -259,3 +259,25 @@ def test_projection_class_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(p.y[:20], eager)
+
+
+@pytest.mark.gpu
+def test_replaced_parameters_are_checked():
+    w, x = torch.zeros(16, 8).cuda(), torch.ones(2, 8).cuda()
+    p = moe.Linear(w, torch.zeros(16).cuda(), max_rows=2)
+    p(x)
+    p.bias = torch.zeros(8).cuda()
+    with pytest.raises(ValueError, match="bias"):
+        p(x)
+    p.bias = None
+    p.weight = w.bfloat16()
+    with pytest.raises(ValueError, match="weight"):
+        p(x)
+    p.weight = w
+    with pytest.raises(ValueError, match="GPU"):
+        p(x, residual=torch.zeros(2, 16))
+    p.bias = torch.zeros(16)
+    with pytest.raises(ValueError, match="GPU"):
+        p(x)
+    p.bias = torch.full((16,), 3.0).cuda()
+    assert (p(x) == 3).all()
