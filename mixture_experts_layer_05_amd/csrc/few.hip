@@ -37,8 +37,8 @@
 // What bounds it, measured (wall time of a call; a large copy moves 5.0 TB/s here):
 //   256 experts, top-8, I 2048, H 7168, fp8, 16 tokens on 64 experts   2911 MB  557 us  5.2 TB/s
 //   512 experts, top-10, I 512, S 2048, H 5120, bf16, 7 tokens         1108 MB  239 us  4.6 TB/s
-//   the same in MXFP4, 16 tokens, top-p 0.9                             545 MB  168 us  3.2 TB/s
-//   16 experts, top-2, I 1024, S 2048, H 5120, bf16, 7 tokens           260 MB   80 us  3.3 TB/s
+//   the same in MXFP4, 16 tokens, top-p 0.9                             545 MB  163 us  3.3 TB/s
+//   16 experts, top-2, I 1024, S 2048, H 5120, bf16, 7 tokens           260 MB   78 us  3.3 TB/s
 //   the same, 1 token                                                   126 MB   49 us  2.6 TB/s
 // The large calls are bound by the memory.  In the smallest the memory stands idle
 // between the steps: with 1 token the router takes 6 us, the routing 4, the gate/up

@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(256, 2) linear_tile_kernel(LinearArgs a, int p
 // which keeps two stages of the HBM stream in flight within the LDS.  Tiles are walked
 // in bands of 8 row blocks, so that the 32 tiles that run on an XCD at a time share 8
 // row blocks and 4 column blocks in its L2.
-// 8192 x 7168 x 4096: 418 us, 1.15 PFLOP/s (the library's product alone 371 us), bound by
+// 8192 x 7168 x 4096: 418 to 429 us, 1.12 to 1.15 PFLOP/s (the library's product alone 371 us), bound by
 // the matrix cores; 224 x 5120 x 5120 in 240 items of 6 parts: 20 us, bound by the bytes
 // that a CU takes in (36 KB in a microsecond), and 7 for its parts' sum (the library's
 // product alone 47).
