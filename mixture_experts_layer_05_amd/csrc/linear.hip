@@ -738,13 +738,20 @@ LinearPlan linear_plan(const moe_linear_config& c, int64_t M, bool wide) {
     const int64_t tiles = ceil_div(M, t.rows) * ceil_div(N, t.cols);
     const int64_t slots = static_cast<int64_t>(t.on_cu) * kCus;
     for (int parts = 1; parts <= kMaxParts; ++parts) {
-      if (parts > 1 && (tiles * parts > slots || stages / parts < 4 || (t.cols == 256))) break;
+      // f32 tiles are bound by the matrix cores, so a CU may also take a few parts in turn:
+      // 1529 x 4224 x 1920 took 307 us in 180 tiles of 128 x 128 (76 CUs idle), 239 in 720
+      // half tiles of 64 x 128 (the library's product with the epilogue apart: 205).
+      const int64_t most = f32 ? int64_t{2} * slots : slots;
+      if (parts > 1 && (tiles * parts > most || parts * M * part_stride(N) * 4 > static_cast<int64_t>(kMaxPartBytes) ||
+                        stages / parts < 4 || t.cols == 256))
+        break;
       const int64_t items = tiles * parts, rounds = ceil_div(items, slots);
       const double shared = items > kCus ? t.on_cu : 1;             // tiles that share a CU
       const double deep = static_cast<double>(ceil_div(stages, parts));
       const double load = (t.rows + t.cols) * 0.128 * deep / (t.rows == kWideRows ? 36 : shared > 1 ? 28 : 20);
       const double mult = f32 ? t.rows * t.cols * 64 * deep / 0.5e6 : 0;
-      const double us = rounds * shared * std::max(load, mult) + 2 + 0.5 * rounds +
+      const double in_turn = f32 ? static_cast<double>(ceil_div(items, kCus)) : rounds * shared;
+      const double us = in_turn * std::max(load, mult) + 2 + 0.5 * rounds +
                         (parts > 1 ? 4 + parts * static_cast<double>(M) * N * 8 / 5e6 : 0);
       if (p.tiles == 0 || us < best) {
         best = us;

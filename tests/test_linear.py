@@ -176,6 +176,14 @@ def test_largest(M, K, N):
     _run(M, K, N, "bf16", "bf16", "none", True, True, seed=6, rows=rows)
 
 
+# More parts of tiles than run at a time.
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K,N,pads", [(1529, 2048, 1920, (0, 0, 0, 0)), (1300, 2501, 2051, (1, 3, 5, 7))])
+def test_large_f32(M, K, N, pads):
+    rows = torch.cat([torch.arange(0, 140), torch.arange(M - 140, M)])
+    _run(M, K, N, "f32", "f32", "silu", True, True, seed=12, pads=pads, rows=rows)
+
+
 # 256 x 256 tiles, cut at both edges; rows of x and W further apart than they are long, y and
 # the residual aligned to four elements or not.
 @pytest.mark.gpu
