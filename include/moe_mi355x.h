@@ -152,7 +152,9 @@ int moe_workspace_size(const moe_config* cfg, int32_t max_tokens, size_t* bytes)
  * runs before the budget]; then, if expert_budget > 0 and
  * the batch uses more than B distinct experts, keep the B experts with the
  * largest summed weight (ties: lower id), drop the other slots and renormalise
- * each token's kept weights [colibri issue_budget.md, "How it works" steps 1-5].
+ * each token's kept weights [colibri issue_budget.md, "How it works" steps 1-5];
+ * a token whose kept weights are all 0 in float32 (masked experts, below) keeps them
+ * as they are.
  *   x            (device) [T, H] act_dtype
  *   w_router     (device) [E, H] act_dtype
  *   w_shared_gate(device) [H] act_dtype; required iff S > 0, else ignored

@@ -558,7 +558,7 @@ __device__ __forceinline__ void finish_routing(const FewArgs& a, Routing& R, Rou
           if (keep) {
             const int at = __popcll(kept & ((1ull << lane) - 1));
             ir[at] = id;
-            wr[at] = a.norm ? w / sum : w;
+            wr[at] = a.norm && sum != 0.f ? w / sum : w;   // only weights of 0: they stay
           }
           if (lane == 0) atomicAdd(&C.dropped, __popcll(dropped));
         }

@@ -219,7 +219,8 @@ __global__ void __launch_bounds__(256) topk_kernel(
 //     few microseconds in each, instead of a third launch); then one thread per
 //     token compacts its kept slots to the front in
 //     their original order, -1 / 0 into the tail, and renormalises the kept
-//     weights if norm_topk (not when none is left) [steps 4-5].  Workgroup 0
+//     weights if norm_topk (not when none is left, or only weights of 0: masked
+//     experts that other tokens keep in the budget) [steps 4-5].  Workgroup 0
 //     writes statistics 0-1; dropped slots and emptied tokens go into statistics
 //     2-3 by integer atomics (zeroed by the first pass).
 // With B = 0 or union <= B the routing is left as it is and only the statistics
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(kBudgetChunk) budget_apply_kernel(
         if (e >= 0 && e < E && keep[e]) {
           const float v = wr[k];
           ir[j] = e;
-          wr[j] = norm_topk ? v / sum : v;
+          wr[j] = norm_topk && sum != 0.f ? v / sum : v;
           ++j;
         }
       }

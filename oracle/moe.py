@@ -227,7 +227,7 @@ def expert_budget(ids: np.ndarray, w: np.ndarray, budget: int, norm_topk: bool =
         w[t, :] = 0.0
         for k, (e, v) in enumerate(kept):
             ids[t, k] = e
-            w[t, k] = v / total if norm_topk else v
+            w[t, k] = v / total if norm_topk and total != 0 else v   # weights of 0 alone stay 0
     # Step 5 (compacting the union) is implicit: the union is now the kept set.
     return ids, w, np.array([nu, budget, dropped, empty], dtype=np.int64)
 
