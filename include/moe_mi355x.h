@@ -283,8 +283,8 @@ int moe_forward_noalloc(const moe_config* cfg, int32_t num_tokens, const void* x
  * A slot of weight 0 is not computed.  x, w_router, w_shared_gate and the weights
  * must be 16-byte aligned (with F32 weights 4-byte), scales, y, y_act and the other
  * outputs to their element size, the workspace to 16 bytes (MOE_ERR_UNSUPPORTED
- * otherwise, and for more than MOE_FEW_TOKENS tokens or for an expert matrix, a router
- * or intermediate activations of 4 GiB or more).  The workspace is not that
+ * otherwise, and for more than MOE_FEW_TOKENS tokens or for x, an expert matrix, a
+ * router or intermediate activations of 4 GiB or more).  The workspace is not that
  * of moe_workspace_size; moe_layer_few_workspace_size gives its bytes for any
  * T <= max_tokens <= MOE_FEW_TOKENS.  It needs no initial contents; calls that
  * overlap in time (other streams, graphs replayed side by side) need one each. */

@@ -1049,14 +1049,14 @@ FewLayout few_layout(const moe_config& c, int64_t T) {
 }
 
 // The second kernel numbers its gate/up tiles and its down blocks in 32 bits; offsets
-// within one expert's matrix and within a plane of h are 32-bit byte offsets.
-bool few_countable(const moe_config& c) {
+// within x, one expert's matrix and a plane of h are 32-bit byte offsets.
+bool few_countable(const moe_config& c, int64_t T) {
   const int64_t experts = std::min<int64_t>(c.n_routed_experts, kFewSlots);
   const int64_t H = c.hidden_size, I = c.moe_intermediate_size, S = c.shared_expert_intermediate_size;
   const int64_t nblk = experts * ceil_div(I, 32) + ceil_div(S, 32), lim = int64_t{1} << 31;
   const int64_t size = c.weight_dtype == MOE_DTYPE_F32 ? 4 : 2;
-  return (experts * ceil_div(I, 8) + ceil_div(S, 8)) * kQueues < lim && ceil_div(H, 16) * nblk < lim && H * I * size < 2 * lim &&
-         H * S * size < 2 * lim && H * c.n_routed_experts * size < 2 * lim &&
+  return (experts * ceil_div(I, 8) + ceil_div(S, 8)) * kQueues < lim && ceil_div(H, 16) * nblk < lim && T * H * size < 2 * lim &&
+         H * I * size < 2 * lim && H * S * size < 2 * lim && H * c.n_routed_experts * size < 2 * lim &&
          (kFewSlots * I + kFewTokens * S) * size < 2 * lim;
 }
 
@@ -1082,7 +1082,7 @@ int moe_layer_few_workspace_size(const moe_config* cfg, int32_t max_tokens, size
   size_t n = 0;
   const int st = moe_workspace_size(cfg, max_tokens, bytes ? &n : nullptr);   // the layer's checks
   if (st) return st;
-  if (max_tokens > kFewTokens || !few_countable(*cfg)) return MOE_ERR_UNSUPPORTED;
+  if (max_tokens > kFewTokens || !few_countable(*cfg, max_tokens)) return MOE_ERR_UNSUPPORTED;
   *bytes = few_layout(*cfg, max_tokens).total;
   return MOE_OK;
 }
