@@ -273,7 +273,8 @@ int moe_forward_noalloc(const moe_config* cfg, int32_t num_tokens, const void* x
  * option of cfg included, with one difference: with FP8 and MXFP4 weights the
  * activations are not quantised (the weights are decoded, w = decode(q) * s) and with
  * BF16 weights h is not rounded to bf16, so y lies closer to the exact layer than
- * moe_forward's.  y is bit-reproducible.
+ * moe_forward's.  The decoded weights are bf16: an MXFP4 weight of 2^128 or more (scale
+ * codes 253 and 254 only) is infinite.  y is bit-reproducible.
  *   topk_ids     (device) out [T, K] int32 or NULL, as moe_route writes it
  *   topk_weights (device) out [T, K] float32 or NULL
  *   shared_gate  (device) out [T] float32 or NULL; ignored when S = 0

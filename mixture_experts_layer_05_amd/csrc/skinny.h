@@ -244,7 +244,8 @@ __device__ __forceinline__ f32x4 mma_planes(const XBlk<FMT> (&x)[N], WBlk<FMT> w
     }
     return acc;
   } else {
-    // 2^(e - 127) of the lane's E8M0 blocks, code g of either half.
+    // 2^(e - 127) of the lane's E8M0 blocks, code g of either half: the conversion takes a
+    // scale's exponent field, so 0.0f stands for 2^-127 and inf (code 255) gives NaN.
     float e8[2] = {0.f, 0.f};
     if constexpr (FMT == kDtypeMxfp4) {
       const int at = 8 * (lane >> 4);
