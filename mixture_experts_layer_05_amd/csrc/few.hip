@@ -47,6 +47,7 @@
 // them saved 1 us of that with one token and cost up to 15 % with sixteen; a ring of
 // loads in place of batches changed nothing, nor did longer batches in the down half.
 #include <algorithm>
+#include <cstddef>
 
 #include "moe_mi355x.h"
 #include "skinny.h"
@@ -347,8 +348,9 @@ struct Routing {
   int n;                           // touched experts
   int seg_expert[kFewSlots];
   int16_t seg_slot[kFewSlots + 1][kFewTokens];   // row of h of (segment, token), -1: not served
-  float seg_w[kFewSlots + 1][kFewTokens];        // its weight, 0 if not served
+  alignas(16) float seg_w[kFewSlots + 1][kFewTokens];   // its weight, 0 if not served
 };
+static_assert(offsetof(Routing, seg_w) % 16 == 0 && alignof(Routing) >= 16, "seg_w is read four floats at a time");
 struct RouteScratch {
   unsigned long long agg[kMaxExperts];
   int seg_of[kMaxExperts];
