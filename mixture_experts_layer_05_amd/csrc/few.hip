@@ -84,7 +84,7 @@ struct FewArgs {
   void* h[3];              // planes of [T*K, I] routed then [T, S] shared rows
   int* routed;             // published routing: ids and weights [T, K], shared gates [T]
   float* part;             // [2 * kMaxRanges, sets, 256] partial down tiles
-  int T, H, E, I, K, S, ncols, ldz, parts, norm, budget;
+  int T, H, E, I, K, S, ldz, parts, norm, budget;
   float top_p;
   int hvec, ivec, svec;   // f32: rows of that length can be read in 16-byte pieces
 };
@@ -1156,7 +1156,6 @@ int moe_layer_few(const moe_config* cfg, int32_t T, const void* x, const void* w
   a.I = cfg->moe_intermediate_size;
   a.K = cfg->num_experts_per_tok;
   a.S = cfg->shared_expert_intermediate_size;
-  a.ncols = a.E + (shared ? 1 : 0);
   a.ldz = L.ldz;
   a.parts = L.parts;
   a.norm = cfg->norm_topk_prob;

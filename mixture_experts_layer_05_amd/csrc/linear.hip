@@ -590,6 +590,7 @@ __global__ void __launch_bounds__(kWideThreads) linear_wide_kernel(LinearArgs a,
     // whole row segments, four columns to a lane.  NI rounds of 32 rows of each wave row;
     // rows padded by 8 floats.
     constexpr int kStride = BN + 8;
+    static_assert(32 * WM * kStride * 4 <= 2 * kStage, "a round fits the stage buffers");
     float* stg = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
