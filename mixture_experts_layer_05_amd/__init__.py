@@ -53,6 +53,7 @@ class _Weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "w_gate", "w_up", "w_down", "s_gate", "s_up", "s_down",
         "ws_gate", "ws_up", "ws_down", "ss_gate", "ss_up", "ss_down")]
+    devices = frozenset()     # of the tensors behind the addresses (expert_weights_struct sets it)
 
 
 class _LinearConfig(ctypes.Structure):
@@ -202,6 +203,8 @@ def expert_weights_struct(cfg: MoEConfig, w: Dict[str, torch.Tensor],
     _expect(w["up"], (E, I, H // per), wdt, "w_up")
     _expect(w["down"], (E, H, I // per), wdt, "w_down")
     s = _Weights(_ptr(w["gate"]), _ptr(w["up"]), _ptr(w["down"]))
+    names = ("gate", "up", "down") + (("gate_s", "up_s", "down_s") if quant else ())
+    s.devices = frozenset(d[n].device for d in ((w, shared) if S > 0 and shared is not None else (w,)) for n in names)
     if quant:
         _expect(w["gate_s"], (E, I, H // sgroup), sdt, "s_gate")
         _expect(w["up_s"], (E, I, H // sgroup), sdt, "s_up")
@@ -288,26 +291,28 @@ def layer_few(cfg: MoEConfig, x, w_router, w_shared_gate, logit_bias, weights: _
     _expect(route_stats, (4,), torch.int32, "route_stats")
     _expect(y, (T, H), torch.float32, "y")
     _expect(y_act, (T, H), act, "y_act")
-    _together(x.device, w_router, w_shared_gate, topk_ids, topk_weights, shared_gate, route_stats, y, y_act)
-    _layer_few_call(ctypes.byref(cfg.c()), cfg, x, logit_bias,
-                    (_ptr(w_router), _ptr(w_shared_gate), ctypes.byref(weights)),
+    _together(x.device, topk_ids, topk_weights, shared_gate, route_stats, y, y_act, workspace)
+    _layer_few_call(ctypes.byref(cfg.c()), cfg, x, logit_bias, w_router, w_shared_gate, weights,
                     (_ptr(topk_ids), _ptr(topk_weights), _ptr(shared_gate), _ptr(route_stats), _ptr(y), _ptr(y_act),
-                     _ptr(workspace), workspace.numel()), workspace, stream)
+                     _ptr(workspace), workspace.numel()), stream)
 
 
-def _layer_few_call(c, cfg, x, logit_bias, weights, outputs, home, stream) -> None:
-    """moe_layer_few with the addresses of the weights and of the outputs; checks what a
-    caller brings to each call (home: a tensor of the layer's, for its device)."""
+def _layer_few_call(c, cfg, x, logit_bias, w_router, w_shared_gate, weights, outputs, stream) -> None:
+    """moe_layer_few with the addresses of the outputs and the workspace, whose device the
+    caller has compared with x's; the others' is compared here."""
     T = x.shape[0]
     _expect(x, (T, cfg.hidden_size), cfg.act_torch_dtype, "x")
     bp = None
     if logit_bias is not None:
         _expect(logit_bias, (T, cfg.n_routed_experts), torch.float32, "logit_bias")
         bp = _ptr(logit_bias)
-    xp, (wr, wg, w) = _ptr(x), weights
-    _together(x.device, logit_bias, home)
+    xp = _ptr(x)
+    _together(x.device, logit_bias, w_router, w_shared_gate)
+    for d in weights.devices:
+        _same_device(x.device, d)
     with _on(x.device):
-        status = lib().moe_layer_few(c, T, xp, wr, wg, bp, w, *outputs, _stream_of(x.device, stream))
+        status = lib().moe_layer_few(c, T, xp, _ptr(w_router), _ptr(w_shared_gate), bp, ctypes.byref(weights), *outputs,
+                                     _stream_of(x.device, stream))
     if status != 0:
         raise MoEError(status, "moe_layer_few")
 
@@ -349,19 +354,19 @@ def linear(x, weight, bias, residual, y, workspace, activation: str = "none", st
     cfg = _LinearConfig(K, N, _dtype_code(x, "x"), _dtype_code(y, "y"), ACTIVATIONS[activation])
     wp, ldw = _rows(weight, (N, K), x.dtype, "weight")
     _expect(bias, (N,), x.dtype, "bias")
-    _together(x.device, bias, workspace)
-    _linear_call(ctypes.byref(cfg), M, N, K, x, weight, wp, ldw, _ptr(bias), residual, y, _ptr(workspace),
-                 workspace.numel(), x.dtype, y.dtype, stream)
+    _together(x.device, bias)
+    _linear_call(ctypes.byref(cfg), M, N, K, x, weight, wp, ldw, _ptr(bias), residual, y, workspace, x.dtype, y.dtype,
+                 stream)
 
 
-def _linear_call(cfg, M, N, K, x, weight, wp, ldw, bp, residual, y, ws, ws_bytes, in_dtype, out_dtype, stream) -> None:
+def _linear_call(cfg, M, N, K, x, weight, wp, ldw, bp, residual, y, workspace, in_dtype, out_dtype, stream) -> None:
     xp, ldx = _rows(x, (M, K), in_dtype, "x")
     rp, ldr = (None, 0) if residual is None else _rows(residual, (M, N), out_dtype, "residual")
     yp, ldy = _rows(y, (M, N), out_dtype, "y")
-    _together(x.device, weight, residual, y)
+    _together(x.device, weight, residual, y, workspace)
     with _on(x.device):
-        status = lib().moe_linear(cfg, M, xp, ldx, wp, ldw, bp, rp, ldr, yp, ldy, ws, ws_bytes,
-                                  _stream_of(x.device, stream))
+        status = lib().moe_linear(cfg, M, xp, ldx, wp, ldw, bp, rp, ldr, yp, ldy, _ptr(workspace),
+                                  workspace.numel(), _stream_of(x.device, stream))
     if status != 0:
         raise MoEError(status, "moe_linear")
 
@@ -369,7 +374,12 @@ def _linear_call(cfg, M, N, K, x, weight, wp, ldw, bp, residual, y, ws, ws_bytes
 def _together(device: torch.device, *tensors) -> None:
     for t in tensors:
         if t is not None and t.device != device:
-            raise ValueError(f"tensors passed to the MoE library must be on one GPU, got {device} and {t.device}")
+            _same_device(device, t.device)
+
+
+def _same_device(device: torch.device, other: torch.device) -> None:
+    if other != device:
+        raise ValueError(f"tensors passed to the MoE library must be on one GPU, got {device} and {other}")
 
 
 class _Here:
@@ -392,6 +402,8 @@ def _stream_of(device: torch.device, stream) -> int:
     """The stream's handle, by default that of the device's current stream."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device.index)
+    if getattr(stream, "device", device) != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
     return _stream(stream)
 
 
@@ -438,7 +450,7 @@ class Linear:
             _expect(self.bias, (self.N,), self.in_dtype, "bias")
             _together(x.device, self.bias)
         _linear_call(ctypes.byref(self._cfg), M, self.N, self.K, x, self.weight, wp, ldw, _ptr(self.bias), residual, y,
-                     self.workspace.data_ptr(), self.workspace.numel(), self.in_dtype, self.out_dtype, stream)
+                     self.workspace, self.in_dtype, self.out_dtype, stream)
         return y
 
 
@@ -520,6 +532,7 @@ class MoELayer:
                    self.few_workspace)
         call = self._few_calls.get(T)
         if call is None or any(a is not b for a, b in zip(call[0], buffers)):
+            _together(self.few_workspace.device, *buffers)
             v = self.views(T)
             shared = v["shared_gate"] if self.cfg.shared_expert_intermediate_size > 0 else None
             call = self._few_calls[T] = (
@@ -528,6 +541,7 @@ class MoELayer:
                  _ptr(v["y_act"]), _ptr(self.few_workspace), self.few_workspace.numel()))
         _expect(self.w_router, (self.cfg.n_routed_experts, self.cfg.hidden_size), self.cfg.act_torch_dtype, "w_router")
         _expect(self.w_shared_gate, (self.cfg.hidden_size,), self.cfg.act_torch_dtype, "w_shared_gate")
-        weights = (_ptr(self.w_router), _ptr(self.w_shared_gate), ctypes.byref(self.weights))
-        _layer_few_call(ctypes.byref(self.cfg.c()), self.cfg, x, logit_bias, weights, call[2], self.w_router, stream)
+        _together(x.device, self.few_workspace)      # and with it the other buffers
+        _layer_few_call(ctypes.byref(self.cfg.c()), self.cfg, x, logit_bias, self.w_router, self.w_shared_gate,
+                        self.weights, call[2], stream)
         return call[1]
