@@ -35,15 +35,19 @@
 // error in y by far; the others cost L2 reads and MFMAs that are idle here.
 //
 // What bounds it, measured (wall time of a call; a large copy moves 5.0 TB/s here):
-//   256 experts, top-8, I 2048, H 7168, fp8, 16 tokens on 64 experts   2911 MB  557 us  5.2 TB/s
-//   512 experts, top-10, I 512, S 2048, H 5120, bf16, 7 tokens         1108 MB  239 us  4.6 TB/s
-//   the same in MXFP4, 16 tokens, top-p 0.9                             545 MB  163 us  3.3 TB/s
-//   16 experts, top-2, I 1024, S 2048, H 5120, bf16, 7 tokens           260 MB   78 us  3.3 TB/s
-//   the same, 1 token                                                   126 MB   49 us  2.6 TB/s
+//   256 experts, top-8, I 2048, H 7168, fp8, 16 tokens on 64 experts   2911 MB  553 to 568 us  5.2 TB/s
+//   512 experts, top-10, I 512, S 2048, H 5120, bf16, 7 tokens         1108 MB  241 us  4.6 TB/s
+//   the same in MXFP4, 16 tokens, top-p 0.9                             545 MB  163 to 168 us  3.3 TB/s
+//   16 experts, top-2, I 1024, S 2048, H 5120, bf16, 7 tokens           260 MB   77 to 85 us  3.1 to 3.4 TB/s
+//   the same, 1 token                                                   126 MB   50 us  2.5 TB/s
 // The large calls are bound by the memory.  In the smallest the memory stands idle
-// between the steps: with 1 token the router takes 6 us, the routing 4, the gate/up
-// half 20, the wait for the last h and the down weights 8 (which arrive meanwhile),
-// h's loads 6, the parts' sum 2.  Reading h past the caches instead of invalidating
+// between the steps: with 1 token the router takes 6 us (on 4 workgroups, while the
+// shared expert's weights wait), the routing 4, the gate/up half 20, the wait for the
+// last h and the down weights 8 (which arrive meanwhile), h's loads 6, the parts' sum 2.
+// In MXFP4 each decoded operand of the down half meets three planes of h: without the
+// second and third the call above takes 150 of 168 us, the fp8 one 535 of 568, the
+// bf16 one 232 of 241.  The rest above the memory's time is decoding, and pieces of 41 KB.
+// Reading h past the caches instead of invalidating
 // them saved 1 us of that with one token and cost up to 15 % with sixteen; a ring of
 // loads in place of batches changed nothing, nor did longer batches in the down half.
 #include <algorithm>
@@ -704,7 +708,9 @@ __device__ __forceinline__ int gate_up_half(const FewArgs& a, const Routing& R, 
   const int tid = threadIdx.x, home = blockIdx.x % kQueues;
   int tried = 0, finished = 0;
   // Workgroups 0 to 255 lie on different CUs.  If there is no more than one item for
-  // each CU the others come two microseconds later, so that no CU runs two.
+  // each CU the others come two microseconds later, so that no CU runs two: 24.4 us instead
+  // of 25.9 (8 experts, top-2, I 512, shared 512, H 2048, 1 token, bf16), 112.1 instead of
+  // 113.6 (512 experts, fp8, 5 tokens), elsewhere within 1 % of each other.
   if (items <= kFewGrid / 2 && blockIdx.x >= kFewGrid / 2) __builtin_amdgcn_s_sleep(64);
   if (tid == 0) s_next = take_item(queues, items, home, tried);
   __syncthreads();

@@ -209,8 +209,8 @@ __device__ __forceinline__ uint4 ld_piece(const void* row, int k, int kdim) {
 // an eighth for each wave.  Short batches and many waves (three workgroups on a CU with
 // 8 columns, two with 16): four waves with batches three times as long took twice the
 // time on 1 x 5120 x 5120, which now takes 13.6 us (52 MB: 3.9 TB/s; bound by the start
-// and the drain of one short grid); 7 x 5120 x 17408 takes 40.6 (178 MB: 4.4 TB/s, the
-// memory).  With 8 columns the weights of a block are one register,
+// and the drain of one short grid); 7 x 5120 x 17408 takes 40.6 (178 MB: 4.4 TB/s; the
+// loads of x are about 15 % of it, the rest is the memory's).  With 8 columns the weights of a block are one register,
 // and the two halves of the block are multiplied apart (each over all 16 columns of
 // the MFMA, of which 8 are its own).
 constexpr int kSkinnyWaves = 8;
@@ -323,7 +323,10 @@ __global__ void __launch_bounds__(kSkinnyWaves * kWave, SETS == 1 ? 6 : 4) linea
 // are stored unpadded with their 16-byte pieces permuted by (row / 2) mod 8, so that a
 // fragment read touches each bank group once per 16 rows.
 // Bound by the bytes that a CU takes in, about 28 KB in a microsecond: 1001 x 1537 x 2049
-// bf16 with odd row strides 27 us and 9 for its parts' sum, 333 x 1023 x 515 f32 16 and 4.
+// bf16 with odd row strides 27 us and 9 for its parts' sum.  Small products are bound by
+// the loads' latency before the first multiplication and by the results' way out:
+// 333 x 1023 x 515 f32 in 8 parts of 4 stages takes 17 us and 4 for the sum, a product
+// of one stage 15; on 16-byte boundaries, one load in place of four, 12 and 4.
 // The results leave through LDS as row segments with four residual loads in flight; with
 // one element at a time 715 x 64 x 15104 took 72 us instead of 28.
 // Tiles that share rows of W are neighbours on one XCD (workgroup b runs on XCD b % 8).
@@ -463,10 +466,11 @@ __global__ void __launch_bounds__(256, 2) linear_tile_kernel(LinearArgs a, int p
 // which keeps two stages of the HBM stream in flight within the LDS.  Tiles are walked
 // in bands of 8 row blocks, so that the 32 tiles that run on an XCD at a time share 8
 // row blocks and 4 column blocks in its L2.
-// 8192 x 7168 x 4096: 418 to 429 us, 1.12 to 1.15 PFLOP/s (the library's product alone 371 us), bound by
-// the matrix cores; 224 x 5120 x 5120 in 240 items of 6 parts: 20 us, bound by the bytes
-// that a CU takes in (36 KB in a microsecond), and 7 for its parts' sum (the library's
-// product alone 47).
+// 8192 x 7168 x 4096: 418 to 439 us in a row of calls, 1.10 to 1.15 PFLOP/s (the library's product
+// alone 371 us; under the profiler 442 to 553 us, the median 471), bound by the matrix
+// cores; 224 x 5120 x 5120 in 240 items of 6 parts: 20 to 24 us, bound by the bytes that a
+// CU takes in (36 KB in a microsecond), and 8 for its parts' sum (the library's product
+// alone 47).
 constexpr int kWideRows = 256, kWideThreads = 512;
 constexpr int kWideRow = 128;
 constexpr int kWideBand = 8;
@@ -710,13 +714,15 @@ struct LinearPlan {
 };
 constexpr int kCus = 256;
 constexpr int kMaxParts = 16;
-// Most bytes of partial sums: a plan with parts fills the GPU at most once, with two
-// 128 x 128 tiles or one 256 x 128 tile on each CU.
+// Most bytes of partial sums, which linear_plan keeps to: those of two 128 x 128 tiles or
+// one 256 x 128 tile on each CU.
 constexpr size_t kMaxPartBytes = size_t{2} * kCus * 128 * 128 * sizeof(float);
 
 // The cheapest plan by an estimate in microseconds.  A CU takes about 36 KB of operands
 // in a microsecond in the 256-row kernel and 28 KB in the other (measured; what limits
 // both in bf16), multiplies about 0.5 MFLOP f32, and partial sums cross at 5 TB/s twice.
+// That prices the second launch at about twice its time: 15 us for 224 x 5120 x 5120 in 6
+// parts and 14 for 1001 x 1537 x 2049 in 3, which take 8 and 9.
 LinearPlan linear_plan(const moe_linear_config& c, int64_t M, bool wide) {
   const int64_t N = c.out_features, K = c.in_features;
   const bool f32 = c.in_dtype == MOE_DTYPE_F32;
