@@ -37,7 +37,7 @@
 // What bounds it, measured (wall time of a call; a large copy moves 5.0 TB/s here):
 //   256 experts, top-8, I 2048, H 7168, fp8, 16 tokens on 64 experts   2911 MB  553 to 568 us  5.2 TB/s
 //   512 experts, top-10, I 512, S 2048, H 5120, bf16, 7 tokens         1108 MB  241 us  4.6 TB/s
-//   the same in MXFP4, 16 tokens, top-p 0.9                             545 MB  163 to 168 us  3.3 TB/s
+//   the same in MXFP4, 16 tokens, top-p 0.9                             545 MB  161 to 168 us  3.3 TB/s
 //   16 experts, top-2, I 1024, S 2048, H 5120, bf16, 7 tokens           260 MB   77 to 85 us  3.1 to 3.4 TB/s
 //   the same, 1 token                                                   126 MB   50 us  2.5 TB/s
 // The large calls are bound by the memory.  In the smallest the memory stands idle
