@@ -339,6 +339,52 @@ int moe_linear(const moe_linear_config* cfg, int32_t num_rows, const void* x, in
                int64_t ldw, const void* bias, const void* residual, int64_t ldr, void* y, int64_t ldy,
                void* workspace, size_t workspace_bytes, void* stream);
 
+typedef struct moe_ffn_config {
+  int32_t hidden_size;        /* H, 1..MOE_LINEAR_MAX_FEATURES                          */
+  int32_t intermediate_size;  /* I, 1..MOE_LINEAR_MAX_FEATURES / 4                      */
+  int32_t dtype;              /* moe_dtype of every tensor: F32 or BF16                 */
+  int32_t activation;         /* moe_activation of the gate                             */
+} moe_ffn_config;
+
+/* Dense gated feed-forward block (the drafter's dense layer, or a shared expert alone):
+ *   y[t] = w_down (act(w_gate x[t]) * (w_up x[t]))
+ * in two products: the first computes the gate and the up projection together and
+ * writes h = act(gate) * up, the second is the down projection.  Sums and activations
+ * are float32; h, a matrix operand, and y are rounded once to dtype.  y and the
+ * gradients are bit-reproducible for given sizes and alignments.
+ *   x, y           (device) [num_rows, H], rows ldx and ldy elements apart
+ *   w_gate, w_up   (device) [I, H];  w_down (device) [H, I]; the expert weights' layout
+ *   kept           (device) out, what the backward pass of the same rows needs (h, and
+ *                  act(gate) and up * act'(gate) in float32), or NULL to keep nothing;
+ *                  moe_ffn_kept_size bytes for any num_rows <= max_rows
+ * Strides are in elements, at least H (MOE_ERR_BAD_SHAPE otherwise) and at most 2^40.
+ * Tensors need only be aligned to their element size (rows of whole 16-byte pieces on
+ * 16-byte boundaries are the fast case), kept and the workspace to 16 bytes.
+ * num_rows = 0 returns MOE_OK; num_rows <= MOE_LINEAR_MAX_ROWS.  No output may overlap
+ * an input.  The workspace (moe_ffn_workspace_size bytes for any num_rows <= max_rows;
+ * `backward` != 0: for moe_ffn_backward) needs no initial contents; calls that overlap
+ * in time need one each. */
+int moe_ffn_workspace_size(const moe_ffn_config* cfg, int32_t max_rows, int32_t backward, size_t* bytes);
+int moe_ffn_kept_size(const moe_ffn_config* cfg, int32_t max_rows, size_t* bytes);
+int moe_ffn_forward(const moe_ffn_config* cfg, int32_t num_rows, const void* x, int64_t ldx, const void* w_gate,
+                    const void* w_up, const void* w_down, void* y, int64_t ldy, void* kept, size_t kept_bytes,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of moe_ffn_forward for a gradient dy of y, from the same x, weights and
+ * num_rows and what that call kept:
+ *   dh = dy w_down;  dgate = dh * up * act'(gate);  dup = dh * act(gate)
+ *   dx = dgate w_gate + dup w_up;  dw_gate = dgate^T x;  dw_up = dup^T x;
+ *   dw_down = dy^T h
+ * dgate and dup, matrix operands, and the results are rounded once to dtype.
+ *   dy, dx                   (device) [num_rows, H], rows lddy and lddx elements apart
+ *   dw_gate, dw_up, dw_down  (device) out, as the weights; overwritten
+ * dx, dw_down, and dw_gate together with dw_up, may be NULL and are then not computed.
+ * num_rows = 0 writes zero weight gradients and reads no other pointer. */
+int moe_ffn_backward(const moe_ffn_config* cfg, int32_t num_rows, const void* x, int64_t ldx, const void* w_gate,
+                     const void* w_up, const void* w_down, const void* kept, size_t kept_bytes, const void* dy,
+                     int64_t lddy, void* dx, int64_t lddx, void* dw_gate, void* dw_up, void* dw_down,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* moe_status_string(int status);
 

@@ -27,8 +27,8 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe_mi355x.h")
 DTYPES = {"f32": 0, "bf16": 1, "fp8_e4m3_g128": 2, "mxfp4": 3}
 ENTRY_POINTS = ("moe_workspace_size", "moe_route", "moe_dispatch", "moe_forward",
                 "moe_forward_gate_up", "moe_forward_down", "moe_forward_noalloc", "moe_layer_few",
-                "moe_layer_few_workspace_size", "moe_linear", "moe_linear_workspace_size", "moe_status_string",
-                "moe_version")
+                "moe_layer_few_workspace_size", "moe_linear", "moe_linear_workspace_size", "moe_ffn_workspace_size",
+                "moe_ffn_kept_size", "moe_ffn_forward", "moe_ffn_backward", "moe_status_string", "moe_version")
 # Most tokens of a moe_layer_few call, and moe_linear's activations, as the header states them.
 FEW_TOKENS = 16
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
@@ -86,10 +86,11 @@ def lib() -> ctypes.CDLL:
                                     vp, sz, vp]
         L.moe_linear_workspace_size.argtypes = [lincfgp, i32, ctypes.POINTER(sz)]
         L.moe_linear.argtypes = [lincfgp, i32, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, sz, vp]
-        for name in ("moe_workspace_size", "moe_route", "moe_dispatch", "moe_forward",
-                     "moe_forward_gate_up", "moe_forward_down", "moe_forward_noalloc", "moe_version",
-                     "moe_layer_few", "moe_layer_few_workspace_size", "moe_linear",
-                     "moe_linear_workspace_size"):
+        L.moe_ffn_workspace_size.argtypes = [vp, i32, i32, ctypes.POINTER(sz)]
+        L.moe_ffn_kept_size.argtypes = [vp, i32, ctypes.POINTER(sz)]
+        L.moe_ffn_forward.argtypes = [vp, i32, vp, i64, vp, vp, vp, vp, i64, vp, sz, vp, sz, vp]
+        L.moe_ffn_backward.argtypes = [vp, i32, vp, i64, vp, vp, vp, vp, sz, vp, i64, vp, i64, vp, vp, vp, vp, sz, vp]
+        for name in ENTRY_POINTS:
             getattr(L, name).restype = ctypes.c_int
         L.moe_status_string.argtypes = [ctypes.c_int]
         L.moe_status_string.restype = ctypes.c_char_p
@@ -552,3 +553,6 @@ class MoELayer:
         _layer_few_call(ctypes.byref(self.cfg.c()), self.cfg, x, logit_bias, self.w_router, self.w_shared_gate,
                         self.weights, call[2], stream)
         return call[1]
+
+
+from .dense import GatedFFN, ffn, ffn_backward, ffn_kept_size, ffn_workspace_size  # noqa: E402,F401

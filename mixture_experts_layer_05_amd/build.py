@@ -13,7 +13,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_mi355x.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "route.hip", "dispatch.hip", "experts.hip", "tile_gemm.hip", "stream_gemm.hip",
-           "few.hip", "linear.hip"]
+           "few.hip", "linear.hip", "ffn.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950",

@@ -1,0 +1,355 @@
+// The dense gated FFN, y = (act(x Wg^T) * (x Wu^T)) Wd^T, and its gradients.
+//
+// Forward: one product computes g = x Wg^T and u = x Wu^T side by side (their columns
+// take turns in blocks of 32, so that a lane holds both of an element) and its epilogue
+// writes h = act(g) u; the down projection is moe_linear's.  For a backward pass the
+// epilogue also keeps a = act(g) and b = u act'(g), in float32.
+//
+// Backward, from dy:
+//   dh = dy Wd,  du = dh a,  dg = dh b         one product, the two gradients its epilogue
+//   dx = dg Wg + du Wu                         one product over both halves of [dg du]
+//   dWg = dg^T x, dWu = du^T x                 one product of 2 I rows
+//   dWd = dy^T h
+// h, dg and du are matrix operands and have the weights' type: with bf16 weights each is
+// rounded once.  a and b stay in float32: one more rounding of either would add to dg's
+// and du's own (weight gradients off by 1.7 roundings instead of 1.4).
+#include "gemm.h"
+
+namespace moe {
+namespace {
+
+// ---------------------------------------------------------------- epilogues
+
+// act(v) and act'(v).
+template <bool QUICK>
+__device__ __forceinline__ void act_slope(float v, int act, float& f, float& d) {
+  const auto sigmoid = [](float u) {
+    if constexpr (QUICK) return __builtin_amdgcn_rcpf(1.0f + __expf(-u));
+    else return 1.0f / (1.0f + expf(-u));
+  };
+  switch (act) {
+    case MOE_ACT_RELU:
+      f = v < 0.0f ? 0.0f : v;                    // NaN stays NaN
+      d = v > 0.0f ? 1.0f : 0.0f;
+      break;
+    case MOE_ACT_GELU: {
+      const float c = 0.5f * (1.0f + erff(v * 0.70710678f));
+      f = v * c;
+      d = c + (fabsf(v) < 40.0f ? v * 0.39894228f * expf(-0.5f * v * v) : 0.0f);
+      break;
+    }
+    case MOE_ACT_GELU_TANH: {
+      const float s = sigmoid(1.59576912f * (v + 0.044715f * v * v * v)), t = s * (1.0f - s);
+      f = v * s;
+      // s (1 - s) is 0 far out, where v^2 may be infinite.
+      d = s + (t > 0.0f ? v * t * 1.59576912f * (1.0f + 0.134145f * v * v) : 0.0f);
+      break;
+    }
+    case MOE_ACT_SILU: {
+      const float s = sigmoid(v);
+      f = v * s;
+      d = s + f * (1.0f - s);
+      break;
+    }
+    default:
+      f = v;
+      d = 1.0f;
+      break;
+  }
+}
+
+// h = act(g) u, and a and b where they are kept; their rows lie `ld`, a multiple of four,
+// apart, so that a whole quad may be written at their ends.
+template <bool F32, bool KEEP>
+struct GatedOut {
+  static constexpr int kAhead = 2;
+  void* h;
+  float *a, *b;
+  int64_t ld;
+  int M, N, act;
+  template <int D>
+  __device__ __forceinline__ void quads(const int (&m)[D], int n, const f32x4 (&g)[D], const f32x4 (&u)[D]) const {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (m[d] >= M) continue;
+      float h4[4], a4[4], b4[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float f, df;
+        act_slope<!F32>(g[d][c], act, f, df);
+        const bool in = n + c < N;
+        a4[c] = in ? f : 0.0f;
+        h4[c] = in ? f * u[d][c] : 0.0f;
+        b4[c] = in ? u[d][c] * df : 0.0f;
+      }
+      const size_t o = static_cast<size_t>(m[d]) * ld + n;
+      store4<F32>(h, o, h4);
+      if constexpr (KEEP) {
+        store4<true>(a, o, a4);
+        store4<true>(b, o, b4);
+      }
+    }
+  }
+};
+
+// dg = dh b and du = dh a, side by side in rows of 2 ld.
+template <bool F32>
+struct SlopesOut {
+  static constexpr int kAhead = 4;
+  const float *a, *b;
+  void* d;
+  int64_t ld;
+  int M, N;
+  template <int D>
+  __device__ __forceinline__ void quads(const int (&m)[D], int n, const f32x4 (&s)[D], const f32x4 (&)[D]) const {
+    f32x4 va[D], vb[D];
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+      va[i] = vb[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (m[i] < M) {
+        va[i] = load4<true>(a, static_cast<size_t>(m[i]) * ld + n);
+        vb[i] = load4<true>(b, static_cast<size_t>(m[i]) * ld + n);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+      if (m[i] >= M) continue;
+      float g4[4], u4[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const bool in = n + c < N;
+        g4[c] = in ? s[i][c] * vb[i][c] : 0.0f;
+        u4[c] = in ? s[i][c] * va[i][c] : 0.0f;
+      }
+      const size_t o = static_cast<size_t>(m[i]) * 2 * ld + n;
+      store4<F32>(d, o, g4);
+      store4<F32>(d, o + ld, u4);
+      // Both halves are contracted to their rows' ends.
+      if (n + 4 >= N && n + 4 < ld) {
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+        store4<F32>(d, o + 4, zero);
+        store4<F32>(d, o + ld + 4, zero);
+      }
+    }
+  }
+};
+
+// The sums as they are; rows [0, half) of the product are y's, rows [half, 2 half) y2's,
+// of either the first `live`.
+template <bool F32>
+struct RowsOut {
+  static constexpr int kAhead = 4;
+  void *y, *y2;
+  int64_t ld;
+  int M, N, half, live;
+  template <int D>
+  __device__ __forceinline__ void quads(const int (&m)[D], int n, const f32x4 (&s)[D], const f32x4 (&)[D]) const {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int r = m[d] < half ? m[d] : m[d] - half;
+      if (m[d] >= M || r >= live) continue;
+      void* out = m[d] < half ? y : y2;
+      const size_t o = static_cast<size_t>(r) * ld + n;
+      float v[4] = {s[d][0], s[d][1], s[d][2], s[d][3]};
+      if (n + 4 <= N) {
+        store4<F32>(out, o, v);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (n + c < N) {
+            if constexpr (F32) static_cast<float*>(out)[o + c] = v[c];
+            else static_cast<uint16_t*>(out)[o + c] = f32_to_bf16_bits(v[c]);
+          }
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------- zeros
+
+// n bytes of zeros (a weight's gradient from no rows).
+__global__ void __launch_bounds__(256) ffn_zero_kernel(uint8_t* p, size_t n) {
+  for (size_t i = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 2; i < n; i += static_cast<size_t>(gridDim.x) * 512)
+    *reinterpret_cast<uint16_t*>(p + i) = 0;
+}
+
+// ---------------------------------------------------------------- host
+
+int check_ffn(const moe_ffn_config* c, int32_t rows) {
+  if (!c) return MOE_ERR_NULL_PTR;
+  if (c->dtype != MOE_DTYPE_F32 && c->dtype != MOE_DTYPE_BF16) return MOE_ERR_BAD_DTYPE;
+  if (c->hidden_size <= 0 || c->intermediate_size <= 0 || rows < 0) return MOE_ERR_BAD_SHAPE;
+  if (c->activation < MOE_ACT_NONE || c->activation > MOE_ACT_SILU) return MOE_ERR_BAD_SHAPE;
+  // Grid and index arithmetic inside the kernels.
+  if (c->hidden_size > MOE_LINEAR_MAX_FEATURES || c->intermediate_size > MOE_LINEAR_MAX_FEATURES / 4 ||
+      rows > MOE_LINEAR_MAX_ROWS)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t type_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+// Length of the rows of h, a and b.
+int64_t inner_ld(const moe_ffn_config& c) { return (static_cast<int64_t>(c.intermediate_size) + 7) / 8 * 8; }
+
+// The kept tensors: h, a, b.
+size_t h_bytes(const moe_ffn_config& c, int64_t T) { return align_up(static_cast<size_t>(T) * inner_ld(c) * type_bytes(c.dtype), 256); }
+size_t slope_bytes(const moe_ffn_config& c, int64_t T) { return align_up(static_cast<size_t>(T) * inner_ld(c) * 4, 256); }
+size_t kept_bytes(const moe_ffn_config& c, int64_t T) { return h_bytes(c, T) + 2 * slope_bytes(c, T); }
+
+moe_linear_config down_config(const moe_ffn_config& c) {
+  return moe_linear_config{c.intermediate_size, c.hidden_size, c.dtype, c.dtype, MOE_ACT_NONE};
+}
+
+// The workspace: partial sums, then h (forward) or [dg du] (backward).
+size_t ffn_parts(const moe_ffn_config& c, int64_t T) {
+  const moe_linear_config down = down_config(c);
+  size_t n = 0;
+  moe_linear_workspace_size(&down, static_cast<int32_t>(T), &n);
+  const int64_t H = c.hidden_size, Ip = inner_ld(c);
+  n = std::max(n, part_bytes(true, T, c.intermediate_size));
+  n = std::max({n, part_bytes(false, T, Ip), part_bytes(false, T, H), part_bytes(false, 2 * Ip, H), part_bytes(false, H, Ip)});
+  return align_up(n, 256);
+}
+size_t ffn_workspace(const moe_ffn_config& c, int64_t T, bool backward) {
+  return ffn_parts(c, T) + (backward ? 2 : 1) * h_bytes(c, T);
+}
+
+bool misaligned(const void* p, size_t unit) { return reinterpret_cast<uintptr_t>(p) % unit != 0; }
+constexpr int64_t kFar = int64_t{1} << 40;     // strides whose products with a row index stay in 64 bits
+
+struct FfnArgs {
+  const void *x, *wg, *wu, *wd;
+  int64_t ldx;
+};
+
+template <bool F32>
+int ffn_forward(const moe_ffn_config& c, int T, const FfnArgs& f, void* y, int64_t ldy, void* h, float* a, float* b,
+                uint8_t* ws, hipStream_t s) {
+  constexpr El E = F32 ? El::F32 : El::BF16;
+  const int H = c.hidden_size, I = c.intermediate_size;
+  const int64_t Ip = inner_ld(c);
+  const Product g{{f.x, nullptr, f.ldx, 0, 0}, {f.wg, f.wu, H, 0, 0}, T, I, H};
+  float* part = reinterpret_cast<float*>(ws);
+  const int st = a ? run_product<E, true, true, true>(g, GatedOut<F32, true>{h, a, b, Ip, T, I, c.activation}, part, s)
+                   : run_product<E, true, true, true>(g, GatedOut<F32, false>{h, a, b, Ip, T, I, c.activation}, part, s);
+  if (st) return st;
+  const moe_linear_config down = down_config(c);
+  return moe_linear(&down, T, h, Ip, f.wd, I, nullptr, nullptr, 0, y, ldy, ws, ffn_parts(c, T), s);
+}
+
+template <bool F32>
+int ffn_backward(const moe_ffn_config& c, int T, const FfnArgs& f, const void* h, const float* a, const float* b,
+                 const void* dy, int64_t lddy, void* dx, int64_t lddx, void* dwg, void* dwu, void* dwd, uint8_t* ws,
+                 hipStream_t s) {
+  constexpr El E = F32 ? El::F32 : El::BF16;
+  const int H = c.hidden_size, I = c.intermediate_size, Ip = static_cast<int>(inner_ld(c));
+  float* part = reinterpret_cast<float*>(ws);
+  void* d = ws + ffn_parts(c, T);
+  int st = MOE_OK;
+  if (dwd) {
+    const Product g{{dy, nullptr, lddy, 0, 0}, {h, nullptr, Ip, 0, 0}, H, I, T};
+    st = run_product<E, false, false, false>(g, RowsOut<F32>{dwd, nullptr, I, H, I, H, H}, part, s);
+  }
+  if (st == MOE_OK && (dx || dwg)) {
+    const Product g{{dy, nullptr, lddy, 0, 0}, {f.wd, nullptr, I, 0, 0}, T, I, H};
+    st = run_product<E, true, false, false>(g, SlopesOut<F32>{a, b, d, Ip, T, I}, part, s);
+  }
+  if (st == MOE_OK && dwg) {
+    const Product g{{d, nullptr, 2 * Ip, 0, 0}, {f.x, nullptr, f.ldx, 0, 0}, 2 * Ip, H, T};
+    st = run_product<E, false, false, false>(g, RowsOut<F32>{dwg, dwu, H, 2 * Ip, H, Ip, I}, part, s);
+  }
+  if (st == MOE_OK && dx) {
+    const Product g{{d, nullptr, 2 * Ip, 0, 0}, {f.wg, f.wu, H, Ip, I}, T, H, 2 * Ip};
+    st = run_product<E, true, false, true>(g, RowsOut<F32>{dx, nullptr, lddx, T, H, T, T}, part, s);
+  }
+  return st;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_ffn_workspace_size(const moe_ffn_config* cfg, int32_t max_rows, int32_t backward, size_t* bytes) {
+  const int st = check_ffn(cfg, max_rows);
+  if (st) return st;
+  if (!bytes) return MOE_ERR_NULL_PTR;
+  *bytes = ffn_workspace(*cfg, max_rows, backward != 0);
+  return MOE_OK;
+}
+
+int moe_ffn_kept_size(const moe_ffn_config* cfg, int32_t max_rows, size_t* bytes) {
+  const int st = check_ffn(cfg, max_rows);
+  if (st) return st;
+  if (!bytes) return MOE_ERR_NULL_PTR;
+  *bytes = std::max<size_t>(kept_bytes(*cfg, max_rows), 256);
+  return MOE_OK;
+}
+
+int moe_ffn_forward(const moe_ffn_config* cfg, int32_t T, const void* x, int64_t ldx, const void* w_gate,
+                    const void* w_up, const void* w_down, void* y, int64_t ldy, void* kept, size_t kept_size,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = check_ffn(cfg, T);
+  if (st) return st;
+  if (T == 0) return MOE_OK;
+  if (!x || !w_gate || !w_up || !w_down || !y || !workspace) return MOE_ERR_NULL_PTR;
+  if (ldx < cfg->hidden_size || ldy < cfg->hidden_size) return MOE_ERR_BAD_SHAPE;
+  if (ldx > kFar || ldy > kFar) return MOE_ERR_UNSUPPORTED;
+  if (workspace_bytes < ffn_workspace(*cfg, T, false)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (kept && kept_size < kept_bytes(*cfg, T)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const size_t e = type_bytes(cfg->dtype);
+  if (misaligned(x, e) || misaligned(w_gate, e) || misaligned(w_up, e) || misaligned(w_down, e) || misaligned(y, e) ||
+      misaligned(workspace, 16) || misaligned(kept, 16))
+    return MOE_ERR_UNSUPPORTED;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* k = static_cast<uint8_t*>(kept);
+  void* h = kept ? k : ws + ffn_parts(*cfg, T);
+  float* a = kept ? reinterpret_cast<float*>(k + h_bytes(*cfg, T)) : nullptr;
+  float* b = kept ? reinterpret_cast<float*>(k + h_bytes(*cfg, T) + slope_bytes(*cfg, T)) : nullptr;
+  const FfnArgs f{x, w_gate, w_up, w_down, ldx};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return cfg->dtype == MOE_DTYPE_F32 ? ffn_forward<true>(*cfg, T, f, y, ldy, h, a, b, ws, s)
+                                     : ffn_forward<false>(*cfg, T, f, y, ldy, h, a, b, ws, s);
+}
+
+int moe_ffn_backward(const moe_ffn_config* cfg, int32_t T, const void* x, int64_t ldx, const void* w_gate,
+                     const void* w_up, const void* w_down, const void* kept, size_t kept_size, const void* dy,
+                     int64_t lddy, void* dx, int64_t lddx, void* dw_gate, void* dw_up, void* dw_down, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  const int st = check_ffn(cfg, T);
+  if (st) return st;
+  if (!dw_gate != !dw_up) return MOE_ERR_NULL_PTR;
+  const size_t e = type_bytes(cfg->dtype);
+  if (misaligned(dx, e) || misaligned(dw_gate, e) || misaligned(dw_up, e) || misaligned(dw_down, e)) return MOE_ERR_UNSUPPORTED;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (T == 0) {
+    const size_t n = static_cast<size_t>(cfg->hidden_size) * cfg->intermediate_size * e;
+    const unsigned grid = static_cast<unsigned>(std::min<size_t>(2048, (n + 511) / 512));
+    for (void* w : {dw_gate, dw_up, dw_down})
+      if (w) {
+        ffn_zero_kernel<<<grid, 256, 0, s>>>(static_cast<uint8_t*>(w), n);
+        if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
+      }
+    return MOE_OK;
+  }
+  if (!x || !w_gate || !w_up || !w_down || !kept || !dy || !workspace) return MOE_ERR_NULL_PTR;
+  if (ldx < cfg->hidden_size || lddy < cfg->hidden_size || (dx && lddx < cfg->hidden_size)) return MOE_ERR_BAD_SHAPE;
+  if (ldx > kFar || lddy > kFar || (dx && lddx > kFar)) return MOE_ERR_UNSUPPORTED;
+  if (workspace_bytes < ffn_workspace(*cfg, T, true)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (kept_size < kept_bytes(*cfg, T)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (misaligned(x, e) || misaligned(w_gate, e) || misaligned(w_up, e) || misaligned(w_down, e) || misaligned(dy, e) ||
+      misaligned(workspace, 16) || misaligned(kept, 16))
+    return MOE_ERR_UNSUPPORTED;
+  const uint8_t* k = static_cast<const uint8_t*>(kept);
+  const float* a = reinterpret_cast<const float*>(k + h_bytes(*cfg, T));
+  const float* b = reinterpret_cast<const float*>(k + h_bytes(*cfg, T) + slope_bytes(*cfg, T));
+  const FfnArgs f{x, w_gate, w_up, w_down, ldx};
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  return cfg->dtype == MOE_DTYPE_F32
+             ? ffn_backward<true>(*cfg, T, f, k, a, b, dy, lddy, dx, lddx, dw_gate, dw_up, dw_down, ws, s)
+             : ffn_backward<false>(*cfg, T, f, k, a, b, dy, lddy, dx, lddx, dw_gate, dw_up, dw_down, ws, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,430 @@
+// Matrix products c[m, n] = sum_k a(m, k) b(n, k) whose operands lie in memory either
+// with a row's contraction elements side by side (k-contiguous, as x and the weights of
+// x W^T) or with the rows' elements of one k side by side (k-strided, as both operands of
+// a weight's gradient dy^T x).  What becomes of the sums is the epilogue's, a functor.
+//
+// Sums run in float32 (8-bit integers: exactly, in int32) over the whole contraction.
+#pragma once
+
+#include <algorithm>
+
+#include "dense.h"
+#include "dma.h"
+
+namespace moe {
+namespace {
+
+enum class El { F32, BF16, I8 };
+template <El E>
+struct ElInfo {
+  static constexpr int kSize = E == El::F32 ? 4 : E == El::BF16 ? 2 : 1;
+  static constexpr int kPiece = 16 / kSize;       // elements of 16 bytes
+  static constexpr int kStage = 128 / kSize;      // contraction elements of a stage
+};
+
+// One operand.  k-contiguous: row r starts ld elements after row r - 1; k-strided: the
+// elements of k start ld elements after those of k - 1.
+//   q != null, k-contiguous: two matrices whose rows take turns, 32 of p and 32 of q;
+//   q != null, k-strided: k in [0, half) is p's, k in [half, 2 half) q's; of either
+//   half the first `live` exist, the others are zeros.
+struct Operand {
+  const void *p, *q;
+  int64_t ld;
+  int half, live;
+};
+
+// M x N results (a pair of results for each with a k-contiguous pair in b) over K.
+struct Product {
+  Operand a, b;
+  int M, N, K;
+};
+
+// 16 bytes of a row that holds `left` more elements, zeros past its end.
+template <El E, bool ANY>
+__device__ __forceinline__ uint4 piece_of(const uint8_t* p, int left) {
+  if constexpr (E == El::F32) {
+    if constexpr (ANY) {
+      if (left >= 4) {
+        const f32x4_any v = *reinterpret_cast<const f32x4_any*>(p);
+        return uint4{__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)};
+      }
+    }
+    return ld_f32x4(p, left, !ANY);
+  } else if constexpr (E == El::BF16) {
+    return ld8_bf16<ANY>(reinterpret_cast<const uint16_t*>(p), left);
+  } else {
+    if (left >= 16) {
+      if constexpr (!ANY) return ld16(p);
+      typedef uint32_t u32x4_b __attribute__((ext_vector_type(4), aligned(1)));
+      const u32x4_b v = *reinterpret_cast<const u32x4_b*>(p);
+      return uint4{v.x, v.y, v.z, v.w};
+    }
+    uint32_t v[4] = {0, 0, 0, 0};
+    if constexpr (ANY) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (k < left) v[k >> 2] |= static_cast<uint32_t>(p[k]) << (8 * (k & 3));
+    }
+    return uint4{v[0], v[1], v[2], v[3]};
+  }
+}
+
+typedef int i32x4v __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+template <El E>
+using Acc = std::conditional_t<E == El::I8, i32x16, f32x16>;
+
+// 32 x 32 sums over the 2 x 16 bytes of two lane halves.
+template <El E>
+__device__ __forceinline__ Acc<E> mfma32(const uint4& a, const uint4& b, Acc<E> c) {
+  if constexpr (E == El::F32) {
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.x), __uint_as_float(b.x), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.y), __uint_as_float(b.y), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.z), __uint_as_float(b.z), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.w), __uint_as_float(b.w), c, 0, 0, 0);
+  } else if constexpr (E == El::BF16) {
+    return mfma_bf16_32x32x16(a, b, c);
+  } else {
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4v, a), __builtin_bit_cast(i32x4v, b), c, 0, 0, 0);
+  }
+}
+
+// Two reads of 64 bits, each of which turns a 4 (k) x 16 block of a k-strided operand
+// between the 16 lanes that address it: lane i gets column i's four elements.
+__device__ __forceinline__ uint2 lds_turned(const uint8_t* p) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                       (__attribute__((address_space(3))) s16x4*)(p)));
+}
+
+// ---------------------------------------------------------------- results
+
+// ROWS x BN sums in LDS, rows `stride` floats apart, to the epilogue or to part p's sums:
+// row_of(R) is the row of the product behind row R.  Whole row segments, four columns to
+// a thread.  A PAIR's columns take turns, 32 of the first product and 32 of the second.
+// A part's sums are M rows of the first product's columns, then M of the second's.
+template <bool PAIR, int BN, int ROWS, int THREADS, class Epi, class RowOf>
+__device__ __forceinline__ void results_out(const Product& g, const Epi& epi, const float* stg, int stride, int n0,
+                                            int parts, int p, float* part, RowOf row_of) {
+  constexpr int kCols = PAIR ? BN / 2 : BN;
+  constexpr int kLanes = kCols / 4, kIter = ROWS * kLanes / THREADS, D = Epi::kAhead < kIter ? Epi::kAhead : kIter;
+  static_assert(THREADS % kLanes == 0 && kIter % D == 0, "a thread keeps its columns");
+  const int tid = threadIdx.x, c = 4 * (tid % kLanes), n = n0 + c;
+  const int sc = PAIR ? (c >> 5) * 64 + (c & 31) : c;
+  if (n >= g.N) return;
+#pragma unroll 1
+  for (int k = 0; k < kIter; k += D) {
+    int m[D];
+    f32x4 s[D], u[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int R = (tid + (k + d) * THREADS) / kLanes;
+      m[d] = row_of(R);
+      s[d] = *reinterpret_cast<const f32x4*>(stg + R * stride + sc);
+      if constexpr (PAIR) u[d] = *reinterpret_cast<const f32x4*>(stg + R * stride + sc + 32);
+    }
+    if (parts > 1) {
+      const size_t np = part_stride(g.N), plane = static_cast<size_t>(p) * g.M * (PAIR ? 2 : 1);
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+        if (m[d] < g.M) {
+          *reinterpret_cast<f32x4*>(part + (plane + m[d]) * np + n) = s[d];
+          if constexpr (PAIR) *reinterpret_cast<f32x4*>(part + (plane + g.M + m[d]) * np + n) = u[d];
+        }
+    } else {
+      epi.template quads<D>(m, n, s, u);
+    }
+  }
+}
+
+// The parts' sums added in order.
+constexpr int kSumAhead = 4;
+template <bool PAIR, class Epi>
+__global__ void __launch_bounds__(256) product_sum_kernel(Product g, Epi epi, int parts, const float* part) {
+  const int quads = static_cast<int>(part_stride(g.N) / 4);
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t plane = static_cast<int64_t>(g.M) * quads;
+  if (i >= plane) return;
+  const f32x4* v = reinterpret_cast<const f32x4*>(part) + i;
+  f32x4 s[1] = {{0.f, 0.f, 0.f, 0.f}}, u[1] = {{0.f, 0.f, 0.f, 0.f}};
+  for (int p = 0; p < parts; p += kSumAhead) {
+    f32x4 b[kSumAhead], c[kSumAhead];
+#pragma unroll
+    for (int k = 0; k < kSumAhead; ++k)
+      if (p + k < parts) {
+        b[k] = v[plane * (PAIR ? 2 * (p + k) : p + k)];
+        if constexpr (PAIR) c[k] = v[plane * (2 * (p + k) + 1)];
+      }
+#pragma unroll
+    for (int k = 0; k < kSumAhead; ++k)
+      if (p + k < parts)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[0][e] += b[k][e];
+          if constexpr (PAIR) u[0][e] += c[k][e];
+        }
+  }
+  const int m[1] = {static_cast<int>(i / quads)};
+  epi.template quads<1>(m, 4 * static_cast<int>(i - static_cast<int64_t>(m[0]) * quads), s, u);
+}
+
+// ---------------------------------------------------------------- tiles of any alignment
+//
+// BM x BN sums per workgroup of 2 x 2 waves, from 32x32 MFMAs.  A stage is 128 bytes of
+// contraction (64 bf16, 32 f32, 128 int8), double-buffered in LDS; its loads go to
+// registers two stages ahead, which takes any alignment and fills ends with zeros.  A
+// k-contiguous operand's rows lie unpadded in LDS, their 16-byte pieces permuted by
+// (row / 2) mod 8; a k-strided one's rows are the k, padded so that the four k that a
+// fragment read takes lie in different quarters of the banks.
+template <El E, bool KC, int R>
+struct TileSide {
+  using I = ElInfo<E>;
+  static_assert(KC || E != El::I8, "8-bit operands are k-contiguous");
+  static constexpr int kRow = KC ? 128 : R * I::kSize + (E == El::F32 ? 32 : 64);
+  static constexpr int kBytes = KC ? R * 128 : I::kStage * kRow;
+  static constexpr int kPer = KC ? 8 : R / I::kPiece;           // pieces of a row
+  static constexpr int kStep = 256 / kPer;                      // rows between a thread's pieces
+  static constexpr int kN = (KC ? R : I::kStage) / kStep;       // pieces of a thread
+};
+
+template <El E, bool KA, bool KB, bool PAIR, bool ANY, int BM, int BN, class Epi>
+__global__ void __launch_bounds__(256, 2) product_tile_kernel(Product g, Epi epi, int parts, float* part) {
+  using I = ElInfo<E>;
+  using SA = TileSide<E, KA, BM>;
+  using SB = TileSide<E, KB, BN>;
+  constexpr int NI = BM / 64, NJ = BN / 64, kCols = PAIR && KB ? BN / 2 : BN;
+  constexpr bool kPair = PAIR && KB;
+  constexpr int kStride = BN + 8;
+  constexpr int kBytes = 2 * (SA::kBytes + SB::kBytes) > 64 * kStride * 4 ? 2 * (SA::kBytes + SB::kBytes) : 64 * kStride * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kBytes];
+  constexpr int kStageBytes = SA::kBytes + SB::kBytes;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1, r32 = lane & 31, hi = lane >> 5;
+  const int mt = static_cast<int>(ceil_div(g.M, BM)), nt = static_cast<int>(ceil_div(g.N, kCols));
+  const int item = xcd_tile(blockIdx.x, mt * nt * parts);
+  if (item < 0) return;
+  const int p = item % parts, m0 = (item / parts) % mt * BM, n0 = (item / parts) / mt * kCols;
+  const int stages = static_cast<int>(ceil_div(g.K, I::kStage));
+  const int s0 = static_cast<int>(static_cast<int64_t>(p) * stages / parts), s1 = static_cast<int>(static_cast<int64_t>(p + 1) * stages / parts);
+
+  // k-contiguous: thread t loads piece t % 8 of rows t / 8 + 32 q, rows past the end
+  // repeat the last.  k-strided: piece t % kPer of k t / kPer + kStep q, none past the
+  // end of k or of the columns.
+  const uint8_t* ap[SA::kN];
+  const uint8_t* bp[SB::kN];
+  const int arow = tid / SA::kPer, apiece = tid % SA::kPer, brow = tid / SB::kPer, bpiece = tid % SB::kPer;
+#pragma unroll
+  for (int q = 0; q < SA::kN; ++q) {
+    if constexpr (KA)
+      ap[q] = static_cast<const uint8_t*>(g.a.p) + (static_cast<size_t>(min(m0 + arow + SA::kStep * q, g.M - 1)) * g.a.ld) * I::kSize + 16 * apiece;
+    else
+      ap[q] = static_cast<const uint8_t*>(g.a.p) + (static_cast<size_t>(arow + SA::kStep * q) * g.a.ld + m0) * I::kSize + 16 * apiece;
+  }
+#pragma unroll
+  for (int q = 0; q < SB::kN; ++q) {
+    const int r = brow + SB::kStep * q;
+    if constexpr (kPair) {
+      const void* w = (r & 32) ? g.b.q : g.b.p;
+      bp[q] = static_cast<const uint8_t*>(w) + (static_cast<size_t>(min(n0 + (r >> 6) * 32 + (r & 31), g.N - 1)) * g.b.ld) * I::kSize + 16 * bpiece;
+    } else if constexpr (KB) {
+      bp[q] = static_cast<const uint8_t*>(g.b.p) + (static_cast<size_t>(min(n0 + r, g.N - 1)) * g.b.ld) * I::kSize + 16 * bpiece;
+    } else {
+      bp[q] = static_cast<const uint8_t*>(g.b.p) + (static_cast<size_t>(r) * g.b.ld + n0) * I::kSize + 16 * bpiece;
+    }
+  }
+  struct Regs {
+    uint4 a[SA::kN], b[SB::kN];
+  };
+  auto load = [&](Regs& R, int s) __attribute__((always_inline)) {
+    const int st = min(s, s1 - 1), k0 = st * I::kStage;
+#pragma unroll
+    for (int q = 0; q < SA::kN; ++q) {
+      if constexpr (KA) {
+        R.a[q] = piece_of<E, ANY>(ap[q] + static_cast<size_t>(st) * 128, g.K - k0 - apiece * I::kPiece);
+      } else {
+        const bool ok = k0 + arow + SA::kStep * q < g.K;
+        R.a[q] = piece_of<E, ANY>(ap[q] + static_cast<size_t>(k0) * g.a.ld * I::kSize, ok ? g.M - m0 - apiece * I::kPiece : 0);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < SB::kN; ++q) {
+      if constexpr (KB) {
+        R.b[q] = piece_of<E, ANY>(bp[q] + static_cast<size_t>(st) * 128, g.K - k0 - bpiece * I::kPiece);
+      } else if constexpr (PAIR) {
+        const int k = k0 + brow + SB::kStep * q, kk = k < g.b.half ? k : k - g.b.half;
+        const uint8_t* base = static_cast<const uint8_t*>(k < g.b.half ? g.b.p : g.b.q);
+        const bool ok = k < g.K && kk < g.b.live;
+        R.b[q] = piece_of<E, ANY>(base + (static_cast<size_t>(kk) * g.b.ld + n0) * I::kSize + 16 * bpiece,
+                                  ok ? g.N - n0 - bpiece * I::kPiece : 0);
+      } else {
+        const bool ok = k0 + brow + SB::kStep * q < g.K;
+        R.b[q] = piece_of<E, ANY>(bp[q] + static_cast<size_t>(k0) * g.b.ld * I::kSize, ok ? g.N - n0 - bpiece * I::kPiece : 0);
+      }
+    }
+  };
+  const uint32_t alds = arow * SA::kRow + (KA ? ((apiece ^ ((arow >> 1) & 7)) * 16) : 16 * apiece);
+  const uint32_t blds = SA::kBytes + brow * SB::kRow + (KB ? ((bpiece ^ ((brow >> 1) & 7)) * 16) : 16 * bpiece);
+  auto store = [&](const Regs& R, int buf) __attribute__((always_inline)) {
+    uint8_t* d = smem + buf * kStageBytes;
+#pragma unroll
+    for (int q = 0; q < SA::kN; ++q) *reinterpret_cast<uint4*>(d + alds + q * SA::kStep * SA::kRow) = R.a[q];
+#pragma unroll
+    for (int q = 0; q < SB::kN; ++q) *reinterpret_cast<uint4*>(d + blds + q * SB::kStep * SB::kRow) = R.b[q];
+  };
+  Acc<E> acc[NI][NJ];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+  // Fragment kk of the 32 rows from row on: 16 bytes of contraction of the lane's row, the
+  // same elements of either operand for a lane half.
+  const uint32_t swz = static_cast<uint32_t>(hi ^ ((r32 >> 1) & 7));
+  auto frag = [&](auto side, const uint8_t* base, int row, int kk, bool kc) __attribute__((always_inline)) {
+    using S = decltype(side);
+    if (kc) return *reinterpret_cast<const uint4*>(base + (row + r32) * 128 + ((2 * kk) ^ swz) * 16);
+    if constexpr (E == El::BF16) {
+      const uint8_t* t = base + (16 * kk + 8 * hi + ((lane & 15) >> 2)) * S::kRow + (row + (r32 & 16) + 4 * (lane & 3)) * 2;
+      const uint2 lo = lds_turned(t), up = lds_turned(t + 4 * S::kRow);
+      return uint4{lo.x, lo.y, up.x, up.y};
+    } else {
+      const uint8_t* t = base + (8 * kk + 4 * hi) * S::kRow + (row + r32) * 4;
+      return uint4{*reinterpret_cast<const uint32_t*>(t), *reinterpret_cast<const uint32_t*>(t + S::kRow),
+                   *reinterpret_cast<const uint32_t*>(t + 2 * S::kRow), *reinterpret_cast<const uint32_t*>(t + 3 * S::kRow)};
+    }
+  };
+  auto compute = [&](int buf) __attribute__((always_inline)) {
+    const uint8_t* As = smem + buf * kStageBytes;
+    const uint8_t* Bs = As + SA::kBytes;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      uint4 af[NI], bf[NJ];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) af[i] = frag(SA{}, As, wm * (BM / 2) + 32 * i, kk, KA);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) bf[j] = frag(SB{}, Bs, wn * (BN / 2) + 32 * j, kk, KB);
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = mfma32<E>(af[i], bf[j], acc[i][j]);
+    }
+  };
+
+  // Iteration s: barrier; write stage s + 1 from registers, start loading s + 3 into
+  // them (past the end the last stage again), multiply stage s.
+  Regs R0, R1;
+  load(R0, s0);
+  load(R1, s0 + 1);
+  store(R0, 0);
+  load(R0, s0 + 2);
+  for (int s = s0; s < s1; s += 2) {
+    __syncthreads();
+    store(R1, 1);
+    load(R1, s + 3);
+    compute(0);
+    if (s + 1 == s1) break;
+    __syncthreads();
+    store(R0, 0);
+    load(R0, s + 4);
+    compute(1);
+  }
+
+  // Out through LDS, NI rounds of 32 rows of each wave row, rows padded by 8 floats.
+  // Lane l, element v: row 8 (v / 4) + 4 (l / 32) + v % 4, column l % 32 of a block.
+  float* stg = reinterpret_cast<float*>(smem);
+  __syncthreads();                   // every wave is done reading the stage buffers
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+#pragma unroll
+    for (int v = 0; v < 16; ++v)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        stg[(wm * 32 + 8 * (v >> 2) + 4 * hi + (v & 3)) * kStride + wn * (BN / 2) + 32 * j + r32] = static_cast<float>(acc[i][j][v]);
+    __syncthreads();
+    results_out<kPair, BN, 64, 256>(g, epi, stg, kStride, n0, parts, p, part, [&](int R) {
+      return m0 + (R / 32) * (BM / 2) + 32 * i + R % 32;
+    });
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+constexpr int kCus = 256;
+constexpr int kMaxParts = 16;
+// Most bytes of partial sums: those of two 128 x 128 tiles on each CU.
+constexpr size_t kMaxPartBytes = size_t{2} * kCus * 128 * 128 * sizeof(float);
+
+struct TilePlan {
+  int rows, cols;       // of a tile, in operand rows
+  int64_t tiles;
+  int parts;
+};
+
+// The cheapest tile and split by an estimate in microseconds: what a CU takes in, the
+// f32 matrix rate, and the partial sums' way out and back.
+inline TilePlan plan_tiles(El e, bool pair, int64_t M, int64_t N, int64_t K) {
+  const int size = e == El::F32 ? 4 : e == El::BF16 ? 2 : 1;
+  const int64_t width = pair ? 2 * N : N, stages = ceil_div(K * size, 128);
+  static const struct { int rows, cols; } kTiles[] = {{64, 128}, {128, 128}};
+  TilePlan best{};
+  double least = 0;
+  for (const auto& t : kTiles) {
+    const int64_t tiles = ceil_div(M, t.rows) * ceil_div(width, t.cols), slots = int64_t{2} * kCus;
+    for (int parts = 1; parts <= kMaxParts; ++parts) {
+      const int64_t planes = parts * M * (pair ? 2 : 1) * part_stride(N) * 4;
+      if (parts > 1 && (tiles * parts > (e == El::F32 ? 2 * slots : slots) || planes > static_cast<int64_t>(kMaxPartBytes) || stages / parts < 4)) break;
+      const int64_t items = tiles * parts, rounds = ceil_div(items, slots);
+      const double shared = items > kCus ? 2 : 1, deep = static_cast<double>(ceil_div(stages, parts));
+      const double load = (t.rows + t.cols) * 0.128 * deep / (shared > 1 ? 28 : 20);
+      const double mult = e == El::F32 ? t.rows * t.cols * 64 * deep / 0.5e6 : 0;
+      const double in_turn = e == El::F32 ? static_cast<double>(ceil_div(items, kCus)) : rounds * shared;
+      const double us = in_turn * std::max(load, mult) + 2 + 0.5 * rounds + (parts > 1 ? 4 + planes * 2 / 5e6 : 0);
+      if (best.tiles == 0 || us < least) {
+        least = us;
+        best = TilePlan{t.rows, t.cols, tiles, parts};
+      }
+    }
+  }
+  return best;
+}
+
+// Bytes of partial sums of any product of at most M rows.
+inline size_t part_bytes(bool pair, int64_t M, int64_t N) {
+  const double want = static_cast<double>(kMaxParts) * M * (pair ? 2 : 1) * part_stride(N) * sizeof(float);
+  return want < static_cast<double>(kMaxPartBytes) ? std::max<size_t>(align_up(static_cast<size_t>(want), 256), 256) : kMaxPartBytes;
+}
+
+// 16-byte pieces of an operand lie on 16-byte boundaries.
+inline bool aligned16(const Operand& o, El e, bool kc, int64_t rows, int64_t K) {
+  const int64_t unit = e == El::F32 ? 4 : e == El::BF16 ? 8 : 16;
+  return o.ld % unit == 0 && (kc ? K : rows) % unit == 0 && reinterpret_cast<uintptr_t>(o.p) % 16 == 0 &&
+         reinterpret_cast<uintptr_t>(o.q) % 16 == 0;
+}
+
+template <El E, bool KA, bool KB, bool PAIR, bool ANY, class Epi>
+void launch_tiles(const Product& g, const Epi& epi, const TilePlan& t, float* part, hipStream_t s) {
+  const unsigned grid = static_cast<unsigned>(ceil_div(t.tiles * t.parts, 8) * 8);
+  if (t.rows == 64) product_tile_kernel<E, KA, KB, PAIR, ANY, 64, 128><<<grid, 256, 0, s>>>(g, epi, t.parts, part);
+  else product_tile_kernel<E, KA, KB, PAIR, ANY, 128, 128><<<grid, 256, 0, s>>>(g, epi, t.parts, part);
+}
+
+// Runs a product of M, N, K >= 1; `part` holds part_bytes(pair, M, N).
+template <El E, bool KA, bool KB, bool PAIR, class Epi>
+int run_product(const Product& g, const Epi& epi, float* part, hipStream_t s) {
+  constexpr bool kPair = PAIR && KB;
+  const bool aligned = aligned16(g.a, E, KA, g.M, g.K) && aligned16(g.b, E, KB, g.N, g.K);
+  const TilePlan t = plan_tiles(E, kPair, g.M, g.N, g.K);
+  if (aligned) launch_tiles<E, KA, KB, PAIR, false>(g, epi, t, part, s);
+  else launch_tiles<E, KA, KB, PAIR, true>(g, epi, t, part, s);
+  if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
+  if (t.parts > 1) {
+    product_sum_kernel<kPair><<<static_cast<unsigned>(ceil_div(g.M * part_stride(g.N) / 4, 256)), 256, 0, s>>>(g, epi, t.parts, part);
+    if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
