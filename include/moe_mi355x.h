@@ -99,7 +99,10 @@ typedef enum moe_dtype {
    * block scales in the matrix cores.  The 4-bit group-scaled weights are what
    * the pages point to for the decode-bound layers (NVFP4 and FP8 x FP4 in
    * [DeepGEMM fork PR #5] and [DeepGEMM PR #381]). */
-  MOE_DTYPE_MXFP4 = 3
+  MOE_DTYPE_MXFP4 = 3,
+  /* Symmetric 8-bit integers with a float32 scale for each row (moe_quant_i8,
+   * moe_linear_i8 and moe_norm's out; not a weight_dtype of the layer). */
+  MOE_DTYPE_I8 = 4
 } moe_dtype;
 
 typedef struct moe_config {
@@ -384,6 +387,112 @@ int moe_ffn_backward(const moe_ffn_config* cfg, int32_t num_rows, const void* x,
                      const void* w_up, const void* w_down, const void* kept, size_t kept_bytes, const void* dy,
                      int64_t lddy, void* dx, int64_t lddx, void* dw_gate, void* dw_up, void* dw_down,
                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Norms of moe_norm: n(v) = v / sqrt(mean(v^2) + eps), or of v - mean(v). */
+typedef enum moe_norm_kind { MOE_NORM_RMS = 0, MOE_NORM_LAYER = 1 } moe_norm_kind;
+/* The gate of a block's output: none, one factor for each channel [H], for each token
+ * [T], or for each element [T, H]. */
+typedef enum moe_gate_kind { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 } moe_gate_kind;
+
+#define MOE_NORM_MAX_HIDDEN 16384
+
+typedef struct moe_norm_config {
+  int32_t hidden_size;     /* H, 1..MOE_NORM_MAX_HIDDEN                                 */
+  int32_t kind;            /* moe_norm_kind of both norms                               */
+  int32_t gate;            /* moe_gate_kind                                             */
+  int32_t block_dtype;     /* moe_dtype of y and dy: F32 or BF16 (moe_forward's y: F32) */
+  int32_t stream_dtype;    /* of residual, z and their gradients: F32 or BF16           */
+  int32_t out_dtype;       /* of out (and dout): F32, BF16, or I8 with a scale per row  */
+  int32_t param_dtype;     /* of weights, biases, gate and their gradients: F32 or BF16 */
+  float eps;
+  float residual_scale;    /* a */
+  float block_scale;       /* b */
+} moe_norm_config;
+
+/* The norms after a block and before the next one, with the block's gate and the
+ * residual's scale, in one pass over the rows:
+ *   z[t] = a residual[t] + b gate * post(y[t]);   out[t] = norm(z[t])
+ *   norm(v) = n(v) weight + bias;  post likewise with post_weight and post_bias
+ * in float32 from the loaded elements on; z and out are rounded once (out comes from the
+ * unrounded z).
+ *   y           (device) [num_rows, H], rows ldy elements apart: the block's output
+ *   residual    (device) [num_rows, H] or NULL (then z = b gate * post(y))
+ *   gate        (device) as cfg->gate says, NULL for none; rows ldg apart if [T, H]
+ *   weight      (device) [H] or NULL (1);  bias (device) [H] or NULL (0)
+ *   post_weight (device) [H], or NULL: no norm after the block;  post_bias [H] or NULL
+ *   z           (device) out [num_rows, H] or NULL; may be residual (then ldz = ldr)
+ *   out         (device) out [num_rows, H] or NULL: no norm after the sum; z and out not
+ *               both NULL.  I8: codes as moe_quant_i8 chooses them, and out_scale
+ *   out_scale   (device) out float32 [num_rows] for I8, else ignored
+ * Strides are in elements, at least H (MOE_ERR_BAD_SHAPE otherwise) and at most 2^40;
+ * tensors need only be aligned to their element size.  num_rows = 0 returns MOE_OK;
+ * num_rows <= MOE_LINEAR_MAX_ROWS.  No output may overlap an input otherwise. */
+int moe_norm(const moe_norm_config* cfg, int32_t num_rows, const void* y, int64_t ldy, const void* residual,
+             int64_t ldr, const void* gate, int64_t ldg, const void* weight, const void* bias,
+             const void* post_weight, const void* post_bias, void* z, int64_t ldz, void* out, int64_t ldo,
+             float* out_scale, void* stream);
+
+/* Gradients of moe_norm from those of z and of out, for the same y, gate, weights and the
+ * z that moe_norm stored (out_dtype F32 or BF16):
+ *   zt = dz + the gradient through out's norm;  dresidual = a zt
+ *   dgate = b zt post(y), summed over what the gate is broadcast along
+ *   dy = b gate zt through post;  dweight = sum_t dout n(z);  dbias = sum_t dout;
+ *   dpost_weight, dpost_bias likewise from b gate zt
+ * dz or dout may be NULL (zeros), not both; z is read only with dout.  Every result may be
+ * NULL and is then left out; dweight and dbias need dout, dpost_* need post_weight.
+ * Weights' gradients are summed in float32 in a fixed order: all results are
+ * bit-reproducible for a given num_rows.  num_rows = 0 writes zeros to the gradients of
+ * weights and of a channel gate and reads no other pointer.  dresidual may be dz (then
+ * lddr = lddz); otherwise no output may overlap an input.  The workspace (16-byte
+ * aligned, moe_norm_backward_workspace_size bytes for any num_rows <= max_rows) needs no
+ * initial contents; calls that overlap in time need one each. */
+int moe_norm_backward_workspace_size(const moe_norm_config* cfg, int32_t max_rows, size_t* bytes);
+int moe_norm_backward(const moe_norm_config* cfg, int32_t num_rows, const void* y, int64_t ldy, const void* z,
+                      int64_t ldz, const void* gate, int64_t ldg, const void* weight, const void* post_weight,
+                      const void* post_bias, const void* dz, int64_t lddz, const void* dout, int64_t lddo, void* dy,
+                      int64_t lddy, void* dresidual, int64_t lddr, void* dgate, int64_t lddg, void* dweight,
+                      void* dbias, void* dpost_weight, void* dpost_bias, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* Symmetric 8-bit codes of the rows of x, a weight's or a batch's:
+ *   scale[m] = max(amax_m / 127, 2^-126), amax_m the row's largest magnitude;
+ *   codes[m, k] = x[m, k] / scale[m] to the nearest whole number, ties to even
+ * (decided exactly for scales from 2^-100 on: the code of the exact quotient).  A row that holds an
+ * infinity or a NaN has codes of 0 and that as its scale, so that products of it are NaN.
+ *   dtype  moe_dtype of x: F32 or BF16
+ *   x      (device) [rows, columns], rows ldx elements apart
+ *   codes  (device) out [rows, columns], rows ldc apart;  scale (device) out [rows]
+ * rows <= MOE_LINEAR_MAX_ROWS, columns <= MOE_LINEAR_MAX_FEATURES. */
+int moe_quant_i8(int32_t dtype, int32_t rows, int32_t columns, const void* x, int64_t ldx, int8_t* codes,
+                 int64_t ldc, float* scale, void* stream);
+
+/* |sum| <= in_features 2^14 stays in int32. */
+#define MOE_I8_MAX_FEATURES 131071
+
+typedef struct moe_linear_i8_config {
+  int32_t in_features;   /* 1..MOE_I8_MAX_FEATURES                                       */
+  int32_t out_features;  /* 1..MOE_LINEAR_MAX_FEATURES                                   */
+  int32_t in_dtype;      /* moe_dtype of x: I8 codes, or F32 or BF16, quantised first    */
+  int32_t bias_dtype;    /* moe_dtype of bias: F32 or BF16                               */
+  int32_t out_dtype;     /* moe_dtype of y and residual: F32 or BF16                     */
+  int32_t activation;    /* moe_activation                                               */
+} moe_linear_i8_config;
+
+/* moe_linear with 8-bit operands:
+ *   y[m,n] = act(sx[m] sw[n] sum_k q[m,k] w[n,k] + bias[n]) + residual[m,n]
+ * The sum is exact, the rest float32; y is rounded once, to nearest even.
+ *   x        (device) [num_rows, in_features], rows ldx elements apart: the codes q with
+ *            x_scale (device) [num_rows], or F32 or BF16 values, which are quantised as
+ *            moe_quant_i8 does (x_scale is then ignored)
+ *   w        (device) codes [out_features, in_features], rows ldw apart
+ *   w_scale  (device) [out_features];  bias (device) [out_features] or NULL
+ *   residual, y, strides, alignment, num_rows = 0, limits of num_rows and the workspace
+ *            as for moe_linear */
+int moe_linear_i8_workspace_size(const moe_linear_i8_config* cfg, int32_t max_rows, size_t* bytes);
+int moe_linear_i8(const moe_linear_i8_config* cfg, int32_t num_rows, const void* x, int64_t ldx,
+                  const float* x_scale, const int8_t* w, int64_t ldw, const float* w_scale, const void* bias,
+                  const void* residual, int64_t ldr, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                  void* stream);
 
 /* Static description of a status code (never NULL). */
 const char* moe_status_string(int status);

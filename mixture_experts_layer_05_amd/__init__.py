@@ -24,11 +24,13 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_mi355x.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe_mi355x.h")
 
-DTYPES = {"f32": 0, "bf16": 1, "fp8_e4m3_g128": 2, "mxfp4": 3}
+DTYPES = {"f32": 0, "bf16": 1, "fp8_e4m3_g128": 2, "mxfp4": 3, "i8": 4}
 ENTRY_POINTS = ("moe_workspace_size", "moe_route", "moe_dispatch", "moe_forward",
                 "moe_forward_gate_up", "moe_forward_down", "moe_forward_noalloc", "moe_layer_few",
                 "moe_layer_few_workspace_size", "moe_linear", "moe_linear_workspace_size", "moe_ffn_workspace_size",
-                "moe_ffn_kept_size", "moe_ffn_forward", "moe_ffn_backward", "moe_status_string", "moe_version")
+                "moe_ffn_kept_size", "moe_ffn_forward", "moe_ffn_backward", "moe_norm",
+                "moe_norm_backward", "moe_norm_backward_workspace_size", "moe_quant_i8", "moe_linear_i8",
+                "moe_linear_i8_workspace_size", "moe_status_string", "moe_version")
 # Most tokens of a moe_layer_few call, and moe_linear's activations, as the header states them.
 FEW_TOKENS = 16
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
@@ -90,6 +92,14 @@ def lib() -> ctypes.CDLL:
         L.moe_ffn_kept_size.argtypes = [vp, i32, ctypes.POINTER(sz)]
         L.moe_ffn_forward.argtypes = [vp, i32, vp, i64, vp, vp, vp, vp, i64, vp, sz, vp, sz, vp]
         L.moe_ffn_backward.argtypes = [vp, i32, vp, i64, vp, vp, vp, vp, sz, vp, i64, vp, i64, vp, vp, vp, vp, sz, vp]
+        mat = [vp, i64]                        # a matrix and its row stride
+        L.moe_norm.argtypes = [vp, i32, *mat, *mat, *mat, vp, vp, vp, vp, *mat, *mat, vp, vp]
+        L.moe_norm_backward_workspace_size.argtypes = [vp, i32, ctypes.POINTER(sz)]
+        L.moe_norm_backward.argtypes = [vp, i32, *mat, *mat, *mat, vp, vp, vp, *mat, *mat, *mat, *mat, *mat, vp, vp, vp,
+                                        vp, vp, sz, vp]
+        L.moe_quant_i8.argtypes = [i32, i32, i32, *mat, *mat, vp, vp]
+        L.moe_linear_i8_workspace_size.argtypes = [vp, i32, ctypes.POINTER(sz)]
+        L.moe_linear_i8.argtypes = [vp, i32, *mat, vp, *mat, vp, vp, *mat, *mat, vp, sz, vp]
         for name in ENTRY_POINTS:
             getattr(L, name).restype = ctypes.c_int
         L.moe_status_string.argtypes = [ctypes.c_int]
@@ -555,4 +565,6 @@ class MoELayer:
         return call[1]
 
 
-from .dense import GatedFFN, ffn, ffn_backward, ffn_kept_size, ffn_workspace_size  # noqa: E402,F401
+from .dense import (GatedFFN, LinearI8, ResidualNorm, ffn, ffn_backward, ffn_kept_size,  # noqa: E402,F401
+                    ffn_workspace_size, linear_i8, linear_i8_workspace_size, norm, norm_backward,
+                    norm_backward_workspace_size, quantize_i8)

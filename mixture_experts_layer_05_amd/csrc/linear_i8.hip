@@ -1,0 +1,197 @@
+// Products in 8-bit integers with a scale for each row of either operand:
+//   y = act(sx sw sum_k q[m, k] w[n, k] + bias) + residual
+// The sum is exact in int32; everything behind it is float32, rounded once to y's type.
+// Rows of x in 16 or 32 bits are quantised first (quant_i8_kernel), each by its largest
+// magnitude.
+#include "gemm.h"
+#include "rows.h"
+
+namespace moe {
+namespace {
+
+// ---------------------------------------------------------------- quantiser
+
+// A row of x to a workgroup: its largest magnitude, then its codes; the second reading
+// comes from the caches, which hold any row.
+template <bool F32>
+__global__ void __launch_bounds__(1024) quant_i8_kernel(const void* x, int64_t ldx, int K, int8_t* q, int64_t ldq, float* scale) {
+  __shared__ RowLds<uint32_t> lds;
+  const int64_t m = blockIdx.x;
+  const uint8_t* row = static_cast<const uint8_t*>(x) + m * ldx * (F32 ? 4 : 2);
+  const int waves = blockDim.x >> 6, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), step = 8 * blockDim.x;
+  uint32_t most[1] = {0};
+  const Raw8<F32> head = load8<F32>(row, 8 * threadIdx.x, K - 8 * static_cast<int>(threadIdx.x));
+  for (int i = 8 * threadIdx.x; i < K; i += step) {
+    const Raw8<F32> r = i < step ? head : load8<F32>(row, i, K - i);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) most[0] = max(most[0], __float_as_uint(value<F32>(r, e)) & 0x7fffffffu);
+  }
+  int turn = 0;
+  row_all(most, wave, waves, lds, turn, Most{});
+  const float s = i8_scale(most[0]), inv = 1.0f / s;
+  if (threadIdx.x == 0) scale[m] = s;
+  for (int i = 8 * threadIdx.x; i < K; i += step) {
+    const Raw8<F32> r = i < step ? head : load8<F32>(row, i, K - i);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = value<F32>(r, e);
+    store_codes(q + m * ldq + i, v, s, inv, K - i);
+  }
+}
+
+int quantise(bool f32, int M, int K, const void* x, int64_t ldx, int8_t* q, int64_t ldq, float* scale, hipStream_t s) {
+  const unsigned block = 64u * static_cast<unsigned>(std::min<int64_t>(16, ceil_div(K, 512)));
+  if (f32) quant_i8_kernel<true><<<static_cast<unsigned>(M), block, 0, s>>>(x, ldx, K, q, ldq, scale);
+  else quant_i8_kernel<false><<<static_cast<unsigned>(M), block, 0, s>>>(x, ldx, K, q, ldq, scale);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH_FAILED;
+}
+
+// ---------------------------------------------------------------- epilogue
+
+template <bool OUT32>
+struct I8Out {
+  static constexpr int kAhead = 4;
+  const float *sx, *sw;
+  const void *bias, *residual;
+  void* y;
+  int64_t ldr, ldy;
+  int M, N, act;
+  bool bias_f32;
+  template <int D>
+  __device__ __forceinline__ void quads(const int (&m)[D], int n, const f32x4 (&s)[D], const f32x4 (&)[D]) const {
+    const bool whole = n + 4 <= N;
+    f32x4 res[D], w = {0.f, 0.f, 0.f, 0.f}, b = {0.f, 0.f, 0.f, 0.f};
+    float x[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      res[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+      x[d] = m[d] < M ? sx[m[d]] : 0.0f;
+      if (residual && m[d] < M) {
+        const size_t o = static_cast<size_t>(m[d]) * ldr + n;
+        if (whole) res[d] = load4<OUT32>(residual, o);
+        else
+          for (int c = 0; c < 4; ++c)
+            if (n + c < N) res[d][c] = elem<OUT32>(residual, o + c);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (n + c < N) {
+        w[c] = sw[n + c];
+        if (bias) b[c] = bias_f32 ? elem<true>(bias, n + c) : elem<false>(bias, n + c);
+      }
+    float v[4 * D];
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[4 * d + c] = s[d][c] * x[d] * w[c] + b[c];
+    activate<!OUT32>(v, act);
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (m[d] >= M) continue;
+      const size_t o = static_cast<size_t>(m[d]) * ldy + n;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[4 * d + c] += res[d][c];
+      if (whole) {
+        store4<OUT32>(y, o, v + 4 * d);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (n + c < N) {
+            if constexpr (OUT32) static_cast<float*>(y)[o + c] = v[4 * d + c];
+            else static_cast<uint16_t*>(y)[o + c] = f32_to_bf16_bits(v[4 * d + c]);
+          }
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------- host
+
+bool plain(int d) { return d == MOE_DTYPE_F32 || d == MOE_DTYPE_BF16; }
+size_t size_of(int d) { return d == MOE_DTYPE_F32 ? 4 : d == MOE_DTYPE_BF16 ? 2 : 1; }
+bool off(const void* p, size_t unit) { return reinterpret_cast<uintptr_t>(p) % unit != 0; }
+constexpr int64_t kFar = int64_t{1} << 40;     // strides whose products with a row index stay in 64 bits
+
+int check_i8(const moe_linear_i8_config* c, int32_t rows) {
+  if (!c) return MOE_ERR_NULL_PTR;
+  if ((!plain(c->in_dtype) && c->in_dtype != MOE_DTYPE_I8) || !plain(c->bias_dtype) || !plain(c->out_dtype)) return MOE_ERR_BAD_DTYPE;
+  if (c->in_features <= 0 || c->out_features <= 0 || rows < 0) return MOE_ERR_BAD_SHAPE;
+  if (c->activation < MOE_ACT_NONE || c->activation > MOE_ACT_SILU) return MOE_ERR_BAD_SHAPE;
+  if (c->in_features > MOE_I8_MAX_FEATURES || c->out_features > MOE_LINEAR_MAX_FEATURES || rows > MOE_LINEAR_MAX_ROWS)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// The workspace: partial sums, then the codes of x in rows of whole 16-byte pieces, then
+// their scales.
+int64_t codes_ld(const moe_linear_i8_config& c) { return align_up(c.in_features, 16); }
+size_t codes_bytes(const moe_linear_i8_config& c, int64_t M) { return align_up(static_cast<size_t>(M) * codes_ld(c), 256); }
+size_t i8_workspace(const moe_linear_i8_config& c, int64_t M) {
+  return part_bytes(false, M, c.out_features) + (c.in_dtype == MOE_DTYPE_I8 ? 0 : codes_bytes(c, M) + align_up(M * 4, 256));
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_quant_i8(int32_t dtype, int32_t rows, int32_t columns, const void* x, int64_t ldx, int8_t* codes, int64_t ldc,
+                 float* scale, void* stream) {
+  if (!plain(dtype)) return MOE_ERR_BAD_DTYPE;
+  if (rows < 0 || columns <= 0) return MOE_ERR_BAD_SHAPE;
+  if (rows > MOE_LINEAR_MAX_ROWS || columns > MOE_LINEAR_MAX_FEATURES) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!x || !codes || !scale) return MOE_ERR_NULL_PTR;
+  if (ldx < columns || ldc < columns) return MOE_ERR_BAD_SHAPE;
+  if (ldx > kFar || ldc > kFar || off(x, size_of(dtype)) || off(scale, 4)) return MOE_ERR_UNSUPPORTED;
+  return quantise(dtype == MOE_DTYPE_F32, rows, columns, x, ldx, codes, ldc, scale, static_cast<hipStream_t>(stream));
+}
+
+int moe_linear_i8_workspace_size(const moe_linear_i8_config* cfg, int32_t max_rows, size_t* bytes) {
+  const int st = check_i8(cfg, max_rows);
+  if (st) return st;
+  if (!bytes) return MOE_ERR_NULL_PTR;
+  *bytes = i8_workspace(*cfg, max_rows);
+  return MOE_OK;
+}
+
+int moe_linear_i8(const moe_linear_i8_config* cfg, int32_t M, const void* x, int64_t ldx, const float* x_scale,
+                  const int8_t* w, int64_t ldw, const float* w_scale, const void* bias, const void* residual,
+                  int64_t ldr, void* y, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = check_i8(cfg, M);
+  if (st) return st;
+  if (M == 0) return MOE_OK;
+  const moe_linear_i8_config& c = *cfg;
+  const bool codes = c.in_dtype == MOE_DTYPE_I8;
+  if (!x || !w || !w_scale || !y || !workspace || (codes && !x_scale)) return MOE_ERR_NULL_PTR;
+  const int N = c.out_features, K = c.in_features;
+  if (ldx < K || ldw < K || ldy < N || (residual && ldr < N)) return MOE_ERR_BAD_SHAPE;
+  if (ldx > kFar || ldw > kFar || ldy > kFar || (residual && ldr > kFar)) return MOE_ERR_UNSUPPORTED;
+  if (residual == y && ldr != ldy) return MOE_ERR_BAD_SHAPE;
+  if (workspace_bytes < i8_workspace(c, M)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (off(x, size_of(c.in_dtype)) || off(x_scale, 4) || off(w_scale, 4) || off(bias, size_of(c.bias_dtype)) ||
+      off(residual, size_of(c.out_dtype)) || off(y, size_of(c.out_dtype)) || off(workspace, 16))
+    return MOE_ERR_UNSUPPORTED;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  float* part = static_cast<float*>(workspace);
+  Product g{{x, nullptr, ldx, 0, 0}, {w, nullptr, ldw, 0, 0}, M, N, K};
+  const float* sx = x_scale;
+  if (!codes) {
+    int8_t* q = static_cast<int8_t*>(workspace) + part_bytes(false, M, N);
+    float* qs = reinterpret_cast<float*>(q + codes_bytes(c, M));
+    const int bad = quantise(c.in_dtype == MOE_DTYPE_F32, M, K, x, ldx, q, codes_ld(c), qs, s);
+    if (bad) return bad;
+    g.a.p = q;
+    g.a.ld = codes_ld(c);
+    sx = qs;
+  }
+  const bool bf = c.bias_dtype == MOE_DTYPE_F32;
+  if (c.out_dtype == MOE_DTYPE_F32)
+    return run_product<El::I8, true, true, false>(g, I8Out<true>{sx, w_scale, bias, residual, y, ldr, ldy, M, N, c.activation, bf}, part, s);
+  return run_product<El::I8, true, true, false>(g, I8Out<false>{sx, w_scale, bias, residual, y, ldr, ldy, M, N, c.activation, bf}, part, s);
+}
+
+}  // extern "C"
