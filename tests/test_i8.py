@@ -1,0 +1,297 @@
+"""moe_quant_i8 and moe_linear_i8 against float64 on the host.
+
+Codes and scales are compared for equality: the scale is one float32 division, a code the
+rounding of an exact quotient.  Tolerance of a product, per element: the integer sum is
+exact, its conversion, two scales and the bias round to 2^-24 each (and every part of a
+split sum once more), the activations' slope is at most 1.13 and their own error at most
+2^-21 (|v| + 1); the residual's sum rounds to 2^-24, storing to half a step of y's type."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import mixture_experts_layer_05_amd as moe
+from mixture_experts_layer_05_amd.dense import _LinearI8Config
+
+OK, NULL_PTR, BAD_SHAPE, BAD_DTYPE, UNSUPPORTED, WS_SMALL = 0, -1, -2, -3, -4, -5
+FAKE = 0x1000
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+F32, BF16, I8 = 0, 1, 4
+
+
+# ----------------------------------------------------------------------------- refusals (no GPU)
+
+def _call(M=4, K=64, N=32, i=BF16, b=BF16, o=BF16, act=0, **kw):
+    p = dict(x=FAKE, ldx=K, xs=FAKE, w=FAKE, ldw=K, ws=FAKE, bias=None, residual=None, ldr=0, y=2 * FAKE, ldy=N,
+             work=FAKE, work_bytes=1 << 40)
+    p.update(kw)
+    c = _LinearI8Config(K, N, i, b, o, act)
+    return moe.lib().moe_linear_i8(ctypes.byref(c), M, p["x"], p["ldx"], p["xs"], p["w"], p["ldw"], p["ws"], p["bias"],
+                                   p["residual"], p["ldr"], p["y"], p["ldy"], p["work"], p["work_bytes"], None)
+
+
+def _quant(dtype=BF16, M=4, K=64, x=FAKE, ldx=64, q=FAKE, ldq=64, s=FAKE):
+    return moe.lib().moe_quant_i8(dtype, M, K, x, ldx, q, ldq, s, None)
+
+
+def test_refusals():
+    assert _call(M=0, x=None, w=None, ws=None, y=None, work=None) == OK
+    assert _call(M=-1) == BAD_SHAPE and _call(K=0) == BAD_SHAPE and _call(N=0) == BAD_SHAPE
+    assert _call(act=5) == BAD_SHAPE and _call(act=-1) == BAD_SHAPE
+    for kw in (dict(i=2), dict(i=3), dict(i=5), dict(b=4), dict(b=2), dict(o=4), dict(o=3)):
+        assert _call(**kw) == BAD_DTYPE
+    assert _call(M=(1 << 21) + 1) == UNSUPPORTED and _call(K=131072) == UNSUPPORTED and _call(N=(1 << 20) + 1) == UNSUPPORTED
+    for name in ("x", "w", "ws", "y", "work"):
+        assert _call(**{name: None}) == NULL_PTR
+    assert _call(i=I8, xs=None) == NULL_PTR
+    for kw in (dict(ldx=63), dict(ldw=63), dict(ldy=31), dict(residual=FAKE, ldr=31), dict(residual=2 * FAKE, ldr=33)):
+        assert _call(**kw) == BAD_SHAPE
+    far = (1 << 40) + 1
+    for kw in (dict(ldx=far), dict(ldw=far), dict(ldy=far), dict(residual=FAKE, ldr=far), dict(x=FAKE + 1),
+               dict(ws=FAKE + 2), dict(xs=FAKE + 2), dict(bias=FAKE + 1), dict(residual=FAKE + 1, ldr=32), dict(y=FAKE + 1),
+               dict(work=FAKE + 8)):
+        assert _call(**kw) == UNSUPPORTED, kw
+    assert _call(work_bytes=16) == WS_SMALL
+    assert _quant(M=0, x=None, q=None, s=None) == OK
+    assert _quant(M=-1) == BAD_SHAPE and _quant(K=0) == BAD_SHAPE and _quant(ldx=63) == BAD_SHAPE and _quant(ldq=63) == BAD_SHAPE
+    assert _quant(dtype=I8) == BAD_DTYPE and _quant(dtype=3) == BAD_DTYPE
+    assert _quant(x=None) == NULL_PTR and _quant(q=None) == NULL_PTR and _quant(s=None) == NULL_PTR
+    assert _quant(x=FAKE + 1) == UNSUPPORTED and _quant(s=FAKE + 2) == UNSUPPORTED and _quant(M=(1 << 21) + 1) == UNSUPPORTED
+
+
+def test_the_binding_checks_its_arguments():
+    w, s = torch.zeros(8, 4, dtype=torch.int8), torch.ones(8)
+    with pytest.raises(ValueError, match="activation"):
+        moe.LinearI8(w, s, activation="tanh")
+    with pytest.raises(ValueError, match="weight"):
+        moe.LinearI8(w.float(), s)
+    with pytest.raises(ValueError, match="weight_scale"):
+        moe.LinearI8(w, s[:7])
+    op = moe.LinearI8(w, s, max_rows=2)
+    for x in (torch.zeros(2, 4, dtype=torch.int8), torch.zeros(2, 4, dtype=torch.float16), (torch.zeros(2, 4), s[:2])):
+        with pytest.raises(ValueError, match="x:"):
+            op(x)
+    with pytest.raises(ValueError, match="sized for"):
+        op(torch.zeros(3, 4))
+    with pytest.raises(ValueError, match="GPU"):
+        op(torch.zeros(2, 4))
+    with pytest.raises(ValueError, match="x_scale"):
+        moe.linear_i8(torch.zeros(2, 4), w, s, None, None, torch.zeros(2, 8), torch.zeros(64), x_scale=s[:2])
+
+
+# ----------------------------------------------------------------------------- codes
+
+def _codes(x):
+    """(codes, scale) of the rows of x by the definition; the quotient of two float32
+    numbers that is not a tie lies further from one than float64 rounds."""
+    amax = x.float().abs().amax(dim=1)
+    s = (amax.double() / 127).float().clamp(min=2.0 ** -126)
+    q = (x.double() / s.double()[:, None]).round()
+    return q.to(torch.int8), s
+
+
+def _rows(M, K, dtype, seed, pad=0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(M, K + pad, generator=g) * torch.exp2(torch.randint(-20, 20, (M, 1), generator=g).float())
+    return x.to(DT[dtype])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,K,pad", [(1, 1, 0), (3, 7, 2), (5, 64, 0), (40, 513, 1), (7, 5120, 8), (2, 8193, 3), (3, 40000, 0)])
+def test_codes(M, K, pad, dtype):
+    print(f"\n[case] quant {M}x{K} {dtype} pad={pad}", flush=True)
+    x = _rows(M, K, dtype, M + K, pad)
+    want, ws = _codes(x[:, :K])
+    buf = torch.full((M, K + 5), 99, dtype=torch.int8, device="cuda")
+    q, s = moe.quantize_i8(x.cuda()[:, :K], buf[:, :K])
+    assert torch.equal(s.cpu(), ws) and torch.equal(q.cpu(), want)
+    assert (buf[:, K:] == 99).all()
+    q, s = moe.quantize_i8(x.cuda()[:, :K])
+    assert torch.equal(s.cpu(), ws) and torch.equal(q.cpu(), want)
+
+
+@pytest.mark.gpu
+def test_codes_at_the_borders():
+    """Values at (k + 1/2) s and the float32 numbers on either side of it."""
+    g = torch.Generator().manual_seed(5)
+    amax = torch.rand(200, 1, generator=g) * 10 + 1
+    s = (amax.double() / 127).float()
+    k = torch.randint(-126, 126, (200, 300), generator=g).float()
+    mid = (k + 0.5) * s
+    up, down = (torch.nextafter(mid, torch.full_like(mid, v)) for v in (math.inf, -math.inf))
+    x = torch.cat([amax, mid, up, down], dim=1)
+    want, ws = _codes(x)
+    q, got = moe.quantize_i8(x.cuda())
+    assert torch.equal(got.cpu(), ws) and torch.equal(q.cpu(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_codes_of_unusual_rows(dtype):
+    x = torch.zeros(7, 50)
+    x[1, 3] = 1e-39                                # below the smallest scale
+    x[2, 4], x[2, 7] = float("inf"), 3.0
+    x[3, 49] = float("nan")
+    x[4, 0], x[4, 1] = float("nan"), float("inf")
+    x[5] = -2.5
+    x[6, 9] = torch.finfo(DT[dtype]).max
+    q, s = moe.quantize_i8(x.to(DT[dtype]).cuda())
+    q, s = q.cpu(), s.cpu()
+    assert s[0] == 2.0 ** -126 and s[1] == 2.0 ** -126 and (q[:5] == 0).all()
+    assert s[2] == float("inf") and s[3].isnan() and s[4].isnan()
+    assert (q[5] == -127).all() and q[6, 9] == 127 and s[6].isfinite()
+
+
+# ----------------------------------------------------------------------------- products
+
+def _act64(v, name):
+    if name == "relu":
+        return v.clamp(min=0)
+    if name == "gelu":
+        return 0.5 * v * (1 + torch.erf(v / math.sqrt(2)))
+    if name == "gelu_tanh":
+        return 0.5 * v * (1 + torch.tanh(math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)))
+    if name == "silu":
+        return v * torch.sigmoid(v)
+    return v
+
+
+def _expect(q, sx, w, sw, b, r, act, o):
+    scale = sx.double()[:, None] * sw.double()
+    v = (q.double() @ w.double().t()) * scale
+    mag = (q.double().abs() @ w.double().abs().t()) * scale
+    tol = 2.0 ** -24 * (4 * v.abs() + 2 * mag)         # parts round their own sums
+    if b is not None:
+        v = v + b.double()
+        tol = tol + 2.0 ** -24 * v.abs()
+    y = _act64(v, act)
+    tol = 1.13 * tol + 2.0 ** -21 * (v.abs() + 1) * (act != "none")
+    if r is not None:
+        y = y + r.double()
+    return y, tol + (2.0 ** -24 + torch.finfo(DT[o]).eps / 2) * (y.abs() + tol)
+
+
+def _gpu(t):
+    if t is None:
+        return None
+    base = t if t._base is None else t._base
+    return base.cuda()[tuple(slice(0, n) for n in t.shape)]
+
+
+def _run(M, K, N, i, o, act="none", bias=None, residual=False, seed=0, pads=(0, 0, 0, 0), rows=None, low=-127):
+    print(f"\n[case] i8 {M}x{K}x{N} {i}->{o} {act} bias={bias} residual={residual} pads={pads}", flush=True)
+    g = torch.Generator().manual_seed(seed)
+    if i == "i8":
+        x = torch.randint(low, 128, (M, K + pads[0]), generator=g, dtype=torch.int8)[:, :K]
+        q, sx = x, torch.rand(M, generator=g) / 64 + 0.001
+    else:
+        x = _rows(M, K, i, seed, pads[0])[:, :K]
+        q, sx = _codes(x)
+    w = torch.randint(low, 128, (N, K + pads[1]), generator=g, dtype=torch.int8)[:, :K]
+    sw = torch.rand(N, generator=g) / 64 + 0.001
+    b = None if bias is None else torch.randn(N, generator=g).to(DT[bias])
+    r = torch.randn(M, N + pads[2], generator=g).to(DT[o])[:, :N] if residual else None
+    ws = torch.full((moe.linear_i8_workspace_size(K, N, M, i),), 0xFF, dtype=torch.uint8, device="cuda")
+    full = torch.full((M, N + pads[3]), 77.0, dtype=DT[o], device="cuda")
+    y = full[:, :N]
+    moe.linear_i8(_gpu(x), _gpu(w), sw.cuda(), _gpu(b), _gpu(r), y, ws, act, sx.cuda() if i == "i8" else None)
+    torch.cuda.synchronize()
+    assert (full[:, N:] == 77.0).all()
+    if rows is not None:
+        q, sx, r, y = q[rows], sx[rows], None if r is None else r[rows], y[rows.cuda()]
+    want, tol = _expect(q, sx, w, sw, b, r, act, o)
+    err = (y.cpu().double() - want).abs()
+    print(f"[case] worst error / tolerance {(err / tol).max():.3f}", flush=True)
+    assert (err <= tol).all()
+
+
+SIZES = [(1, 1, 1), (1, 5120, 64), (1, 128, 5120), (2, 16, 7), (3, 129, 33), (7, 640, 515), (15, 256, 48), (16, 128, 16),
+         (16, 4097, 31), (17, 64, 64), (33, 1000, 130), (64, 64, 64), (65, 2048, 100), (128, 512, 256), (129, 144, 257),
+         (224, 1280, 640), (257, 1023, 515), (300, 80, 1025), (1, 16384, 16), (40, 8192, 24)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("i,o", [("bf16", "bf16"), ("f32", "f32"), ("i8", "bf16"), ("i8", "f32")])
+@pytest.mark.parametrize("M,K,N", SIZES)
+def test_sizes(M, K, N, i, o):
+    _run(M, K, N, i, o, "silu", "bf16", True, seed=M + K + N)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("i,o,b", [("bf16", "bf16", "f32"), ("f32", "f32", "bf16")])
+@pytest.mark.parametrize("M", [3, 50, 300])
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+def test_epilogues(act, M, i, o, b):
+    for bias, residual in ((None, False), (b, False), (None, True)):
+        _run(M, 192, 160, i, o, act, bias, residual, seed=3)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("i,o", [("bf16", "bf16"), ("i8", "f32")])
+@pytest.mark.parametrize("pads", [(16, 0, 0, 0), (0, 16, 0, 8), (1, 0, 0, 0), (0, 3, 0, 0), (0, 0, 1, 3), (5, 5, 5, 5)])
+@pytest.mark.parametrize("M", [1, 9, 70, 400])
+def test_strides(M, pads, i, o):
+    _run(M, 320, 200, i, o, "gelu", "f32", True, seed=4, pads=pads)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K,N", [(1024, 1024, 2048), (2048, 4096, 1024), (1001, 1537, 2049), (4100, 528, 776)])
+@pytest.mark.parametrize("i,o", [("bf16", "bf16"), ("i8", "f32")])
+def test_large(M, K, N, i, o):
+    rows = torch.cat([torch.arange(0, 300), torch.arange(M - 300, M)])
+    _run(M, K, N, i, o, "gelu_tanh", "bf16", True, seed=5, rows=rows)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 40])
+def test_largest_sums(M):
+    """Codes of -128 over the longest contraction: 131071 x 2^14, just inside int32."""
+    x = torch.full((M, 131071), -128, dtype=torch.int8, device="cuda")
+    w = torch.full((3, 131071), -128, dtype=torch.int8, device="cuda")
+    ws = torch.empty(moe.linear_i8_workspace_size(131071, 3, M), dtype=torch.uint8, device="cuda")
+    y = torch.empty(M, 3, device="cuda")
+    one = torch.ones(M, device="cuda")
+    moe.linear_i8(x, w, torch.ones(3, device="cuda"), None, None, y, ws, x_scale=one)
+    want = 131071.0 * 2 ** 14
+    assert ((y.double() - want).abs() <= 2.0 ** -22 * want).all()
+
+
+@pytest.mark.gpu
+def test_in_place_on_the_residual_and_rows_that_are_not_finite():
+    x = _rows(9, 64, "bf16", 8)
+    x[4, 5] = float("nan")
+    w, sw = moe.quantize_i8(_rows(40, 64, "f32", 9).cuda())
+    op = moe.LinearI8(w, sw, max_rows=9)
+    r = torch.ones(9, 40, dtype=torch.bfloat16, device="cuda")
+    want = op(x.cuda(), r).clone()
+    assert want[4].isnan().all() and want[:4].isfinite().all() and want[5:].isfinite().all()
+    y = op(x.cuda(), r, out=r)
+    assert torch.equal(y.nan_to_num(7.0), want.nan_to_num(7.0)) and y.data_ptr() == r.data_ptr()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 130])
+def test_a_graph_and_another_stream_give_the_same(M):
+    x = _rows(M, 512, "bf16", 10).cuda()
+    w, sw = moe.quantize_i8(_rows(300, 512, "f32", 11).cuda())
+    op, other = (moe.LinearI8(w, sw, activation="silu", max_rows=M) for _ in range(2))
+    want = other(x).clone()
+    codes = other(moe.quantize_i8(x))
+    assert torch.equal(codes, want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = op(x, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = op(x)
+    for k in range(4):
+        got.fill_(float("nan"))
+        again = other(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(again, want), k
