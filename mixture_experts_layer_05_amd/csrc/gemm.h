@@ -7,6 +7,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "dense.h"
 #include "dma.h"
@@ -105,11 +106,11 @@ __device__ __forceinline__ uint2 lds_turned(const uint8_t* p) {
 // A part's sums are M rows of the first product's columns, then M of the second's.
 template <bool PAIR, int BN, int ROWS, int THREADS, class Epi, class RowOf>
 __device__ __forceinline__ void results_out(const Product& g, const Epi& epi, const float* stg, int stride, int n0,
-                                            int parts, int p, float* part, RowOf row_of) {
+                                            int parts, int p, float* part, int tid, RowOf row_of) {
   constexpr int kCols = PAIR ? BN / 2 : BN;
   constexpr int kLanes = kCols / 4, kIter = ROWS * kLanes / THREADS, D = Epi::kAhead < kIter ? Epi::kAhead : kIter;
   static_assert(THREADS % kLanes == 0 && kIter % D == 0, "a thread keeps its columns");
-  const int tid = threadIdx.x, c = 4 * (tid % kLanes), n = n0 + c;
+  const int c = 4 * (tid % kLanes), n = n0 + c;
   const int sc = PAIR ? (c >> 5) * 64 + (c & 31) : c;
   if (n >= g.N) return;
 #pragma unroll 1
@@ -342,10 +343,244 @@ __global__ void __launch_bounds__(256, 2) product_tile_kernel(Product g, Epi epi
       for (int j = 0; j < NJ; ++j)
         stg[(wm * 32 + 8 * (v >> 2) + 4 * hi + (v & 3)) * kStride + wn * (BN / 2) + 32 * j + r32] = static_cast<float>(acc[i][j][v]);
     __syncthreads();
-    results_out<kPair, BN, 64, 256>(g, epi, stg, kStride, n0, parts, p, part, [&](int R) {
+    results_out<kPair, BN, 64, 256>(g, epi, stg, kStride, n0, parts, p, part, tid, [&](int R) {
       return m0 + (R / 32) * (BM / 2) + 32 * i + R % 32;
     });
     __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- 256 x 256 tiles
+//
+// 256 x 256 sums per workgroup of four waves, one on each SIMD, 128 x 128 to a wave: a
+// stage's fragments leave LDS twice, not three times as with eight waves of 128 x 64.  A
+// stage is 64 bf16 (128 int8) of contraction, 64 KiB, double-buffered, and goes to LDS by
+// DMA.  A wave is alone on its SIMD, so nothing but its own instructions hides latencies:
+// the fragments of a quarter stage are read while the quarter before is multiplied, across
+// the stages' border too, and the DMA of stage s + 2 starts in the last quarter of s.
+// One barrier a stage, in front of that quarter: by then every wave has the stage's last
+// fragments in registers and stage s + 1 is in LDS.
+//
+// k-contiguous operands: rows of 128 bytes, 16-byte pieces permuted by (row / 2) mod 8.
+// k-strided: 512 bytes of each k, 64-byte pieces permuted by k mod 4, so that the four k
+// of a turning read lie in different quarters of the banks.
+constexpr int kWideTile = 256, kWideStage = 65536, kWideSide = 32768;
+constexpr int kWideBandRows = 8;
+// Results leave through LDS too, 32 rows of a wave at a time, in the buffer that the last
+// stage is not in; rows padded by 4 floats, so 2 KiB more on either side of the buffers.
+constexpr int kWideOut = 132, kWidePad = 2048, kWideLds = 2 * kWideStage + 2 * kWidePad;
+static_assert(4 * 32 * kWideOut * 4 <= kWideStage + kWidePad, "the staged rows fit");
+
+// One instruction: lane l loads 16 bytes at voff + soff to LDS at lds + 16 l.
+__device__ __forceinline__ void dma_line(i32x4_t rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %[lds]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[v], %[rs], %[so] offen lds"
+               :
+               : [v] "v"(voff), [rs] "s"(rsrc), [so] "s"(soff), [lds] "s"(lds)
+               : "memory");
+}
+
+// What a wave loads of one operand: eight instructions a stage.
+template <El E, bool KC, bool PAIR>
+struct WideSide {
+  using I = ElInfo<E>;
+  const uint8_t *p, *q;          // first row (k-contiguous) or column (k-strided) of the tile, k = 0
+  int64_t step;                  // bytes of a stage
+  uint32_t bytes;                // of the tile's part of a stage, from p on
+  uint32_t voff[8];
+  uint32_t row2;                 // k-strided: bytes of two k
+  int half;                      // k-strided pair: stages of p
+  __device__ __forceinline__ WideSide(const Operand& o, int r0, int rows, int wave, int lane) {
+    const uint32_t ld = static_cast<uint32_t>(o.ld) * I::kSize;
+    if constexpr (KC) {
+      constexpr int kRows = PAIR ? 128 : 256;
+      const int last = min(kRows, rows - r0) - 1;
+      p = static_cast<const uint8_t*>(o.p) + static_cast<size_t>(r0) * ld;
+      q = PAIR ? static_cast<const uint8_t*>(o.q) + static_cast<size_t>(r0) * ld : nullptr;
+      step = 128;
+      bytes = static_cast<uint32_t>(last) * ld + 128;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        // Row of the LDS side: 64 wave + 8 k + lane / 8; of a pair, 32 rows by turns.
+        const int row = PAIR ? 32 * wave + 8 * (k & 3) + (lane >> 3) : 64 * wave + 8 * k + (lane >> 3);
+        voff[k] = static_cast<uint32_t>(min(row, last)) * ld + ((lane & 7) ^ ((4 * (k & 1) + (lane >> 4)) & 7)) * 16;
+      }
+    } else {
+      p = static_cast<const uint8_t*>(o.p) + static_cast<size_t>(r0) * I::kSize;
+      q = PAIR ? static_cast<const uint8_t*>(o.q) + static_cast<size_t>(r0) * I::kSize : nullptr;
+      step = static_cast<int64_t>(I::kStage) * ld;
+      row2 = 2 * ld;
+      half = PAIR ? o.half / I::kStage : 0;
+      const int last = min(256, rows - r0) / I::kPiece - 1;    // pieces of a row of the tile
+      bytes = static_cast<uint32_t>(I::kStage - 1) * ld + static_cast<uint32_t>(last + 1) * 16;
+      // k of the stage: 16 wave + 2 i + lane / 32.
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = 16 * wave + 2 * h + (lane >> 5);
+        voff[h] = static_cast<uint32_t>(16 * wave + (lane >> 5)) * ld + min((lane & 31) ^ ((k & 3) << 2), last) * 16;
+      }
+    }
+  }
+  // The resource of a stage.
+  __device__ __forceinline__ i32x4_t rsrc(int ks, bool second) const {
+    if constexpr (KC) return dma_rsrc((PAIR && second ? q : p) + ks * step, bytes);
+    else if constexpr (PAIR) return dma_rsrc(ks < half ? p + ks * step : q + (ks - half) * step, bytes);
+    else return dma_rsrc(p + ks * step, bytes);
+  }
+  // Instruction k of the eight.
+  __device__ __forceinline__ void issue(const i32x4_t& r, int k, uint32_t lds) const {
+    if constexpr (KC) dma_line(r, voff[k], 0, lds + 1024 * k);
+    else dma_line(r, voff[k & 1], __builtin_amdgcn_readfirstlane(row2 * k), lds + 1024 * k);
+  }
+};
+
+template <El E, bool KA, bool KB, bool PAIR, class Epi>
+__global__ void __launch_bounds__(256, 1) product_wide_kernel(Product g, Epi epi, int parts, float* part) {
+  constexpr bool kPair = PAIR && KB;
+  constexpr int kCols = kPair ? 128 : 256;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kWideLds];
+  uint8_t* smem = lds + kWidePad;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1, r32 = lane & 31, hi = lane >> 5;
+  const int mt = static_cast<int>(ceil_div(g.M, 256)), nt = static_cast<int>(ceil_div(g.N, kCols));
+  const int stages = g.K / ElInfo<E>::kStage;
+  const uint32_t lds_a = __builtin_amdgcn_readfirstlane(lds_address(smem)) + 8192 * wave, lds_b = lds_a + kWideSide;
+
+  // Offsets of the wave's fragments in a side: k-contiguous by quarter (block x is 4 KiB
+  // on), k-strided by block (quarter kk is 8 KiB on).
+  uint32_t fa[4], fb[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const uint32_t kc = static_cast<uint32_t>(r32 * 128 + (((2 * x) ^ hi ^ ((r32 >> 1) & 7)) * 16));
+    const uint32_t s = (lane & 15) >> 2;
+    const uint32_t ks = (8 * hi + s) * 512 + ((x ^ s) * 64) + (r32 & 16) * 2 + 8 * (lane & 3);
+    fa[x] = KA ? kc + wm * 128 * 128 : ks + wm * 256;
+    fb[x] = (KB ? kc + wn * 128 * 128 : ks + wn * 256) + kWideSide;
+  }
+  auto frag = [&](const uint8_t* base, const uint32_t (&f)[4], int blk, int kk, auto kc) __attribute__((always_inline)) {
+    if constexpr (decltype(kc)::value) {
+      return *reinterpret_cast<const uint4*>(base + f[kk] + blk * 4096);
+    } else {
+      const uint8_t* t = base + f[blk] + kk * 8192;
+      const uint2 lo = lds_turned(t), up = lds_turned(t + 2048);
+      return uint4{lo.x, lo.y, up.x, up.y};
+    }
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
+
+  const XcdWalk walk(mt * nt * parts);
+  for (int item = walk.tile; item < walk.end; item += walk.step) {
+    const int tile = item / parts, p = item - tile * parts;
+    const int k0 = static_cast<int>(static_cast<int64_t>(p) * stages / parts), nk = static_cast<int>(static_cast<int64_t>(p + 1) * stages / parts);
+    const int band = tile / (kWideBandRows * nt), in_band = tile - band * kWideBandRows * nt;
+    const int bm = min(kWideBandRows, mt - band * kWideBandRows);
+    const int m0 = (band * kWideBandRows + in_band % bm) * 256, n0 = in_band / bm * kCols;
+    const WideSide<E, KA, false> A(g.a, m0, g.M, wave, lane);
+    const WideSide<E, KB, PAIR> B(g.b, n0, g.N, wave, lane);
+    auto dma_a = [&](int ks, uint32_t buf) __attribute__((always_inline)) {
+      const i32x4_t r = A.rsrc(ks, false);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) A.issue(r, k, lds_a + buf);
+    };
+    auto dma_b = [&](int ks, uint32_t buf) __attribute__((always_inline)) {
+      const i32x4_t r = B.rsrc(ks, false), r2 = kPair ? B.rsrc(ks, true) : r;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) B.issue(k < 4 ? r : r2, k, lds_b + buf);
+    };
+    __syncthreads();                 // the tile before is done with LDS
+    dma_a(k0, 0);
+    dma_b(k0, 0);
+    if (k0 + 1 < nk) {
+      dma_a(k0 + 1, kWideStage);
+      wait_vm<8>();
+    } else {
+      wait_vm<0>();
+    }
+    __syncthreads();
+    Acc<E> acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+    uint4 af[2][4], bf[2][4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      bf[0][x] = frag(smem, fb, x, 0, std::bool_constant<KB>{});
+      af[0][x] = frag(smem, fa, x, 0, std::bool_constant<KA>{});
+    }
+    // The 16 MFMAs of quarter kk, by twos; between them the fragments of the quarter after
+    // it (`read`) and eight instructions of a stage's DMA.
+    auto quarter = [&](int kk, const uint8_t* next, int nkk, auto read, auto dma) __attribute__((always_inline)) {
+      const int c = kk & 1, d = c ^ 1;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        if constexpr (decltype(read)::value) {
+          if (x < 4) bf[d][x] = frag(next, fb, x, nkk, std::bool_constant<KB>{});
+          else af[d][x - 4] = frag(next, fa, x - 4, nkk, std::bool_constant<KA>{});
+        }
+        dma(x);
+        const int i = x >> 1, j = 2 * (x & 1);
+        acc[i][j] = mfma32<E>(bf[c][j], af[c][i], acc[i][j]);
+        acc[i][j + 1] = mfma32<E>(bf[c][j + 1], af[c][i], acc[i][j + 1]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    const auto nothing = [](int) __attribute__((always_inline)) {};
+    // Stage ks; B of stage ks + 1 and A of stage ks + 2 are loaded meanwhile, where they are.
+    auto stage = [&](int ks, auto load_b, auto load_a) __attribute__((always_inline)) {
+      const uint32_t buf = static_cast<uint32_t>((ks - k0) & 1) * kWideStage, other = kWideStage - buf;
+      const uint8_t* here = smem + buf;
+      if constexpr (decltype(load_b)::value) {
+        const i32x4_t r = B.rsrc(ks + 1, false), r2 = kPair ? B.rsrc(ks + 1, true) : r;
+        quarter(0, here, 1, Yes{}, [&](int k) __attribute__((always_inline)) { B.issue(k < 4 ? r : r2, k, lds_b + other); });
+      } else {
+        quarter(0, here, 1, Yes{}, nothing);
+      }
+      quarter(1, here, 2, Yes{}, nothing);
+      quarter(2, here, 3, Yes{}, nothing);
+      if constexpr (decltype(load_b)::value) {
+        // The stage's last fragments are in registers, the next stage is in LDS.
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        const uint8_t* there = smem + other;
+        if constexpr (decltype(load_a)::value) {
+          const i32x4_t r = A.rsrc(ks + 2, false);
+          quarter(3, there, 0, Yes{}, [&](int k) __attribute__((always_inline)) { A.issue(r, k, lds_a + buf); });
+        } else {
+          quarter(3, there, 0, Yes{}, nothing);
+        }
+      } else {
+        quarter(3, here, 0, No{}, nothing);
+      }
+    };
+    int ks = k0;
+    for (; ks + 2 < nk; ++ks) stage(ks, Yes{}, Yes{});
+    if (ks + 1 < nk) stage(ks++, Yes{}, No{});
+    stage(ks, No{}, No{});
+
+    // Lane l, element v of a block (the operands' roles are exchanged): row l % 32, column
+    // 8 (v / 4) + 4 (l / 32) + v % 4.  A wave's staged rows are its own.
+    const uint32_t free_buf = ((ks - k0) & 1) ? 0 : kWidePad + kWideStage;
+    float* stg = reinterpret_cast<float*>(lds + free_buf) + wave * 32 * kWideOut;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          f32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(acc[i][j][4 * q + e]);
+          *reinterpret_cast<f32x4*>(stg + r32 * kWideOut + 32 * j + 8 * q + 4 * hi) = v;
+        }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      results_out<kPair, 128, 32, 64>(g, epi, stg, kWideOut, n0 + wn * (kPair ? 64 : 128), parts, p, part, lane,
+                                      [&](int R) { return m0 + wm * 128 + 32 * i + R; });
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
   }
 }
 
@@ -364,7 +599,7 @@ struct TilePlan {
 
 // The cheapest tile and split by an estimate in microseconds: what a CU takes in, the
 // f32 matrix rate, and the partial sums' way out and back.
-inline TilePlan plan_tiles(El e, bool pair, int64_t M, int64_t N, int64_t K) {
+inline TilePlan plan_tiles(El e, bool pair, bool wide, int64_t M, int64_t N, int64_t K) {
   const int size = e == El::F32 ? 4 : e == El::BF16 ? 2 : 1;
   const int64_t width = pair ? 2 * N : N, stages = ceil_div(K * size, 128);
   static const struct { int rows, cols; } kTiles[] = {{64, 128}, {128, 128}};
@@ -385,6 +620,16 @@ inline TilePlan plan_tiles(El e, bool pair, int64_t M, int64_t N, int64_t K) {
         least = us;
         best = TilePlan{t.rows, t.cols, tiles, parts};
       }
+    }
+  }
+  for (int parts = 1; wide && parts <= kMaxParts; ++parts) {
+    const int64_t tiles = ceil_div(M, 256) * ceil_div(width, 256);
+    const int64_t planes = parts * M * (pair ? 2 : 1) * part_stride(N) * 4;
+    if (parts > 1 && (tiles * parts > kCus || planes > static_cast<int64_t>(kMaxPartBytes) || stages / parts < 4)) break;
+    const double us = ceil_div(tiles * parts, kCus) * (1.15 * ceil_div(stages, parts) + 6) + 2 + (parts > 1 ? 4 + planes * 2 / 5e6 : 0);
+    if (us < least) {
+      least = us;
+      best = TilePlan{256, 256, tiles, parts};
     }
   }
   return best;
@@ -410,13 +655,29 @@ void launch_tiles(const Product& g, const Epi& epi, const TilePlan& t, float* pa
   else product_tile_kernel<E, KA, KB, PAIR, ANY, 128, 128><<<grid, 256, 0, s>>>(g, epi, t.parts, part);
 }
 
+// Whole stages, and rows whose offsets in a tile are 32-bit.
+template <El E, bool KB, bool PAIR>
+bool fits_wide(const Product& g) {
+  constexpr int kStage = ElInfo<E>::kStage;
+  const int64_t far = int64_t{1} << 24;
+  return g.K % kStage == 0 && g.a.ld * ElInfo<E>::kSize < far && g.b.ld * ElInfo<E>::kSize < far &&
+         (KB || !PAIR || (g.b.half % kStage == 0 && g.b.live == g.b.half));
+}
+
 // Runs a product of M, N, K >= 1; `part` holds part_bytes(pair, M, N).
 template <El E, bool KA, bool KB, bool PAIR, class Epi>
 int run_product(const Product& g, const Epi& epi, float* part, hipStream_t s) {
   constexpr bool kPair = PAIR && KB;
   const bool aligned = aligned16(g.a, E, KA, g.M, g.K) && aligned16(g.b, E, KB, g.N, g.K);
-  const TilePlan t = plan_tiles(E, kPair, g.M, g.N, g.K);
-  if (aligned) launch_tiles<E, KA, KB, PAIR, false>(g, epi, t, part, s);
+  bool wide = false;
+  if constexpr (E != El::F32) wide = aligned && fits_wide<E, KB, PAIR>(g);
+  const TilePlan t = plan_tiles(E, kPair, wide, g.M, g.N, g.K);
+  if (t.rows == 256) {
+    if constexpr (E != El::F32) {
+      const unsigned grid = static_cast<unsigned>(std::min<int64_t>(kCus, ceil_div(t.tiles * t.parts, 8) * 8));
+      product_wide_kernel<E, KA, KB, PAIR><<<grid, 256, 0, s>>>(g, epi, t.parts, part);
+    }
+  } else if (aligned) launch_tiles<E, KA, KB, PAIR, false>(g, epi, t, part, s);
   else launch_tiles<E, KA, KB, PAIR, true>(g, epi, t, part, s);
   if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
   if (t.parts > 1) {
