@@ -80,6 +80,60 @@ __device__ __forceinline__ void store4(void* p, size_t i, const float* v) {
   }
 }
 
+// The first `left` of four neighbouring elements as they lie in memory, zeros behind them.
+template <bool F32>
+struct Raw4 {
+  uint32_t v[F32 ? 4 : 2];
+};
+template <bool F32>
+__device__ __forceinline__ Raw4<F32> raw4(const void* p, size_t i, int left) {
+  typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+  typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+  Raw4<F32> r;
+  if constexpr (F32) {
+    const uint32_t* q = static_cast<const uint32_t*>(p) + i;
+    if (left >= 4) {
+      const u32x4_any v = *reinterpret_cast<const u32x4_any*>(q);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) r.v[c] = v[c];
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) r.v[c] = c < left ? q[c] : 0u;
+    }
+  } else {
+    const uint16_t* q = static_cast<const uint16_t*>(p) + i;
+    if (left >= 4) {
+      const u32x2_any v = *reinterpret_cast<const u32x2_any*>(q);
+      r.v[0] = v.x;
+      r.v[1] = v.y;
+    } else {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        r.v[c] = (2 * c < left ? q[2 * c] : 0u) | (2 * c + 1 < left ? static_cast<uint32_t>(q[2 * c + 1]) << 16 : 0u);
+    }
+  }
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ float value4(const Raw4<F32>& r, int c) {
+  if constexpr (F32) return __uint_as_float(r.v[c]);
+  else return __uint_as_float((c & 1) ? r.v[c >> 1] & 0xffff0000u : r.v[c >> 1] << 16);
+}
+// The first `left` of four elements.
+template <bool F32>
+__device__ __forceinline__ void put4(void* p, size_t i, const float* v, int left) {
+  if (left >= 4) {
+    store4<F32>(p, i, v);
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (c < left) {
+      if constexpr (F32) static_cast<float*>(p)[i + c] = v[c];
+      else static_cast<uint16_t*>(p)[i + c] = f32_to_bf16_bits(v[c]);
+    }
+}
+
 // Eight bf16 of a row, of which it holds the first n more (ANY: 2-byte aligned).
 template <bool ANY>
 __device__ __forceinline__ uint4 ld8_bf16(const uint16_t* p, int n) {

@@ -58,36 +58,37 @@ __device__ __forceinline__ void act_slope(float v, int act, float& f, float& d) 
   }
 }
 
+struct None {};
+
 // h = act(g) u, and a and b where they are kept; their rows lie `ld`, a multiple of four,
 // apart, so that a whole quad may be written at their ends.
 template <bool F32, bool KEEP>
 struct GatedOut {
-  static constexpr int kAhead = 2;
+  static constexpr int kAhead = 4;
+  using Cols = None;
+  using Ahead = None;
   void* h;
   float *a, *b;
   int64_t ld;
-  int M, N, act;
-  template <int D>
-  __device__ __forceinline__ void quads(const int (&m)[D], int n, const f32x4 (&g)[D], const f32x4 (&u)[D]) const {
+  int N, act;
+  __device__ __forceinline__ None cols(int) const { return {}; }
+  __device__ __forceinline__ None ahead(int, int) const { return {}; }
+  __device__ __forceinline__ void put(int m, int n, const f32x4& g, const f32x4& u, None, None) const {
+    float h4[4], a4[4], b4[4];
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-      if (m[d] >= M) continue;
-      float h4[4], a4[4], b4[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float f, df;
-        act_slope<!F32>(g[d][c], act, f, df);
-        const bool in = n + c < N;
-        a4[c] = in ? f : 0.0f;
-        h4[c] = in ? f * u[d][c] : 0.0f;
-        b4[c] = in ? u[d][c] * df : 0.0f;
-      }
-      const size_t o = static_cast<size_t>(m[d]) * ld + n;
-      store4<F32>(h, o, h4);
-      if constexpr (KEEP) {
-        store4<true>(a, o, a4);
-        store4<true>(b, o, b4);
-      }
+    for (int c = 0; c < 4; ++c) {
+      float f, df;
+      act_slope<!F32>(g[c], act, f, df);
+      const bool in = n + c < N;
+      a4[c] = in ? f : 0.0f;
+      h4[c] = in ? f * u[c] : 0.0f;
+      b4[c] = in ? u[c] * df : 0.0f;
+    }
+    const size_t o = static_cast<size_t>(m) * ld + n;
+    store4<F32>(h, o, h4);
+    if constexpr (KEEP) {
+      store4<true>(a, o, a4);
+      store4<true>(b, o, b4);
     }
   }
 };
@@ -96,40 +97,35 @@ struct GatedOut {
 template <bool F32>
 struct SlopesOut {
   static constexpr int kAhead = 4;
+  using Cols = None;
+  struct Ahead {
+    f32x4 a, b;
+  };
   const float *a, *b;
   void* d;
   int64_t ld;
-  int M, N;
-  template <int D>
-  __device__ __forceinline__ void quads(const int (&m)[D], int n, const f32x4 (&s)[D], const f32x4 (&)[D]) const {
-    f32x4 va[D], vb[D];
+  int N;
+  __device__ __forceinline__ None cols(int) const { return {}; }
+  __device__ __forceinline__ Ahead ahead(int m, int n) const {
+    const size_t o = static_cast<size_t>(m) * ld + n;
+    return {load4<true>(a, o), load4<true>(b, o)};
+  }
+  __device__ __forceinline__ void put(int m, int n, const f32x4& s, const f32x4&, None, const Ahead& k) const {
+    float g4[4], u4[4];
 #pragma unroll
-    for (int i = 0; i < D; ++i) {
-      va[i] = vb[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (m[i] < M) {
-        va[i] = load4<true>(a, static_cast<size_t>(m[i]) * ld + n);
-        vb[i] = load4<true>(b, static_cast<size_t>(m[i]) * ld + n);
-      }
+    for (int c = 0; c < 4; ++c) {
+      const bool in = n + c < N;
+      g4[c] = in ? s[c] * k.b[c] : 0.0f;
+      u4[c] = in ? s[c] * k.a[c] : 0.0f;
     }
-#pragma unroll
-    for (int i = 0; i < D; ++i) {
-      if (m[i] >= M) continue;
-      float g4[4], u4[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const bool in = n + c < N;
-        g4[c] = in ? s[i][c] * vb[i][c] : 0.0f;
-        u4[c] = in ? s[i][c] * va[i][c] : 0.0f;
-      }
-      const size_t o = static_cast<size_t>(m[i]) * 2 * ld + n;
-      store4<F32>(d, o, g4);
-      store4<F32>(d, o + ld, u4);
-      // Both halves are contracted to their rows' ends.
-      if (n + 4 >= N && n + 4 < ld) {
-        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-        store4<F32>(d, o + 4, zero);
-        store4<F32>(d, o + ld + 4, zero);
-      }
+    const size_t o = static_cast<size_t>(m) * 2 * ld + n;
+    store4<F32>(d, o, g4);
+    store4<F32>(d, o + ld, u4);
+    // Both halves are contracted to their rows' ends.
+    if (n + 4 >= N && n + 4 < ld) {
+      const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+      store4<F32>(d, o + 4, zero);
+      store4<F32>(d, o + ld + 4, zero);
     }
   }
 };
@@ -139,29 +135,18 @@ struct SlopesOut {
 template <bool F32>
 struct RowsOut {
   static constexpr int kAhead = 4;
+  using Cols = None;
+  using Ahead = None;
   void *y, *y2;
   int64_t ld;
-  int M, N, half, live;
-  template <int D>
-  __device__ __forceinline__ void quads(const int (&m)[D], int n, const f32x4 (&s)[D], const f32x4 (&)[D]) const {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      const int r = m[d] < half ? m[d] : m[d] - half;
-      if (m[d] >= M || r >= live) continue;
-      void* out = m[d] < half ? y : y2;
-      const size_t o = static_cast<size_t>(r) * ld + n;
-      float v[4] = {s[d][0], s[d][1], s[d][2], s[d][3]};
-      if (n + 4 <= N) {
-        store4<F32>(out, o, v);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (n + c < N) {
-            if constexpr (F32) static_cast<float*>(out)[o + c] = v[c];
-            else static_cast<uint16_t*>(out)[o + c] = f32_to_bf16_bits(v[c]);
-          }
-      }
-    }
+  int N, half, live;
+  __device__ __forceinline__ None cols(int) const { return {}; }
+  __device__ __forceinline__ None ahead(int, int) const { return {}; }
+  __device__ __forceinline__ void put(int m, int n, const f32x4& s, const f32x4&, None, None) const {
+    const int r = m < half ? m : m - half;
+    if (r >= live) return;
+    const float v[4] = {s[0], s[1], s[2], s[3]};
+    put4<F32>(m < half ? y : y2, static_cast<size_t>(r) * ld + n, v, N - n);
   }
 };
 
@@ -196,18 +181,18 @@ size_t h_bytes(const moe_ffn_config& c, int64_t T) { return align_up(static_cast
 size_t slope_bytes(const moe_ffn_config& c, int64_t T) { return align_up(static_cast<size_t>(T) * inner_ld(c) * 4, 256); }
 size_t kept_bytes(const moe_ffn_config& c, int64_t T) { return h_bytes(c, T) + 2 * slope_bytes(c, T); }
 
+// The down projection of a few rows streams its weights as any product of a few rows.
 moe_linear_config down_config(const moe_ffn_config& c) {
   return moe_linear_config{c.intermediate_size, c.hidden_size, c.dtype, c.dtype, MOE_ACT_NONE};
 }
 
 // The workspace: partial sums, then h (forward) or [dg du] (backward).
 size_t ffn_parts(const moe_ffn_config& c, int64_t T) {
+  const int64_t H = c.hidden_size, Ip = inner_ld(c);
   const moe_linear_config down = down_config(c);
   size_t n = 0;
-  moe_linear_workspace_size(&down, static_cast<int32_t>(T), &n);
-  const int64_t H = c.hidden_size, Ip = inner_ld(c);
-  n = std::max(n, part_bytes(true, T, c.intermediate_size));
-  n = std::max({n, part_bytes(false, T, Ip), part_bytes(false, T, H), part_bytes(false, 2 * Ip, H), part_bytes(false, H, Ip)});
+  moe_linear_workspace_size(&down, static_cast<int32_t>(std::min<int64_t>(T, kSkinnyRows)), &n);
+  n = std::max({n, part_bytes(true, T, Ip), part_bytes(false, T, Ip), part_bytes(false, T, H), part_bytes(false, 2 * Ip, H), part_bytes(false, H, Ip)});
   return align_up(n, 256);
 }
 size_t ffn_workspace(const moe_ffn_config& c, int64_t T, bool backward) {
@@ -230,9 +215,13 @@ int ffn_forward(const moe_ffn_config& c, int T, const FfnArgs& f, void* y, int64
   const int64_t Ip = inner_ld(c);
   const Product g{{f.x, nullptr, f.ldx, 0, 0}, {f.wg, f.wu, H, 0, 0}, T, I, H};
   float* part = reinterpret_cast<float*>(ws);
-  const int st = a ? run_product<E, true, true, true>(g, GatedOut<F32, true>{h, a, b, Ip, T, I, c.activation}, part, s)
-                   : run_product<E, true, true, true>(g, GatedOut<F32, false>{h, a, b, Ip, T, I, c.activation}, part, s);
+  const int st = a ? run_product<E, true, true, true>(g, GatedOut<F32, true>{h, a, b, Ip, I, c.activation}, part, s)
+                   : run_product<E, true, true, true>(g, GatedOut<F32, false>{h, a, b, Ip, I, c.activation}, part, s);
   if (st) return st;
+  if (T > kSkinnyRows) {
+    const Product d{{h, nullptr, Ip, 0, 0}, {f.wd, nullptr, I, 0, 0}, T, H, I};
+    return run_product<E, true, true, false>(d, RowsOut<F32>{y, nullptr, ldy, H, T, T}, part, s);
+  }
   const moe_linear_config down = down_config(c);
   return moe_linear(&down, T, h, Ip, f.wd, I, nullptr, nullptr, 0, y, ldy, ws, ffn_parts(c, T), s);
 }
@@ -248,19 +237,19 @@ int ffn_backward(const moe_ffn_config& c, int T, const FfnArgs& f, const void* h
   int st = MOE_OK;
   if (dwd) {
     const Product g{{dy, nullptr, lddy, 0, 0}, {h, nullptr, Ip, 0, 0}, H, I, T};
-    st = run_product<E, false, false, false>(g, RowsOut<F32>{dwd, nullptr, I, H, I, H, H}, part, s);
+    st = run_product<E, false, false, false>(g, RowsOut<F32>{dwd, nullptr, I, I, H, H}, part, s);
   }
   if (st == MOE_OK && (dx || dwg)) {
     const Product g{{dy, nullptr, lddy, 0, 0}, {f.wd, nullptr, I, 0, 0}, T, I, H};
-    st = run_product<E, true, false, false>(g, SlopesOut<F32>{a, b, d, Ip, T, I}, part, s);
+    st = run_product<E, true, false, false>(g, SlopesOut<F32>{a, b, d, Ip, I}, part, s);
   }
   if (st == MOE_OK && dwg) {
     const Product g{{d, nullptr, 2 * Ip, 0, 0}, {f.x, nullptr, f.ldx, 0, 0}, 2 * Ip, H, T};
-    st = run_product<E, false, false, false>(g, RowsOut<F32>{dwg, dwu, H, 2 * Ip, H, Ip, I}, part, s);
+    st = run_product<E, false, false, false>(g, RowsOut<F32>{dwg, dwu, H, H, Ip, I}, part, s);
   }
   if (st == MOE_OK && dx) {
     const Product g{{d, nullptr, 2 * Ip, 0, 0}, {f.wg, f.wu, H, Ip, I}, T, H, 2 * Ip};
-    st = run_product<E, true, false, true>(g, RowsOut<F32>{dx, nullptr, lddx, T, H, T, T}, part, s);
+    st = run_product<E, true, false, true>(g, RowsOut<F32>{dx, nullptr, lddx, H, T, T}, part, s);
   }
   return st;
 }

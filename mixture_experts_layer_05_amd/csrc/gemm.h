@@ -90,6 +90,10 @@ __device__ __forceinline__ Acc<E> mfma32(const uint4& a, const uint4& b, Acc<E> 
   }
 }
 
+// A sum as it is staged (by value: a bit cast of a vector's element takes element 0).
+__device__ __forceinline__ float as_float(float v) { return v; }
+__device__ __forceinline__ float as_float(int v) { return __int_as_float(v); }
+
 // Two reads of 64 bits, each of which turns a 4 (k) x 16 block of a k-strided operand
 // between the 16 lanes that address it: lane i gets column i's four elements.
 __device__ __forceinline__ uint2 lds_turned(const uint8_t* p) {
@@ -99,42 +103,72 @@ __device__ __forceinline__ uint2 lds_turned(const uint8_t* p) {
 }
 
 // ---------------------------------------------------------------- results
+//
+// An epilogue takes four neighbouring columns of a row at a time:
+//   Cols cols(n)                  what it needs of columns n to n + 3
+//   Ahead ahead(m, n)             what it reads of row m there, as loaded
+//   put(m, n, s, u, cols, ahead)  the results of the sums s (and u, of a pair)
+//   kAhead                        the rows of a batch in 256 x 256 tiles, by its registers
+// Rows past the end are left out by its caller.
+
+// The rows behind D rows of staged sums, from row R on, and what is read for them.
+template <class Epi, int D>
+struct Batch {
+  int m[D];
+  typename Epi::Ahead a[D];
+  template <class RowOf>
+  __device__ __forceinline__ void load(const Epi& epi, int M, int n, int R, int step, RowOf row_of) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      m[d] = row_of(R + d * step);
+      if (m[d] < M) a[d] = epi.ahead(m[d], n);
+    }
+  }
+};
 
 // ROWS x BN sums in LDS, rows `stride` floats apart, to the epilogue or to part p's sums:
-// row_of(R) is the row of the product behind row R.  Whole row segments, four columns to
-// a thread.  A PAIR's columns take turns, 32 of the first product and 32 of the second.
-// A part's sums are M rows of the first product's columns, then M of the second's.
-template <bool PAIR, int BN, int ROWS, int THREADS, class Epi, class RowOf>
-__device__ __forceinline__ void results_out(const Product& g, const Epi& epi, const float* stg, int stride, int n0,
-                                            int parts, int p, float* part, int tid, RowOf row_of) {
-  constexpr int kCols = PAIR ? BN / 2 : BN;
-  constexpr int kLanes = kCols / 4, kIter = ROWS * kLanes / THREADS, D = Epi::kAhead < kIter ? Epi::kAhead : kIter;
+// row_of(R) is the row of the product behind row R, and `from` the first of these rows.
+// Whole row segments, four columns to a thread.  A PAIR's columns take turns, 32 of the
+// first product and 32 of the second.  A part's sums go to part_of(R), those of the second
+// product `second` floats on; null leaves a row out.  Sums of 8-bit products are staged as
+// the integers they are.  What the epilogue reads for D rows is in flight while D others are finished: `now`
+// holds what it reads for the first, and then for the D rows behind the last (if `more`).
+template <El E, bool PAIR, int BN, int ROWS, int THREADS, int D, class Epi, class RowOf, class PartOf>
+__device__ __forceinline__ void results_out(const Product& g, const Epi& epi, const typename Epi::Cols& cols, Batch<Epi, D>& now,
+                                            const float* stg, int stride, int n, int tid, int from, bool more, RowOf row_of,
+                                            bool cut, PartOf part_of, size_t second) {
+  constexpr int kLanes = (PAIR ? BN / 2 : BN) / 4, kIter = ROWS * kLanes / THREADS, kStep = THREADS / kLanes;
   static_assert(THREADS % kLanes == 0 && kIter % D == 0, "a thread keeps its columns");
-  const int c = 4 * (tid % kLanes), n = n0 + c;
-  const int sc = PAIR ? (c >> 5) * 64 + (c & 31) : c;
   if (n >= g.N) return;
+  const int c = 4 * (tid % kLanes), sc = PAIR ? (c >> 5) * 64 + (c & 31) : c;
 #pragma unroll 1
   for (int k = 0; k < kIter; k += D) {
-    int m[D];
+    const int R = tid / kLanes + k * kStep;
     f32x4 s[D], u[D];
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      const int R = (tid + (k + d) * THREADS) / kLanes;
-      m[d] = row_of(R);
-      s[d] = *reinterpret_cast<const f32x4*>(stg + R * stride + sc);
-      if constexpr (PAIR) u[d] = *reinterpret_cast<const f32x4*>(stg + R * stride + sc + 32);
-    }
-    if (parts > 1) {
-      const size_t np = part_stride(g.N), plane = static_cast<size_t>(p) * g.M * (PAIR ? 2 : 1);
+      s[d] = *reinterpret_cast<const f32x4*>(stg + (R + d * kStep) * stride + sc);
+      if constexpr (PAIR) u[d] = *reinterpret_cast<const f32x4*>(stg + (R + d * kStep) * stride + sc + 32);
+      if constexpr (E == El::I8)
 #pragma unroll
-      for (int d = 0; d < D; ++d)
-        if (m[d] < g.M) {
-          *reinterpret_cast<f32x4*>(part + (plane + m[d]) * np + n) = s[d];
-          if constexpr (PAIR) *reinterpret_cast<f32x4*>(part + (plane + g.M + m[d]) * np + n) = u[d];
-        }
-    } else {
-      epi.template quads<D>(m, n, s, u);
+        for (int e = 0; e < 4; ++e) s[d][e] = static_cast<float>(__float_as_int(s[d][e]));
     }
+    if (cut) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        float* q = part_of(from + R + d * kStep);
+        if (!q) continue;
+        *reinterpret_cast<f32x4*>(q) = s[d];
+        if constexpr (PAIR) *reinterpret_cast<f32x4*>(q + second) = u[d];
+      }
+      continue;
+    }
+    Batch<Epi, D> next;
+    if (more || k + D < kIter) next.load(epi, g.M, n, from + R + D * kStep, kStep, row_of);
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (now.m[d] < g.M) epi.put(now.m[d], n, s[d], u[d], cols, now.a[d]);
+    now = next;
   }
 }
 
@@ -147,7 +181,7 @@ __global__ void __launch_bounds__(256) product_sum_kernel(Product g, Epi epi, in
   const int64_t plane = static_cast<int64_t>(g.M) * quads;
   if (i >= plane) return;
   const f32x4* v = reinterpret_cast<const f32x4*>(part) + i;
-  f32x4 s[1] = {{0.f, 0.f, 0.f, 0.f}}, u[1] = {{0.f, 0.f, 0.f, 0.f}};
+  f32x4 s = {0.f, 0.f, 0.f, 0.f}, u = {0.f, 0.f, 0.f, 0.f};
   for (int p = 0; p < parts; p += kSumAhead) {
     f32x4 b[kSumAhead], c[kSumAhead];
 #pragma unroll
@@ -161,12 +195,12 @@ __global__ void __launch_bounds__(256) product_sum_kernel(Product g, Epi epi, in
       if (p + k < parts)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[0][e] += b[k][e];
-          if constexpr (PAIR) u[0][e] += c[k][e];
+          s[e] += b[k][e];
+          if constexpr (PAIR) u[e] += c[k][e];
         }
   }
-  const int m[1] = {static_cast<int>(i / quads)};
-  epi.template quads<1>(m, 4 * static_cast<int>(i - static_cast<int64_t>(m[0]) * quads), s, u);
+  const int m = static_cast<int>(i / quads), n = 4 * static_cast<int>(i - static_cast<int64_t>(m) * quads);
+  epi.put(m, n, s, u, epi.cols(n), epi.ahead(m, n));
 }
 
 // ---------------------------------------------------------------- tiles of any alignment
@@ -334,6 +368,20 @@ __global__ void __launch_bounds__(256, 2) product_tile_kernel(Product g, Epi epi
   // Out through LDS, NI rounds of 32 rows of each wave row, rows padded by 8 floats.
   // Lane l, element v: row 8 (v / 4) + 4 (l / 32) + v % 4, column l % 32 of a block.
   float* stg = reinterpret_cast<float*>(smem);
+  const int n = n0 + 4 * (tid % (kCols / 4));
+  const auto row_of = [&](int R) { return m0 + (R >> 5 & 1) * (BM / 2) + 32 * (R >> 6) + (R & 31); };
+  typename Epi::Cols cols;
+  Batch<Epi, 4> ahead;
+  if (parts == 1 && n < g.N) {
+    cols = epi.cols(n);
+    ahead.load(epi, g.M, n, tid / (kCols / 4), 256 / (kCols / 4), row_of);
+  }
+  // A part: M rows of the first product's columns, then M of the second's.
+  const size_t np = part_stride(g.N), second = static_cast<size_t>(g.M) * np;
+  const auto part_of = [&](int R) {
+    const int m = row_of(R);
+    return m < g.M ? part + (static_cast<size_t>(p) * g.M * (kPair ? 2 : 1) + m) * np + n : nullptr;
+  };
   __syncthreads();                   // every wave is done reading the stage buffers
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
@@ -341,11 +389,9 @@ __global__ void __launch_bounds__(256, 2) product_tile_kernel(Product g, Epi epi
     for (int v = 0; v < 16; ++v)
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
-        stg[(wm * 32 + 8 * (v >> 2) + 4 * hi + (v & 3)) * kStride + wn * (BN / 2) + 32 * j + r32] = static_cast<float>(acc[i][j][v]);
+        stg[(wm * 32 + 8 * (v >> 2) + 4 * hi + (v & 3)) * kStride + wn * (BN / 2) + 32 * j + r32] = as_float(acc[i][j][v]);
     __syncthreads();
-    results_out<kPair, BN, 64, 256>(g, epi, stg, kStride, n0, parts, p, part, tid, [&](int R) {
-      return m0 + (R / 32) * (BM / 2) + 32 * i + R % 32;
-    });
+    results_out<E, kPair, BN, 64, 256, 4>(g, epi, cols, ahead, stg, kStride, n, tid, 64 * i, i + 1 < NI, row_of, parts > 1, part_of, second);
     __syncthreads();
   }
 }
@@ -433,8 +479,18 @@ struct WideSide {
   }
 };
 
+// Tiles are walked in bands of 8 row blocks, so that the 32 tiles that run on an XCD at a
+// time share 8 row blocks and 4 column blocks in its L2.
+template <int COLS>
+__device__ __forceinline__ void wide_place(int tile, int mt, int nt, int& m0, int& n0) {
+  const int band = tile / (kWideBandRows * nt), in_band = tile - band * kWideBandRows * nt;
+  const int bm = min(kWideBandRows, mt - band * kWideBandRows);
+  m0 = (band * kWideBandRows + in_band % bm) * 256;
+  n0 = in_band / bm * COLS;
+}
+
 template <El E, bool KA, bool KB, bool PAIR, class Epi>
-__global__ void __launch_bounds__(256, 1) product_wide_kernel(Product g, Epi epi, int parts, float* part) {
+__global__ void __launch_bounds__(256, 1) product_wide_kernel(Product g, Epi epi, int whole, int parts, float* part) {
   constexpr bool kPair = PAIR && KB;
   constexpr int kCols = kPair ? 128 : 256;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kWideLds];
@@ -468,13 +524,24 @@ __global__ void __launch_bounds__(256, 1) product_wide_kernel(Product g, Epi epi
   using Yes = std::true_type;
   using No = std::false_type;
 
-  const XcdWalk walk(mt * nt * parts);
-  for (int item = walk.tile; item < walk.end; item += walk.step) {
-    const int tile = item / parts, p = item - tile * parts;
-    const int k0 = static_cast<int>(static_cast<int64_t>(p) * stages / parts), nk = static_cast<int>(static_cast<int64_t>(p + 1) * stages / parts);
-    const int band = tile / (kWideBandRows * nt), in_band = tile - band * kWideBandRows * nt;
-    const int bm = min(kWideBandRows, mt - band * kWideBandRows);
-    const int m0 = (band * kWideBandRows + in_band % bm) * 256, n0 = in_band / bm * kCols;
+  // Workgroup b runs on XCD b % 8 and takes every step'th of that XCD's share of the whole
+  // tiles, which come in full rounds; then one of its share of the rest, in parts.
+  const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3, step = gridDim.x >> 3;
+  const int rest = (mt * nt - whole) * parts, share = whole / 8, rest_share = (rest + 7) / 8;
+  for (int turn = at; turn < share + step; turn += step) {
+    int tile, p = 0, cut = 1;
+    if (turn < share) {
+      tile = xcd * share + turn;
+    } else {
+      const int item = xcd * rest_share + at;
+      if (at >= rest_share || item >= rest) break;
+      tile = whole + item / parts;
+      p = item % parts;
+      cut = parts;
+    }
+    const int k0 = static_cast<int>(static_cast<int64_t>(p) * stages / cut), nk = static_cast<int>(static_cast<int64_t>(p + 1) * stages / cut);
+    int m0, n0;
+    wide_place<kCols>(tile, mt, nt, m0, n0);
     const WideSide<E, KA, false> A(g.a, m0, g.M, wave, lane);
     const WideSide<E, KB, PAIR> B(g.b, n0, g.N, wave, lane);
     auto dma_a = [&](int ks, uint32_t buf) __attribute__((always_inline)) {
@@ -563,38 +630,96 @@ __global__ void __launch_bounds__(256, 1) product_wide_kernel(Product g, Epi epi
     // 8 (v / 4) + 4 (l / 32) + v % 4.  A wave's staged rows are its own.
     const uint32_t free_buf = ((ks - k0) & 1) ? 0 : kWidePad + kWideStage;
     float* stg = reinterpret_cast<float*>(lds + free_buf) + wave * 32 * kWideOut;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    const int c = 4 * (lane % (kPair ? 16 : 32)), n = n0 + wn * (kPair ? 64 : 128) + c;
+    const int stg_col = kPair ? (c >> 5) * 64 + (c & 31) : c;
+    const auto row_of = [&](int R) { return m0 + wm * 128 + R; };
+    typename Epi::Cols cols;
+    Batch<Epi, Epi::kAhead> ahead;
+    float* mine = part + (static_cast<size_t>(tile - whole) * parts + p) * 65536 + wm * 32768 + wn * 128 + stg_col;
+    if (cut == 1 && n < g.N) {
+      cols = epi.cols(n);
+      ahead.load(epi, g.M, n, lane / (kPair ? 16 : 32), kPair ? 4 : 2, row_of);
+    }
+    auto stage_rows = [&](const Acc<E> (&r)[4]) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           f32x4 v;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(acc[i][j][4 * q + e]);
+          for (int e = 0; e < 4; ++e) v[e] = as_float(r[j][4 * q + e]);
           *reinterpret_cast<f32x4*>(stg + r32 * kWideOut + 32 * j + 8 * q + 4 * hi) = v;
         }
+    };
+    // One copy of the epilogue for the four: unrolled, its activations do not fit the
+    // instruction cache.
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      if (i == 0) stage_rows(acc[0]);
+      else if (i == 1) stage_rows(acc[1]);
+      else if (i == 2) stage_rows(acc[2]);
+      else stage_rows(acc[3]);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
-      results_out<kPair, 128, 32, 64>(g, epi, stg, kWideOut, n0 + wn * (kPair ? 64 : 128), parts, p, part, lane,
-                                      [&](int R) { return m0 + wm * 128 + 32 * i + R; });
+      results_out<E, kPair, 128, 32, 64, Epi::kAhead>(g, epi, cols, ahead, stg, kWideOut, n, lane, 32 * i, i < 3, row_of,
+                                                      cut > 1, [&](int R) { return mine + R * 256; }, 32);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
     }
   }
 }
 
+// The rest's parts added in order: 1024 sums (of a pair: 512 of either) to a workgroup.
+template <bool PAIR, class Epi>
+__global__ void __launch_bounds__(256) product_rest_kernel(Product g, Epi epi, int whole, int parts, const float* part) {
+  constexpr int kCols = PAIR ? 128 : 256, kGroups = PAIR ? 32 : 64, kQuads = kCols / 4;
+  const int mt = static_cast<int>(ceil_div(g.M, 256)), nt = static_cast<int>(ceil_div(g.N, kCols));
+  const int tile = blockIdx.x / kGroups, i = (blockIdx.x % kGroups) * 256 + threadIdx.x;
+  int m0, n0;
+  wide_place<kCols>(whole + tile, mt, nt, m0, n0);
+  const int R = i / kQuads, c = 4 * (i % kQuads), m = m0 + R, n = n0 + c;
+  if (m >= g.M || n >= g.N) return;
+  const typename Epi::Cols cols = epi.cols(n);
+  const typename Epi::Ahead ahead = epi.ahead(m, n);
+  const float* q = part + static_cast<size_t>(tile) * parts * 65536 + R * 256 + (PAIR ? (c >> 5) * 64 + (c & 31) : c);
+  f32x4 s = {0.f, 0.f, 0.f, 0.f}, u = {0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < parts; p += kSumAhead) {
+    f32x4 b[kSumAhead], d[kSumAhead];
+#pragma unroll
+    for (int k = 0; k < kSumAhead; ++k)
+      if (p + k < parts) {
+        b[k] = *reinterpret_cast<const f32x4*>(q + static_cast<size_t>(p + k) * 65536);
+        if constexpr (PAIR) d[k] = *reinterpret_cast<const f32x4*>(q + static_cast<size_t>(p + k) * 65536 + 32);
+      }
+#pragma unroll
+    for (int k = 0; k < kSumAhead; ++k)
+      if (p + k < parts)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[e] += b[k][e];
+          if constexpr (PAIR) u[e] += d[k][e];
+        }
+  }
+  epi.put(m, n, s, u, cols, ahead);
+}
+
 // ---------------------------------------------------------------- host
 
 constexpr int kCus = 256;
 constexpr int kMaxParts = 16;
-// Most bytes of partial sums: those of two 128 x 128 tiles on each CU.
-constexpr size_t kMaxPartBytes = size_t{2} * kCus * 128 * 128 * sizeof(float);
+// Most bytes of partial sums: those of a 256 x 256 tile on each CU.
+constexpr size_t kMaxPartBytes = size_t{kCus} * 256 * 256 * sizeof(float);
+// Bytes of partial sums of any product of at most M rows.
+inline size_t part_bytes(bool pair, int64_t M, int64_t N) {
+  const double want = static_cast<double>(kMaxParts) * M * (pair ? 2 : 1) * part_stride(N) * sizeof(float);
+  return want < static_cast<double>(kMaxPartBytes) ? std::max<size_t>(align_up(static_cast<size_t>(want), 256), 256) : kMaxPartBytes;
+}
 
 struct TilePlan {
   int rows, cols;       // of a tile, in operand rows
   int64_t tiles;
-  int parts;
+  int64_t whole;        // 256 x 256: tiles that are not cut
+  int parts;            // of the others
 };
 
 // The cheapest tile and split by an estimate in microseconds: what a CU takes in, the
@@ -602,14 +727,15 @@ struct TilePlan {
 inline TilePlan plan_tiles(El e, bool pair, bool wide, int64_t M, int64_t N, int64_t K) {
   const int size = e == El::F32 ? 4 : e == El::BF16 ? 2 : 1;
   const int64_t width = pair ? 2 * N : N, stages = ceil_div(K * size, 128);
+  const double room = static_cast<double>(part_bytes(pair, M, N));
   static const struct { int rows, cols; } kTiles[] = {{64, 128}, {128, 128}};
   TilePlan best{};
   double least = 0;
   for (const auto& t : kTiles) {
     const int64_t tiles = ceil_div(M, t.rows) * ceil_div(width, t.cols), slots = int64_t{2} * kCus;
     for (int parts = 1; parts <= kMaxParts; ++parts) {
-      const int64_t planes = parts * M * (pair ? 2 : 1) * part_stride(N) * 4;
-      if (parts > 1 && (tiles * parts > (e == El::F32 ? 2 * slots : slots) || planes > static_cast<int64_t>(kMaxPartBytes) || stages / parts < 4)) break;
+      const double planes = static_cast<double>(parts) * M * (pair ? 2 : 1) * part_stride(N) * 4;
+      if (parts > 1 && (tiles * parts > (e == El::F32 ? 2 * slots : slots) || planes > room || stages / parts < 4)) break;
       const int64_t items = tiles * parts, rounds = ceil_div(items, slots);
       const double shared = items > kCus ? 2 : 1, deep = static_cast<double>(ceil_div(stages, parts));
       const double load = (t.rows + t.cols) * 0.128 * deep / (shared > 1 ? 28 : 20);
@@ -618,27 +744,24 @@ inline TilePlan plan_tiles(El e, bool pair, bool wide, int64_t M, int64_t N, int
       const double us = in_turn * std::max(load, mult) + 2 + 0.5 * rounds + (parts > 1 ? 4 + planes * 2 / 5e6 : 0);
       if (best.tiles == 0 || us < least) {
         least = us;
-        best = TilePlan{t.rows, t.cols, tiles, parts};
+        best = TilePlan{t.rows, t.cols, tiles, 0, parts};
       }
     }
   }
-  for (int parts = 1; wide && parts <= kMaxParts; ++parts) {
-    const int64_t tiles = ceil_div(M, 256) * ceil_div(width, 256);
-    const int64_t planes = parts * M * (pair ? 2 : 1) * part_stride(N) * 4;
-    if (parts > 1 && (tiles * parts > kCus || planes > static_cast<int64_t>(kMaxPartBytes) || stages / parts < 4)) break;
-    const double us = ceil_div(tiles * parts, kCus) * (1.15 * ceil_div(stages, parts) + 6) + 2 + (parts > 1 ? 4 + planes * 2 / 5e6 : 0);
+  if (!wide) return best;
+  // Full rounds of whole tiles; what is left over, which would leave CUs idle, in parts.
+  const int64_t tiles = ceil_div(M, 256) * ceil_div(width, 256), whole = tiles / kCus * kCus, rest = tiles - whole;
+  for (int parts = 1; parts <= kMaxParts; ++parts) {
+    const double planes = static_cast<double>(rest) * parts * 256 * 256 * 4;
+    if (parts > 1 && (rest == 0 || rest * parts > kCus || planes > room || stages / parts < 4)) break;
+    const double us = whole / kCus * (1.5 * stages + 8) + (rest ? 1.5 * ceil_div(stages, parts) + 8 : 0) + 2 +
+                      (parts > 1 ? 4 + planes * 2 / 5e6 : 0);
     if (us < least) {
       least = us;
-      best = TilePlan{256, 256, tiles, parts};
+      best = TilePlan{256, 256, tiles, whole, parts};
     }
   }
   return best;
-}
-
-// Bytes of partial sums of any product of at most M rows.
-inline size_t part_bytes(bool pair, int64_t M, int64_t N) {
-  const double want = static_cast<double>(kMaxParts) * M * (pair ? 2 : 1) * part_stride(N) * sizeof(float);
-  return want < static_cast<double>(kMaxPartBytes) ? std::max<size_t>(align_up(static_cast<size_t>(want), 256), 256) : kMaxPartBytes;
 }
 
 // 16-byte pieces of an operand lie on 16-byte boundaries.
@@ -672,12 +795,19 @@ int run_product(const Product& g, const Epi& epi, float* part, hipStream_t s) {
   bool wide = false;
   if constexpr (E != El::F32) wide = aligned && fits_wide<E, KB, PAIR>(g);
   const TilePlan t = plan_tiles(E, kPair, wide, g.M, g.N, g.K);
-  if (t.rows == 256) {
-    if constexpr (E != El::F32) {
-      const unsigned grid = static_cast<unsigned>(std::min<int64_t>(kCus, ceil_div(t.tiles * t.parts, 8) * 8));
-      product_wide_kernel<E, KA, KB, PAIR><<<grid, 256, 0, s>>>(g, epi, t.parts, part);
+  if constexpr (E != El::F32) {
+    if (t.rows == 256) {
+      const int64_t rest = t.tiles - t.whole;
+      const unsigned grid = t.whole ? kCus : static_cast<unsigned>(ceil_div(rest * t.parts, 8) * 8);
+      product_wide_kernel<E, KA, KB, PAIR><<<grid, 256, 0, s>>>(g, epi, static_cast<int>(t.whole), t.parts, part);
+      if (t.parts > 1) {
+        if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
+        product_rest_kernel<kPair><<<static_cast<unsigned>(rest * (kPair ? 32 : 64)), 256, 0, s>>>(g, epi, static_cast<int>(t.whole), t.parts, part);
+      }
+      return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH_FAILED;
     }
-  } else if (aligned) launch_tiles<E, KA, KB, PAIR, false>(g, epi, t, part, s);
+  }
+  if (aligned) launch_tiles<E, KA, KB, PAIR, false>(g, epi, t, part, s);
   else launch_tiles<E, KA, KB, PAIR, true>(g, epi, t, part, s);
   if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
   if (t.parts > 1) {

@@ -50,59 +50,47 @@ int quantise(bool f32, int M, int K, const void* x, int64_t ldx, int8_t* q, int6
 
 template <bool OUT32>
 struct I8Out {
-  static constexpr int kAhead = 4;
+  static constexpr int kAhead = OUT32 ? 4 : 8;
+  struct Cols {
+    float w[4], b[4];
+  };
+  struct Ahead {
+    float sx;
+    Raw4<OUT32> r;
+  };
   const float *sx, *sw;
   const void *bias, *residual;
   void* y;
   int64_t ldr, ldy;
-  int M, N, act;
+  int N, act;
   bool bias_f32;
-  template <int D>
-  __device__ __forceinline__ void quads(const int (&m)[D], int n, const f32x4 (&s)[D], const f32x4 (&)[D]) const {
-    const bool whole = n + 4 <= N;
-    f32x4 res[D], w = {0.f, 0.f, 0.f, 0.f}, b = {0.f, 0.f, 0.f, 0.f};
-    float x[D];
+  __device__ __forceinline__ Cols cols(int n) const {
+    Cols c;
+    const Raw4<true> w = raw4<true>(sw, n, N - n);
+    Raw4<true> b{};
+    Raw4<false> h{};
+    if (bias && bias_f32) b = raw4<true>(bias, n, N - n);
+    if (bias && !bias_f32) h = raw4<false>(bias, n, N - n);
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-      res[d] = f32x4{0.f, 0.f, 0.f, 0.f};
-      x[d] = m[d] < M ? sx[m[d]] : 0.0f;
-      if (residual && m[d] < M) {
-        const size_t o = static_cast<size_t>(m[d]) * ldr + n;
-        if (whole) res[d] = load4<OUT32>(residual, o);
-        else
-          for (int c = 0; c < 4; ++c)
-            if (n + c < N) res[d][c] = elem<OUT32>(residual, o + c);
-      }
+    for (int k = 0; k < 4; ++k) {
+      c.w[k] = value4<true>(w, k);
+      c.b[k] = bias_f32 ? value4<true>(b, k) : value4<false>(h, k);
     }
+    return c;
+  }
+  __device__ __forceinline__ Ahead ahead(int m, int n) const {
+    Ahead a{sx[m], {}};
+    if (residual) a.r = raw4<OUT32>(residual, static_cast<size_t>(m) * ldr + n, N - n);
+    return a;
+  }
+  __device__ __forceinline__ void put(int m, int n, const f32x4& s, const f32x4&, const Cols& c, const Ahead& a) const {
+    float v[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (n + c < N) {
-        w[c] = sw[n + c];
-        if (bias) b[c] = bias_f32 ? elem<true>(bias, n + c) : elem<false>(bias, n + c);
-      }
-    float v[4 * D];
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[4 * d + c] = s[d][c] * x[d] * w[c] + b[c];
+    for (int k = 0; k < 4; ++k) v[k] = s[k] * a.sx * c.w[k] + c.b[k];
     activate<!OUT32>(v, act);
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-      if (m[d] >= M) continue;
-      const size_t o = static_cast<size_t>(m[d]) * ldy + n;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[4 * d + c] += res[d][c];
-      if (whole) {
-        store4<OUT32>(y, o, v + 4 * d);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (n + c < N) {
-            if constexpr (OUT32) static_cast<float*>(y)[o + c] = v[4 * d + c];
-            else static_cast<uint16_t*>(y)[o + c] = f32_to_bf16_bits(v[4 * d + c]);
-          }
-      }
-    }
+    for (int k = 0; k < 4; ++k) v[k] += value4<OUT32>(a.r, k);
+    put4<OUT32>(y, static_cast<size_t>(m) * ldy + n, v, N - n);
   }
 };
 
@@ -190,8 +178,8 @@ int moe_linear_i8(const moe_linear_i8_config* cfg, int32_t M, const void* x, int
   }
   const bool bf = c.bias_dtype == MOE_DTYPE_F32;
   if (c.out_dtype == MOE_DTYPE_F32)
-    return run_product<El::I8, true, true, false>(g, I8Out<true>{sx, w_scale, bias, residual, y, ldr, ldy, M, N, c.activation, bf}, part, s);
-  return run_product<El::I8, true, true, false>(g, I8Out<false>{sx, w_scale, bias, residual, y, ldr, ldy, M, N, c.activation, bf}, part, s);
+    return run_product<El::I8, true, true, false>(g, I8Out<true>{sx, w_scale, bias, residual, y, ldr, ldy, N, c.activation, bf}, part, s);
+  return run_product<El::I8, true, true, false>(g, I8Out<false>{sx, w_scale, bias, residual, y, ldr, ldy, N, c.activation, bf}, part, s);
 }
 
 }  // extern "C"
