@@ -11,38 +11,51 @@ namespace {
 
 // ---------------------------------------------------------------- quantiser
 
-// A row of x to a workgroup: its largest magnitude, then its codes; the second reading
-// comes from the caches, which hold any row.
-template <bool F32>
+constexpr int kFewRows = 512;
+
+// A row of x to a workgroup: its largest magnitude, then its codes.  A lane keeps C times
+// eight elements; what is left of a longer row is read again, from the caches.
+template <bool F32, int C>
 __global__ void __launch_bounds__(1024) quant_i8_kernel(const void* x, int64_t ldx, int K, int8_t* q, int64_t ldq, float* scale) {
   __shared__ RowLds<uint32_t> lds;
   const int64_t m = blockIdx.x;
   const uint8_t* row = static_cast<const uint8_t*>(x) + m * ldx * (F32 ? 4 : 2);
   const int waves = blockDim.x >> 6, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), step = 8 * blockDim.x;
+  const int first = 8 * threadIdx.x;
   uint32_t most[1] = {0};
-  const Raw8<F32> head = load8<F32>(row, 8 * threadIdx.x, K - 8 * static_cast<int>(threadIdx.x));
-  for (int i = 8 * threadIdx.x; i < K; i += step) {
-    const Raw8<F32> r = i < step ? head : load8<F32>(row, i, K - i);
+  const auto add = [&](const Raw8<F32>& r) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) most[0] = max(most[0], __float_as_uint(value<F32>(r, e)) & 0x7fffffffu);
-  }
+  };
+  Raw8<F32> head[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) head[c] = load8<F32>(row, first + c * step, K - first - c * step);
+#pragma unroll
+  for (int c = 0; c < C; ++c) add(head[c]);
+  for (int i = first + C * step; i < K; i += step) add(load8<F32>(row, i, K - i));
   int turn = 0;
   row_all(most, wave, waves, lds, turn, Most{});
   const float s = i8_scale(most[0]), inv = 1.0f / s;
   if (threadIdx.x == 0) scale[m] = s;
-  for (int i = 8 * threadIdx.x; i < K; i += step) {
-    const Raw8<F32> r = i < step ? head : load8<F32>(row, i, K - i);
+  const auto put = [&](const Raw8<F32>& r, int i) {
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = value<F32>(r, e);
-    store_codes(q + m * ldq + i, v, s, inv, K - i);
-  }
+    if (i < K) store_codes(q + m * ldq + i, v, s, inv, K - i);
+  };
+#pragma unroll
+  for (int c = 0; c < C; ++c) put(head[c], first + c * step);
+  for (int i = first + C * step; i < K; i += step) put(load8<F32>(row, i, K - i), i);
 }
 
+// Few rows: a lane for every eight elements, for the latency.  Many: four times as many to
+// a lane, for the loads in flight and the workgroups on a CU.
 int quantise(bool f32, int M, int K, const void* x, int64_t ldx, int8_t* q, int64_t ldq, float* scale, hipStream_t s) {
-  const unsigned block = 64u * static_cast<unsigned>(std::min<int64_t>(16, ceil_div(K, 512)));
-  if (f32) quant_i8_kernel<true><<<static_cast<unsigned>(M), block, 0, s>>>(x, ldx, K, q, ldq, scale);
-  else quant_i8_kernel<false><<<static_cast<unsigned>(M), block, 0, s>>>(x, ldx, K, q, ldq, scale);
+  const bool few = M <= kFewRows;
+  const unsigned block = 64u * static_cast<unsigned>(std::min<int64_t>(16, ceil_div(K, few ? 512 : 2048)));
+  const unsigned grid = static_cast<unsigned>(M);
+  if (f32) few ? quant_i8_kernel<true, 1><<<grid, block, 0, s>>>(x, ldx, K, q, ldq, scale) : quant_i8_kernel<true, 4><<<grid, block, 0, s>>>(x, ldx, K, q, ldq, scale);
+  else few ? quant_i8_kernel<false, 1><<<grid, block, 0, s>>>(x, ldx, K, q, ldq, scale) : quant_i8_kernel<false, 4><<<grid, block, 0, s>>>(x, ldx, K, q, ldq, scale);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH_FAILED;
 }
 

@@ -151,20 +151,33 @@ struct Most {
 __device__ __forceinline__ float i8_scale(uint32_t amax) {
   return amax >= 0x7f800000u ? __uint_as_float(amax) : fmaxf(__uint_as_float(amax) / 127.0f, 0x1p-126f);
 }
-// x / s rounded to the nearest whole number, ties to even.  x (1 / s) may land on the
+// x / s rounded to the nearest whole number, ties to even, where x (1 / s) may land on the
 // wrong side of a border; x - (q -+ 1/2) s, rounded once, has its sign right.
-__device__ __forceinline__ int i8_code(float x, float s, float inv) {
-  if (!(inv > 0.0f)) return 0;                 // a scale of inf or NaN
-  const float q = rintf(x * inv);
-  const int n = static_cast<int>(q);
+__device__ __forceinline__ float i8_border(float x, float s, float q) {
   const float lo = fmaf(0.5f - q, s, x), hi = fmaf(-0.5f - q, s, x);
-  const int odd = n & 1;
-  return lo < 0.0f || (lo == 0.0f && odd) ? n - 1 : hi > 0.0f || (hi == 0.0f && odd) ? n + 1 : n;
+  const bool odd = static_cast<int>(q) & 1;
+  return lo < 0.0f || (lo == 0.0f && odd) ? q - 1.0f : hi > 0.0f || (hi == 0.0f && odd) ? q + 1.0f : q;
 }
+// Codes of eight elements.  |x / s| <= 127 (1 + 2^-24), so x (1 / s) is off by less than
+// 2^-15: only quotients within that of a border, a few in a hundred thousand, are decided
+// by the exact remainder.
 __device__ __forceinline__ void store_codes(int8_t* p, const float (&v)[8], float s, float inv, int left) {
   uint32_t w[2] = {0, 0};
+  if (inv > 0.0f) {                            // else a scale of inf or NaN
+    float q[8], far = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w[e >> 2] |= (static_cast<uint32_t>(i8_code(v[e], s, inv)) & 0xffu) << (8 * (e & 3));
+    for (int e = 0; e < 8; ++e) {
+      const float t = v[e] * inv;
+      q[e] = rintf(t);
+      far = fmaxf(far, fabsf(t - q[e]));
+    }
+    if (far > 0.5f - 0x1p-14f) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] = i8_border(v[e], s, q[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e >> 2] |= (static_cast<uint32_t>(static_cast<int>(q[e])) & 0xffu) << (8 * (e & 3));
+  }
   if (left >= 8) {
     typedef uint32_t u32x2_b __attribute__((ext_vector_type(2), aligned(1)));
     *reinterpret_cast<u32x2_b*>(p) = u32x2_b{w[0], w[1]};
