@@ -14,7 +14,7 @@ LIB = os.path.join(HERE, "libmoe_mi355x.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "route.hip", "dispatch.hip", "experts.hip", "tile_gemm.hip", "stream_gemm.hip",
            "few.hip", "linear.hip", "ffn.hip",
-           "norm.hip", "linear_i8.hip"]
+           "norm_back_f32.hip", "norm_back_bf16.hip", "norm.hip", "linear_i8.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950",

@@ -122,10 +122,12 @@ struct SlopesOut {
     store4<F32>(d, o, g4);
     store4<F32>(d, o + ld, u4);
     // Both halves are contracted to their rows' ends.
-    if (n + 4 >= N && n + 4 < ld) {
+    if (n + 4 >= N) {
       const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-      store4<F32>(d, o + 4, zero);
-      store4<F32>(d, o + ld + 4, zero);
+      for (int64_t k = n + 4; k < ld; k += 4) {
+        store4<F32>(d, o - n + k, zero);
+        store4<F32>(d, o - n + ld + k, zero);
+      }
     }
   }
 };
@@ -173,8 +175,8 @@ int check_ffn(const moe_ffn_config* c, int32_t rows) {
 }
 
 size_t type_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
-// Length of the rows of h, a and b.
-int64_t inner_ld(const moe_ffn_config& c) { return (static_cast<int64_t>(c.intermediate_size) + 7) / 8 * 8; }
+// Length of the rows of h, a and b: whole stages of a contraction over them.
+int64_t inner_ld(const moe_ffn_config& c) { return (static_cast<int64_t>(c.intermediate_size) + 63) / 64 * 64; }
 
 // The kept tensors: h, a, b.
 size_t h_bytes(const moe_ffn_config& c, int64_t T) { return align_up(static_cast<size_t>(T) * inner_ld(c) * type_bytes(c.dtype), 256); }

@@ -396,130 +396,166 @@ __global__ void __launch_bounds__(256, 2) product_tile_kernel(Product g, Epi epi
   }
 }
 
-// ---------------------------------------------------------------- 256 x 256 tiles
+// ---------------------------------------------------------------- aligned tiles
 //
-// 256 x 256 sums per workgroup of four waves, one on each SIMD, 128 x 128 to a wave: a
-// stage's fragments leave LDS twice, not three times as with eight waves of 128 x 64.  A
-// stage is 64 bf16 (128 int8) of contraction, 64 KiB, double-buffered, and goes to LDS by
-// DMA.  A wave is alone on its SIMD, so nothing but its own instructions hides latencies:
-// the fragments of a quarter stage are read while the quarter before is multiplied, across
-// the stages' border too, and the DMA of stage s + 2 starts in the last quarter of s.
-// One barrier a stage, in front of that quarter: by then every wave has the stage's last
-// fragments in registers and stage s + 1 is in LDS.
+// BM x BN sums per workgroup of 2 x 2 waves, for operands in whole 16-byte pieces (bf16 and
+// 8-bit).  In 256 x 256 tiles a wave computes 128 x 128, alone on its SIMD: a stage's
+// fragments leave LDS twice, not three times as with eight waves of 128 x 64.  A stage is
+// 64 bf16 (128 int8) of contraction, double-buffered, and goes to LDS by DMA.  Nothing but
+// a wave's own instructions hides its latencies: the fragments of a quarter stage are read
+// while the quarter before is multiplied, across the stages' border too; the DMA of A of
+// stage s + 2 is issued in the last quarter of s and that of B in the first of s + 1 (both
+// in one quarter fill the queue and hold up the MFMAs: 8 % slower).  One barrier a stage, in
+// front of the last quarter: by then every wave has the stage's last fragments in registers
+// and stage s + 1 is in LDS.
 //
 // k-contiguous operands: rows of 128 bytes, 16-byte pieces permuted by (row / 2) mod 8.
-// k-strided: 512 bytes of each k, 64-byte pieces permuted by k mod 4, so that the four k
-// of a turning read lie in different quarters of the banks.
-constexpr int kWideTile = 256, kWideStage = 65536, kWideSide = 32768;
-constexpr int kWideBandRows = 8;
+// k-strided: a row for each k, 64-byte pieces permuted by k mod 4, so that the four k of a
+// turning read lie in different quarters of the banks.  What lies behind the end of the
+// contraction is out of the resource's range, and such loads bring zeros.
+//
 // Results leave through LDS too, 32 rows of a wave at a time, in the buffer that the last
-// stage is not in; rows padded by 4 floats, so 2 KiB more on either side of the buffers.
-constexpr int kWideOut = 132, kWidePad = 2048, kWideLds = 2 * kWideStage + 2 * kWidePad;
-static_assert(4 * 32 * kWideOut * 4 <= kWideStage + kWidePad, "the staged rows fit");
+// stage is not in; rows padded by 4 floats, for which there is room on its other side.
+template <El E, bool KA, bool KB, bool PAIR, int BM, int BN>
+struct Aligned {
+  static constexpr bool kPair = PAIR && KB;
+  static constexpr int kCols = kPair ? BN / 2 : BN;
+  static constexpr int kSideA = BM * 128, kStage = (BM + BN) * 128;
+  static constexpr int kOut = BN / 2 + 4, kStaged = 4 * 32 * kOut * 4;
+  static constexpr int kPad = kStaged > kStage ? (kStaged - kStage + 1023) / 1024 * 1024 : 0, kLds = 2 * kStage + 2 * kPad;
+  static_assert(BM > 64 || KA, "the banks of a k-strided side need 128 columns");
+  static constexpr int kBand = 2048 / BM;        // row blocks of a band of tiles
+};
 
-// One instruction: lane l loads 16 bytes at voff + soff to LDS at lds + 16 l.
-__device__ __forceinline__ void dma_line(i32x4_t rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %[lds]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[v], %[rs], %[so] offen lds"
+// One instruction: lane l loads 16 bytes at voff to LDS at lds + 16 l, zeros out of range.
+// (No scalar offset: the range check takes it off the range.)
+__device__ __forceinline__ void dma_line(i32x4_t rsrc, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %[lds]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[v], %[rs], 0 offen lds"
                :
-               : [v] "v"(voff), [rs] "s"(rsrc), [so] "s"(soff), [lds] "s"(lds)
+               : [v] "v"(voff), [rs] "s"(rsrc), [lds] "s"(lds)
                : "memory");
 }
 
-// What a wave loads of one operand: eight instructions a stage.
-template <El E, bool KC, bool PAIR>
-struct WideSide {
+// What a wave loads of one operand: kN instructions a stage.
+template <El E, bool KC, bool PAIR, int R>
+struct AlignedSide {
   using I = ElInfo<E>;
-  const uint8_t *p, *q;          // first row (k-contiguous) or column (k-strided) of the tile, k = 0
-  int64_t step;                  // bytes of a stage
-  uint32_t bytes;                // of the tile's part of a stage, from p on
-  uint32_t voff[8];
-  uint32_t row2;                 // k-strided: bytes of two k
-  int half;                      // k-strided pair: stages of p
-  __device__ __forceinline__ WideSide(const Operand& o, int r0, int rows, int wave, int lane) {
-    const uint32_t ld = static_cast<uint32_t>(o.ld) * I::kSize;
+  static constexpr int kN = R / 32;
+  static constexpr int kLanes = R * I::kSize / 16, kStep = 64 / kLanes;   // k-strided: lanes of a k, k of an instruction
+  static constexpr uint32_t kNowhere = 0x80000000u;                       // out of any range
+  const uint8_t *p, *q;          // the tile's first row (k-contiguous) or column (k-strided), k = 0
+  uint32_t ld, bytes;            // of a row or k; k-contiguous: of the tile's part of a stage
+  uint32_t voff[kN];
+  int last;                      // k-strided: the last 16-byte piece of the tile's columns
+  int piece;                     // k-contiguous: the lane's piece of rows of even instructions; odd ones ^ 4
+  int K, half, live;
+  __device__ __forceinline__ AlignedSide(const Operand& o, int r0, int rows, int k, int wave, int lane) {
+    ld = static_cast<uint32_t>(o.ld) * I::kSize;
+    K = k;
+    half = o.half;
+    live = o.live;
     if constexpr (KC) {
-      constexpr int kRows = PAIR ? 128 : 256;
-      const int last = min(kRows, rows - r0) - 1;
+      last = min(PAIR ? R / 2 : R, rows - r0) - 1;
       p = static_cast<const uint8_t*>(o.p) + static_cast<size_t>(r0) * ld;
       q = PAIR ? static_cast<const uint8_t*>(o.q) + static_cast<size_t>(r0) * ld : nullptr;
-      step = 128;
       bytes = static_cast<uint32_t>(last) * ld + 128;
+      piece = (lane & 7) ^ (lane >> 4);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        // Row of the LDS side: 64 wave + 8 k + lane / 8; of a pair, 32 rows by turns.
-        const int row = PAIR ? 32 * wave + 8 * (k & 3) + (lane >> 3) : 64 * wave + 8 * k + (lane >> 3);
-        voff[k] = static_cast<uint32_t>(min(row, last)) * ld + ((lane & 7) ^ ((4 * (k & 1) + (lane >> 4)) & 7)) * 16;
+      for (int i = 0; i < kN; ++i) {
+        const int r = R / 4 * wave + 8 * i + (lane >> 3), row = PAIR ? (r >> 6) * 32 + (r & 31) : r;
+        voff[i] = static_cast<uint32_t>(min(row, last)) * ld + (piece ^ (i & 1) * 4) * 16;
       }
     } else {
       p = static_cast<const uint8_t*>(o.p) + static_cast<size_t>(r0) * I::kSize;
       q = PAIR ? static_cast<const uint8_t*>(o.q) + static_cast<size_t>(r0) * I::kSize : nullptr;
-      step = static_cast<int64_t>(I::kStage) * ld;
-      row2 = 2 * ld;
-      half = PAIR ? o.half / I::kStage : 0;
-      const int last = min(256, rows - r0) / I::kPiece - 1;    // pieces of a row of the tile
-      bytes = static_cast<uint32_t>(I::kStage - 1) * ld + static_cast<uint32_t>(last + 1) * 16;
-      // k of the stage: 16 wave + 2 i + lane / 32.
+      last = min(R, rows - r0) / I::kPiece - 1;
+      // Instructions of a stage repeat after two (two k each) or one (four k).
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = 16 * wave + 2 * h + (lane >> 5);
-        voff[h] = static_cast<uint32_t>(16 * wave + (lane >> 5)) * ld + min((lane & 31) ^ ((k & 3) << 2), last) * 16;
+      for (int i = 0; i < 2; ++i) {
+        const int k0 = lane / kLanes, s = (kStep * i + k0) & 3;
+        voff[i] = static_cast<uint32_t>(I::kStage / 4 * wave + k0) * ld + min((lane % kLanes) ^ (s << 2), last) * 16;
       }
     }
   }
-  // The resource of a stage.
-  __device__ __forceinline__ i32x4_t rsrc(int ks, bool second) const {
-    if constexpr (KC) return dma_rsrc((PAIR && second ? q : p) + ks * step, bytes);
-    else if constexpr (PAIR) return dma_rsrc(ks < half ? p + ks * step : q + (ks - half) * step, bytes);
-    else return dma_rsrc(p + ks * step, bytes);
+  // The resource of stage ks, and of the pair's second matrix.
+  __device__ __forceinline__ i32x4_t rsrc(int ks, bool second = false) const {
+    if constexpr (KC) {
+      return dma_rsrc((PAIR && second ? q : p) + static_cast<size_t>(ks) * 128, bytes);
+    } else {
+      const bool up = PAIR && ks * I::kStage >= half;
+      const int k = ks * I::kStage - (up ? half : 0), left = min((PAIR ? live : K) - k, I::kStage);
+      return dma_rsrc((up ? q : p) + static_cast<size_t>(max(min(k, (PAIR ? live : K) - 1), 0)) * ld,
+                      left > 0 ? static_cast<uint32_t>(left - 1) * ld + static_cast<uint32_t>(last + 1) * 16 : 0u);
+    }
   }
-  // Instruction k of the eight.
-  __device__ __forceinline__ void issue(const i32x4_t& r, int k, uint32_t lds) const {
-    if constexpr (KC) dma_line(r, voff[k], 0, lds + 1024 * k);
-    else dma_line(r, voff[k & 1], __builtin_amdgcn_readfirstlane(row2 * k), lds + 1024 * k);
+  // k-contiguous: before the last stage, if it is cut, its pieces past the end go nowhere.
+  __device__ __forceinline__ void cut(int ks) {
+    if constexpr (KC) {
+      const int left = (K - ks * I::kStage) / I::kPiece;
+      if (left >= 8) return;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) voff[i] += (piece ^ (i & 1) * 4) < left ? 0u : kNowhere;
+    }
   }
+  __device__ __forceinline__ void issue(const i32x4_t& r, int i, uint32_t lds) const {
+    if constexpr (KC) dma_line(r, voff[i], lds + 1024 * i);
+    else dma_line(r, voff[kStep == 2 ? i & 1 : 0] + ld * (kStep * i), lds + 1024 * i);
+  }
+  // Whether instruction i of the wave loads rows of the pair's second matrix.
+  static __device__ __forceinline__ bool second(int wave, int i) { return (R / 4 * wave + 8 * i) >> 5 & 1; }
 };
 
-// Tiles are walked in bands of 8 row blocks, so that the 32 tiles that run on an XCD at a
-// time share 8 row blocks and 4 column blocks in its L2.
-template <int COLS>
-__device__ __forceinline__ void wide_place(int tile, int mt, int nt, int& m0, int& n0) {
-  const int band = tile / (kWideBandRows * nt), in_band = tile - band * kWideBandRows * nt;
-  const int bm = min(kWideBandRows, mt - band * kWideBandRows);
-  m0 = (band * kWideBandRows + in_band % bm) * 256;
+// Tiles are walked in bands of 2048 rows, so that the tiles that run on an XCD at a time
+// share few row and column blocks in its L2.
+template <int BM, int BAND, int COLS>
+__device__ __forceinline__ void tile_place(int tile, int mt, int nt, int& m0, int& n0) {
+  const int band = tile / (BAND * nt), in_band = tile - band * BAND * nt;
+  const int bm = min(BAND, mt - band * BAND);
+  m0 = (band * BAND + in_band % bm) * BM;
   n0 = in_band / bm * COLS;
 }
 
-template <El E, bool KA, bool KB, bool PAIR, class Epi>
-__global__ void __launch_bounds__(256, 1) product_wide_kernel(Product g, Epi epi, int whole, int parts, float* part) {
-  constexpr bool kPair = PAIR && KB;
-  constexpr int kCols = kPair ? 128 : 256;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kWideLds];
-  uint8_t* smem = lds + kWidePad;
+template <El E, bool KA, bool KB, bool PAIR, int BM, int BN, class Epi>
+__global__ void __launch_bounds__(256, BM + BN > 256 ? 1 : 2) product_aligned_kernel(Product g, Epi epi, int whole, int parts, float* part) {
+  using L = Aligned<E, KA, KB, PAIR, BM, BN>;
+  constexpr bool kPair = L::kPair;
+  constexpr int kCols = L::kCols, NI = BM / 64, NJ = BN / 64;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[L::kLds];
+  uint8_t* smem = lds + L::kPad;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1, r32 = lane & 31, hi = lane >> 5;
-  const int mt = static_cast<int>(ceil_div(g.M, 256)), nt = static_cast<int>(ceil_div(g.N, kCols));
-  const int stages = g.K / ElInfo<E>::kStage;
-  const uint32_t lds_a = __builtin_amdgcn_readfirstlane(lds_address(smem)) + 8192 * wave, lds_b = lds_a + kWideSide;
+  const int mt = static_cast<int>(ceil_div(g.M, BM)), nt = static_cast<int>(ceil_div(g.N, kCols));
+  const int stages = static_cast<int>(ceil_div(g.K, ElInfo<E>::kStage));
+  using SideA = AlignedSide<E, KA, false, BM>;
+  using SideB = AlignedSide<E, KB, PAIR, BN>;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_address(smem));
+  const uint32_t lds_a = lds0 + SideA::kN * 1024 * wave, lds_b = lds0 + L::kSideA + SideB::kN * 1024 * wave;
 
   // Offsets of the wave's fragments in a side: k-contiguous by quarter (block x is 4 KiB
-  // on), k-strided by block (quarter kk is 8 KiB on).
+  // on), k-strided by block (quarter kk is 16 rows on).
+  constexpr int kRowA = BM * ElInfo<E>::kSize, kRowB = BN * ElInfo<E>::kSize;
   uint32_t fa[4], fb[4];
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
     const uint32_t kc = static_cast<uint32_t>(r32 * 128 + (((2 * x) ^ hi ^ ((r32 >> 1) & 7)) * 16));
-    const uint32_t s = (lane & 15) >> 2;
-    const uint32_t ks = (8 * hi + s) * 512 + ((x ^ s) * 64) + (r32 & 16) * 2 + 8 * (lane & 3);
-    fa[x] = KA ? kc + wm * 128 * 128 : ks + wm * 256;
-    fb[x] = (KB ? kc + wn * 128 * 128 : ks + wn * 256) + kWideSide;
+    const uint32_t s = (lane & 15) >> 2, in = (r32 & 16) * 2 + 8 * (lane & 3);
+    fa[x] = KA ? kc + wm * BM / 2 * 128 : (8 * hi + s) * kRowA + ((wm * NI + x) ^ s) * 64 + in;
+    fb[x] = L::kSideA + (KB ? kc + wn * BN / 2 * 128 : (8 * hi + s) * kRowB + ((wn * NJ + x) ^ s) * 64 + in);
   }
-  auto frag = [&](const uint8_t* base, const uint32_t (&f)[4], int blk, int kk, auto kc) __attribute__((always_inline)) {
+  auto frag = [&](const uint8_t* base, const uint32_t (&f)[4], int blk, int kk, auto kc, auto row) __attribute__((always_inline)) {
     if constexpr (decltype(kc)::value) {
       return *reinterpret_cast<const uint4*>(base + f[kk] + blk * 4096);
     } else {
-      const uint8_t* t = base + f[blk] + kk * 8192;
-      const uint2 lo = lds_turned(t), up = lds_turned(t + 2048);
+      const uint8_t* t = base + f[blk] + kk * 16 * decltype(row)::value;
+      const uint2 lo = lds_turned(t), up = lds_turned(t + 4 * decltype(row)::value);
       return uint4{lo.x, lo.y, up.x, up.y};
     }
+  };
+  auto frag_a = [&](const uint8_t* base, int i, int kk) __attribute__((always_inline)) {
+    return frag(base, fa, i, kk, std::bool_constant<KA>{}, std::integral_constant<int, kRowA>{});
+  };
+  auto frag_b = [&](const uint8_t* base, int j, int kk) __attribute__((always_inline)) {
+    return frag(base, fb, j, kk, std::bool_constant<KB>{}, std::integral_constant<int, kRowB>{});
   };
   using Yes = std::true_type;
   using No = std::false_type;
@@ -541,84 +577,97 @@ __global__ void __launch_bounds__(256, 1) product_wide_kernel(Product g, Epi epi
     }
     const int k0 = static_cast<int>(static_cast<int64_t>(p) * stages / cut), nk = static_cast<int>(static_cast<int64_t>(p + 1) * stages / cut);
     int m0, n0;
-    wide_place<kCols>(tile, mt, nt, m0, n0);
-    const WideSide<E, KA, false> A(g.a, m0, g.M, wave, lane);
-    const WideSide<E, KB, PAIR> B(g.b, n0, g.N, wave, lane);
+    tile_place<BM, L::kBand, kCols>(tile, mt, nt, m0, n0);
+    SideA A(g.a, m0, g.M, g.K, wave, lane);
+    SideB B(g.b, n0, g.N, g.K, wave, lane);
     auto dma_a = [&](int ks, uint32_t buf) __attribute__((always_inline)) {
-      const i32x4_t r = A.rsrc(ks, false);
+      const i32x4_t r = A.rsrc(ks);
+      A.cut(ks);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) A.issue(r, k, lds_a + buf);
+      for (int i = 0; i < SideA::kN; ++i) A.issue(r, i, lds_a + buf);
     };
     auto dma_b = [&](int ks, uint32_t buf) __attribute__((always_inline)) {
-      const i32x4_t r = B.rsrc(ks, false), r2 = kPair ? B.rsrc(ks, true) : r;
+      const i32x4_t r = B.rsrc(ks), r2 = kPair ? B.rsrc(ks, true) : r;
+      B.cut(ks);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) B.issue(k < 4 ? r : r2, k, lds_b + buf);
+      for (int i = 0; i < SideB::kN; ++i) B.issue(kPair && SideB::second(wave, i) ? r2 : r, i, lds_b + buf);
     };
     __syncthreads();                 // the tile before is done with LDS
     dma_a(k0, 0);
     dma_b(k0, 0);
     if (k0 + 1 < nk) {
-      dma_a(k0 + 1, kWideStage);
-      wait_vm<8>();
+      dma_a(k0 + 1, L::kStage);
+      wait_vm<SideA::kN>();
     } else {
       wait_vm<0>();
     }
     __syncthreads();
-    Acc<E> acc[4][4];
+    Acc<E> acc[NI][NJ];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
-    uint4 af[2][4], bf[2][4];
+    uint4 af[2][NI], bf[2][NJ];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      bf[0][x] = frag(smem, fb, x, 0, std::bool_constant<KB>{});
-      af[0][x] = frag(smem, fa, x, 0, std::bool_constant<KA>{});
-    }
-    // The 16 MFMAs of quarter kk, by twos; between them the fragments of the quarter after
-    // it (`read`) and eight instructions of a stage's DMA.
-    auto quarter = [&](int kk, const uint8_t* next, int nkk, auto read, auto dma) __attribute__((always_inline)) {
+    for (int j = 0; j < NJ; ++j) bf[0][j] = frag_b(smem, j, 0);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) af[0][i] = frag_a(smem, i, 0);
+    // The MFMAs of quarter kk, by twos; between them the fragments of the quarter after it
+    // (`read`) and `n` instructions of a stage's DMA.
+    constexpr int kPairs = NI * NJ / 2;
+    auto quarter = [&](int kk, const uint8_t* next, int nkk, auto read, auto n, auto dma) __attribute__((always_inline)) {
       const int c = kk & 1, d = c ^ 1;
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
+      for (int x = 0; x < kPairs; ++x) {
         if constexpr (decltype(read)::value) {
-          if (x < 4) bf[d][x] = frag(next, fb, x, nkk, std::bool_constant<KB>{});
-          else af[d][x - 4] = frag(next, fa, x - 4, nkk, std::bool_constant<KA>{});
+#pragma unroll
+          for (int y = x * (NI + NJ) / kPairs; y < (x + 1) * (NI + NJ) / kPairs; ++y) {
+            if (y < NJ) bf[d][y] = frag_b(next, y, nkk);
+            else af[d][y - NJ] = frag_a(next, y - NJ, nkk);
+          }
         }
-        dma(x);
-        const int i = x >> 1, j = 2 * (x & 1);
+#pragma unroll
+        for (int y = x * decltype(n)::value / kPairs; y < (x + 1) * decltype(n)::value / kPairs; ++y) dma(y);
+        const int i = 2 * x / NJ, j = 2 * x % NJ;
         acc[i][j] = mfma32<E>(bf[c][j], af[c][i], acc[i][j]);
         acc[i][j + 1] = mfma32<E>(bf[c][j + 1], af[c][i], acc[i][j + 1]);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
     const auto nothing = [](int) __attribute__((always_inline)) {};
+    using Zero = std::integral_constant<int, 0>;
     // Stage ks; B of stage ks + 1 and A of stage ks + 2 are loaded meanwhile, where they are.
     auto stage = [&](int ks, auto load_b, auto load_a) __attribute__((always_inline)) {
-      const uint32_t buf = static_cast<uint32_t>((ks - k0) & 1) * kWideStage, other = kWideStage - buf;
+      const uint32_t buf = static_cast<uint32_t>((ks - k0) & 1) * L::kStage, other = L::kStage - buf;
       const uint8_t* here = smem + buf;
       if constexpr (decltype(load_b)::value) {
-        const i32x4_t r = B.rsrc(ks + 1, false), r2 = kPair ? B.rsrc(ks + 1, true) : r;
-        quarter(0, here, 1, Yes{}, [&](int k) __attribute__((always_inline)) { B.issue(k < 4 ? r : r2, k, lds_b + other); });
+        const i32x4_t r = B.rsrc(ks + 1), r2 = kPair ? B.rsrc(ks + 1, true) : r;
+        B.cut(ks + 1);
+        quarter(0, here, 1, Yes{}, std::integral_constant<int, SideB::kN>{}, [&](int i) __attribute__((always_inline)) {
+          B.issue(kPair && SideB::second(wave, i) ? r2 : r, i, lds_b + other);
+        });
       } else {
-        quarter(0, here, 1, Yes{}, nothing);
+        quarter(0, here, 1, Yes{}, Zero{}, nothing);
       }
-      quarter(1, here, 2, Yes{}, nothing);
-      quarter(2, here, 3, Yes{}, nothing);
+      quarter(1, here, 2, Yes{}, Zero{}, nothing);
+      quarter(2, here, 3, Yes{}, Zero{}, nothing);
       if constexpr (decltype(load_b)::value) {
         // The stage's last fragments are in registers, the next stage is in LDS.
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
         const uint8_t* there = smem + other;
         if constexpr (decltype(load_a)::value) {
-          const i32x4_t r = A.rsrc(ks + 2, false);
-          quarter(3, there, 0, Yes{}, [&](int k) __attribute__((always_inline)) { A.issue(r, k, lds_a + buf); });
+          const i32x4_t r = A.rsrc(ks + 2);
+          A.cut(ks + 2);
+          quarter(3, there, 0, Yes{}, std::integral_constant<int, SideA::kN>{}, [&](int i) __attribute__((always_inline)) {
+            A.issue(r, i, lds_a + buf);
+          });
         } else {
-          quarter(3, there, 0, Yes{}, nothing);
+          quarter(3, there, 0, Yes{}, Zero{}, nothing);
         }
       } else {
-        quarter(3, here, 0, No{}, nothing);
+        quarter(3, here, 0, No{}, Zero{}, nothing);
       }
     };
     int ks = k0;
@@ -628,41 +677,46 @@ __global__ void __launch_bounds__(256, 1) product_wide_kernel(Product g, Epi epi
 
     // Lane l, element v of a block (the operands' roles are exchanged): row l % 32, column
     // 8 (v / 4) + 4 (l / 32) + v % 4.  A wave's staged rows are its own.
-    const uint32_t free_buf = ((ks - k0) & 1) ? 0 : kWidePad + kWideStage;
-    float* stg = reinterpret_cast<float*>(lds + free_buf) + wave * 32 * kWideOut;
-    const int c = 4 * (lane % (kPair ? 16 : 32)), n = n0 + wn * (kPair ? 64 : 128) + c;
-    const int stg_col = kPair ? (c >> 5) * 64 + (c & 31) : c;
-    const auto row_of = [&](int R) { return m0 + wm * 128 + R; };
+    constexpr int kWaveCols = kCols / 2, kLanes = kWaveCols / 4;
+    constexpr int kAhead = Epi::kAhead < 32 / (64 / kLanes) ? Epi::kAhead : 32 / (64 / kLanes);
+    const uint32_t free_buf = ((ks - k0) & 1) ? 0 : L::kPad + L::kStage;
+    float* stg = reinterpret_cast<float*>(lds + free_buf) + wave * 32 * L::kOut;
+    const int c = 4 * (lane % kLanes), n = n0 + wn * kWaveCols + c;
+    const int staged = kPair ? (c >> 5) * 64 + (c & 31) : c;
+    const auto row_of = [&](int R) { return m0 + wm * (BM / 2) + R; };
+    float* mine = part + ((static_cast<size_t>(tile - whole) * parts + p) * BM + wm * (BM / 2)) * BN + wn * (BN / 2) + staged;
     typename Epi::Cols cols;
-    Batch<Epi, Epi::kAhead> ahead;
-    float* mine = part + (static_cast<size_t>(tile - whole) * parts + p) * 65536 + wm * 32768 + wn * 128 + stg_col;
+    Batch<Epi, kAhead> ahead;
     if (cut == 1 && n < g.N) {
       cols = epi.cols(n);
-      ahead.load(epi, g.M, n, lane / (kPair ? 16 : 32), kPair ? 4 : 2, row_of);
+      ahead.load(epi, g.M, n, lane / kLanes, 64 / kLanes, row_of);
     }
-    auto stage_rows = [&](const Acc<E> (&r)[4]) __attribute__((always_inline)) {
+    auto stage_rows = [&](const Acc<E> (&r)[NJ]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           f32x4 v;
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = as_float(r[j][4 * q + e]);
-          *reinterpret_cast<f32x4*>(stg + r32 * kWideOut + 32 * j + 8 * q + 4 * hi) = v;
+          *reinterpret_cast<f32x4*>(stg + r32 * L::kOut + 32 * j + 8 * q + 4 * hi) = v;
         }
     };
-    // One copy of the epilogue for the four: unrolled, its activations do not fit the
-    // instruction cache.
+    // One copy of the epilogue for all blocks of rows: unrolled, its activations do not fit
+    // the instruction cache.
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NI; ++i) {
       if (i == 0) stage_rows(acc[0]);
-      else if (i == 1) stage_rows(acc[1]);
-      else if (i == 2) stage_rows(acc[2]);
-      else stage_rows(acc[3]);
+      if constexpr (NI > 1)
+        if (i == 1) stage_rows(acc[1]);
+      if constexpr (NI > 2) {
+        if (i == 2) stage_rows(acc[2]);
+        if (i == 3) stage_rows(acc[3]);
+      }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
-      results_out<E, kPair, 128, 32, 64, Epi::kAhead>(g, epi, cols, ahead, stg, kWideOut, n, lane, 32 * i, i < 3, row_of,
-                                                      cut > 1, [&](int R) { return mine + R * 256; }, 32);
+      results_out<E, kPair, BN / 2, 32, 64, kAhead>(g, epi, cols, ahead, stg, L::kOut, n, lane, 32 * i, i + 1 < NI, row_of,
+                                                    cut > 1, [&](int R) { return mine + R * BN; }, 32);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
     }
@@ -670,26 +724,26 @@ __global__ void __launch_bounds__(256, 1) product_wide_kernel(Product g, Epi epi
 }
 
 // The rest's parts added in order: 1024 sums (of a pair: 512 of either) to a workgroup.
-template <bool PAIR, class Epi>
+template <bool PAIR, int BM, int BN, class Epi>
 __global__ void __launch_bounds__(256) product_rest_kernel(Product g, Epi epi, int whole, int parts, const float* part) {
-  constexpr int kCols = PAIR ? 128 : 256, kGroups = PAIR ? 32 : 64, kQuads = kCols / 4;
-  const int mt = static_cast<int>(ceil_div(g.M, 256)), nt = static_cast<int>(ceil_div(g.N, kCols));
+  constexpr int kCols = PAIR ? BN / 2 : BN, kQuads = kCols / 4, kGroups = BM * kQuads / 256, kBand = 2048 / BM;
+  const int mt = static_cast<int>(ceil_div(g.M, BM)), nt = static_cast<int>(ceil_div(g.N, kCols));
   const int tile = blockIdx.x / kGroups, i = (blockIdx.x % kGroups) * 256 + threadIdx.x;
   int m0, n0;
-  wide_place<kCols>(whole + tile, mt, nt, m0, n0);
+  tile_place<BM, kBand, kCols>(whole + tile, mt, nt, m0, n0);
   const int R = i / kQuads, c = 4 * (i % kQuads), m = m0 + R, n = n0 + c;
   if (m >= g.M || n >= g.N) return;
   const typename Epi::Cols cols = epi.cols(n);
   const typename Epi::Ahead ahead = epi.ahead(m, n);
-  const float* q = part + static_cast<size_t>(tile) * parts * 65536 + R * 256 + (PAIR ? (c >> 5) * 64 + (c & 31) : c);
+  const float* q = part + (static_cast<size_t>(tile) * parts * BM + R) * BN + (PAIR ? (c >> 5) * 64 + (c & 31) : c);
   f32x4 s = {0.f, 0.f, 0.f, 0.f}, u = {0.f, 0.f, 0.f, 0.f};
   for (int p = 0; p < parts; p += kSumAhead) {
     f32x4 b[kSumAhead], d[kSumAhead];
 #pragma unroll
     for (int k = 0; k < kSumAhead; ++k)
       if (p + k < parts) {
-        b[k] = *reinterpret_cast<const f32x4*>(q + static_cast<size_t>(p + k) * 65536);
-        if constexpr (PAIR) d[k] = *reinterpret_cast<const f32x4*>(q + static_cast<size_t>(p + k) * 65536 + 32);
+        b[k] = *reinterpret_cast<const f32x4*>(q + static_cast<size_t>(p + k) * BM * BN);
+        if constexpr (PAIR) d[k] = *reinterpret_cast<const f32x4*>(q + static_cast<size_t>(p + k) * BM * BN + 32);
       }
 #pragma unroll
     for (int k = 0; k < kSumAhead; ++k)
@@ -717,20 +771,26 @@ inline size_t part_bytes(bool pair, int64_t M, int64_t N) {
 
 struct TilePlan {
   int rows, cols;       // of a tile, in operand rows
+  bool aligned;         // by DMA
   int64_t tiles;
-  int64_t whole;        // 256 x 256: tiles that are not cut
+  int64_t whole;        // aligned: tiles that are not cut
   int parts;            // of the others
 };
 
 // The cheapest tile and split by an estimate in microseconds: what a CU takes in, the
 // f32 matrix rate, and the partial sums' way out and back.
-inline TilePlan plan_tiles(El e, bool pair, bool wide, int64_t M, int64_t N, int64_t K) {
+inline TilePlan plan_tiles(El e, bool pair, bool by_dma, bool rows64, int64_t M, int64_t N, int64_t K) {
   const int size = e == El::F32 ? 4 : e == El::BF16 ? 2 : 1;
   const int64_t width = pair ? 2 * N : N, stages = ceil_div(K * size, 128);
   const double room = static_cast<double>(part_bytes(pair, M, N));
-  static const struct { int rows, cols; } kTiles[] = {{64, 128}, {128, 128}};
   TilePlan best{};
   double least = 0;
+  const auto offer = [&](double us, const TilePlan& t) {
+    if (best.tiles && us >= least) return;
+    least = us;
+    best = t;
+  };
+  static const struct { int rows, cols; } kTiles[] = {{64, 128}, {128, 128}};
   for (const auto& t : kTiles) {
     const int64_t tiles = ceil_div(M, t.rows) * ceil_div(width, t.cols), slots = int64_t{2} * kCus;
     for (int parts = 1; parts <= kMaxParts; ++parts) {
@@ -741,24 +801,29 @@ inline TilePlan plan_tiles(El e, bool pair, bool wide, int64_t M, int64_t N, int
       const double load = (t.rows + t.cols) * 0.128 * deep / (shared > 1 ? 28 : 20);
       const double mult = e == El::F32 ? t.rows * t.cols * 64 * deep / 0.5e6 : 0;
       const double in_turn = e == El::F32 ? static_cast<double>(ceil_div(items, kCus)) : rounds * shared;
-      const double us = in_turn * std::max(load, mult) + 2 + 0.5 * rounds + (parts > 1 ? 4 + planes * 2 / 5e6 : 0);
-      if (best.tiles == 0 || us < least) {
-        least = us;
-        best = TilePlan{t.rows, t.cols, tiles, 0, parts};
-      }
+      offer(in_turn * std::max(load, mult) + 2 + 0.5 * rounds + (parts > 1 ? 4 + planes * 2 / 5e6 : 0),
+            TilePlan{t.rows, t.cols, false, tiles, 0, parts});
     }
   }
-  if (!wide) return best;
-  // Full rounds of whole tiles; what is left over, which would leave CUs idle, in parts.
-  const int64_t tiles = ceil_div(M, 256) * ceil_div(width, 256), whole = tiles / kCus * kCus, rest = tiles - whole;
-  for (int parts = 1; parts <= kMaxParts; ++parts) {
-    const double planes = static_cast<double>(rest) * parts * 256 * 256 * 4;
-    if (parts > 1 && (rest == 0 || rest * parts > kCus || planes > room || stages / parts < 4)) break;
-    const double us = whole / kCus * (1.5 * stages + 8) + (rest ? 1.5 * ceil_div(stages, parts) + 8 : 0) + 2 +
-                      (parts > 1 ? 4 + planes * 2 / 5e6 : 0);
-    if (us < least) {
-      least = us;
-      best = TilePlan{256, 256, tiles, whole, parts};
+  if (!by_dma) return best;
+  // Microseconds of a stage with all CUs at work (the clock falls with the power) or each
+  // alone, and of a tile's begin and end; `on` tiles run on a CU at a time.  Partial sums
+  // are mostly still in the caches.  224 x 4096 x 5120: 128 x 128 in 4 parts 24 us
+  // (estimate 25), 256 x 256 in 8 29 (29), 1000 x 5120 x 5120 in 128 x 128 60 (82).
+  static const struct { int rows, cols, on; double stage, alone, end; } kDma[] = {
+      {256, 256, 1, 1.55, 1.1, 8}, {256, 128, 1, 1.0, 0.8, 6}, {128, 128, 2, 1.0, 0.6, 6}, {64, 128, 2, 0.8, 0.5, 5}};
+  for (const auto& t : kDma) {
+    if (t.rows == 64 && !rows64) continue;
+    // Full rounds of whole tiles; what is left over, which would leave CUs idle, in parts.
+    const int64_t slots = int64_t{t.on} * kCus, tiles = ceil_div(M, t.rows) * ceil_div(width, t.cols);
+    const int64_t whole = tiles / slots * slots, rest = tiles - whole;
+    for (int parts = 1; parts <= kMaxParts; ++parts) {
+      const double planes = static_cast<double>(rest) * parts * t.rows * t.cols * 4;
+      if (parts > 1 && (rest == 0 || rest * parts > slots || planes > room || stages / parts < 4)) break;
+      const double pace = rest * parts <= kCus ? t.alone : t.stage;
+      offer(whole / slots * (t.stage * stages + t.end) + (rest ? pace * ceil_div(stages, parts) + t.end : 0) + 2 +
+                (parts > 1 ? 2 + planes / 5e6 : 0),
+            TilePlan{t.rows, t.cols, true, tiles, whole, parts});
     }
   }
   return best;
@@ -778,13 +843,26 @@ void launch_tiles(const Product& g, const Epi& epi, const TilePlan& t, float* pa
   else product_tile_kernel<E, KA, KB, PAIR, ANY, 128, 128><<<grid, 256, 0, s>>>(g, epi, t.parts, part);
 }
 
-// Whole stages, and rows whose offsets in a tile are 32-bit.
+// Rows whose offsets in a tile are 31-bit, and for a k-strided pair whole stages of either
+// matrix.
 template <El E, bool KB, bool PAIR>
-bool fits_wide(const Product& g) {
-  constexpr int kStage = ElInfo<E>::kStage;
-  const int64_t far = int64_t{1} << 24;
-  return g.K % kStage == 0 && g.a.ld * ElInfo<E>::kSize < far && g.b.ld * ElInfo<E>::kSize < far &&
-         (KB || !PAIR || (g.b.half % kStage == 0 && g.b.live == g.b.half));
+bool fits_dma(const Product& g) {
+  const int64_t far = int64_t{1} << 23;
+  return g.a.ld * ElInfo<E>::kSize < far && g.b.ld * ElInfo<E>::kSize < far && (KB || !PAIR || g.b.half % ElInfo<E>::kStage == 0);
+}
+
+template <El E, bool KA, bool KB, bool PAIR, int BM, int BN, class Epi>
+int launch_aligned(const Product& g, const Epi& epi, const TilePlan& t, float* part, hipStream_t s) {
+  constexpr bool kPair = PAIR && KB;
+  constexpr int kSlots = kCus * (BM + BN > 256 ? 1 : 2), kGroups = BM * (kPair ? BN / 2 : BN) / 1024;
+  const int64_t rest = t.tiles - t.whole;
+  const unsigned grid = t.whole ? kSlots : static_cast<unsigned>(ceil_div(rest * t.parts, 8) * 8);
+  product_aligned_kernel<E, KA, KB, PAIR, BM, BN><<<grid, 256, 0, s>>>(g, epi, static_cast<int>(t.whole), t.parts, part);
+  if (t.parts > 1) {
+    if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
+    product_rest_kernel<kPair, BM, BN><<<static_cast<unsigned>(rest * kGroups), 256, 0, s>>>(g, epi, static_cast<int>(t.whole), t.parts, part);
+  }
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH_FAILED;
 }
 
 // Runs a product of M, N, K >= 1; `part` holds part_bytes(pair, M, N).
@@ -792,20 +870,15 @@ template <El E, bool KA, bool KB, bool PAIR, class Epi>
 int run_product(const Product& g, const Epi& epi, float* part, hipStream_t s) {
   constexpr bool kPair = PAIR && KB;
   const bool aligned = aligned16(g.a, E, KA, g.M, g.K) && aligned16(g.b, E, KB, g.N, g.K);
-  bool wide = false;
-  if constexpr (E != El::F32) wide = aligned && fits_wide<E, KB, PAIR>(g);
-  const TilePlan t = plan_tiles(E, kPair, wide, g.M, g.N, g.K);
+  bool by_dma = false;
+  if constexpr (E != El::F32) by_dma = aligned && fits_dma<E, KB, PAIR>(g);
+  const TilePlan t = plan_tiles(E, kPair, by_dma, KA, g.M, g.N, g.K);
   if constexpr (E != El::F32) {
-    if (t.rows == 256) {
-      const int64_t rest = t.tiles - t.whole;
-      const unsigned grid = t.whole ? kCus : static_cast<unsigned>(ceil_div(rest * t.parts, 8) * 8);
-      product_wide_kernel<E, KA, KB, PAIR><<<grid, 256, 0, s>>>(g, epi, static_cast<int>(t.whole), t.parts, part);
-      if (t.parts > 1) {
-        if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
-        product_rest_kernel<kPair><<<static_cast<unsigned>(rest * (kPair ? 32 : 64)), 256, 0, s>>>(g, epi, static_cast<int>(t.whole), t.parts, part);
-      }
-      return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH_FAILED;
-    }
+    if constexpr (KA)
+      if (t.aligned && t.rows == 64) return launch_aligned<E, KA, KB, PAIR, 64, 128>(g, epi, t, part, s);
+    if (t.aligned && t.rows == 128) return launch_aligned<E, KA, KB, PAIR, 128, 128>(g, epi, t, part, s);
+    if (t.aligned && t.cols == 128) return launch_aligned<E, KA, KB, PAIR, 256, 128>(g, epi, t, part, s);
+    if (t.aligned) return launch_aligned<E, KA, KB, PAIR, 256, 256>(g, epi, t, part, s);
   }
   if (aligned) launch_tiles<E, KA, KB, PAIR, false>(g, epi, t, part, s);
   else launch_tiles<E, KA, KB, PAIR, true>(g, epi, t, part, s);

@@ -15,9 +15,9 @@
 // A row belongs to as many waves as give each lane C times eight of its elements; a wave
 // that holds a whole row needs no barrier.
 #include <algorithm>
+#include <initializer_list>
 
-#include "moe_mi355x.h"
-#include "rows.h"
+#include "norm_back.h"
 
 namespace moe {
 namespace {
@@ -30,12 +30,6 @@ struct NormArgs {
   int T, H, waves;
   float eps, a, b;
   int layer, gate_kind, params_f32, out_dtype;
-};
-
-// Eight columns of a row: chunk c of lane `at`, of a row's `width` lanes.
-struct Columns {
-  int i, left;
-  __device__ __forceinline__ Columns(int c, int at, int width, int H) : i(8 * (at + c * width)), left(H - i) {}
 };
 
 // mean (layer norms) and 1 / deviation of the C x 8 elements of each lane.
@@ -192,209 +186,18 @@ __global__ void __launch_bounds__(C == 1 ? 1024 : 512) norm_kernel(NormArgs a) {
   }
 }
 
-// ---------------------------------------------------------------- backward
+// ---------------------------------------------------------------- sums over rows
 
-struct NormBackArgs {
-  const void *y, *z, *gate, *w, *pw, *pb, *dz, *dout;
-  void *dy, *dr, *dgate;
-  float* part;                       // [groups][sums][H]
-  int64_t ldy, ldz, ldg, lddz, lddo, lddy, lddr, lddg;
-  int T, H, waves, groups;
-  float eps, a, b;
-  int layer, gate_kind, params_f32;
-  int sums;                          // bits of Sum
-};
-// The sums over rows, in the order in which a group stores them.
-enum Sum { kSumW = 1, kSumWb = 2, kSumPw = 4, kSumPb = 8, kSumGate = 16 };
-constexpr int kSums = 5;
-
-template <bool YF32, bool SF32, bool OF32, int C>
-__global__ void __launch_bounds__(512) norm_back_kernel(NormBackArgs a) {
-  __shared__ RowLds<float> lds;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int in_row = a.waves > 1 ? wave : 0;
-  const int group = a.waves > 1 ? blockIdx.x : static_cast<int>(blockIdx.x) * (blockDim.x >> 6) + wave;
-  if (group >= a.groups) return;
-  const int at = in_row * 64 + lane, width = a.waves * 64;
-  int turn = 0;
-  const bool pf = a.params_f32;
-  const float inv_h = 1.0f / a.H;
-  float acc[kSums][C][8];
-#pragma unroll
-  for (int k = 0; k < kSums; ++k)
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[k][c][e] = 0.0f;
-  struct Row {
-    Raw8<YF32> y[C];
-    Raw8<SF32> z[C], dz[C];
-    Raw8<OF32> dout[C];
-  };
-  const bool need_y = a.pw || (a.gate_kind != MOE_GATE_NONE && a.dgate) || (a.sums & kSumGate);
-  const auto load = [&](Row& R, int64_t t) __attribute__((always_inline)) {
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const Columns col(c, at, width, a.H);
-      if (need_y) R.y[c] = load8<YF32>(static_cast<const uint8_t*>(a.y) + t * a.ldy * (YF32 ? 4 : 2), col.i, col.left);
-      if (a.dz) R.dz[c] = load8<SF32>(static_cast<const uint8_t*>(a.dz) + t * a.lddz * (SF32 ? 4 : 2), col.i, col.left);
-      if (a.dout) {
-        R.z[c] = load8<SF32>(static_cast<const uint8_t*>(a.z) + t * a.ldz * (SF32 ? 4 : 2), col.i, col.left);
-        R.dout[c] = load8<OF32>(static_cast<const uint8_t*>(a.dout) + t * a.lddo * (OF32 ? 4 : 2), col.i, col.left);
-      }
-    }
-  };
-  const auto param = [&](const void* p, int c, float (&v)[8]) {
-    const Columns col(c, at, width, a.H);
-    load8_of(pf, p, col.i, col.left, v);
-  };
-  Row R;
-  load(R, group);
-  for (int64_t t = group; t < a.T; t += a.groups) {
-    float y[C][8], z[C][8], zt[C][8], dn[C][8];
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[c][e] = need_y ? value<YF32>(R.y[c], e) : 0.0f;
-        zt[c][e] = a.dz ? value<SF32>(R.dz[c], e) : 0.0f;
-        z[c][e] = a.dout ? value<SF32>(R.z[c], e) : 0.0f;
-        dn[c][e] = a.dout ? value<OF32>(R.dout[c], e) : 0.0f;
-      }
-    // The next row's loads are in flight meanwhile.
-    load(R, min(t + a.groups, static_cast<int64_t>(a.T) - 1));
-    const float gate_token = a.gate_kind == MOE_GATE_TOKEN ? load_of(pf, a.gate, t) : 1.0f;
-    float t8[8];
-
-    // Statistics of z and y, and z's sums with dn.
-    float zmean = 0.0f, ymean = 0.0f, zr = 1.0f, yr = 1.0f, m = 0.0f, dmean = 0.0f;
-    if (a.layer) {
-      float s[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s[0] += z[c][e];
-          s[1] += y[c][e];
-        }
-      row_all(s, in_row, a.waves, lds, turn, Add{});
-      zmean = s[0] * inv_h;
-      ymean = s[1] * inv_h;
-    }
-    {
-      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const Columns col(c, at, width, a.H);
-        if (a.sums & kSumWb) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[1][c][e] += dn[c][e];
-        }
-        if (a.w && a.dout) param(a.w, c, t8);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float zc = e < col.left ? z[c][e] - zmean : 0.0f, yc = e < col.left ? y[c][e] - ymean : 0.0f;
-          const float d = a.w && a.dout ? dn[c][e] * t8[e] : dn[c][e];
-          s[0] = fmaf(zc, zc, s[0]);
-          s[1] = fmaf(d, zc, s[1]);
-          s[2] += d;
-          s[3] = fmaf(yc, yc, s[3]);
-          z[c][e] = zc;
-          y[c][e] = a.pw ? yc : y[c][e];
-        }
-      }
-      row_all(s, in_row, a.waves, lds, turn, Add{});
-      zr = 1.0f / sqrtf(s[0] * inv_h + a.eps);
-      yr = 1.0f / sqrtf(s[3] * inv_h + a.eps);
-      m = s[1] * inv_h * zr;
-      dmean = a.layer ? s[2] * inv_h : 0.0f;
-    }
-    // zt, dr, dv; y becomes n(y), zt becomes dv.
-    float s[3] = {0.0f, 0.0f, 0.0f};
-    const void* gate_row = a.gate_kind == MOE_GATE_FULL ? static_cast<const uint8_t*>(a.gate) + t * a.ldg * (pf ? 4 : 2) : a.gate;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const Columns col(c, at, width, a.H);
-      float w8[8], p8[8], b8[8], g8[8];
-      if (a.dout) {
-        if (a.w) param(a.w, c, w8);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float n = z[c][e] * zr, d = a.w ? dn[c][e] * w8[e] : dn[c][e];
-          if (a.sums & kSumW) acc[0][c][e] = fmaf(dn[c][e], n, acc[0][c][e]);
-          zt[c][e] += zr * (d - n * m - dmean);
-        }
-      }
-      if (a.dr) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) t8[e] = a.a * zt[c][e];
-        store8<SF32>(a.dr, t * a.lddr + col.i, t8, col.left);
-      }
-      if (a.pw) param(a.pw, c, p8);
-      if (a.pb) param(a.pb, c, b8);
-      const bool columns = a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL;
-      if (columns) param(gate_row, c, g8);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float n = a.pw ? y[c][e] * yr : y[c][e];
-        const float v = a.pw ? n * p8[e] + (a.pb ? b8[e] : 0.0f) : n;
-        const float dv0 = a.b * zt[c][e], dg = dv0 * v;
-        if (a.sums & kSumGate) acc[4][c][e] += dg;
-        if (a.gate_kind == MOE_GATE_TOKEN) s[2] += e < col.left ? dg : 0.0f;
-        t8[e] = dg;
-        const float dv = dv0 * (columns ? g8[e] : gate_token);
-        if (a.sums & kSumPw) acc[2][c][e] = fmaf(dv, n, acc[2][c][e]);
-        if (a.sums & kSumPb) acc[3][c][e] += dv;
-        const float dp = e < col.left ? (a.pw ? dv * p8[e] : dv) : 0.0f;
-        s[0] = fmaf(dp, n, s[0]);
-        s[1] += dp;
-        y[c][e] = n;
-        zt[c][e] = dp;
-      }
-      if (a.gate_kind == MOE_GATE_FULL && a.dgate) {
-        if (pf) store8<true>(a.dgate, t * a.lddg + col.i, t8, col.left);
-        else store8<false>(a.dgate, t * a.lddg + col.i, t8, col.left);
-      }
-    }
-    if (a.pw || (a.gate_kind == MOE_GATE_TOKEN && a.dgate)) row_all(s, in_row, a.waves, lds, turn, Add{});
-    if (a.gate_kind == MOE_GATE_TOKEN && a.dgate && at == 0) store_of(pf, a.dgate, t, s[2]);
-    if (a.dy) {
-      const float pm = s[0] * inv_h, pd = a.layer ? s[1] * inv_h : 0.0f;
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const Columns col(c, at, width, a.H);
-        if (a.pw) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) zt[c][e] = yr * (zt[c][e] - y[c][e] * pm - pd);
-        }
-        store8<YF32>(a.dy, t * a.lddy + col.i, zt[c], col.left);
-      }
-    }
-  }
-  int k = 0;
-#pragma unroll
-  for (int n = 0; n < kSums; ++n) {
-    if (!(a.sums & (1 << n))) continue;
-    float* p = a.part + (static_cast<size_t>(group) * __popc(a.sums) + k) * a.H;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const Columns col(c, at, width, a.H);
-      store8<true>(p, col.i, acc[n][c], col.left);
-    }
-    ++k;
-  }
-}
-
-// The groups' sums added in order: 64 columns to a workgroup, the groups in four ranges.
+// The groups' sums added in order: 16 columns to a workgroup, the groups in 64 ranges.
 struct NormSums {
   void* out[kSums];
   const float* part;
   int H, groups, n, f32;
 };
-__global__ void __launch_bounds__(256) norm_sums_kernel(NormSums a) {
-  __shared__ float red[4][64];
-  const int col = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6, k = blockIdx.y;
-  const int lo = q * a.groups / 4, hi = (q + 1) * a.groups / 4;
+__global__ void __launch_bounds__(1024) norm_sums_kernel(NormSums a) {
+  __shared__ float red[64][16];
+  const int c = threadIdx.x & 15, q = threadIdx.x >> 4, k = blockIdx.y, col = blockIdx.x * 16 + c;
+  const int lo = q * a.groups / 64, hi = (q + 1) * a.groups / 64;
   float s = 0.0f;
   if (col < a.H) {
     const float* p = a.part + static_cast<size_t>(k) * a.H + col;
@@ -408,11 +211,16 @@ __global__ void __launch_bounds__(256) norm_sums_kernel(NormSums a) {
       for (int i = 0; i < kAhead; ++i) s += v[i];
     }
   }
-  red[q][threadIdx.x & 63] = s;
+  red[q][c] = s;
   __syncthreads();
-  if (q || col >= a.H) return;
-  const int c = threadIdx.x & 63;
-  store_of(a.f32, a.out[k], col, (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]));
+  if (q >= 4) return;
+  s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s += red[16 * q + i][c];
+  // The four ranges' lanes of a column are 16 apart in one wave.
+  s += __shfl_xor(s, 16, kWave);
+  s += __shfl_xor(s, 32, kWave);
+  if (q == 0 && col < a.H) store_of(a.f32, a.out[k], col, s);
 }
 
 // ---------------------------------------------------------------- host
@@ -459,8 +267,6 @@ RowPlan row_plan(int H, int max_waves_of_one) {
   return {4, 8};
 }
 
-constexpr int kRowsOfOneWave = 4;      // to a workgroup
-
 template <bool YF32, bool SF32>
 int launch_norm(const NormArgs& a, int chunks, hipStream_t s) {
   const unsigned grid = static_cast<unsigned>(a.waves > 1 ? a.T : ceil_div(a.T, kRowsOfOneWave));
@@ -473,21 +279,15 @@ int launch_norm(const NormArgs& a, int chunks, hipStream_t s) {
 
 // Groups of rows of a backward pass: a workgroup or, for rows of one wave, four to a CU.
 int norm_groups(const moe_norm_config& c, int64_t T) {
-  const RowPlan p = row_plan(c.hidden_size, 8);
-  const int64_t most = p.waves == 1 ? 256 * 4 * 2 : 256 * std::max(1, 8 / p.waves);
-  return static_cast<int>(std::min(T, most));
+  const int waves = static_cast<int>(ceil_div(c.hidden_size, 512));
+  const int64_t most = waves == 1 ? 256 * 4 * 2 : 256 * std::max(1, 16 / waves);
+  // A group of few rows writes nearly as much as it reads: 1001 x 1537 with five sums, one
+  // row to a group, took 43 us.
+  const int64_t rows = waves == 1 ? 4 : 8;
+  return static_cast<int>(std::min({T, most, std::max<int64_t>(256, T / rows)}));
 }
 size_t norm_back_bytes(const moe_norm_config& c, int64_t T) {
   return std::max<size_t>(static_cast<size_t>(norm_groups(c, T)) * kSums * c.hidden_size * sizeof(float), 256);
-}
-
-template <bool YF32, bool SF32, bool OF32>
-void launch_norm_back(const NormBackArgs& a, int chunks, hipStream_t s) {
-  const unsigned grid = static_cast<unsigned>(a.waves > 1 ? a.groups : ceil_div(a.groups, kRowsOfOneWave));
-  const unsigned block = 64u * static_cast<unsigned>(a.waves > 1 ? a.waves : kRowsOfOneWave);
-  if (chunks == 1) norm_back_kernel<YF32, SF32, OF32, 1><<<grid, block, 0, s>>>(a);
-  else if (chunks == 2) norm_back_kernel<YF32, SF32, OF32, 2><<<grid, block, 0, s>>>(a);
-  else norm_back_kernel<YF32, SF32, OF32, 4><<<grid, block, 0, s>>>(a);
 }
 
 }  // namespace
@@ -567,12 +367,11 @@ int moe_norm_backward(const moe_norm_config* cfg, int32_t T, const void* y, int6
     if (bad) return bad;
     if (workspace_bytes < norm_back_bytes(c, T)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   }
-  const RowPlan p = row_plan(c.hidden_size, 8);
   NormBackArgs a{};
   a.y = y, a.z = z, a.gate = c.gate == MOE_GATE_NONE ? nullptr : gate, a.w = weight, a.pw = post_weight, a.pb = post_bias;
   a.dz = dz, a.dout = dout, a.dy = dy, a.dr = dresidual, a.dgate = dgate, a.part = static_cast<float*>(workspace);
   a.ldy = ldy, a.ldz = ldz, a.ldg = ldg, a.lddz = lddz, a.lddo = lddo, a.lddy = lddy, a.lddr = lddr, a.lddg = lddg;
-  a.T = T, a.H = c.hidden_size, a.waves = p.waves, a.groups = norm_groups(c, T);
+  a.T = T, a.H = c.hidden_size, a.groups = norm_groups(c, T);
   a.eps = c.eps, a.a = c.residual_scale, a.b = c.block_scale;
   a.layer = c.kind == MOE_NORM_LAYER, a.gate_kind = c.gate, a.params_f32 = c.param_dtype == MOE_DTYPE_F32;
   NormSums sums{};
@@ -585,18 +384,14 @@ int moe_norm_backward(const moe_norm_config* cfg, int32_t T, const void* y, int6
   sums.part = a.part, sums.H = c.hidden_size, sums.groups = a.groups, sums.f32 = a.params_f32;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (T > 0) {
-    const bool yf = c.block_dtype == MOE_DTYPE_F32, sf = c.stream_dtype == MOE_DTYPE_F32, of = c.out_dtype == MOE_DTYPE_F32;
-    if (yf) {
-      if (sf) of ? launch_norm_back<true, true, true>(a, p.chunks, s) : launch_norm_back<true, true, false>(a, p.chunks, s);
-      else of ? launch_norm_back<true, false, true>(a, p.chunks, s) : launch_norm_back<true, false, false>(a, p.chunks, s);
-    } else {
-      if (sf) of ? launch_norm_back<false, true, true>(a, p.chunks, s) : launch_norm_back<false, true, false>(a, p.chunks, s);
-      else of ? launch_norm_back<false, false, true>(a, p.chunks, s) : launch_norm_back<false, false, false>(a, p.chunks, s);
-    }
+    const bool sf = c.stream_dtype == MOE_DTYPE_F32, of = c.out_dtype == MOE_DTYPE_F32, pf = c.param_dtype == MOE_DTYPE_F32;
+    const bool bias = dbias || dpost_bias || post_bias;
+    if (c.block_dtype == MOE_DTYPE_F32) launch_norm_back_f32(a, s, sf, of, pf, bias);
+    else launch_norm_back_bf16(a, s, sf, of, pf, bias);
     if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
   }
   if (sums.n) {
-    norm_sums_kernel<<<dim3(static_cast<unsigned>(ceil_div(H, 64)), static_cast<unsigned>(sums.n)), 256, 0, s>>>(sums);
+    norm_sums_kernel<<<dim3(static_cast<unsigned>(ceil_div(H, 16)), static_cast<unsigned>(sums.n)), 1024, 0, s>>>(sums);
     if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
   }
   return MOE_OK;

@@ -100,12 +100,17 @@ __device__ __forceinline__ void store_of(bool f32, void* p, int64_t i, float v) 
 // Rotations within 16 lanes, then the two halves of 32 and of 64 swapped: every lane
 // combines equal operands in every step, so all get the same bits.
 template <class T, class F>
-__device__ __forceinline__ T wave_all(T x, F f) {
+__device__ __forceinline__ T sixteen_all(T x, F f) {
   const auto step = [&](auto rotated) { x = f(x, __builtin_bit_cast(T, rotated)); };
   step(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x128, 0xf, 0xf, true));   // row_ror:8
   step(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x124, 0xf, 0xf, true));
   step(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x122, 0xf, 0xf, true));
   step(__builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x121, 0xf, 0xf, true));
+  return x;
+}
+template <class T, class F>
+__device__ __forceinline__ T wave_all(T x, F f) {
+  x = sixteen_all(x, f);
   const auto a = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, x), __builtin_bit_cast(unsigned, x), false, false);
   x = f(__builtin_bit_cast(T, static_cast<unsigned>(a[0])), __builtin_bit_cast(T, static_cast<unsigned>(a[1])));
   const auto b = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, x), __builtin_bit_cast(unsigned, x), false, false);
@@ -129,12 +134,12 @@ __device__ __forceinline__ void row_all(T (&v)[N], int wave, int waves, RowLds<T
 #pragma unroll
   for (int i = 0; i < N; ++i) lds.v[turn][i][wave] = v[i];     // every lane the same value
   __syncthreads();
+  // Lane l takes wave l % 16's value (a sum's or a magnitude's identity is 0).
+  const int w = threadIdx.x & 15;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    T s = lds.v[turn][i][0];
-    for (int w = 1; w < waves; ++w) s = f(s, lds.v[turn][i][w]);
-    v[i] = s;
-  }
+  for (int i = 0; i < N; ++i) v[i] = w < waves ? lds.v[turn][i][w] : T(0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = sixteen_all(v[i], f);
   turn ^= 1;
 }
 struct Add {
