@@ -14,6 +14,7 @@
 // rounded once.  a and b stay in float32: one more rounding of either would add to dg's
 // and du's own (weight gradients off by 1.7 roundings instead of 1.4).
 #include "gemm.h"
+#include "pack.h"
 
 namespace moe {
 namespace {
@@ -60,8 +61,9 @@ __device__ __forceinline__ void act_slope(float v, int act, float& f, float& d) 
 
 struct None {};
 
-// h = act(g) u, and a and b where they are kept; their rows lie `ld`, a multiple of four,
-// apart, so that a whole quad may be written at their ends.
+// h = act(g) u, and a and b where they are kept; their rows lie `ld`, a multiple of eight,
+// apart, so that a whole quad may be written at their ends.  The eight elements that h's
+// row ends in are written, zeros behind its end.
 template <bool F32, bool KEEP>
 struct GatedOut {
   static constexpr int kAhead = 4;
@@ -86,6 +88,10 @@ struct GatedOut {
     }
     const size_t o = static_cast<size_t>(m) * ld + n;
     store4<F32>(h, o, h4);
+    if (n + 4 >= N && (n & 4) == 0) {
+      const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+      store4<F32>(h, o + 4, zero);
+    }
     if constexpr (KEEP) {
       store4<true>(a, o, a4);
       store4<true>(b, o, b4);
@@ -188,9 +194,22 @@ moe_linear_config down_config(const moe_ffn_config& c) {
   return moe_linear_config{c.intermediate_size, c.hidden_size, c.dtype, c.dtype, MOE_ACT_NONE};
 }
 
-// The workspace: partial sums, then h (forward) or [dg du] (backward).
+// Rows that do not lie in whole 16-byte pieces are laid out afresh where the products are
+// large: loads of odd rows take in less than half as much.  1001 x 1537 x 2049, a training
+// step: 290 us as it lies, see below.  Room for x and dy is always there, room for the
+// weights where their sizes are odd.
+constexpr int64_t kPackFrom = int64_t{1} << 29;      // multiply-adds of a product
+int64_t eights(int64_t n) { return (n + 7) / 8 * 8; }
+bool large(const moe_ffn_config& c, int64_t T) {
+  return c.dtype == MOE_DTYPE_BF16 && T > kSkinnyRows && T * c.hidden_size * c.intermediate_size >= kPackFrom;
+}
+bool odd_sizes(const moe_ffn_config& c) { return c.hidden_size % 8 || c.intermediate_size % 8; }
+size_t packed_bytes(int64_t rows, int64_t ld) { return align_up(static_cast<size_t>(rows) * ld * 2, 256); }
+
+// The workspace: partial sums, then h (forward) or [dg du] (backward), then x, dy
+// (backward), gate, up and down laid out afresh.
 size_t ffn_parts(const moe_ffn_config& c, int64_t T) {
-  const int64_t H = c.hidden_size, Ip = inner_ld(c);
+  const int64_t H = eights(c.hidden_size), Ip = inner_ld(c);
   const moe_linear_config down = down_config(c);
   size_t n = 0;
   moe_linear_workspace_size(&down, static_cast<int32_t>(std::min<int64_t>(T, kSkinnyRows)), &n);
@@ -198,16 +217,49 @@ size_t ffn_parts(const moe_ffn_config& c, int64_t T) {
   return align_up(n, 256);
 }
 size_t ffn_workspace(const moe_ffn_config& c, int64_t T, bool backward) {
-  return ffn_parts(c, T) + (backward ? 2 : 1) * h_bytes(c, T);
+  size_t n = ffn_parts(c, T) + (backward ? 2 : 1) * h_bytes(c, T);
+  const int64_t H = eights(c.hidden_size), I = eights(c.intermediate_size);
+  // Of any smaller number of rows too: the weights' room does not depend on it.
+  if (c.dtype == MOE_DTYPE_BF16) n += (backward ? 2 : 1) * packed_bytes(T, H) + (odd_sizes(c) ? 2 * packed_bytes(I, H) + packed_bytes(H, I) : 0);
+  return n;
 }
 
 bool misaligned(const void* p, size_t unit) { return reinterpret_cast<uintptr_t>(p) % unit != 0; }
 constexpr int64_t kFar = int64_t{1} << 40;     // strides whose products with a row index stay in 64 bits
 
 struct FfnArgs {
-  const void *x, *wg, *wu, *wd;
-  int64_t ldx;
+  const void *x, *dy, *wg, *wu, *wd;
+  int64_t ldx, lddy, ldw, ldd;       // of x, dy, gate and up, down
+  int H, I;                          // of the products: the sizes, or whole pieces of them
 };
+
+// The operands as they lie, or laid out afresh behind `room`.
+int ffn_operands(const moe_ffn_config& c, int T, const void* x, int64_t ldx, const void* dy, int64_t lddy, const void* wg,
+                 const void* wu, const void* wd, uint8_t* room, hipStream_t s, FfnArgs& f) {
+  f = FfnArgs{x, dy, wg, wu, wd, ldx, lddy, c.hidden_size, c.intermediate_size, c.hidden_size, c.intermediate_size};
+  if (!large(c, T)) return MOE_OK;
+  const bool odd = odd_sizes(c);
+  const int H = c.hidden_size, I = c.intermediate_size, Hp = static_cast<int>(eights(H)), Ip = static_cast<int>(eights(I));
+  const auto lies_odd = [](const void* p, int64_t ld) { return ld % 8 || reinterpret_cast<uintptr_t>(p) % 16; };
+  PackArgs a{};
+  const auto pack = [&](const void*& p, int64_t& ld, int rows, int cols, int to_rows, int to_ld) {
+    a.item[a.n++] = PackItem{p, room, ld, to_ld, rows, cols, to_rows};
+    p = room;
+    ld = to_ld;
+    room += packed_bytes(to_rows, to_ld);
+  };
+  if (odd || lies_odd(x, ldx)) pack(f.x, f.ldx, T, H, T, Hp);
+  if (dy && (odd || lies_odd(dy, lddy))) pack(f.dy, f.lddy, T, H, T, Hp);
+  if (odd) {
+    pack(f.wg, f.ldw, I, H, Ip, Hp);
+    f.ldw = H;
+    pack(f.wu, f.ldw, I, H, Ip, Hp);
+    pack(f.wd, f.ldd, H, I, Hp, Ip);
+    f.H = Hp;
+    f.I = Ip;
+  }
+  return a.n == 0 || pack_rows<uint16_t>(a, s) ? MOE_OK : MOE_ERR_LAUNCH_FAILED;
+}
 
 template <bool F32>
 int ffn_forward(const moe_ffn_config& c, int T, const FfnArgs& f, void* y, int64_t ldy, void* h, float* a, float* b,
@@ -215,13 +267,13 @@ int ffn_forward(const moe_ffn_config& c, int T, const FfnArgs& f, void* y, int64
   constexpr El E = F32 ? El::F32 : El::BF16;
   const int H = c.hidden_size, I = c.intermediate_size;
   const int64_t Ip = inner_ld(c);
-  const Product g{{f.x, nullptr, f.ldx, 0, 0}, {f.wg, f.wu, H, 0, 0}, T, I, H};
+  const Product g{{f.x, nullptr, f.ldx, 0, 0}, {f.wg, f.wu, f.ldw, 0, 0}, T, I, f.H};
   float* part = reinterpret_cast<float*>(ws);
   const int st = a ? run_product<E, true, true, true>(g, GatedOut<F32, true>{h, a, b, Ip, I, c.activation}, part, s)
                    : run_product<E, true, true, true>(g, GatedOut<F32, false>{h, a, b, Ip, I, c.activation}, part, s);
   if (st) return st;
   if (T > kSkinnyRows) {
-    const Product d{{h, nullptr, Ip, 0, 0}, {f.wd, nullptr, I, 0, 0}, T, H, I};
+    const Product d{{h, nullptr, Ip, 0, 0}, {f.wd, nullptr, f.ldd, 0, 0}, T, H, f.I};
     return run_product<E, true, true, false>(d, RowsOut<F32>{y, nullptr, ldy, H, T, T}, part, s);
   }
   const moe_linear_config down = down_config(c);
@@ -229,28 +281,26 @@ int ffn_forward(const moe_ffn_config& c, int T, const FfnArgs& f, void* y, int64
 }
 
 template <bool F32>
-int ffn_backward(const moe_ffn_config& c, int T, const FfnArgs& f, const void* h, const float* a, const float* b,
-                 const void* dy, int64_t lddy, void* dx, int64_t lddx, void* dwg, void* dwu, void* dwd, uint8_t* ws,
-                 hipStream_t s) {
+int ffn_backward(const moe_ffn_config& c, int T, const FfnArgs& f, const void* h, const float* a, const float* b, void* dx,
+                 int64_t lddx, void* dwg, void* dwu, void* dwd, void* d, uint8_t* ws, hipStream_t s) {
   constexpr El E = F32 ? El::F32 : El::BF16;
   const int H = c.hidden_size, I = c.intermediate_size, Ip = static_cast<int>(inner_ld(c));
   float* part = reinterpret_cast<float*>(ws);
-  void* d = ws + ffn_parts(c, T);
   int st = MOE_OK;
   if (dwd) {
-    const Product g{{dy, nullptr, lddy, 0, 0}, {h, nullptr, Ip, 0, 0}, H, I, T};
-    st = run_product<E, false, false, false>(g, RowsOut<F32>{dwd, nullptr, I, I, H, H}, part, s);
+    const Product g{{f.dy, nullptr, f.lddy, 0, 0}, {h, nullptr, Ip, 0, 0}, f.H, f.I, T};
+    st = run_product<E, false, false, false>(g, RowsOut<F32>{dwd, nullptr, I, I, f.H, H}, part, s);
   }
   if (st == MOE_OK && (dx || dwg)) {
-    const Product g{{dy, nullptr, lddy, 0, 0}, {f.wd, nullptr, I, 0, 0}, T, I, H};
+    const Product g{{f.dy, nullptr, f.lddy, 0, 0}, {f.wd, nullptr, f.ldd, 0, 0}, T, f.I, f.H};
     st = run_product<E, true, false, false>(g, SlopesOut<F32>{a, b, d, Ip, I}, part, s);
   }
   if (st == MOE_OK && dwg) {
-    const Product g{{d, nullptr, 2 * Ip, 0, 0}, {f.x, nullptr, f.ldx, 0, 0}, 2 * Ip, H, T};
+    const Product g{{d, nullptr, 2 * Ip, 0, 0}, {f.x, nullptr, f.ldx, 0, 0}, 2 * Ip, f.H, T};
     st = run_product<E, false, false, false>(g, RowsOut<F32>{dwg, dwu, H, H, Ip, I}, part, s);
   }
   if (st == MOE_OK && dx) {
-    const Product g{{d, nullptr, 2 * Ip, 0, 0}, {f.wg, f.wu, H, Ip, I}, T, H, 2 * Ip};
+    const Product g{{d, nullptr, 2 * Ip, 0, 0}, {f.wg, f.wu, f.ldw, Ip, I}, T, f.H, 2 * Ip};
     st = run_product<E, true, false, true>(g, RowsOut<F32>{dx, nullptr, lddx, H, T, T}, part, s);
   }
   return st;
@@ -299,8 +349,10 @@ int moe_ffn_forward(const moe_ffn_config* cfg, int32_t T, const void* x, int64_t
   void* h = kept ? k : ws + ffn_parts(*cfg, T);
   float* a = kept ? reinterpret_cast<float*>(k + h_bytes(*cfg, T)) : nullptr;
   float* b = kept ? reinterpret_cast<float*>(k + h_bytes(*cfg, T) + slope_bytes(*cfg, T)) : nullptr;
-  const FfnArgs f{x, w_gate, w_up, w_down, ldx};
   hipStream_t s = static_cast<hipStream_t>(stream);
+  FfnArgs f;
+  const int bad = ffn_operands(*cfg, T, x, ldx, nullptr, 0, w_gate, w_up, w_down, ws + ffn_parts(*cfg, T) + h_bytes(*cfg, T), s, f);
+  if (bad) return bad;
   return cfg->dtype == MOE_DTYPE_F32 ? ffn_forward<true>(*cfg, T, f, y, ldy, h, a, b, ws, s)
                                      : ffn_forward<false>(*cfg, T, f, y, ldy, h, a, b, ws, s);
 }
@@ -336,11 +388,13 @@ int moe_ffn_backward(const moe_ffn_config* cfg, int32_t T, const void* x, int64_
   const uint8_t* k = static_cast<const uint8_t*>(kept);
   const float* a = reinterpret_cast<const float*>(k + h_bytes(*cfg, T));
   const float* b = reinterpret_cast<const float*>(k + h_bytes(*cfg, T) + slope_bytes(*cfg, T));
-  const FfnArgs f{x, w_gate, w_up, w_down, ldx};
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  return cfg->dtype == MOE_DTYPE_F32
-             ? ffn_backward<true>(*cfg, T, f, k, a, b, dy, lddy, dx, lddx, dw_gate, dw_up, dw_down, ws, s)
-             : ffn_backward<false>(*cfg, T, f, k, a, b, dy, lddy, dx, lddx, dw_gate, dw_up, dw_down, ws, s);
+  uint8_t* d = ws + ffn_parts(*cfg, T);
+  FfnArgs f;
+  const int bad = ffn_operands(*cfg, T, x, ldx, dy, lddy, w_gate, w_up, w_down, d + 2 * h_bytes(*cfg, T), s, f);
+  if (bad) return bad;
+  return cfg->dtype == MOE_DTYPE_F32 ? ffn_backward<true>(*cfg, T, f, k, a, b, dx, lddx, dw_gate, dw_up, dw_down, d, ws, s)
+                                     : ffn_backward<false>(*cfg, T, f, k, a, b, dx, lddx, dw_gate, dw_up, dw_down, d, ws, s);
 }
 
 }  // extern "C"

@@ -4,6 +4,7 @@
 // Rows of x in 16 or 32 bits are quantised first (quant_i8_kernel), each by its largest
 // magnitude.
 #include "gemm.h"
+#include "pack.h"
 #include "rows.h"
 
 namespace moe {
@@ -14,9 +15,10 @@ namespace {
 constexpr int kFewRows = 512;
 
 // A row of x to a workgroup: its largest magnitude, then its codes.  A lane keeps C times
-// eight elements; what is left of a longer row is read again, from the caches.
+// eight elements; what is left of a longer row is read again, from the caches.  Zeros
+// behind the row up to `width` codes.
 template <bool F32, int C>
-__global__ void __launch_bounds__(1024) quant_i8_kernel(const void* x, int64_t ldx, int K, int8_t* q, int64_t ldq, float* scale) {
+__global__ void __launch_bounds__(1024) quant_i8_kernel(const void* x, int64_t ldx, int K, int8_t* q, int64_t ldq, int width, float* scale) {
   __shared__ RowLds<uint32_t> lds;
   const int64_t m = blockIdx.x;
   const uint8_t* row = static_cast<const uint8_t*>(x) + m * ldx * (F32 ? 4 : 2);
@@ -41,21 +43,21 @@ __global__ void __launch_bounds__(1024) quant_i8_kernel(const void* x, int64_t l
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = value<F32>(r, e);
-    if (i < K) store_codes(q + m * ldq + i, v, s, inv, K - i);
+    if (i < width) store_codes(q + m * ldq + i, v, s, inv, width - i);
   };
 #pragma unroll
   for (int c = 0; c < C; ++c) put(head[c], first + c * step);
-  for (int i = first + C * step; i < K; i += step) put(load8<F32>(row, i, K - i), i);
+  for (int i = first + C * step; i < width; i += step) put(load8<F32>(row, i, K - i), i);
 }
 
 // Few rows: a lane for every eight elements, for the latency.  Many: four times as many to
 // a lane, for the loads in flight and the workgroups on a CU.
-int quantise(bool f32, int M, int K, const void* x, int64_t ldx, int8_t* q, int64_t ldq, float* scale, hipStream_t s) {
+int quantise(bool f32, int M, int K, const void* x, int64_t ldx, int8_t* q, int64_t ldq, int width, float* scale, hipStream_t s) {
   const bool few = M <= kFewRows;
-  const unsigned block = 64u * static_cast<unsigned>(std::min<int64_t>(16, ceil_div(K, few ? 512 : 2048)));
+  const unsigned block = 64u * static_cast<unsigned>(std::min<int64_t>(16, ceil_div(width, few ? 512 : 2048)));
   const unsigned grid = static_cast<unsigned>(M);
-  if (f32) few ? quant_i8_kernel<true, 1><<<grid, block, 0, s>>>(x, ldx, K, q, ldq, scale) : quant_i8_kernel<true, 4><<<grid, block, 0, s>>>(x, ldx, K, q, ldq, scale);
-  else few ? quant_i8_kernel<false, 1><<<grid, block, 0, s>>>(x, ldx, K, q, ldq, scale) : quant_i8_kernel<false, 4><<<grid, block, 0, s>>>(x, ldx, K, q, ldq, scale);
+  if (f32) few ? quant_i8_kernel<true, 1><<<grid, block, 0, s>>>(x, ldx, K, q, ldq, width, scale) : quant_i8_kernel<true, 4><<<grid, block, 0, s>>>(x, ldx, K, q, ldq, width, scale);
+  else few ? quant_i8_kernel<false, 1><<<grid, block, 0, s>>>(x, ldx, K, q, ldq, width, scale) : quant_i8_kernel<false, 4><<<grid, block, 0, s>>>(x, ldx, K, q, ldq, width, scale);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH_FAILED;
 }
 
@@ -124,12 +126,18 @@ int check_i8(const moe_linear_i8_config* c, int32_t rows) {
   return MOE_OK;
 }
 
-// The workspace: partial sums, then the codes of x in rows of whole 16-byte pieces, then
-// their scales.
+// Codes that do not lie in whole 16-byte pieces are laid out afresh where the product is
+// large.
+constexpr int64_t kPackFrom = int64_t{1} << 29;      // multiply-adds
+bool large(const moe_linear_i8_config& c, int64_t M) { return M > kSkinnyRows && M * c.in_features * c.out_features >= kPackFrom; }
+
+// The workspace: partial sums, then the codes of x in rows of whole 16-byte pieces, their
+// scales, and where rows of that length do not end with a piece, room for w's codes.
 int64_t codes_ld(const moe_linear_i8_config& c) { return align_up(c.in_features, 16); }
-size_t codes_bytes(const moe_linear_i8_config& c, int64_t M) { return align_up(static_cast<size_t>(M) * codes_ld(c), 256); }
+size_t codes_bytes(const moe_linear_i8_config& c, int64_t rows) { return align_up(static_cast<size_t>(rows) * codes_ld(c), 256); }
 size_t i8_workspace(const moe_linear_i8_config& c, int64_t M) {
-  return part_bytes(false, M, c.out_features) + (c.in_dtype == MOE_DTYPE_I8 ? 0 : codes_bytes(c, M) + align_up(M * 4, 256));
+  return part_bytes(false, M, c.out_features) + codes_bytes(c, M) + align_up(M * 4, 256) +
+         (c.in_features % 16 ? codes_bytes(c, c.out_features) : 0);
 }
 
 }  // namespace
@@ -148,7 +156,7 @@ int moe_quant_i8(int32_t dtype, int32_t rows, int32_t columns, const void* x, in
   if (!x || !codes || !scale) return MOE_ERR_NULL_PTR;
   if (ldx < columns || ldc < columns) return MOE_ERR_BAD_SHAPE;
   if (ldx > kFar || ldc > kFar || off(x, size_of(dtype)) || off(scale, 4)) return MOE_ERR_UNSUPPORTED;
-  return quantise(dtype == MOE_DTYPE_F32, rows, columns, x, ldx, codes, ldc, scale, static_cast<hipStream_t>(stream));
+  return quantise(dtype == MOE_DTYPE_F32, rows, columns, x, ldx, codes, ldc, columns, scale, static_cast<hipStream_t>(stream));
 }
 
 int moe_linear_i8_workspace_size(const moe_linear_i8_config* cfg, int32_t max_rows, size_t* bytes) {
@@ -180,14 +188,32 @@ int moe_linear_i8(const moe_linear_i8_config* cfg, int32_t M, const void* x, int
   float* part = static_cast<float*>(workspace);
   Product g{{x, nullptr, ldx, 0, 0}, {w, nullptr, ldw, 0, 0}, M, N, K};
   const float* sx = x_scale;
+  int8_t* q = static_cast<int8_t*>(workspace) + part_bytes(false, M, N);
+  float* qs = reinterpret_cast<float*>(q + codes_bytes(c, M));
+  const int64_t ld = codes_ld(c);
+  PackArgs p{};
   if (!codes) {
-    int8_t* q = static_cast<int8_t*>(workspace) + part_bytes(false, M, N);
-    float* qs = reinterpret_cast<float*>(q + codes_bytes(c, M));
-    const int bad = quantise(c.in_dtype == MOE_DTYPE_F32, M, K, x, ldx, q, codes_ld(c), qs, s);
+    const int bad = quantise(c.in_dtype == MOE_DTYPE_F32, M, K, x, ldx, q, ld, static_cast<int>(ld), qs, s);
     if (bad) return bad;
     g.a.p = q;
-    g.a.ld = codes_ld(c);
+    g.a.ld = ld;
     sx = qs;
+  }
+  if (large(c, M)) {
+    const auto lies_odd = [&](const void* a, int64_t l) { return K % 16 || l % 16 || off(a, 16); };
+    if (codes && lies_odd(x, ldx)) {
+      p.item[p.n++] = PackItem{x, q, ldx, ld, M, K, M};
+      g.a.p = q;
+      g.a.ld = ld;
+    }
+    if (K % 16) {
+      int8_t* wq = reinterpret_cast<int8_t*>(qs) + align_up(static_cast<size_t>(M) * 4, 256);
+      p.item[p.n++] = PackItem{w, wq, ldw, ld, N, K, N};
+      g.b.p = wq;
+      g.b.ld = ld;
+      g.K = static_cast<int>(ld);
+    }
+    if (p.n && !pack_rows<uint8_t>(p, s)) return MOE_ERR_LAUNCH_FAILED;
   }
   const bool bf = c.bias_dtype == MOE_DTYPE_F32;
   if (c.out_dtype == MOE_DTYPE_F32)
