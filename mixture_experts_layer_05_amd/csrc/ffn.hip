@@ -2,7 +2,7 @@
 //
 // Forward: one product computes g = x Wg^T and u = x Wu^T side by side (their columns
 // take turns in blocks of 32, so that a lane holds both of an element) and its epilogue
-// writes h = act(g) u; the down projection is moe_linear's.  For a backward pass the
+// writes h = act(g) u; the down projection is another product.  For a backward pass the
 // epilogue also keeps a = act(g) and b = u act'(g), in float32.
 //
 // Backward, from dy:
@@ -189,16 +189,11 @@ size_t h_bytes(const moe_ffn_config& c, int64_t T) { return align_up(static_cast
 size_t slope_bytes(const moe_ffn_config& c, int64_t T) { return align_up(static_cast<size_t>(T) * inner_ld(c) * 4, 256); }
 size_t kept_bytes(const moe_ffn_config& c, int64_t T) { return h_bytes(c, T) + 2 * slope_bytes(c, T); }
 
-// The down projection of a few rows streams its weights as any product of a few rows.
-moe_linear_config down_config(const moe_ffn_config& c) {
-  return moe_linear_config{c.intermediate_size, c.hidden_size, c.dtype, c.dtype, MOE_ACT_NONE};
-}
-
 // Rows that do not lie in whole 16-byte pieces are laid out afresh where the products are
 // large: loads of odd rows take in less than half as much.  1001 x 1537 x 2049, a training
 // step: 290 us as it lies, see below.  Room for x and dy is always there, room for the
 // weights where their sizes are odd.
-constexpr int64_t kPackFrom = int64_t{1} << 29;      // multiply-adds of a product
+constexpr int64_t kPackFrom = int64_t{1} << 27;      // multiply-adds of a product
 int64_t eights(int64_t n) { return (n + 7) / 8 * 8; }
 bool large(const moe_ffn_config& c, int64_t T) {
   return c.dtype == MOE_DTYPE_BF16 && T > kSkinnyRows && T * c.hidden_size * c.intermediate_size >= kPackFrom;
@@ -210,10 +205,7 @@ size_t packed_bytes(int64_t rows, int64_t ld) { return align_up(static_cast<size
 // (backward), gate, up and down laid out afresh.
 size_t ffn_parts(const moe_ffn_config& c, int64_t T) {
   const int64_t H = eights(c.hidden_size), Ip = inner_ld(c);
-  const moe_linear_config down = down_config(c);
-  size_t n = 0;
-  moe_linear_workspace_size(&down, static_cast<int32_t>(std::min<int64_t>(T, kSkinnyRows)), &n);
-  n = std::max({n, part_bytes(true, T, Ip), part_bytes(false, T, Ip), part_bytes(false, T, H), part_bytes(false, 2 * Ip, H), part_bytes(false, H, Ip)});
+  const size_t n = std::max({part_bytes(true, T, Ip), part_bytes(false, T, Ip), part_bytes(false, T, H), part_bytes(false, 2 * Ip, H), part_bytes(false, H, Ip)});
   return align_up(n, 256);
 }
 size_t ffn_workspace(const moe_ffn_config& c, int64_t T, bool backward) {
@@ -272,12 +264,8 @@ int ffn_forward(const moe_ffn_config& c, int T, const FfnArgs& f, void* y, int64
   const int st = a ? run_product<E, true, true, true>(g, GatedOut<F32, true>{h, a, b, Ip, I, c.activation}, part, s)
                    : run_product<E, true, true, true>(g, GatedOut<F32, false>{h, a, b, Ip, I, c.activation}, part, s);
   if (st) return st;
-  if (T > kSkinnyRows) {
-    const Product d{{h, nullptr, Ip, 0, 0}, {f.wd, nullptr, f.ldd, 0, 0}, T, H, f.I};
-    return run_product<E, true, true, false>(d, RowsOut<F32>{y, nullptr, ldy, H, T, T}, part, s);
-  }
-  const moe_linear_config down = down_config(c);
-  return moe_linear(&down, T, h, Ip, f.wd, I, nullptr, nullptr, 0, y, ldy, ws, ffn_parts(c, T), s);
+  const Product d{{h, nullptr, Ip, 0, 0}, {f.wd, nullptr, f.ldd, 0, 0}, T, H, f.I};
+  return run_product<E, true, true, false>(d, RowsOut<F32>{y, nullptr, ldy, H, T, T}, part, s);
 }
 
 template <bool F32>

@@ -396,6 +396,134 @@ __global__ void __launch_bounds__(256, 2) product_tile_kernel(Product g, Epi epi
   }
 }
 
+// ---------------------------------------------------------------- at most 16 rows
+//
+// The weights go from memory straight into the registers of the MFMAs (skinny.h): eight
+// waves compute 8 SETS operand columns over one part of the contraction, an eighth for
+// each.  Of a pair the two sets are eight columns of either product.
+constexpr int kSkinnyEight = 8;
+
+typedef int i32x4s __attribute__((ext_vector_type(4)));
+template <El E>
+using Acc16 = std::conditional_t<E == El::I8, i32x4s, f32x4>;
+template <El E>
+__device__ __forceinline__ Acc16<E> mfma16(const uint4& a, const uint4& b, Acc16<E> c) {
+  if constexpr (E == El::F32) {
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.x), __uint_as_float(b.x), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.y), __uint_as_float(b.y), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.z), __uint_as_float(b.z), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.w), __uint_as_float(b.w), c, 0, 0, 0);
+  } else if constexpr (E == El::BF16) {
+    return mfma_bf16_16x16x32(a, b, c);
+  } else {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4v, a), __builtin_bit_cast(i32x4v, b), c, 0, 0, 0);
+  }
+}
+
+template <El E, bool PAIR, bool ANY, int SETS, class Epi>
+__global__ void __launch_bounds__(kSkinnyEight * kWave, SETS == 1 ? 6 : 4) product_skinny_kernel(Product g, Epi epi, int parts, float* part) {
+  using I = ElInfo<E>;
+  static_assert(!PAIR || SETS == 2, "a set for either product");
+  constexpr int kCols = PAIR ? 8 : 8 * SETS, D = SETS == 1 ? 4 : 5;
+  __shared__ f32x4 red[kSkinnyEight][kWave];
+  __shared__ float out[16][20];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  const int n0 = blockIdx.x * kCols, p = blockIdx.y;
+  const int nb = static_cast<int>(ceil_div(g.K, I::kStage));
+  const int b0 = static_cast<int>(static_cast<int64_t>(p) * nb / parts), b1 = static_cast<int>(static_cast<int64_t>(p + 1) * nb / parts);
+  const int lo = b0 + wave * (b1 - b0) / kSkinnyEight, hi = b0 + (wave + 1) * (b1 - b0) / kSkinnyEight;
+  const uint8_t* wbase[SETS];
+  uint32_t woff[SETS];
+#pragma unroll
+  for (int h = 0; h < SETS; ++h) {
+    wbase[h] = static_cast<const uint8_t*>(PAIR && h ? g.b.q : g.b.p) + static_cast<size_t>(n0) * g.b.ld * I::kSize;
+    woff[h] = static_cast<uint32_t>(min((PAIR ? 0 : 8 * h) + (lane & 7), g.N - 1 - n0)) * static_cast<uint32_t>(g.b.ld) * I::kSize + 16 * lane_piece(lane);
+  }
+  const uint8_t* xbase = static_cast<const uint8_t*>(g.a.p);
+  const uint32_t xoff = static_cast<uint32_t>(min(r, g.M - 1)) * static_cast<uint32_t>(g.a.ld) * I::kSize + 16 * q;
+  const bool live = r < g.M, tail = g.K % I::kStage != 0;
+
+  struct Blk {
+    uint4 w[SETS], x[2];
+  };
+  Acc16<E> acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  int at = lo;
+  batches<D, Blk>(
+      hi - lo,
+      [&](Blk& k) __attribute__((always_inline)) {
+        const size_t o = static_cast<size_t>(at) * 128;
+        const int left = g.K - at * I::kStage;     // elements from this block on; only the last can be cut
+        k.x[0] = k.x[1] = uint4{0, 0, 0, 0};
+        if (!ANY && !tail) {
+#pragma unroll
+          for (int h = 0; h < SETS; ++h) k.w[h] = ld16_stream(wbase[h] + o + woff[h]);
+          if (live) {
+            k.x[0] = ld16(xbase + o + xoff);
+            k.x[1] = ld16(xbase + o + xoff + 64);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < SETS; ++h) k.w[h] = piece_of<E, ANY>(wbase[h] + o + woff[h], left - I::kPiece * lane_piece(lane));
+          if (live) {
+            k.x[0] = piece_of<E, ANY>(xbase + o + xoff, left - I::kPiece * q);
+            k.x[1] = piece_of<E, ANY>(xbase + o + xoff + 64, left - I::kPiece * (q + 4));
+          }
+        }
+        ++at;
+      },
+      [&](Blk& k) __attribute__((always_inline)) {
+        if constexpr (SETS == 2) {
+          const bool upper = lane & 8;
+          trade(k.w[0].x, k.w[1].x, upper);
+          trade(k.w[0].y, k.w[1].y, upper);
+          trade(k.w[0].z, k.w[1].z, upper);
+          trade(k.w[0].w, k.w[1].w, upper);
+          acc[0] = mfma16<E>(k.x[0], k.w[0], acc[0]);
+          acc[0] = mfma16<E>(k.x[1], k.w[1], acc[0]);
+        } else {
+          acc[0] = mfma16<E>(k.x[0], k.w[0], acc[0]);
+          acc[1] = mfma16<E>(k.x[1], k.w[0], acc[1]);
+        }
+      },
+      [] {});
+  f32x4 s;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (SETS == 2) {
+      s[i] = static_cast<float>(acc[0][i]);
+    } else {
+      // Eight columns: the halves of a block were multiplied over all sixteen, of which the
+      // lower eight are the first half's and the upper eight the second's.
+      const auto v = (lane & 8) ? acc[1][i] : acc[0][i];
+      s[i] = static_cast<float>(v + __shfl_xor(v, 8, kWave));
+    }
+  }
+  red[wave][lane] = s;
+  __syncthreads();
+  // Wave w < 4 adds elements i = w: rows 4 q + w.
+  if (wave < 4) {
+    float v = red[0][lane][wave];
+#pragma unroll
+    for (int o = 1; o < kSkinnyEight; ++o) v += red[o][lane][wave];
+    out[4 * q + wave][r] = v;
+  }
+  __syncthreads();
+  constexpr int kQuads = kCols / 4;
+  const int m = tid / kQuads, c = 4 * (tid % kQuads), n = n0 + c;
+  if (m >= g.M || n >= g.N) return;
+  const f32x4 a = *reinterpret_cast<const f32x4*>(&out[m][c]);
+  f32x4 u = {0.f, 0.f, 0.f, 0.f};
+  if constexpr (PAIR) u = *reinterpret_cast<const f32x4*>(&out[m][c + 8]);
+  if (parts > 1) {
+    const size_t np = part_stride(g.N), o = (static_cast<size_t>(p) * g.M * (PAIR ? 2 : 1) + m) * np + n;
+    *reinterpret_cast<f32x4*>(part + o) = a;
+    if constexpr (PAIR) *reinterpret_cast<f32x4*>(part + o + g.M * np) = u;
+  } else {
+    epi.put(m, n, a, u, epi.cols(n), epi.ahead(m, n));
+  }
+}
+
 // ---------------------------------------------------------------- aligned tiles
 //
 // BM x BN sums per workgroup of 2 x 2 waves, for operands in whole 16-byte pieces (bf16 and
@@ -865,6 +993,30 @@ int launch_aligned(const Product& g, const Epi& epi, const TilePlan& t, float* p
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH_FAILED;
 }
 
+// At most 16 rows: 16 operand columns to a workgroup while that gives two for each CU, else
+// 8; below one for each CU parts of at least 16 blocks of 128 bytes.
+template <El E, bool PAIR, class Epi>
+int launch_skinny(const Product& g, const Epi& epi, bool aligned, float* part, hipStream_t s) {
+  const bool wide = PAIR || ceil_div(g.N, 16) >= 2 * kCus;
+  const int64_t tiles = ceil_div(g.N, PAIR || !wide ? 8 : 16), blocks = ceil_div(g.K, ElInfo<E>::kStage);
+  const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kCus / tiles, blocks / 16, kMaxParts})));
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(parts));
+  constexpr int kThreads = kSkinnyEight * kWave;
+  if (wide) {
+    if (aligned) product_skinny_kernel<E, PAIR, false, 2><<<grid, kThreads, 0, s>>>(g, epi, parts, part);
+    else product_skinny_kernel<E, PAIR, true, 2><<<grid, kThreads, 0, s>>>(g, epi, parts, part);
+  } else if constexpr (!PAIR) {
+    if (aligned) product_skinny_kernel<E, false, false, 1><<<grid, kThreads, 0, s>>>(g, epi, parts, part);
+    else product_skinny_kernel<E, false, true, 1><<<grid, kThreads, 0, s>>>(g, epi, parts, part);
+  }
+  if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
+  if (parts > 1) {
+    product_sum_kernel<PAIR><<<static_cast<unsigned>(ceil_div(g.M * part_stride(g.N) / 4, 256)), 256, 0, s>>>(g, epi, parts, part);
+    if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
+  }
+  return MOE_OK;
+}
+
 // Runs a product of M, N, K >= 1; `part` holds part_bytes(pair, M, N).
 template <El E, bool KA, bool KB, bool PAIR, class Epi>
 int run_product(const Product& g, const Epi& epi, float* part, hipStream_t s) {
@@ -872,6 +1024,10 @@ int run_product(const Product& g, const Epi& epi, float* part, hipStream_t s) {
   const bool aligned = aligned16(g.a, E, KA, g.M, g.K) && aligned16(g.b, E, KB, g.N, g.K);
   bool by_dma = false;
   if constexpr (E != El::F32) by_dma = aligned && fits_dma<E, KB, PAIR>(g);
+  if constexpr (KA && KB) {
+    // 32-bit offsets of the rows.
+    if (g.M <= kSkinnyRows && std::max(g.a.ld, g.b.ld) < (int64_t{1} << 24)) return launch_skinny<E, PAIR>(g, epi, aligned, part, s);
+  }
   const TilePlan t = plan_tiles(E, kPair, by_dma, KA, g.M, g.N, g.K);
   if constexpr (E != El::F32) {
     if constexpr (KA)

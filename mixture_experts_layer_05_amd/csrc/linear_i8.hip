@@ -128,7 +128,7 @@ int check_i8(const moe_linear_i8_config* c, int32_t rows) {
 
 // Codes that do not lie in whole 16-byte pieces are laid out afresh where the product is
 // large.
-constexpr int64_t kPackFrom = int64_t{1} << 29;      // multiply-adds
+constexpr int64_t kPackFrom = int64_t{1} << 24;      // multiply-adds
 bool large(const moe_linear_i8_config& c, int64_t M) { return M > kSkinnyRows && M * c.in_features * c.out_features >= kPackFrom; }
 
 // The workspace: partial sums, then the codes of x in rows of whole 16-byte pieces, their
