@@ -193,7 +193,7 @@ size_t kept_bytes(const moe_ffn_config& c, int64_t T) { return h_bytes(c, T) + 2
 // large: loads of odd rows take in less than half as much.  1001 x 1537 x 2049, a training
 // step: 290 us as it lies, see below.  Room for x and dy is always there, room for the
 // weights where their sizes are odd.
-constexpr int64_t kPackFrom = int64_t{1} << 27;      // multiply-adds of a product
+constexpr int64_t kPackFrom = int64_t{1} << 22;      // multiply-adds of a product
 int64_t eights(int64_t n) { return (n + 7) / 8 * 8; }
 bool large(const moe_ffn_config& c, int64_t T) {
   return c.dtype == MOE_DTYPE_BF16 && T > kSkinnyRows && T * c.hidden_size * c.intermediate_size >= kPackFrom;

@@ -420,8 +420,15 @@ __device__ __forceinline__ Acc16<E> mfma16(const uint4& a, const uint4& b, Acc16
   }
 }
 
-template <El E, bool PAIR, bool ANY, int SETS, class Epi>
-__global__ void __launch_bounds__(kSkinnyEight * kWave, SETS == 1 ? 6 : 4) product_skinny_kernel(Product g, Epi epi, int parts, float* part) {
+// Where the rows of x come from: as they lie, as operands, or a single row that a functor
+// puts into LDS once the first weights are on their way; it also gives what the epilogue
+// reads of that row.
+struct AsTheyLie {
+  static constexpr bool kStaged = false;
+};
+
+template <El E, bool PAIR, bool ANY, int SETS, class Rows, class Epi>
+__global__ void __launch_bounds__(kSkinnyEight * kWave, SETS == 1 ? 6 : 4) product_skinny_kernel(Product g, Rows rows, Epi epi, int parts, float* part) {
   using I = ElInfo<E>;
   static_assert(!PAIR || SETS == 2, "a set for either product");
   constexpr int kCols = PAIR ? 8 : 8 * SETS, D = SETS == 1 ? 4 : 5;
@@ -443,50 +450,69 @@ __global__ void __launch_bounds__(kSkinnyEight * kWave, SETS == 1 ? 6 : 4) produ
   const uint8_t* xbase = static_cast<const uint8_t*>(g.a.p);
   const uint32_t xoff = static_cast<uint32_t>(min(r, g.M - 1)) * static_cast<uint32_t>(g.a.ld) * I::kSize + 16 * q;
   const bool live = r < g.M, tail = g.K % I::kStage != 0;
+  extern __shared__ __attribute__((aligned(16))) uint8_t staged[];
 
   struct Blk {
-    uint4 w[SETS], x[2];
+    uint4 w[SETS], x[Rows::kStaged ? 1 : 2];
   };
   Acc16<E> acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-  int at = lo;
+  int at = lo, use = lo;
   batches<D, Blk>(
       hi - lo,
       [&](Blk& k) __attribute__((always_inline)) {
         const size_t o = static_cast<size_t>(at) * 128;
         const int left = g.K - at * I::kStage;     // elements from this block on; only the last can be cut
-        k.x[0] = k.x[1] = uint4{0, 0, 0, 0};
+        if constexpr (!Rows::kStaged) k.x[0] = k.x[1] = uint4{0, 0, 0, 0};
         if (!ANY && !tail) {
 #pragma unroll
           for (int h = 0; h < SETS; ++h) k.w[h] = ld16_stream(wbase[h] + o + woff[h]);
-          if (live) {
-            k.x[0] = ld16(xbase + o + xoff);
-            k.x[1] = ld16(xbase + o + xoff + 64);
+          if constexpr (!Rows::kStaged) {
+            if (live) {
+              k.x[0] = ld16(xbase + o + xoff);
+              k.x[1] = ld16(xbase + o + xoff + 64);
+            }
           }
         } else {
 #pragma unroll
           for (int h = 0; h < SETS; ++h) k.w[h] = piece_of<E, ANY>(wbase[h] + o + woff[h], left - I::kPiece * lane_piece(lane));
-          if (live) {
-            k.x[0] = piece_of<E, ANY>(xbase + o + xoff, left - I::kPiece * q);
-            k.x[1] = piece_of<E, ANY>(xbase + o + xoff + 64, left - I::kPiece * (q + 4));
+          if constexpr (!Rows::kStaged) {
+            if (live) {
+              k.x[0] = piece_of<E, ANY>(xbase + o + xoff, left - I::kPiece * q);
+              k.x[1] = piece_of<E, ANY>(xbase + o + xoff + 64, left - I::kPiece * (q + 4));
+            }
           }
         }
         ++at;
       },
       [&](Blk& k) __attribute__((always_inline)) {
+        uint4 x[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        if constexpr (Rows::kStaged) {
+          if (live) {
+            const uint8_t* b = staged + use * 128 + 16 * q;
+            x[0] = *reinterpret_cast<const uint4*>(b);
+            x[1] = *reinterpret_cast<const uint4*>(b + 64);
+          }
+          ++use;
+        } else {
+          x[0] = k.x[0];
+          x[1] = k.x[1];
+        }
         if constexpr (SETS == 2) {
           const bool upper = lane & 8;
           trade(k.w[0].x, k.w[1].x, upper);
           trade(k.w[0].y, k.w[1].y, upper);
           trade(k.w[0].z, k.w[1].z, upper);
           trade(k.w[0].w, k.w[1].w, upper);
-          acc[0] = mfma16<E>(k.x[0], k.w[0], acc[0]);
-          acc[0] = mfma16<E>(k.x[1], k.w[1], acc[0]);
+          acc[0] = mfma16<E>(x[0], k.w[0], acc[0]);
+          acc[0] = mfma16<E>(x[1], k.w[1], acc[0]);
         } else {
-          acc[0] = mfma16<E>(k.x[0], k.w[0], acc[0]);
-          acc[1] = mfma16<E>(k.x[1], k.w[0], acc[1]);
+          acc[0] = mfma16<E>(x[0], k.w[0], acc[0]);
+          acc[1] = mfma16<E>(x[1], k.w[0], acc[1]);
         }
       },
-      [] {});
+      [&] {
+        if constexpr (Rows::kStaged) rows.put(staged, g.K, blockIdx.x == 0 && p == 0);
+      });
   f32x4 s;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -520,7 +546,8 @@ __global__ void __launch_bounds__(kSkinnyEight * kWave, SETS == 1 ? 6 : 4) produ
     *reinterpret_cast<f32x4*>(part + o) = a;
     if constexpr (PAIR) *reinterpret_cast<f32x4*>(part + o + g.M * np) = u;
   } else {
-    epi.put(m, n, a, u, epi.cols(n), epi.ahead(m, n));
+    if constexpr (Rows::kStaged) epi.put(m, n, a, u, epi.cols(n), rows.ahead(staged, epi, n));
+    else epi.put(m, n, a, u, epi.cols(n), epi.ahead(m, n));
   }
 }
 
@@ -918,8 +945,9 @@ inline TilePlan plan_tiles(El e, bool pair, bool by_dma, bool rows64, int64_t M,
     least = us;
     best = t;
   };
-  static const struct { int rows, cols; } kTiles[] = {{64, 128}, {128, 128}};
+  static const struct { int rows, cols; } kTiles[] = {{64, 64}, {64, 128}, {128, 128}};
   for (const auto& t : kTiles) {
+    if (t.cols == 64 && (e != El::F32 || pair)) continue;
     const int64_t tiles = ceil_div(M, t.rows) * ceil_div(width, t.cols), slots = int64_t{2} * kCus;
     for (int parts = 1; parts <= kMaxParts; ++parts) {
       const double planes = static_cast<double>(parts) * M * (pair ? 2 : 1) * part_stride(N) * 4;
@@ -970,6 +998,13 @@ void launch_tiles(const Product& g, const Epi& epi, const TilePlan& t, float* pa
   if (t.rows == 64) product_tile_kernel<E, KA, KB, PAIR, ANY, 64, 128><<<grid, 256, 0, s>>>(g, epi, t.parts, part);
   else product_tile_kernel<E, KA, KB, PAIR, ANY, 128, 128><<<grid, 256, 0, s>>>(g, epi, t.parts, part);
 }
+// float32 is bound by the matrix cores whatever the tile: small ones fill the CUs without
+// parts and their sums.
+template <bool KA, bool KB, bool PAIR, bool ANY, class Epi>
+void launch_small_tiles(const Product& g, const Epi& epi, const TilePlan& t, float* part, hipStream_t s) {
+  const unsigned grid = static_cast<unsigned>(ceil_div(t.tiles * t.parts, 8) * 8);
+  product_tile_kernel<El::F32, KA, KB, PAIR, ANY, 64, 64><<<grid, 256, 0, s>>>(g, epi, t.parts, part);
+}
 
 // Rows whose offsets in a tile are 31-bit, and for a k-strided pair whole stages of either
 // matrix.
@@ -995,19 +1030,19 @@ int launch_aligned(const Product& g, const Epi& epi, const TilePlan& t, float* p
 
 // At most 16 rows: 16 operand columns to a workgroup while that gives two for each CU, else
 // 8; below one for each CU parts of at least 16 blocks of 128 bytes.
-template <El E, bool PAIR, class Epi>
-int launch_skinny(const Product& g, const Epi& epi, bool aligned, float* part, hipStream_t s) {
+template <El E, bool PAIR, class Epi, class Rows = AsTheyLie>
+int launch_skinny(const Product& g, const Epi& epi, bool aligned, float* part, hipStream_t s, const Rows& rows = {}, size_t lds = 0) {
   const bool wide = PAIR || ceil_div(g.N, 16) >= 2 * kCus;
   const int64_t tiles = ceil_div(g.N, PAIR || !wide ? 8 : 16), blocks = ceil_div(g.K, ElInfo<E>::kStage);
   const int parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kCus / tiles, blocks / 16, kMaxParts})));
   const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(parts));
   constexpr int kThreads = kSkinnyEight * kWave;
   if (wide) {
-    if (aligned) product_skinny_kernel<E, PAIR, false, 2><<<grid, kThreads, 0, s>>>(g, epi, parts, part);
-    else product_skinny_kernel<E, PAIR, true, 2><<<grid, kThreads, 0, s>>>(g, epi, parts, part);
+    if (aligned) product_skinny_kernel<E, PAIR, false, 2><<<grid, kThreads, lds, s>>>(g, rows, epi, parts, part);
+    else product_skinny_kernel<E, PAIR, true, 2><<<grid, kThreads, lds, s>>>(g, rows, epi, parts, part);
   } else if constexpr (!PAIR) {
-    if (aligned) product_skinny_kernel<E, false, false, 1><<<grid, kThreads, 0, s>>>(g, epi, parts, part);
-    else product_skinny_kernel<E, false, true, 1><<<grid, kThreads, 0, s>>>(g, epi, parts, part);
+    if (aligned) product_skinny_kernel<E, false, false, 1><<<grid, kThreads, lds, s>>>(g, rows, epi, parts, part);
+    else product_skinny_kernel<E, false, true, 1><<<grid, kThreads, lds, s>>>(g, rows, epi, parts, part);
   }
   if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
   if (parts > 1) {
@@ -1036,8 +1071,16 @@ int run_product(const Product& g, const Epi& epi, float* part, hipStream_t s) {
     if (t.aligned && t.cols == 128) return launch_aligned<E, KA, KB, PAIR, 256, 128>(g, epi, t, part, s);
     if (t.aligned) return launch_aligned<E, KA, KB, PAIR, 256, 256>(g, epi, t, part, s);
   }
-  if (aligned) launch_tiles<E, KA, KB, PAIR, false>(g, epi, t, part, s);
-  else launch_tiles<E, KA, KB, PAIR, true>(g, epi, t, part, s);
+  if (t.cols == 64) {
+    if constexpr (E == El::F32 && !kPair) {
+      if (aligned) launch_small_tiles<KA, KB, PAIR, false>(g, epi, t, part, s);
+      else launch_small_tiles<KA, KB, PAIR, true>(g, epi, t, part, s);
+    }
+  } else if (aligned) {
+    launch_tiles<E, KA, KB, PAIR, false>(g, epi, t, part, s);
+  } else {
+    launch_tiles<E, KA, KB, PAIR, true>(g, epi, t, part, s);
+  }
   if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
   if (t.parts > 1) {
     product_sum_kernel<kPair><<<static_cast<unsigned>(ceil_div(g.M * part_stride(g.N) / 4, 256)), 256, 0, s>>>(g, epi, t.parts, part);
