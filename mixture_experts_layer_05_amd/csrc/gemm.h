@@ -25,7 +25,7 @@ struct ElInfo {
 
 // One operand.  k-contiguous: row r starts ld elements after row r - 1; k-strided: the
 // elements of k start ld elements after those of k - 1.
-//   q != null, k-contiguous: two matrices whose rows take turns, 32 of p and 32 of q;
+//   q != null, k-contiguous: two matrices whose rows take turns in a tile;
 //   q != null, k-strided: k in [0, half) is p's, k in [half, 2 half) q's; of either
 //   half the first `live` exist, the others are zeros.
 struct Operand {
@@ -128,19 +128,19 @@ struct Batch {
 
 // ROWS x BN sums in LDS, rows `stride` floats apart, to the epilogue or to part p's sums:
 // row_of(R) is the row of the product behind row R, and `from` the first of these rows.
-// Whole row segments, four columns to a thread.  A PAIR's columns take turns, 32 of the
-// first product and 32 of the second.  A part's sums go to part_of(R), those of the second
+// Whole row segments, four columns to a thread.  A PAIR's columns take turns, TURN of the
+// first product and TURN of the second.  A part's sums go to part_of(R), those of the second
 // product `second` floats on; null leaves a row out.  Sums of 8-bit products are staged as
 // the integers they are.  What the epilogue reads for D rows is in flight while D others are finished: `now`
 // holds what it reads for the first, and then for the D rows behind the last (if `more`).
-template <El E, bool PAIR, int BN, int ROWS, int THREADS, int D, class Epi, class RowOf, class PartOf>
+template <El E, bool PAIR, int TURN, int BN, int ROWS, int THREADS, int D, class Epi, class RowOf, class PartOf>
 __device__ __forceinline__ void results_out(const Product& g, const Epi& epi, const typename Epi::Cols& cols, Batch<Epi, D>& now,
                                             const float* stg, int stride, int n, int tid, int from, bool more, RowOf row_of,
                                             bool cut, PartOf part_of, size_t second) {
   constexpr int kLanes = (PAIR ? BN / 2 : BN) / 4, kIter = ROWS * kLanes / THREADS, kStep = THREADS / kLanes;
   static_assert(THREADS % kLanes == 0 && kIter % D == 0, "a thread keeps its columns");
   if (n >= g.N) return;
-  const int c = 4 * (tid % kLanes), sc = PAIR ? (c >> 5) * 64 + (c & 31) : c;
+  const int c = 4 * (tid % kLanes), sc = PAIR ? c / TURN * 2 * TURN + c % TURN : c;
 #pragma unroll 1
   for (int k = 0; k < kIter; k += D) {
     const int R = tid / kLanes + k * kStep;
@@ -148,7 +148,7 @@ __device__ __forceinline__ void results_out(const Product& g, const Epi& epi, co
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       s[d] = *reinterpret_cast<const f32x4*>(stg + (R + d * kStep) * stride + sc);
-      if constexpr (PAIR) u[d] = *reinterpret_cast<const f32x4*>(stg + (R + d * kStep) * stride + sc + 32);
+      if constexpr (PAIR) u[d] = *reinterpret_cast<const f32x4*>(stg + (R + d * kStep) * stride + sc + TURN);
       if constexpr (E == El::I8)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[d][e] = static_cast<float>(__float_as_int(s[d][e]));
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(256) product_sum_kernel(Product g, Epi epi, in
 //
 // BM x BN sums per workgroup of 2 x 2 waves, from 32x32 MFMAs.  A stage is 128 bytes of
 // contraction (64 bf16, 32 f32, 128 int8), double-buffered in LDS; its loads go to
-// registers two stages ahead, which takes any alignment and fills ends with zeros.  A
+// registers two to four stages ahead, which takes any alignment and fills ends with zeros.  A
 // k-contiguous operand's rows lie unpadded in LDS, their 16-byte pieces permuted by
 // (row / 2) mod 8; a k-strided one's rows are the k, padded so that the four k that a
 // fragment read takes lie in different quarters of the banks.
@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(256, 2) product_tile_kernel(Product g, Epi epi
   using SB = TileSide<E, KB, BN>;
   constexpr int NI = BM / 64, NJ = BN / 64, kCols = PAIR && KB ? BN / 2 : BN;
   constexpr bool kPair = PAIR && KB;
-  constexpr int kStride = BN + 8;
+  // Of a pair a wave's 32 or 64 columns are half the first product's and half the second's.
+  constexpr int kStride = BN + 8, kTurn = BN / 4 < 32 ? BN / 4 : 32;
   constexpr int kBytes = 2 * (SA::kBytes + SB::kBytes) > 64 * kStride * 4 ? 2 * (SA::kBytes + SB::kBytes) : 64 * kStride * 4;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kBytes];
   constexpr int kStageBytes = SA::kBytes + SB::kBytes;
@@ -243,42 +244,71 @@ __global__ void __launch_bounds__(256, 2) product_tile_kernel(Product g, Epi epi
   const int s0 = static_cast<int>(static_cast<int64_t>(p) * stages / parts), s1 = static_cast<int>(static_cast<int64_t>(p + 1) * stages / parts);
 
   // k-contiguous: thread t loads piece t % 8 of rows t / 8 + 32 q, rows past the end
-  // repeat the last.  k-strided: piece t % kPer of k t / kPer + kStep q, none past the
-  // end of k or of the columns.
+  // repeat the last.  k-strided: piece t % kPer of k t / kPer + kStep q.
   const uint8_t* ap[SA::kN];
   const uint8_t* bp[SB::kN];
   const int arow = tid / SA::kPer, apiece = tid % SA::kPer, brow = tid / SB::kPer, bpiece = tid % SB::kPer;
+  // k-strided: columns that the thread's piece holds, none or less where it is past the end.
+  const int aleft = g.M - m0 - apiece * I::kPiece, bleft = g.N - n0 - bpiece * I::kPiece;
+  const int apast = aleft > 0 ? 0 : static_cast<int>(ceil_div(1 - aleft, I::kPiece)), bpast = bleft > 0 ? 0 : static_cast<int>(ceil_div(1 - bleft, I::kPiece));
 #pragma unroll
   for (int q = 0; q < SA::kN; ++q) {
     if constexpr (KA)
       ap[q] = static_cast<const uint8_t*>(g.a.p) + (static_cast<size_t>(min(m0 + arow + SA::kStep * q, g.M - 1)) * g.a.ld) * I::kSize + 16 * apiece;
     else
-      ap[q] = static_cast<const uint8_t*>(g.a.p) + (static_cast<size_t>(arow + SA::kStep * q) * g.a.ld + m0) * I::kSize + 16 * apiece;
+      ap[q] = static_cast<const uint8_t*>(g.a.p) + (static_cast<size_t>(arow + SA::kStep * q) * g.a.ld + m0) * I::kSize + 16 * (apiece - apast);
   }
 #pragma unroll
   for (int q = 0; q < SB::kN; ++q) {
     const int r = brow + SB::kStep * q;
     if constexpr (kPair) {
-      const void* w = (r & 32) ? g.b.q : g.b.p;
-      bp[q] = static_cast<const uint8_t*>(w) + (static_cast<size_t>(min(n0 + (r >> 6) * 32 + (r & 31), g.N - 1)) * g.b.ld) * I::kSize + 16 * bpiece;
+      const void* w = (r & kTurn) ? g.b.q : g.b.p;
+      bp[q] = static_cast<const uint8_t*>(w) + (static_cast<size_t>(min(n0 + r / (2 * kTurn) * kTurn + r % kTurn, g.N - 1)) * g.b.ld) * I::kSize + 16 * bpiece;
     } else if constexpr (KB) {
       bp[q] = static_cast<const uint8_t*>(g.b.p) + (static_cast<size_t>(min(n0 + r, g.N - 1)) * g.b.ld) * I::kSize + 16 * bpiece;
     } else {
-      bp[q] = static_cast<const uint8_t*>(g.b.p) + (static_cast<size_t>(r) * g.b.ld + n0) * I::kSize + 16 * bpiece;
+      bp[q] = static_cast<const uint8_t*>(g.b.p) + (static_cast<size_t>(r) * g.b.ld + n0) * I::kSize + 16 * (bpiece - bpast);
     }
   }
   struct Regs {
     uint4 a[SA::kN], b[SB::kN];
   };
-  auto load = [&](Regs& R, int s) __attribute__((always_inline)) {
-    const int st = min(s, s1 - 1), k0 = st * I::kStage;
+  // The stages [0, full), of a k-strided pair also [up, up + full), are loaded without a
+  // condition, which keeps several on their way: no k of theirs is past an end.  A piece of
+  // a k-strided row may reach past the row's end, into the next row at most, so the last
+  // row, and rows shorter than a piece, are no such stage's.  The sums of columns past the
+  // end are not stored.
+  constexpr bool kStrided = !KA || !KB;
+  const int rows = PAIR && !KB ? g.b.live : g.K;
+  int full = ANY && kStrided ? (rows - 1) / I::kStage : rows / I::kStage;
+  if (ANY && ((!KA && g.a.ld < I::kPiece) || (!KB && g.b.ld < I::kPiece))) full = 0;
+  const int up = PAIR && !KB ? g.b.half / I::kStage : stages;
+  auto fast = [](const uint8_t* p) __attribute__((always_inline)) {
+    typedef uint32_t u32x4_el __attribute__((ext_vector_type(4), aligned(1)));
+    if constexpr (!ANY) return ld16(p);
+    const u32x4_el v = *reinterpret_cast<const u32x4_el*>(p);
+    return uint4{v.x, v.y, v.z, v.w};
+  };
+  auto load_full = [&](Regs& R, int st) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < SA::kN; ++q)
+      R.a[q] = fast(ap[q] + (KA ? static_cast<size_t>(st) * 128 : static_cast<size_t>(st) * I::kStage * g.a.ld * I::kSize));
+    // (Of a pair the second matrix instead of the first, from its own first row.)
+    const ptrdiff_t over = PAIR && !KB && st >= up ? static_cast<const uint8_t*>(g.b.q) - static_cast<const uint8_t*>(g.b.p) : 0;
+    const int row = PAIR && !KB && st >= up ? st - up : st;
+#pragma unroll
+    for (int q = 0; q < SB::kN; ++q)
+      R.b[q] = fast(bp[q] + (KB ? static_cast<size_t>(st) * 128 : static_cast<size_t>(row) * I::kStage * g.b.ld * I::kSize) + over);
+  };
+  auto load_part = [&](Regs& R, int st) __attribute__((always_inline)) {
+    const int k0 = st * I::kStage;
 #pragma unroll
     for (int q = 0; q < SA::kN; ++q) {
       if constexpr (KA) {
         R.a[q] = piece_of<E, ANY>(ap[q] + static_cast<size_t>(st) * 128, g.K - k0 - apiece * I::kPiece);
       } else {
         const bool ok = k0 + arow + SA::kStep * q < g.K;
-        R.a[q] = piece_of<E, ANY>(ap[q] + static_cast<size_t>(k0) * g.a.ld * I::kSize, ok ? g.M - m0 - apiece * I::kPiece : 0);
+        R.a[q] = piece_of<E, ANY>(ap[q] + static_cast<size_t>(k0) * g.a.ld * I::kSize, ok ? aleft : 0);
       }
     }
 #pragma unroll
@@ -289,11 +319,10 @@ __global__ void __launch_bounds__(256, 2) product_tile_kernel(Product g, Epi epi
         const int k = k0 + brow + SB::kStep * q, kk = k < g.b.half ? k : k - g.b.half;
         const uint8_t* base = static_cast<const uint8_t*>(k < g.b.half ? g.b.p : g.b.q);
         const bool ok = k < g.K && kk < g.b.live;
-        R.b[q] = piece_of<E, ANY>(base + (static_cast<size_t>(kk) * g.b.ld + n0) * I::kSize + 16 * bpiece,
-                                  ok ? g.N - n0 - bpiece * I::kPiece : 0);
+        R.b[q] = piece_of<E, ANY>(base + (static_cast<size_t>(kk) * g.b.ld + n0) * I::kSize + 16 * bpiece, ok ? bleft : 0);
       } else {
         const bool ok = k0 + brow + SB::kStep * q < g.K;
-        R.b[q] = piece_of<E, ANY>(bp[q] + static_cast<size_t>(k0) * g.b.ld * I::kSize, ok ? g.N - n0 - bpiece * I::kPiece : 0);
+        R.b[q] = piece_of<E, ANY>(bp[q] + static_cast<size_t>(k0) * g.b.ld * I::kSize, ok ? bleft : 0);
       }
     }
   };
@@ -346,23 +375,43 @@ __global__ void __launch_bounds__(256, 2) product_tile_kernel(Product g, Epi epi
     }
   };
 
-  // Iteration s: barrier; write stage s + 1 from registers, start loading s + 3 into
-  // them (past the end the last stage again), multiply stage s.
-  Regs R0, R1;
-  load(R0, s0);
-  load(R1, s0 + 1);
-  store(R0, 0);
-  load(R0, s0 + 2);
-  for (int s = s0; s < s1; s += 2) {
+  // This part's full stages: the f'th is lo + f, or, from n0f on, lo2 + f - n0f.
+  const int lo = min(s0, full), n_lo = max(min(s1, full) - lo, 0), lo2 = max(s0, up), n_up = max(min(s1, up + full) - lo2, 0);
+  const int n_full = n_lo + n_up;
+  auto full_at = [&](int f) { const int t = min(f, n_full - 1); return t < n_lo ? lo + t : lo2 + t - n_lo; };
+  // Iteration f: barrier; write full stage f + 1 from registers, start loading f + 1 + kDepth
+  // into them (past the end the last one again), multiply f.  Small tiles, which are few
+  // when the product is, have more stages on their way.
+  constexpr int kDepth = BM * BN > 64 * 64 ? 2 : 4;
+  if (n_full > 0) {
+    Regs R[kDepth];
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) load_full(R[d], full_at(d));
+    store(R[0], 0);
+    load_full(R[0], full_at(kDepth));
+    for (int f = 0; f < n_full; f += kDepth) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        if (f + d >= n_full) break;
+        __syncthreads();
+        store(R[(d + 1) % kDepth], (d + 1) & 1);
+        load_full(R[(d + 1) % kDepth], full_at(f + d + 1 + kDepth));
+        compute(d & 1);
+      }
+    }
+  }
+  // The others, one at most but for a pair, for which there are at most two of either half.
+  for (int st = s0; st < s1; ++st) {
+    if (st < full || (st >= up && st < up + full)) {
+      st = (st < full ? full : up + full) - 1;
+      continue;
+    }
+    Regs R;
+    load_part(R, st);
     __syncthreads();
-    store(R1, 1);
-    load(R1, s + 3);
+    store(R, 0);
+    __syncthreads();
     compute(0);
-    if (s + 1 == s1) break;
-    __syncthreads();
-    store(R0, 0);
-    load(R0, s + 4);
-    compute(1);
   }
 
   // Out through LDS, NI rounds of 32 rows of each wave row, rows padded by 8 floats.
@@ -371,7 +420,8 @@ __global__ void __launch_bounds__(256, 2) product_tile_kernel(Product g, Epi epi
   const int n = n0 + 4 * (tid % (kCols / 4));
   const auto row_of = [&](int R) { return m0 + (R >> 5 & 1) * (BM / 2) + 32 * (R >> 6) + (R & 31); };
   typename Epi::Cols cols;
-  Batch<Epi, 4> ahead;
+  constexpr int kRows = kCols / 16 < 4 ? kCols / 16 : 4;         // of a batch
+  Batch<Epi, kRows> ahead;
   if (parts == 1 && n < g.N) {
     cols = epi.cols(n);
     ahead.load(epi, g.M, n, tid / (kCols / 4), 256 / (kCols / 4), row_of);
@@ -391,7 +441,7 @@ __global__ void __launch_bounds__(256, 2) product_tile_kernel(Product g, Epi epi
       for (int j = 0; j < NJ; ++j)
         stg[(wm * 32 + 8 * (v >> 2) + 4 * hi + (v & 3)) * kStride + wn * (BN / 2) + 32 * j + r32] = as_float(acc[i][j][v]);
     __syncthreads();
-    results_out<E, kPair, BN, 64, 256, 4>(g, epi, cols, ahead, stg, kStride, n, tid, 64 * i, i + 1 < NI, row_of, parts > 1, part_of, second);
+    results_out<E, kPair, kTurn, BN, 64, 256, kRows>(g, epi, cols, ahead, stg, kStride, n, tid, 64 * i, i + 1 < NI, row_of, parts > 1, part_of, second);
     __syncthreads();
   }
 }
@@ -870,7 +920,7 @@ __global__ void __launch_bounds__(256, BM + BN > 256 ? 1 : 2) product_aligned_ke
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
-      results_out<E, kPair, BN / 2, 32, 64, kAhead>(g, epi, cols, ahead, stg, L::kOut, n, lane, 32 * i, i + 1 < NI, row_of,
+      results_out<E, kPair, 32, BN / 2, 32, 64, kAhead>(g, epi, cols, ahead, stg, L::kOut, n, lane, 32 * i, i + 1 < NI, row_of,
                                                     cut > 1, [&](int R) { return mine + R * BN; }, 32);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
@@ -947,7 +997,7 @@ inline TilePlan plan_tiles(El e, bool pair, bool by_dma, bool rows64, int64_t M,
   };
   static const struct { int rows, cols; } kTiles[] = {{64, 64}, {64, 128}, {128, 128}};
   for (const auto& t : kTiles) {
-    if (t.cols == 64 && (e != El::F32 || pair)) continue;
+    if (t.cols == 64 && e != El::F32) continue;
     const int64_t tiles = ceil_div(M, t.rows) * ceil_div(width, t.cols), slots = int64_t{2} * kCus;
     for (int parts = 1; parts <= kMaxParts; ++parts) {
       const double planes = static_cast<double>(parts) * M * (pair ? 2 : 1) * part_stride(N) * 4;
@@ -1072,7 +1122,7 @@ int run_product(const Product& g, const Epi& epi, float* part, hipStream_t s) {
     if (t.aligned) return launch_aligned<E, KA, KB, PAIR, 256, 256>(g, epi, t, part, s);
   }
   if (t.cols == 64) {
-    if constexpr (E == El::F32 && !kPair) {
+    if constexpr (E == El::F32) {
       if (aligned) launch_small_tiles<KA, KB, PAIR, false>(g, epi, t, part, s);
       else launch_small_tiles<KA, KB, PAIR, true>(g, epi, t, part, s);
     }
