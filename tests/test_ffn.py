@@ -383,3 +383,96 @@ def test_training_step_in_a_graph_and_on_a_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(got[n], want[n]) and torch.equal(again[n], want[n]) for n in want), k
+
+
+# ----------------------------------------------------------------------------- every tile, every end
+
+def _check_on_the_gpu(T, H, I, act, seed, pad=0, train=True):
+    """As _run for bf16, the float64 results taken on the GPU for sizes that the host would
+    take long for, through the class alone."""
+    print(f"\n[case] ffn T={T} H={H} I={I} bf16 {act} pad={pad}", flush=True)
+    x, dy, w = _inputs(T, H, I, "bf16", seed, pad)
+    x, dy, w = x.cuda()[:, :H], dy.cuda()[:, :H], {n: t.cuda() for n, t in w.items()}
+    want = _expect(x, w, dy if train else None, act, "bf16")
+    op = moe.GatedFFN(w, act, max_rows=T, training=train)
+    op.workspace.fill_(0xFF)
+    got = {"y": op(x)}
+    if train:
+        op.workspace.fill_(0xFF)
+        got.update(op.backward(x, dy))
+    torch.cuda.synchronize()
+    for n, (v, tol) in want.items():
+        worst = ((got[n].double() - v).abs() / tol).max().item()
+        print(f"[case] {n}: worst error / tolerance {worst:.3f}", flush=True)
+        assert worst <= 1, n
+
+
+# Rows, widths and contractions that end inside tiles, stages and pieces of 8, around every
+# tile height, with rows aligned (the DMA kernels), laid out afresh (odd sizes or strides)
+# and too small for that.
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,I", [(17, 72, 40), (31, 136, 200), (40, 264, 328), (64, 1024, 2048), (65, 2040, 1544), (100, 520, 72),
+                                   (129, 4096, 264), (191, 1000, 2056), (250, 3000, 1000), (255, 64, 4096), (256, 256, 8), (257, 8, 256),
+                                   (500, 2056, 1032), (1000, 1032, 2080), (1023, 4104, 1096)])
+def test_ends_of_tiles(T, H, I):
+    _check_on_the_gpu(T, H, I, "silu", seed=T)
+    _check_on_the_gpu(T, H, I, "gelu_tanh", seed=T + 1, pad=5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,I", [(20, 31, 35), (33, 129, 257), (200, 1001, 777), (300, 1025, 65), (513, 2049, 1027)])
+def test_odd_ends(T, H, I):
+    _check_on_the_gpu(T, H, I, "gelu", seed=T, pad=3)
+
+
+# Whole rounds of 256 x 256 tiles and a rest in parts, in every product of a step.
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,I,pad", [(4200, 2056, 4104, 0), (5000, 4096, 2560, 8), (4099, 2049, 4101, 1)])
+def test_rounds_of_tiles_and_their_rest(T, H, I, pad):
+    _check_on_the_gpu(T, H, I, "silu", seed=14, pad=pad)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [2, 16, 150])
+def test_far_strides(T):
+    """Rows 2^23 elements and more apart: beyond the aligned kernels' offsets."""
+    H, I = 64, 96
+    x, dy, w = _inputs(T, H, I, "bf16", 15)
+    far = torch.zeros(2, T * ((1 << 23) + 8), dtype=torch.bfloat16, device="cuda")
+    xs, ds = (far[i].view(T, -1)[:, :H] for i in range(2))
+    xs.copy_(x[:, :H])
+    ds.copy_(dy[:, :H])
+    op = moe.GatedFFN({n: t.cuda() for n, t in w.items()}, max_rows=T, training=True)
+    want = _expect(x[:, :H], w, dy[:, :H], "silu", "bf16")
+    y = op(xs)
+    _compare(dict(op.backward(xs, ds), y=y), want, "far")
+
+
+@pytest.mark.gpu
+def test_weights_off_their_boundaries():
+    """Weights and rows that start two bytes behind a 16-byte boundary."""
+    for T, H, I in ((5, 64, 72), (300, 264, 520)):
+        x, dy, w = _inputs(T, H, I, "bf16", 16)
+
+        def shifted(t):
+            buf = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+            return buf[1:].view(t.shape).copy_(t)
+
+        op = moe.GatedFFN({n: shifted(t) for n, t in w.items()}, max_rows=T, training=True)
+        y = op(shifted(x))
+        want = _expect(x, w, dy, "silu", "bf16")
+        _compare(dict(op.backward(shifted(x), shifted(dy)), y=y), want, "shifted")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [40, 300])
+def test_an_infinity_behind_the_end_stays_there(T):
+    """Padding between the rows of x and dy that holds infinities and NaN: nothing of it
+    reaches a result, whichever way the rows are read."""
+    for H, I, pad in ((72, 88, 8), (264, 520, 8), (71, 88, 9), (265, 519, 3)):
+        x, dy, w = _inputs(T, H, I, "bf16", 17, pad)
+        x[:, H:], dy[:, H:] = float("inf"), float("nan")
+        op = moe.GatedFFN({n: t.cuda() for n, t in w.items()}, max_rows=T, training=True)
+        want = _expect(x[:, :H], w, dy[:, :H], "silu", "bf16")
+        y = op(x.cuda()[:, :H])
+        _compare(dict(op.backward(x.cuda()[:, :H], dy.cuda()[:, :H]), y=y), want, "padding")

@@ -295,3 +295,48 @@ def test_a_graph_and_another_stream_give_the_same(M):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(got, want) and torch.equal(again, want), k
+
+
+# Ends inside tiles and pieces around every tile height; whole rounds of 256 x 256 tiles and
+# a rest in parts.  The float64 results come from the GPU.
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,K,N,pad", [(17, 96, 40, 0), (64, 1040, 2048, 16), (65, 2000, 1544, 0), (129, 4096, 264, 0), (250, 3001, 1000, 3),
+                                       (257, 16, 256, 0), (1000, 1040, 2080, 0), (1023, 4104, 1096, 1), (4200, 2064, 4104, 0),
+                                       (5000, 4096, 5120, 0), (16, 5120, 8192, 0), (1, 5120, 8193, 0), (1, 33000, 500, 0)])
+@pytest.mark.parametrize("i,o", [("bf16", "bf16"), ("i8", "f32")])
+def test_ends_of_tiles(M, K, N, pad, i, o):
+    print(f"\n[case] i8 {M}x{K}x{N} {i}->{o} pad={pad}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    w = torch.randint(-128, 128, (N, K + pad), generator=g, device="cuda", dtype=torch.int8)[:, :K]
+    sw = torch.rand(N, generator=g, device="cuda") / 64 + 0.001
+    b = torch.randn(N, generator=g, device="cuda")
+    r = torch.randn(M, N, generator=g, device="cuda").to(DT[o])
+    if i == "i8":
+        x = torch.randint(-128, 128, (M, K + pad), generator=g, device="cuda", dtype=torch.int8)[:, :K]
+        q, sx = x, torch.rand(M, generator=g, device="cuda") / 64 + 0.001
+    else:
+        x = torch.randn(M, K + pad, generator=g, device="cuda").bfloat16()[:, :K]
+        q, sx = _codes(x)
+    op = moe.LinearI8(w, sw, b, "gelu_tanh", o, max_rows=M)
+    op.workspace.fill_(0xFF)
+    y = op((x, sx) if i == "i8" else x, r)
+    want, tol = _expect(q, sx, w, sw, b, r, "gelu_tanh", o)
+    worst = ((y.double() - want).abs() / tol).max().item()
+    print(f"[case] worst error / tolerance {worst:.3f}", flush=True)
+    assert worst <= 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [2, 16, 40])
+def test_far_strides(M):
+    """Rows 2^24 codes and more apart."""
+    K, N = 64, 48
+    far = torch.zeros(M, (1 << 24) + 16, dtype=torch.int8, device="cuda")
+    g = torch.Generator().manual_seed(18)
+    x = torch.randint(-127, 128, (M, K), generator=g, dtype=torch.int8)
+    w = torch.randint(-127, 128, (N, K), generator=g, dtype=torch.int8)
+    far[:, :K] = x.cuda()
+    y = torch.empty(M, N, device="cuda")
+    ws = torch.empty(moe.linear_i8_workspace_size(K, N, M, "i8"), dtype=torch.uint8, device="cuda")
+    moe.linear_i8(far[:, :K], w.cuda(), torch.ones(N, device="cuda"), None, None, y, ws, x_scale=torch.ones(M, device="cuda"))
+    assert torch.equal(y.cpu().double(), x.double() @ w.double().t())
