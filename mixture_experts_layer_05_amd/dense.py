@@ -240,20 +240,36 @@ def _norm_struct(T, H, kind, gate, block_t, stream_t, out_t, params, eps, a, b):
 
 def _norm_call(c, T, H, y, residual, z, out, out_scale, weight, bias, post_weight, post_bias, gate, stream_t, pt,
                stream) -> None:
-    shape = (T, H)
-    yp, ldy = _rows(y, shape, y.dtype, "y")
-    rp, ldr = _opt_rows(residual, shape, stream_t, "residual")
-    zp, ldz = _opt_rows(z, shape, stream_t, "z")
-    op, ldo = _opt_rows(out, shape, out.dtype if out is not None else None, "out")
-    gp, ldg = _gate_rows(gate, c.gate, T, H, pt)
+    zp, ldz = _opt_rows(z, (T, H), stream_t, "z")
+    op, ldo = _opt_rows(out, (T, H), out.dtype if out is not None else None, "out")
     _expect(out_scale, (T,), torch.float32, "out_scale")
-    _together(y.device, residual, z, out, gate, weight, bias, post_weight, post_bias, out_scale)
-    with _on(y.device):
-        status = lib().moe_norm(ctypes.byref(c), T, yp, ldy, rp, ldr, gp, ldg, _vector(weight, H, pt, "weight"),
-                                _vector(bias, H, pt, "bias"), _vector(post_weight, H, pt, "post_weight"),
-                                _vector(post_bias, H, pt, "post_bias"), zp, ldz, op, ldo, _ptr(out_scale),
-                                _stream_of(y.device, stream))
-    _check(status, "moe_norm")
+    _together(y.device, z, out, out_scale)
+    _norm_to(c, T, H, y, residual, (zp, ldz, op, ldo, _ptr(out_scale)), weight, bias, post_weight, post_bias, gate,
+             stream_t, pt, stream)
+
+
+def _norm_to(c, T, H, y, residual, outputs, weight, bias, post_weight, post_bias, gate, stream_t, pt, stream) -> None:
+    """moe_norm with the addresses and strides of its outputs, whose device the caller has
+    compared with y's; the others' is compared here."""
+    shape, device = (T, H), y.device
+    yp, ldy = _rows(y, shape, y.dtype, "y")
+    rp, ldr = (None, 0) if residual is None else _rows(residual, shape, stream_t, "residual")
+    gp, ldg = (None, 0) if gate is None else _gate_rows(gate, c.gate, T, H, pt)
+    wp = bp = pp = qp = None
+    if weight is not None:
+        wp = _vector(weight, H, pt, "weight")
+    if bias is not None:
+        bp = _vector(bias, H, pt, "bias")
+    if post_weight is not None:
+        pp = _vector(post_weight, H, pt, "post_weight")
+    if post_bias is not None:
+        qp = _vector(post_bias, H, pt, "post_bias")
+    _together(device, residual, gate, weight, bias, post_weight, post_bias)
+    with _on(device):
+        status = lib().moe_norm(ctypes.byref(c), T, yp, ldy, rp, ldr, gp, ldg, wp, bp, pp, qp, *outputs,
+                                _stream_of(device, stream))
+    if status:
+        _check(status, "moe_norm")
 
 
 def norm_backward_workspace_size(hidden_size: int, max_rows: int) -> int:
@@ -328,6 +344,7 @@ class ResidualNorm:
         self.param_t = params[0].dtype if params else self.stream_t
         self._c, _ = _norm_struct(max_rows, hidden_size, _norm_kind(kind), None, self.block_t, self.stream_t, self.out_t,
                                   params, eps, residual_scale, block_scale)
+        self._set = self._mine = None
         dev = params[0].device if params else torch.device(device)
         self.z = torch.empty(max_rows, hidden_size, dtype=self.stream_t, device=dev)
         self.out = torch.empty(max_rows, hidden_size, dtype=self.out_t, device=dev)
@@ -348,10 +365,11 @@ class ResidualNorm:
         return t if T == self.max_rows else t[:T]
 
     def _config(self, T: int, gate) -> _NormConfig:
+        now = (self.kind, self.eps, self.residual_scale, self.block_scale, 0 if gate is None else _gate_kind(gate, T, self.H))
         c = self._c
-        c.kind, c.eps = _norm_kind(self.kind), self.eps
-        c.residual_scale, c.block_scale = self.residual_scale, self.block_scale
-        c.gate = 0 if gate is None else _gate_kind(gate, T, self.H)
+        if now != self._set:
+            c.kind, c.eps, c.residual_scale, c.block_scale, c.gate = _norm_kind(self.kind), *now[1:]
+            self._set = now
         return c
 
     def __call__(self, y: torch.Tensor, residual: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
@@ -361,11 +379,19 @@ class ResidualNorm:
             raise ValueError("more rows than the norm was sized for")
         if y.dtype != self.block_t:
             raise ValueError(f"y: expected {self.block_t}, got {y.dtype}")
-        z, out = self._here(self.z, T), self._here(self.out, T)
-        scale = None if self.out_scale is None else self._here(self.out_scale, T)
-        _norm_call(self._config(T, gate), T, self.H, y, residual, z, out, scale, self.weight, self.bias, self.post_weight,
-                   self.post_bias, gate, self.stream_t, self.param_t, stream)
-        return z, out if scale is None else (out, scale)
+        # The rows of the norm's own buffers, and their addresses, of the last call's length.
+        mine = self._mine
+        if mine is None or mine[0] != T or mine[1] is not self.z or mine[2] is not self.out or mine[3] is not self.out_scale:
+            z, out = self._here(self.z, T), self._here(self.out, T)
+            scale = None if self.out_scale is None else self._here(self.out_scale, T)
+            _together(z.device, out, scale)
+            outputs = (*_rows(z, (T, self.H), self.stream_t, "z"), *_rows(out, (T, self.H), self.out_t, "out"), _ptr(scale))
+            mine = self._mine = (T, self.z, self.out, self.out_scale, (z, out if scale is None else (out, scale)), outputs)
+        if mine[1].device != y.device:
+            _together(y.device, mine[1])
+        _norm_to(self._config(T, gate), T, self.H, y, residual, mine[5], self.weight, self.bias, self.post_weight,
+                 self.post_bias, gate, self.stream_t, self.param_t, stream)
+        return mine[4]
 
     def backward(self, y: torch.Tensor, z: torch.Tensor, dz: Optional[torch.Tensor], dout: Optional[torch.Tensor],
                  gate: Optional[torch.Tensor] = None, has_residual: bool = True, stream=None) -> Dict[str, torch.Tensor]:
