@@ -606,28 +606,30 @@ __global__ void __launch_bounds__(kSkinnyEight * kWave, SETS == 1 ? 6 : 4) produ
 // BM x BN sums per workgroup of 2 x 2 waves, for operands in whole 16-byte pieces (bf16 and
 // 8-bit).  In 256 x 256 tiles a wave computes 128 x 128, alone on its SIMD: a stage's
 // fragments leave LDS twice, not three times as with eight waves of 128 x 64.  A stage is
-// 64 bf16 (128 int8) of contraction, double-buffered, and goes to LDS by DMA.  Nothing but
-// a wave's own instructions hides its latencies: the fragments of a quarter stage are read
-// while the quarter before is multiplied, across the stages' border too; the DMA of A of
-// stage s + 2 is issued in the last quarter of s and that of B in the first of s + 1 (both
-// in one quarter fill the queue and hold up the MFMAs: 8 % slower).  One barrier a stage, in
-// front of the last quarter: by then every wave has the stage's last fragments in registers
-// and stage s + 1 is in LDS.
+// 64 bf16 (128 int8) of contraction and goes to one of BUFS buffers in LDS by DMA.  Nothing
+// but a wave's own instructions hides its latencies: the fragments of a quarter stage are
+// read while the quarter before is multiplied, across the stages' border too; the DMA of A
+// of stage s + BUFS is issued in the last quarter of s and that of B in the first of s + 1
+// (both in one quarter fill the queue and hold up the MFMAs: 8 % slower).  One barrier a
+// stage, in front of the last quarter: by then every wave has the stage's last fragments in
+// registers and stage s + 1 is in LDS.
 //
 // k-contiguous operands: rows of 128 bytes, 16-byte pieces permuted by (row / 2) mod 8.
 // k-strided: a row for each k, 64-byte pieces permuted by k mod 4, so that the four k of a
 // turning read lie in different quarters of the banks.  What lies behind the end of the
 // contraction is out of the resource's range, and such loads bring zeros.
 //
-// Results leave through LDS too, 32 rows of a wave at a time, in the buffer that the last
-// stage is not in; rows padded by 4 floats, for which there is room on its other side.
-template <El E, bool KA, bool KB, bool PAIR, int BM, int BN>
+// Results leave through LDS too, 32 rows of a wave at a time, in a buffer that the last
+// stage is not in, the first or the last; rows padded by 4 floats, for which there is room on its other side.
+template <El E, bool KA, bool KB, bool PAIR, int BM, int BN, int BUFS>
 struct Aligned {
   static constexpr bool kPair = PAIR && KB;
   static constexpr int kCols = kPair ? BN / 2 : BN;
   static constexpr int kSideA = BM * 128, kStage = (BM + BN) * 128;
   static constexpr int kOut = BN / 2 + 4, kStaged = 4 * 32 * kOut * 4;
-  static constexpr int kPad = kStaged > kStage ? (kStaged - kStage + 1023) / 1024 * 1024 : 0, kLds = 2 * kStage + 2 * kPad;
+  static constexpr int kPad = kStaged > kStage ? (kStaged - kStage + 1023) / 1024 * 1024 : 0, kLds = BUFS * kStage + 2 * kPad;
+  // Tiles that run on a CU at a time, by the LDS.
+  static constexpr int kOnCu = 2 * kLds <= (160 << 10) ? 2 : 1;
   static_assert(BM > 64 || KA, "the banks of a k-strided side need 128 columns");
   static constexpr int kBand = 2048 / BM;        // row blocks of a band of tiles
 };
@@ -720,9 +722,9 @@ __device__ __forceinline__ void tile_place(int tile, int mt, int nt, int& m0, in
   n0 = in_band / bm * COLS;
 }
 
-template <El E, bool KA, bool KB, bool PAIR, int BM, int BN, class Epi>
-__global__ void __launch_bounds__(256, BM + BN > 256 ? 1 : 2) product_aligned_kernel(Product g, Epi epi, int whole, int parts, float* part) {
-  using L = Aligned<E, KA, KB, PAIR, BM, BN>;
+template <El E, bool KA, bool KB, bool PAIR, int BM, int BN, int BUFS, class Epi>
+__global__ void __launch_bounds__(256, (Aligned<E, KA, KB, PAIR, BM, BN, BUFS>::kOnCu)) product_aligned_kernel(Product g, Epi epi, int whole, int parts, float* part) {
+  using L = Aligned<E, KA, KB, PAIR, BM, BN, BUFS>;
   constexpr bool kPair = L::kPair;
   constexpr int kCols = L::kCols, NI = BM / 64, NJ = BN / 64;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[L::kLds];
@@ -797,15 +799,17 @@ __global__ void __launch_bounds__(256, BM + BN > 256 ? 1 : 2) product_aligned_ke
 #pragma unroll
       for (int i = 0; i < SideB::kN; ++i) B.issue(kPair && SideB::second(wave, i) ? r2 : r, i, lds_b + buf);
     };
+    constexpr int kLoads = SideA::kN + SideB::kN;     // of a stage
     __syncthreads();                 // the tile before is done with LDS
-    dma_a(k0, 0);
-    dma_b(k0, 0);
-    if (k0 + 1 < nk) {
-      dma_a(k0 + 1, L::kStage);
-      wait_vm<SideA::kN>();
-    } else {
-      wait_vm<0>();
-    }
+    // BUFS - 1 stages and A of the next, as far as there are any.
+#pragma unroll
+    for (int d = 0; d < BUFS; ++d)
+      if (k0 + d < nk) {
+        dma_a(k0 + d, d * L::kStage);
+        if (d < BUFS - 1) dma_b(k0 + d, d * L::kStage);
+      }
+    if (k0 + BUFS <= nk) wait_vm<(BUFS - 2) * kLoads + SideA::kN>();
+    else wait_vm<0>();
     __syncthreads();
     Acc<E> acc[NI][NJ];
 #pragma unroll
@@ -843,48 +847,56 @@ __global__ void __launch_bounds__(256, BM + BN > 256 ? 1 : 2) product_aligned_ke
     };
     const auto nothing = [](int) __attribute__((always_inline)) {};
     using Zero = std::integral_constant<int, 0>;
-    // Stage ks; B of stage ks + 1 and A of stage ks + 2 are loaded meanwhile, where they are.
-    auto stage = [&](int ks, auto load_b, auto load_a) __attribute__((always_inline)) {
-      const uint32_t buf = static_cast<uint32_t>((ks - k0) & 1) * L::kStage, other = L::kStage - buf;
+    // Stage ks in the buffer at `buf`; B of stage ks + BUFS - 1 and A of stage ks + BUFS are
+    // loaded meanwhile, where they are (`last`: there is no stage ks + 1 either).
+    uint32_t buf = 0;
+    auto stage = [&](int ks, auto load_b, auto load_a, auto last) __attribute__((always_inline)) {
+      const uint32_t next = buf + L::kStage == BUFS * L::kStage ? 0 : buf + L::kStage;
+      const uint32_t before = buf == 0 ? (BUFS - 1) * L::kStage : buf - L::kStage;
       const uint8_t* here = smem + buf;
       if constexpr (decltype(load_b)::value) {
-        const i32x4_t r = B.rsrc(ks + 1), r2 = kPair ? B.rsrc(ks + 1, true) : r;
-        B.cut(ks + 1);
+        const i32x4_t r = B.rsrc(ks + BUFS - 1), r2 = kPair ? B.rsrc(ks + BUFS - 1, true) : r;
+        B.cut(ks + BUFS - 1);
         quarter(0, here, 1, Yes{}, std::integral_constant<int, SideB::kN>{}, [&](int i) __attribute__((always_inline)) {
-          B.issue(kPair && SideB::second(wave, i) ? r2 : r, i, lds_b + other);
+          B.issue(kPair && SideB::second(wave, i) ? r2 : r, i, lds_b + before);
         });
       } else {
         quarter(0, here, 1, Yes{}, Zero{}, nothing);
       }
       quarter(1, here, 2, Yes{}, Zero{}, nothing);
       quarter(2, here, 3, Yes{}, Zero{}, nothing);
-      if constexpr (decltype(load_b)::value) {
-        // The stage's last fragments are in registers, the next stage is in LDS.
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        const uint8_t* there = smem + other;
+      if constexpr (!decltype(last)::value) {
+        // The stage's last fragments are in registers, the next stage is in LDS; the stages
+        // behind it may still be on their way.
+        if constexpr (decltype(load_b)::value) wait_vm<(BUFS - 2) * kLoads>();
+        else wait_vm<0>();
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        const uint8_t* there = smem + next;
         if constexpr (decltype(load_a)::value) {
-          const i32x4_t r = A.rsrc(ks + 2);
-          A.cut(ks + 2);
+          const i32x4_t r = A.rsrc(ks + BUFS);
+          A.cut(ks + BUFS);
           quarter(3, there, 0, Yes{}, std::integral_constant<int, SideA::kN>{}, [&](int i) __attribute__((always_inline)) {
             A.issue(r, i, lds_a + buf);
           });
         } else {
           quarter(3, there, 0, Yes{}, Zero{}, nothing);
         }
+        buf = next;
       } else {
         quarter(3, here, 0, No{}, Zero{}, nothing);
       }
     };
     int ks = k0;
-    for (; ks + 2 < nk; ++ks) stage(ks, Yes{}, Yes{});
-    if (ks + 1 < nk) stage(ks++, Yes{}, No{});
-    stage(ks, No{}, No{});
+    for (; ks + BUFS < nk; ++ks) stage(ks, Yes{}, Yes{}, No{});
+    if (ks + BUFS == nk) stage(ks++, Yes{}, No{}, No{});
+    for (; ks + 1 < nk; ++ks) stage(ks, No{}, No{}, No{});
+    stage(ks, No{}, No{}, Yes{});
 
     // Lane l, element v of a block (the operands' roles are exchanged): row l % 32, column
     // 8 (v / 4) + 4 (l / 32) + v % 4.  A wave's staged rows are its own.
     constexpr int kWaveCols = kCols / 2, kLanes = kWaveCols / 4;
     constexpr int kAhead = Epi::kAhead < 32 / (64 / kLanes) ? Epi::kAhead : 32 / (64 / kLanes);
-    const uint32_t free_buf = ((ks - k0) & 1) ? 0 : L::kPad + L::kStage;
+    const uint32_t free_buf = buf ? 0 : L::kPad + (BUFS - 1) * L::kStage;     // the first or the last
     float* stg = reinterpret_cast<float*>(lds + free_buf) + wave * 32 * L::kOut;
     const int c = 4 * (lane % kLanes), n = n0 + wn * kWaveCols + c;
     const int staged = kPair ? (c >> 5) * 64 + (c & 31) : c;
@@ -976,7 +988,7 @@ inline size_t part_bytes(bool pair, int64_t M, int64_t N) {
 
 struct TilePlan {
   int rows, cols;       // of a tile, in operand rows
-  bool aligned;         // by DMA
+  int bufs;             // of the DMA kernel, 0: any alignment
   int64_t tiles;
   int64_t whole;        // aligned: tiles that are not cut
   int parts;            // of the others
@@ -1008,16 +1020,18 @@ inline TilePlan plan_tiles(El e, bool pair, bool by_dma, bool rows64, int64_t M,
       const double mult = e == El::F32 ? t.rows * t.cols * 64 * deep / 0.5e6 : 0;
       const double in_turn = e == El::F32 ? static_cast<double>(ceil_div(items, kCus)) : rounds * shared;
       offer(in_turn * std::max(load, mult) + 2 + 0.5 * rounds + (parts > 1 ? 4 + planes * 2 / 5e6 : 0),
-            TilePlan{t.rows, t.cols, false, tiles, 0, parts});
+            TilePlan{t.rows, t.cols, 0, tiles, 0, parts});
     }
   }
   if (!by_dma) return best;
   // Microseconds of a stage with all CUs at work (the clock falls with the power) or each
-  // alone, and of a tile's begin and end; `on` tiles run on a CU at a time.  Partial sums
-  // are mostly still in the caches.  224 x 4096 x 5120: 128 x 128 in 4 parts 24 us
-  // (estimate 25), 256 x 256 in 8 29 (29), 1000 x 5120 x 5120 in 128 x 128 60 (82).
-  static const struct { int rows, cols, on; double stage, alone, end; } kDma[] = {
-      {256, 256, 1, 1.55, 1.1, 8}, {256, 128, 1, 1.0, 0.8, 6}, {128, 128, 2, 1.0, 0.6, 6}, {64, 128, 2, 0.8, 0.5, 5}};
+  // alone, and of a tile's begin and end; `on` tiles run on a CU at a time.  Two buffers are
+  // enough where two tiles share a CU or the multiplications take long; elsewhere more keep
+  // more loads on their way: 224 x 4096 x 5120 in 64 x 128 tiles takes 47 us with two, 27
+  // with four, and in two parts 21 (128 x 128 24, 256 x 256 in eight parts 29).
+  static const struct { int rows, cols, bufs, on; double stage, alone, end; } kDma[] = {
+      {256, 256, 2, 1, 1.55, 1.07, 7}, {256, 128, 3, 1, 0.9, 0.62, 6}, {128, 128, 2, 2, 0.93, 0.55, 5}, {128, 128, 3, 1, 0.5, 0.36, 5},
+      {64, 128, 2, 2, 0.69, 0.5, 4}, {64, 128, 4, 1, 0.36, 0.28, 4}};
   for (const auto& t : kDma) {
     if (t.rows == 64 && !rows64) continue;
     // Full rounds of whole tiles; what is left over, which would leave CUs idle, in parts.
@@ -1028,8 +1042,8 @@ inline TilePlan plan_tiles(El e, bool pair, bool by_dma, bool rows64, int64_t M,
       if (parts > 1 && (rest == 0 || rest * parts > slots || planes > room || stages / parts < 4)) break;
       const double pace = rest * parts <= kCus ? t.alone : t.stage;
       offer(whole / slots * (t.stage * stages + t.end) + (rest ? pace * ceil_div(stages, parts) + t.end : 0) + 2 +
-                (parts > 1 ? 2 + planes / 5e6 : 0),
-            TilePlan{t.rows, t.cols, true, tiles, whole, parts});
+                (parts > 1 ? 2 + planes * 0.45e-6 : 0),
+            TilePlan{t.rows, t.cols, t.bufs, tiles, whole, parts});
     }
   }
   return best;
@@ -1064,13 +1078,13 @@ bool fits_dma(const Product& g) {
   return g.a.ld * ElInfo<E>::kSize < far && g.b.ld * ElInfo<E>::kSize < far && (KB || !PAIR || g.b.half % ElInfo<E>::kStage == 0);
 }
 
-template <El E, bool KA, bool KB, bool PAIR, int BM, int BN, class Epi>
+template <El E, bool KA, bool KB, bool PAIR, int BM, int BN, int BUFS, class Epi>
 int launch_aligned(const Product& g, const Epi& epi, const TilePlan& t, float* part, hipStream_t s) {
   constexpr bool kPair = PAIR && KB;
-  constexpr int kSlots = kCus * (BM + BN > 256 ? 1 : 2), kGroups = BM * (kPair ? BN / 2 : BN) / 1024;
+  constexpr int kSlots = kCus * Aligned<E, KA, KB, PAIR, BM, BN, BUFS>::kOnCu, kGroups = BM * (kPair ? BN / 2 : BN) / 1024;
   const int64_t rest = t.tiles - t.whole;
   const unsigned grid = t.whole ? kSlots : static_cast<unsigned>(ceil_div(rest * t.parts, 8) * 8);
-  product_aligned_kernel<E, KA, KB, PAIR, BM, BN><<<grid, 256, 0, s>>>(g, epi, static_cast<int>(t.whole), t.parts, part);
+  product_aligned_kernel<E, KA, KB, PAIR, BM, BN, BUFS><<<grid, 256, 0, s>>>(g, epi, static_cast<int>(t.whole), t.parts, part);
   if (t.parts > 1) {
     if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
     product_rest_kernel<kPair, BM, BN><<<static_cast<unsigned>(rest * kGroups), 256, 0, s>>>(g, epi, static_cast<int>(t.whole), t.parts, part);
@@ -1115,11 +1129,14 @@ int run_product(const Product& g, const Epi& epi, float* part, hipStream_t s) {
   }
   const TilePlan t = plan_tiles(E, kPair, by_dma, KA, g.M, g.N, g.K);
   if constexpr (E != El::F32) {
-    if constexpr (KA)
-      if (t.aligned && t.rows == 64) return launch_aligned<E, KA, KB, PAIR, 64, 128>(g, epi, t, part, s);
-    if (t.aligned && t.rows == 128) return launch_aligned<E, KA, KB, PAIR, 128, 128>(g, epi, t, part, s);
-    if (t.aligned && t.cols == 128) return launch_aligned<E, KA, KB, PAIR, 256, 128>(g, epi, t, part, s);
-    if (t.aligned) return launch_aligned<E, KA, KB, PAIR, 256, 256>(g, epi, t, part, s);
+    if constexpr (KA) {
+      if (t.bufs == 2 && t.rows == 64) return launch_aligned<E, KA, KB, PAIR, 64, 128, 2>(g, epi, t, part, s);
+      if (t.bufs == 4 && t.rows == 64) return launch_aligned<E, KA, KB, PAIR, 64, 128, 4>(g, epi, t, part, s);
+    }
+    if (t.bufs == 2 && t.rows == 128) return launch_aligned<E, KA, KB, PAIR, 128, 128, 2>(g, epi, t, part, s);
+    if (t.bufs == 3 && t.rows == 128) return launch_aligned<E, KA, KB, PAIR, 128, 128, 3>(g, epi, t, part, s);
+    if (t.bufs == 3) return launch_aligned<E, KA, KB, PAIR, 256, 128, 3>(g, epi, t, part, s);
+    if (t.bufs == 2) return launch_aligned<E, KA, KB, PAIR, 256, 256, 2>(g, epi, t, part, s);
   }
   if (t.cols == 64) {
     if constexpr (E == El::F32) {

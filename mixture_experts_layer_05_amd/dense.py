@@ -379,6 +379,7 @@ class ResidualNorm:
             raise ValueError("more rows than the norm was sized for")
         if y.dtype != self.block_t:
             raise ValueError(f"y: expected {self.block_t}, got {y.dtype}")
+        c = self._config(T, gate)
         # The rows of the norm's own buffers, and their addresses, of the last call's length.
         mine = self._mine
         if mine is None or mine[0] != T or mine[1] is not self.z or mine[2] is not self.out or mine[3] is not self.out_scale:
@@ -389,7 +390,7 @@ class ResidualNorm:
             mine = self._mine = (T, self.z, self.out, self.out_scale, (z, out if scale is None else (out, scale)), outputs)
         if mine[1].device != y.device:
             _together(y.device, mine[1])
-        _norm_to(self._config(T, gate), T, self.H, y, residual, mine[5], self.weight, self.bias, self.post_weight,
+        _norm_to(c, T, self.H, y, residual, mine[5], self.weight, self.bias, self.post_weight,
                  self.post_bias, gate, self.stream_t, self.param_t, stream)
         return mine[4]
 
