@@ -66,7 +66,7 @@ struct None {};
 // row ends in are written, zeros behind its end.
 template <bool F32, bool KEEP>
 struct GatedOut {
-  static constexpr int kAhead = 4;
+  static constexpr int kAhead = 4, kBytes = (F32 ? 4 : 2) + (KEEP ? 8 : 0);
   using Cols = None;
   using Ahead = None;
   void* h;
@@ -102,7 +102,7 @@ struct GatedOut {
 // dg = dh b and du = dh a, side by side in rows of 2 ld.
 template <bool F32>
 struct SlopesOut {
-  static constexpr int kAhead = 4;
+  static constexpr int kAhead = 4, kBytes = 8 + (F32 ? 8 : 4);
   using Cols = None;
   struct Ahead {
     f32x4 a, b;
@@ -142,7 +142,7 @@ struct SlopesOut {
 // of either the first `live`.
 template <bool F32>
 struct RowsOut {
-  static constexpr int kAhead = 4;
+  static constexpr int kAhead = 4, kBytes = F32 ? 4 : 2;
   using Cols = None;
   using Ahead = None;
   void *y, *y2;
@@ -199,7 +199,9 @@ bool large(const moe_ffn_config& c, int64_t T) {
   return c.dtype == MOE_DTYPE_BF16 && T > kSkinnyRows && T * c.hidden_size * c.intermediate_size >= kPackFrom;
 }
 bool odd_sizes(const moe_ffn_config& c) { return c.hidden_size % 8 || c.intermediate_size % 8; }
-size_t packed_bytes(int64_t rows, int64_t ld) { return align_up(static_cast<size_t>(rows) * ld * 2, 256); }
+// Rows of whole 128-byte lines, of which a stage takes one.
+int64_t packed_ld(int64_t n) { return (n + 63) / 64 * 64; }
+size_t packed_bytes(int64_t rows, int64_t n) { return align_up(static_cast<size_t>(rows) * packed_ld(n) * 2, 256); }
 
 // The workspace: partial sums, then h (forward) or [dg du] (backward), then x, dy
 // (backward), gate, up and down laid out afresh.
@@ -234,11 +236,11 @@ int ffn_operands(const moe_ffn_config& c, int T, const void* x, int64_t ldx, con
   const int H = c.hidden_size, I = c.intermediate_size, Hp = static_cast<int>(eights(H)), Ip = static_cast<int>(eights(I));
   const auto lies_odd = [](const void* p, int64_t ld) { return ld % 8 || reinterpret_cast<uintptr_t>(p) % 16; };
   PackArgs a{};
-  const auto pack = [&](const void*& p, int64_t& ld, int rows, int cols, int to_rows, int to_ld) {
-    a.item[a.n++] = PackItem{p, room, ld, to_ld, rows, cols, to_rows};
+  const auto pack = [&](const void*& p, int64_t& ld, int rows, int cols, int to_rows, int to_cols) {
+    a.item[a.n++] = PackItem{p, room, ld, packed_ld(to_cols), rows, cols, to_rows};
     p = room;
-    ld = to_ld;
-    room += packed_bytes(to_rows, to_ld);
+    ld = packed_ld(to_cols);
+    room += packed_bytes(to_rows, to_cols);
   };
   if (odd || lies_odd(x, ldx)) pack(f.x, f.ldx, T, H, T, Hp);
   if (dy && (odd || lies_odd(dy, lddy))) pack(f.dy, f.lddy, T, H, T, Hp);

@@ -108,7 +108,8 @@ __device__ __forceinline__ uint2 lds_turned(const uint8_t* p) {
 //   Cols cols(n)                  what it needs of columns n to n + 3
 //   Ahead ahead(m, n)             what it reads of row m there, as loaded
 //   put(m, n, s, u, cols, ahead)  the results of the sums s (and u, of a pair)
-//   kAhead                        the rows of a batch in 256 x 256 tiles, by its registers
+//   kAhead                        the rows of a batch in aligned tiles, by its registers
+//   kBytes                        what it reads and writes of a result
 // Rows past the end are left out by its caller.
 
 // The rows behind D rows of staged sums, from row R on, and what is read for them.
@@ -996,7 +997,7 @@ struct TilePlan {
 
 // The cheapest tile and split by an estimate in microseconds: what a CU takes in, the
 // f32 matrix rate, and the partial sums' way out and back.
-inline TilePlan plan_tiles(El e, bool pair, bool by_dma, bool rows64, int64_t M, int64_t N, int64_t K) {
+inline TilePlan plan_tiles(El e, bool pair, int out_bytes, bool by_dma, bool rows64, int64_t M, int64_t N, int64_t K) {
   const int size = e == El::F32 ? 4 : e == El::BF16 ? 2 : 1;
   const int64_t width = pair ? 2 * N : N, stages = ceil_div(K * size, 128);
   const double room = static_cast<double>(part_bytes(pair, M, N));
@@ -1032,6 +1033,8 @@ inline TilePlan plan_tiles(El e, bool pair, bool by_dma, bool rows64, int64_t M,
   static const struct { int rows, cols, bufs, on; double stage, alone, end; } kDma[] = {
       {256, 256, 2, 1, 1.55, 1.07, 7}, {256, 128, 3, 1, 0.9, 0.62, 6}, {128, 128, 2, 2, 0.93, 0.55, 5}, {128, 128, 3, 1, 0.5, 0.36, 5},
       {64, 128, 2, 2, 0.69, 0.5, 4}, {64, 128, 4, 1, 0.36, 0.28, 4}};
+  // Microseconds of a result's bytes beyond the first two: a CU moves about 15 KB in one.
+  const double out = (out_bytes - 2) * (pair ? 0.5 : 1.0) / 15e3;
   for (const auto& t : kDma) {
     if (t.rows == 64 && !rows64) continue;
     // Full rounds of whole tiles; what is left over, which would leave CUs idle, in parts.
@@ -1041,7 +1044,8 @@ inline TilePlan plan_tiles(El e, bool pair, bool by_dma, bool rows64, int64_t M,
       const double planes = static_cast<double>(rest) * parts * t.rows * t.cols * 4;
       if (parts > 1 && (rest == 0 || rest * parts > slots || planes > room || stages / parts < 4)) break;
       const double pace = rest * parts <= kCus ? t.alone : t.stage;
-      offer(whole / slots * (t.stage * stages + t.end) + (rest ? pace * ceil_div(stages, parts) + t.end : 0) + 2 +
+      const double whole_end = t.end + out * t.rows * t.cols * t.on, rest_end = t.end + (parts > 1 ? 0 : out * t.rows * t.cols);
+      offer(whole / slots * (t.stage * stages + whole_end) + (rest ? pace * ceil_div(stages, parts) + rest_end : 0) + 2 +
                 (parts > 1 ? 2 + planes * 0.45e-6 : 0),
             TilePlan{t.rows, t.cols, t.bufs, tiles, whole, parts});
     }
@@ -1127,7 +1131,7 @@ int run_product(const Product& g, const Epi& epi, float* part, hipStream_t s) {
     // 32-bit offsets of the rows.
     if (g.M <= kSkinnyRows && std::max(g.a.ld, g.b.ld) < (int64_t{1} << 24)) return launch_skinny<E, PAIR>(g, epi, aligned, part, s);
   }
-  const TilePlan t = plan_tiles(E, kPair, by_dma, KA, g.M, g.N, g.K);
+  const TilePlan t = plan_tiles(E, kPair, Epi::kBytes, by_dma, KA, g.M, g.N, g.K);
   if constexpr (E != El::F32) {
     if constexpr (KA) {
       if (t.bufs == 2 && t.rows == 64) return launch_aligned<E, KA, KB, PAIR, 64, 128, 2>(g, epi, t, part, s);

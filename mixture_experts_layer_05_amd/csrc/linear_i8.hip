@@ -65,7 +65,7 @@ int quantise(bool f32, int M, int K, const void* x, int64_t ldx, int8_t* q, int6
 
 template <bool OUT32>
 struct I8Out {
-  static constexpr int kAhead = OUT32 ? 4 : 8;
+  static constexpr int kAhead = OUT32 ? 4 : 8, kBytes = OUT32 ? 8 : 4;
   struct Cols {
     float w[4], b[4];
   };
@@ -184,9 +184,9 @@ int check_i8(const moe_linear_i8_config* c, int32_t rows) {
 constexpr int64_t kPackFrom = int64_t{1} << 24;      // multiply-adds
 bool large(const moe_linear_i8_config& c, int64_t M) { return M > kSkinnyRows && M * c.in_features * c.out_features >= kPackFrom; }
 
-// The workspace: partial sums, then the codes of x in rows of whole 16-byte pieces, their
-// scales, and where rows of that length do not end with a piece, room for w's codes.
-int64_t codes_ld(const moe_linear_i8_config& c) { return align_up(c.in_features, 16); }
+// The workspace: partial sums, then the codes of x in rows of whole 128-byte lines, their
+// scales, and where rows of that length do not end with a 16-byte piece, room for w's codes.
+int64_t codes_ld(const moe_linear_i8_config& c) { return align_up(c.in_features, 128); }
 size_t codes_bytes(const moe_linear_i8_config& c, int64_t rows) { return align_up(static_cast<size_t>(rows) * codes_ld(c), 256); }
 size_t i8_workspace(const moe_linear_i8_config& c, int64_t M) {
   return part_bytes(false, M, c.out_features) + codes_bytes(c, M) + align_up(M * 4, 256) +
@@ -275,7 +275,7 @@ int moe_linear_i8(const moe_linear_i8_config* cfg, int32_t M, const void* x, int
       p.item[p.n++] = PackItem{w, wq, ldw, ld, N, K, N};
       g.b.p = wq;
       g.b.ld = ld;
-      g.K = static_cast<int>(ld);
+      g.K = static_cast<int>(align_up(K, 16));
     }
     if (p.n && !pack_rows<uint8_t>(p, s)) return MOE_ERR_LAUNCH_FAILED;
   }
