@@ -66,7 +66,9 @@ struct None {};
 // row ends in are written, zeros behind its end.
 template <bool F32, bool KEEP>
 struct GatedOut {
-  static constexpr int kAhead = 4, kBytes = (F32 ? 4 : 2) + (KEEP ? 8 : 0);
+  // (kBytes without a and b: the tiles, and with them the sums' order and y's bits, are the
+  // same whether they are kept or not.)
+  static constexpr int kAhead = 4, kBytes = F32 ? 4 : 2;
   using Cols = None;
   using Ahead = None;
   void* h;
