@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(64 * back_waves(!YF32 && !SF32 && !OF32 && !PF
     Raw8<YF32> y[C];
     Raw8<SF32> z[C], dz[C];
     Raw8<OF32> dout[C];
+    float token;
   };
   const bool post = a.pw, weighted = a.w && a.dout;
   const bool need_y = post || (a.gate_kind != MOE_GATE_NONE && a.dgate);
@@ -79,6 +80,7 @@ __global__ void __launch_bounds__(64 * back_waves(!YF32 && !SF32 && !OF32 && !PF
     return load8<decltype(f32)::value>(static_cast<const uint8_t*>(p) + t * ld * (decltype(f32)::value ? 4 : 2), col.i, col.left);
   };
   const auto load = [&](Row& R, int64_t t) __attribute__((always_inline)) {
+    R.token = a.gate_kind == MOE_GATE_TOKEN ? load_of(PF32, a.gate, t) : 1.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       if (need_y) R.y[c] = rows(std::bool_constant<YF32>{}, a.y, a.ldy, t, c);
@@ -118,7 +120,7 @@ __global__ void __launch_bounds__(64 * back_waves(!YF32 && !SF32 && !OF32 && !PF
         z[c][e] = a.dout ? value<SF32>(R.z[c], e) : 0.0f;
         dn[c][e] = a.dout ? value<OF32>(R.dout[c], e) : 0.0f;
       }
-    const float gate_token = a.gate_kind == MOE_GATE_TOKEN ? load_of(PF32, a.gate, t) : 1.0f;
+    const float gate_token = R.token;
     if (by_element) {
 #pragma unroll
       for (int c = 0; c < C; ++c) g[c] = rows(std::bool_constant<PF32>{}, a.gate, a.ldg, t, c);
