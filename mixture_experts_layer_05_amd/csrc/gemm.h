@@ -93,6 +93,24 @@ __device__ __forceinline__ Acc<E> mfma32(const uint4& a, const uint4& b, Acc<E> 
 // A sum as it is staged (by value: a bit cast of a vector's element takes element 0).
 __device__ __forceinline__ float as_float(float v) { return v; }
 __device__ __forceinline__ float as_float(int v) { return __int_as_float(v); }
+// Staged sums added, and as an epilogue takes them: those of 8-bit products stay integers
+// until they are whole, so that however a product is split its sums are exact.
+template <El E>
+__device__ __forceinline__ float add_sums(float a, float b) {
+  if constexpr (E == El::I8) return __int_as_float(__float_as_int(a) + __float_as_int(b));
+  else return a + b;
+}
+template <El E>
+__device__ __forceinline__ f32x4 whole_sums(const f32x4& s) {
+  if constexpr (E != El::I8) return s;
+  f32x4 r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float v = s[e];
+    r[e] = static_cast<float>(__float_as_int(v));
+  }
+  return r;
+}
 
 // Two reads of 64 bits, each of which turns a 4 (k) x 16 block of a k-strided operand
 // between the 16 lanes that address it: lane i gets column i's four elements.
@@ -132,8 +150,9 @@ struct Batch {
 // Whole row segments, four columns to a thread.  A PAIR's columns take turns, TURN of the
 // first product and TURN of the second.  A part's sums go to part_of(R), those of the second
 // product `second` floats on; null leaves a row out.  Sums of 8-bit products are staged as
-// the integers they are.  What the epilogue reads for D rows is in flight while D others are finished: `now`
-// holds what it reads for the first, and then for the D rows behind the last (if `more`).
+// the integers they are.  What the epilogue reads for D rows is in flight while D others
+// are finished: `now` holds what it reads for the first, and then for the D rows behind the
+// last (if `more`).
 template <El E, bool PAIR, int TURN, int BN, int ROWS, int THREADS, int D, class Epi, class RowOf, class PartOf>
 __device__ __forceinline__ void results_out(const Product& g, const Epi& epi, const typename Epi::Cols& cols, Batch<Epi, D>& now,
                                             const float* stg, int stride, int n, int tid, int from, bool more, RowOf row_of,
@@ -150,9 +169,6 @@ __device__ __forceinline__ void results_out(const Product& g, const Epi& epi, co
     for (int d = 0; d < D; ++d) {
       s[d] = *reinterpret_cast<const f32x4*>(stg + (R + d * kStep) * stride + sc);
       if constexpr (PAIR) u[d] = *reinterpret_cast<const f32x4*>(stg + (R + d * kStep) * stride + sc + TURN);
-      if constexpr (E == El::I8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[d][e] = static_cast<float>(__float_as_int(s[d][e]));
     }
     if (cut) {
 #pragma unroll
@@ -168,14 +184,14 @@ __device__ __forceinline__ void results_out(const Product& g, const Epi& epi, co
     if (more || k + D < kIter) next.load(epi, g.M, n, from + R + D * kStep, kStep, row_of);
 #pragma unroll
     for (int d = 0; d < D; ++d)
-      if (now.m[d] < g.M) epi.put(now.m[d], n, s[d], u[d], cols, now.a[d]);
+      if (now.m[d] < g.M) epi.put(now.m[d], n, whole_sums<E>(s[d]), u[d], cols, now.a[d]);
     now = next;
   }
 }
 
 // The parts' sums added in order.
 constexpr int kSumAhead = 4;
-template <bool PAIR, class Epi>
+template <El E, bool PAIR, class Epi>
 __global__ void __launch_bounds__(256) product_sum_kernel(Product g, Epi epi, int parts, const float* part) {
   const int quads = static_cast<int>(part_stride(g.N) / 4);
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -196,12 +212,12 @@ __global__ void __launch_bounds__(256) product_sum_kernel(Product g, Epi epi, in
       if (p + k < parts)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[e] += b[k][e];
+          s[e] = add_sums<E>(s[e], b[k][e]);
           if constexpr (PAIR) u[e] += c[k][e];
         }
   }
   const int m = static_cast<int>(i / quads), n = 4 * static_cast<int>(i - static_cast<int64_t>(m) * quads);
-  epi.put(m, n, s, u, epi.cols(n), epi.ahead(m, n));
+  epi.put(m, n, whole_sums<E>(s), u, epi.cols(n), epi.ahead(m, n));
 }
 
 // ---------------------------------------------------------------- tiles of any alignment
@@ -454,9 +470,8 @@ __global__ void __launch_bounds__(256, 2) product_tile_kernel(Product g, Epi epi
 // each.  Of a pair the two sets are eight columns of either product.
 constexpr int kSkinnyEight = 8;
 
-typedef int i32x4s __attribute__((ext_vector_type(4)));
 template <El E>
-using Acc16 = std::conditional_t<E == El::I8, i32x4s, f32x4>;
+using Acc16 = std::conditional_t<E == El::I8, i32x4v, f32x4>;
 template <El E>
 __device__ __forceinline__ Acc16<E> mfma16(const uint4& a, const uint4& b, Acc16<E> c) {
   if constexpr (E == El::F32) {
@@ -568,12 +583,12 @@ __global__ void __launch_bounds__(kSkinnyEight * kWave, SETS == 1 ? 6 : 4) produ
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if constexpr (SETS == 2) {
-      s[i] = static_cast<float>(acc[0][i]);
+      s[i] = as_float(acc[0][i]);
     } else {
       // Eight columns: the halves of a block were multiplied over all sixteen, of which the
       // lower eight are the first half's and the upper eight the second's.
       const auto v = (lane & 8) ? acc[1][i] : acc[0][i];
-      s[i] = static_cast<float>(v + __shfl_xor(v, 8, kWave));
+      s[i] = as_float(v + __shfl_xor(v, 8, kWave));
     }
   }
   red[wave][lane] = s;
@@ -582,7 +597,7 @@ __global__ void __launch_bounds__(kSkinnyEight * kWave, SETS == 1 ? 6 : 4) produ
   if (wave < 4) {
     float v = red[0][lane][wave];
 #pragma unroll
-    for (int o = 1; o < kSkinnyEight; ++o) v += red[o][lane][wave];
+    for (int o = 1; o < kSkinnyEight; ++o) v = add_sums<E>(v, red[o][lane][wave]);
     out[4 * q + wave][r] = v;
   }
   __syncthreads();
@@ -597,8 +612,8 @@ __global__ void __launch_bounds__(kSkinnyEight * kWave, SETS == 1 ? 6 : 4) produ
     *reinterpret_cast<f32x4*>(part + o) = a;
     if constexpr (PAIR) *reinterpret_cast<f32x4*>(part + o + g.M * np) = u;
   } else {
-    if constexpr (Rows::kStaged) epi.put(m, n, a, u, epi.cols(n), rows.ahead(staged, epi, n));
-    else epi.put(m, n, a, u, epi.cols(n), epi.ahead(m, n));
+    if constexpr (Rows::kStaged) epi.put(m, n, whole_sums<E>(a), u, epi.cols(n), rows.ahead(staged, epi, n));
+    else epi.put(m, n, whole_sums<E>(a), u, epi.cols(n), epi.ahead(m, n));
   }
 }
 
@@ -942,7 +957,7 @@ __global__ void __launch_bounds__(256, (Aligned<E, KA, KB, PAIR, BM, BN, BUFS>::
 }
 
 // The rest's parts added in order: 1024 sums (of a pair: 512 of either) to a workgroup.
-template <bool PAIR, int BM, int BN, class Epi>
+template <El E, bool PAIR, int BM, int BN, class Epi>
 __global__ void __launch_bounds__(256) product_rest_kernel(Product g, Epi epi, int whole, int parts, const float* part) {
   constexpr int kCols = PAIR ? BN / 2 : BN, kQuads = kCols / 4, kGroups = BM * kQuads / 256, kBand = 2048 / BM;
   const int mt = static_cast<int>(ceil_div(g.M, BM)), nt = static_cast<int>(ceil_div(g.N, kCols));
@@ -968,11 +983,11 @@ __global__ void __launch_bounds__(256) product_rest_kernel(Product g, Epi epi, i
       if (p + k < parts)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[e] += b[k][e];
+          s[e] = add_sums<E>(s[e], b[k][e]);
           if constexpr (PAIR) u[e] += d[k][e];
         }
   }
-  epi.put(m, n, s, u, cols, ahead);
+  epi.put(m, n, whole_sums<E>(s), u, cols, ahead);
 }
 
 // ---------------------------------------------------------------- host
@@ -1091,7 +1106,7 @@ int launch_aligned(const Product& g, const Epi& epi, const TilePlan& t, float* p
   product_aligned_kernel<E, KA, KB, PAIR, BM, BN, BUFS><<<grid, 256, 0, s>>>(g, epi, static_cast<int>(t.whole), t.parts, part);
   if (t.parts > 1) {
     if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
-    product_rest_kernel<kPair, BM, BN><<<static_cast<unsigned>(rest * kGroups), 256, 0, s>>>(g, epi, static_cast<int>(t.whole), t.parts, part);
+    product_rest_kernel<E, kPair, BM, BN><<<static_cast<unsigned>(rest * kGroups), 256, 0, s>>>(g, epi, static_cast<int>(t.whole), t.parts, part);
   }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH_FAILED;
 }
@@ -1114,7 +1129,7 @@ int launch_skinny(const Product& g, const Epi& epi, bool aligned, float* part, h
   }
   if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
   if (parts > 1) {
-    product_sum_kernel<PAIR><<<static_cast<unsigned>(ceil_div(g.M * part_stride(g.N) / 4, 256)), 256, 0, s>>>(g, epi, parts, part);
+    product_sum_kernel<E, PAIR><<<static_cast<unsigned>(ceil_div(g.M * part_stride(g.N) / 4, 256)), 256, 0, s>>>(g, epi, parts, part);
     if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
   }
   return MOE_OK;
@@ -1154,7 +1169,7 @@ int run_product(const Product& g, const Epi& epi, float* part, hipStream_t s) {
   }
   if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
   if (t.parts > 1) {
-    product_sum_kernel<kPair><<<static_cast<unsigned>(ceil_div(g.M * part_stride(g.N) / 4, 256)), 256, 0, s>>>(g, epi, t.parts, part);
+    product_sum_kernel<E, kPair><<<static_cast<unsigned>(ceil_div(g.M * part_stride(g.N) / 4, 256)), 256, 0, s>>>(g, epi, t.parts, part);
     if (hipGetLastError() != hipSuccess) return MOE_ERR_LAUNCH_FAILED;
   }
   return MOE_OK;

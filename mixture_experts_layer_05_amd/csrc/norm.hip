@@ -373,7 +373,7 @@ int moe_norm_backward(const moe_norm_config* cfg, int32_t T, const void* y, int6
   a.ldy = ldy, a.ldz = ldz, a.ldg = ldg, a.lddz = lddz, a.lddo = lddo, a.lddy = lddy, a.lddr = lddr, a.lddg = lddg;
   a.T = T, a.H = c.hidden_size, a.groups = norm_groups(c, T);
   a.eps = c.eps, a.a = c.residual_scale, a.b = c.block_scale;
-  a.layer = c.kind == MOE_NORM_LAYER, a.gate_kind = c.gate, a.params_f32 = c.param_dtype == MOE_DTYPE_F32;
+  a.layer = c.kind == MOE_NORM_LAYER, a.gate_kind = c.gate;
   NormSums sums{};
   void* outs[kSums] = {dweight, dbias, dpost_weight, dpost_bias, c.gate == MOE_GATE_CHANNEL ? dgate : nullptr};
   for (int i = 0; i < kSums; ++i)
@@ -381,7 +381,7 @@ int moe_norm_backward(const moe_norm_config* cfg, int32_t T, const void* y, int6
       a.sums |= 1 << i;
       sums.out[sums.n++] = outs[i];
     }
-  sums.part = a.part, sums.H = c.hidden_size, sums.groups = a.groups, sums.f32 = a.params_f32;
+  sums.part = a.part, sums.H = c.hidden_size, sums.groups = a.groups, sums.f32 = c.param_dtype == MOE_DTYPE_F32;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (T > 0) {
     const bool sf = c.stream_dtype == MOE_DTYPE_F32, of = c.out_dtype == MOE_DTYPE_F32, pf = c.param_dtype == MOE_DTYPE_F32;

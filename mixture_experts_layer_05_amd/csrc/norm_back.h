@@ -16,7 +16,7 @@ struct NormBackArgs {
   int64_t ldy, ldz, ldg, lddz, lddo, lddy, lddr, lddg;
   int T, H, waves, groups;           // waves of a row: the launch sets them
   float eps, a, b;
-  int layer, gate_kind, params_f32;
+  int layer, gate_kind;
   int sums;                          // bits of Sum
 };
 // The sums over rows, in the order in which a group stores them.
@@ -29,7 +29,6 @@ constexpr int kRowsOfOneWave = 4;      // to a workgroup, where a row is one wav
 // there are biases or their gradients.
 void launch_norm_back_f32(const NormBackArgs& a, hipStream_t s, bool sf, bool of, bool pf, bool bias);
 void launch_norm_back_bf16(const NormBackArgs& a, hipStream_t s, bool sf, bool of, bool pf, bool bias);
-
 
 namespace {
 
