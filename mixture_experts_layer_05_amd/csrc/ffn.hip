@@ -1,8 +1,8 @@
 // The dense gated FFN, y = (act(x Wg^T) * (x Wu^T)) Wd^T, and its gradients.
 //
 // Forward: one product computes g = x Wg^T and u = x Wu^T side by side (their columns
-// take turns in blocks of 32, so that a lane holds both of an element) and its epilogue
-// writes h = act(g) u; the down projection is another product.  For a backward pass the
+// take turns in a tile, so that a lane gets both of an element) and its epilogue writes
+// h = act(g) u; the down projection is another product.  For a backward pass the
 // epilogue also keeps a = act(g) and b = u act'(g), in float32.
 //
 // Backward, from dy:
@@ -13,6 +13,11 @@
 // h, dg and du are matrix operands and have the weights' type: with bf16 weights each is
 // rounded once.  a and b stay in float32: one more rounding of either would add to dg's
 // and du's own (weight gradients off by 1.7 roundings instead of 1.4).
+//
+// Bound by memory up to 16 rows, by the matrix cores from about 500 on, in between by what
+// a CU takes in and by the launches.  Weights of 5120 x 17408 in bf16: one row 104 us (three
+// matrices at 5.1 TB/s), a training step of 8192 rows 10.6 to 11.3 ms for 13.1 TFLOP (1.16 to
+// 1.24 PFLOP/s; the nine products alone take 12.1 ms in library calls).
 #include "gemm.h"
 #include "pack.h"
 
@@ -191,14 +196,16 @@ size_t h_bytes(const moe_ffn_config& c, int64_t T) { return align_up(static_cast
 size_t slope_bytes(const moe_ffn_config& c, int64_t T) { return align_up(static_cast<size_t>(T) * inner_ld(c) * 4, 256); }
 size_t kept_bytes(const moe_ffn_config& c, int64_t T) { return h_bytes(c, T) + 2 * slope_bytes(c, T); }
 
-// Rows that do not lie in whole 16-byte pieces are laid out afresh where the products are
-// large: loads of odd rows take in less than half as much.  1001 x 1537 x 2049, a training
-// step: 290 us as it lies, see below.  Room for x and dy is always there, room for the
-// weights where their sizes are odd.
-constexpr int64_t kPackFrom = int64_t{1} << 22;      // multiply-adds of a product
+// Rows that do not lie in whole 16-byte pieces are laid out afresh, in one launch, for the
+// products of more than 16 rows: loads of odd rows take in less than half as much.  A
+// training step of 1001 x 1537 x 2049 takes 290 us with the rows as they lie, 163 with 2 x 11
+// for laying them out; forward and backward of 256 x 515 x 1023 27 + 45 and 22 + 39, of
+// 64 x 129 x 257 17.9 + 40.3 and 16.2 + 36.4, of 17 x 65 x 129 13.7 + 31.7 and 14.4 + 27.8.  Room
+// for x and dy is always there, room for the weights where their sizes are odd.
+constexpr int64_t kPackFrom = int64_t{1} << 20;      // multiply-adds of a product, forward
 int64_t eights(int64_t n) { return (n + 7) / 8 * 8; }
-bool large(const moe_ffn_config& c, int64_t T) {
-  return c.dtype == MOE_DTYPE_BF16 && T > kSkinnyRows && T * c.hidden_size * c.intermediate_size >= kPackFrom;
+bool packs(const moe_ffn_config& c, int64_t T, bool backward) {
+  return c.dtype == MOE_DTYPE_BF16 && T > kSkinnyRows && (backward || T * c.hidden_size * c.intermediate_size >= kPackFrom);
 }
 bool odd_sizes(const moe_ffn_config& c) { return c.hidden_size % 8 || c.intermediate_size % 8; }
 // Rows of whole 128-byte lines, of which a stage takes one.
@@ -216,7 +223,8 @@ size_t ffn_workspace(const moe_ffn_config& c, int64_t T, bool backward) {
   size_t n = ffn_parts(c, T) + (backward ? 2 : 1) * h_bytes(c, T);
   const int64_t H = eights(c.hidden_size), I = eights(c.intermediate_size);
   // Of any smaller number of rows too: the weights' room does not depend on it.
-  if (c.dtype == MOE_DTYPE_BF16) n += (backward ? 2 : 1) * packed_bytes(T, H) + (odd_sizes(c) ? 2 * packed_bytes(I, H) + packed_bytes(H, I) : 0);
+  if (c.dtype == MOE_DTYPE_BF16)
+    n += (backward ? 2 : 1) * packed_bytes(T, H) + (odd_sizes(c) ? 2 * packed_bytes(I, H) + packed_bytes(H, I) : 0);
   return n;
 }
 
@@ -233,7 +241,7 @@ struct FfnArgs {
 int ffn_operands(const moe_ffn_config& c, int T, const void* x, int64_t ldx, const void* dy, int64_t lddy, const void* wg,
                  const void* wu, const void* wd, uint8_t* room, hipStream_t s, FfnArgs& f) {
   f = FfnArgs{x, dy, wg, wu, wd, ldx, lddy, c.hidden_size, c.intermediate_size, c.hidden_size, c.intermediate_size};
-  if (!large(c, T)) return MOE_OK;
+  if (!packs(c, T, dy != nullptr)) return MOE_OK;
   const bool odd = odd_sizes(c);
   const int H = c.hidden_size, I = c.intermediate_size, Hp = static_cast<int>(eights(H)), Ip = static_cast<int>(eights(I));
   const auto lies_odd = [](const void* p, int64_t ld) { return ld % 8 || reinterpret_cast<uintptr_t>(p) % 16; };

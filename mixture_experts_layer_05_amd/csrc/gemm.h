@@ -222,12 +222,20 @@ __global__ void __launch_bounds__(256) product_sum_kernel(Product g, Epi epi, in
 
 // ---------------------------------------------------------------- tiles of any alignment
 //
-// BM x BN sums per workgroup of 2 x 2 waves, from 32x32 MFMAs.  A stage is 128 bytes of
-// contraction (64 bf16, 32 f32, 128 int8), double-buffered in LDS; its loads go to
-// registers two to four stages ahead, which takes any alignment and fills ends with zeros.  A
+// BM x BN sums per workgroup of 2 x 2 waves, from 32x32 MFMAs: float32, and what does not
+// lie in whole 16-byte pieces.  A stage is 128 bytes of contraction (64 bf16, 32 f32, 128
+// int8), double-buffered in LDS; its loads go to registers two to four stages ahead, which
+// takes any alignment and fills ends with zeros.  A
 // k-contiguous operand's rows lie unpadded in LDS, their 16-byte pieces permuted by
 // (row / 2) mod 8; a k-strided one's rows are the k, padded so that the four k that a
 // fragment read takes lie in different quarters of the banks.
+//
+// Bound by the f32 matrix rate where tiles are many, below that by a stage's latency: a
+// barrier, the LDS's writes and reads and 16 MFMAs of 64 cycles take about 1 us where the
+// MFMAs alone are 0.45.  333 x 515 x 1023 in f32 with odd rows takes 11 to 19 us a product,
+// six of them and three sums 99 us in a training step (135 in 64 x 128 and 128 x 128 tiles with
+// two stages ahead, 118 in 64 x 64).  Five LDS slots, or the next quarter's fragments read
+// ahead, change nothing there.
 template <El E, bool KC, int R>
 struct TileSide {
   using I = ElInfo<E>;
@@ -468,6 +476,11 @@ __global__ void __launch_bounds__(256, 2) product_tile_kernel(Product g, Epi epi
 // The weights go from memory straight into the registers of the MFMAs (skinny.h): eight
 // waves compute 8 SETS operand columns over one part of the contraction, an eighth for
 // each.  Of a pair the two sets are eight columns of either product.
+//
+// Bound by memory: one row against the two bf16 matrices of 17408 x 5120 takes 64 us
+// (5.5 TB/s), against the third 39 (4.5 TB/s; 640 workgroups only); 17408 x 5120 int8 21 us
+// (4.2 TB/s).  With 16 rows the rows' own reading, by every workgroup, shows: the three
+// matrices take 163 us instead of 103.
 constexpr int kSkinnyEight = 8;
 
 template <El E>
@@ -630,13 +643,20 @@ __global__ void __launch_bounds__(kSkinnyEight * kWave, SETS == 1 ? 6 : 4) produ
 // stage, in front of the last quarter: by then every wave has the stage's last fragments in
 // registers and stage s + 1 is in LDS.
 //
+// Bound by the matrix cores, whose clock falls under full load: they are busy 78 % of the
+// 256 x 256 kernel's time, at 1.8 GHz.  8192 x 17408 x 5120 bf16 with a pair takes 2.36 to 2.48 ms
+// (1.18 to 1.24 PFLOP/s, its results included), one product of these sizes 1.12 to 1.14
+// (1.28 to 1.30; a library product without an epilogue 1.20, or 1.39 with a k-strided side);
+// 8192 x 4096 x 7168 int8 230 to 255 us (1.9 to 2.1 POP/s; a library product 204).
+//
 // k-contiguous operands: rows of 128 bytes, 16-byte pieces permuted by (row / 2) mod 8.
 // k-strided: a row for each k, 64-byte pieces permuted by k mod 4, so that the four k of a
 // turning read lie in different quarters of the banks.  What lies behind the end of the
 // contraction is out of the resource's range, and such loads bring zeros.
 //
 // Results leave through LDS too, 32 rows of a wave at a time, in a buffer that the last
-// stage is not in, the first or the last; rows padded by 4 floats, for which there is room on its other side.
+// stage is not in, the first or the last; rows padded by 4 floats, for which there is room
+// on its other side.
 template <El E, bool KA, bool KB, bool PAIR, int BM, int BN, int BUFS>
 struct Aligned {
   static constexpr bool kPair = PAIR && KB;
@@ -1010,8 +1030,9 @@ struct TilePlan {
   int parts;            // of the others
 };
 
-// The cheapest tile and split by an estimate in microseconds: what a CU takes in, the
-// f32 matrix rate, and the partial sums' way out and back.
+// The cheapest tile and split by an estimate in microseconds: what a CU takes in (28 KB a
+// microsecond with two tiles on it, 20 with one), the f32 matrix rate, and the partial sums'
+// way out and back.
 inline TilePlan plan_tiles(El e, bool pair, int out_bytes, bool by_dma, bool rows64, int64_t M, int64_t N, int64_t K) {
   const int size = e == El::F32 ? 4 : e == El::BF16 ? 2 : 1;
   const int64_t width = pair ? 2 * N : N, stages = ceil_div(K * size, 128);

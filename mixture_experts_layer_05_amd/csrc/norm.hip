@@ -14,6 +14,11 @@
 //
 // A row belongs to as many waves as give each lane C times eight of its elements; a wave
 // that holds a whole row needs no barrier.
+//
+// Bound by memory, or for few rows by one launch: 8192 x 7168 in bf16 with a post norm takes
+// 96 us (4.9 TB/s over four tensors, what a large copy reaches), one row 3 us on the GPU.
+// Backward, six tensors and three sums over rows, 155 (4.5 TB/s), of which 9 are the second
+// launch's.
 #include <algorithm>
 #include <initializer_list>
 
@@ -314,8 +319,9 @@ int moe_norm(const moe_norm_config* cfg, int32_t T, const void* y, int64_t ldy, 
                          check_rows(post_bias, H, H, ps), check_rows(z, ldz, H, ss),
                          check_rows(out, ldo, H, type_size(c.out_dtype)), check_rows(out_scale, 1, 1, 4)});
   if (bad) return bad;
-  // Few rows: as many lanes as there are, for the latency.  Many: several chunks to a
-  // lane, for the loads in flight.
+  // Few rows: as many lanes as there are, for the latency.  Many: several chunks to a lane,
+  // for the loads in flight.  Microseconds of the first and the second (with a post norm):
+  // 16 x 5120 4.0 and 4.5, 256 x 7168 5.4 and 5.6, 512 x 7168 8.9 and 8.0, 4096 x 7168 57 and 40.
   const RowPlan p = row_plan(c.hidden_size, T <= 256 ? 16 : 2);
   NormArgs a{};
   a.y = y, a.r = residual, a.gate = c.gate == MOE_GATE_NONE ? nullptr : gate, a.w = weight, a.wb = bias;
