@@ -11,7 +11,8 @@
 //   dWg = dg^T x, dWu = du^T x                 one product of 2 I rows
 //   dWd = dy^T h
 // h, dg and du are matrix operands and have the weights' type: with bf16 weights each is
-// rounded once.  a and b stay in float32: one more rounding of either would add to dg's
+// rounded once.  (Of up to eight rows the forward pass keeps what h's rounding leaves as eight
+// rows more, which a tile of 16 has free: y's own rounding is then the only one.)  a and b stay in float32: one more rounding of either would add to dg's
 // and du's own (weight gradients off by 1.7 roundings instead of 1.4).
 //
 // Bound by memory up to 16 rows, by the matrix cores from about 500 on, in between by what
@@ -66,9 +67,9 @@ __device__ __forceinline__ void act_slope(float v, int act, float& f, float& d) 
 
 struct None {};
 
-// h = act(g) u, and a and b where they are kept; their rows lie `ld`, a multiple of eight,
-// apart, so that a whole quad may be written at their ends.  The eight elements that h's
-// row ends in are written, zeros behind its end.
+// h = act(g) u, what its rounding leaves (`rests`) eight rows on, and a and b where they are
+// kept; their rows lie `ld`, a multiple of eight, apart, so that a whole quad may be written
+// at their ends.  The eight elements that a row of h ends in are written, zeros behind its end.
 template <bool F32, bool KEEP>
 struct GatedOut {
   // (kBytes without a and b: the tiles, and with them the sums' order and y's bits, are the
@@ -80,6 +81,7 @@ struct GatedOut {
   float *a, *b;
   int64_t ld;
   int N, act;
+  bool rests;
   __device__ __forceinline__ None cols(int) const { return {}; }
   __device__ __forceinline__ None ahead(int, int) const { return {}; }
   __device__ __forceinline__ void put(int m, int n, const f32x4& g, const f32x4& u, None, None) const {
@@ -95,9 +97,20 @@ struct GatedOut {
     }
     const size_t o = static_cast<size_t>(m) * ld + n;
     store4<F32>(h, o, h4);
-    if (n + 4 >= N && (n & 4) == 0) {
-      const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-      store4<F32>(h, o + 4, zero);
+    const bool end = n + 4 >= N && (n & 4) == 0;
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+    if (end) store4<F32>(h, o + 4, zero);
+    if constexpr (!F32) {
+      if (rests) {
+        float r4[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float r = bf16_bits_to_f32(f32_to_bf16_bits(h4[c]));
+          r4[c] = isfinite(r) ? h4[c] - r : 0.0f;
+        }
+        store4<F32>(h, o + kRestRows * ld, r4);
+        if (end) store4<F32>(h, o + kRestRows * ld + 4, zero);
+      }
     }
     if constexpr (KEEP) {
       store4<true>(a, o, a4);
@@ -191,8 +204,11 @@ size_t type_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
 // Length of the rows of h, a and b: whole stages of a contraction over them.
 int64_t inner_ld(const moe_ffn_config& c) { return (static_cast<int64_t>(c.intermediate_size) + 63) / 64 * 64; }
 
-// The kept tensors: h, a, b.
-size_t h_bytes(const moe_ffn_config& c, int64_t T) { return align_up(static_cast<size_t>(T) * inner_ld(c) * type_bytes(c.dtype), 256); }
+// The kept tensors: h (of few rows with their rests), a, b.
+bool with_rests(const moe_ffn_config& c, int64_t T) { return c.dtype == MOE_DTYPE_BF16 && T <= kRestRows; }
+size_t h_bytes(const moe_ffn_config& c, int64_t T) {
+  return align_up(static_cast<size_t>(std::max<int64_t>(T, 2 * kRestRows)) * inner_ld(c) * type_bytes(c.dtype), 256);
+}
 size_t slope_bytes(const moe_ffn_config& c, int64_t T) { return align_up(static_cast<size_t>(T) * inner_ld(c) * 4, 256); }
 size_t kept_bytes(const moe_ffn_config& c, int64_t T) { return h_bytes(c, T) + 2 * slope_bytes(c, T); }
 
@@ -273,11 +289,17 @@ int ffn_forward(const moe_ffn_config& c, int T, const FfnArgs& f, void* y, int64
   const int64_t Ip = inner_ld(c);
   const Product g{{f.x, nullptr, f.ldx, 0, 0}, {f.wg, f.wu, f.ldw, 0, 0}, T, I, f.H};
   float* part = reinterpret_cast<float*>(ws);
-  const int st = a ? run_product<E, true, true, true>(g, GatedOut<F32, true>{h, a, b, Ip, I, c.activation}, part, s)
-                   : run_product<E, true, true, true>(g, GatedOut<F32, false>{h, a, b, Ip, I, c.activation}, part, s);
+  const bool rests = with_rests(c, T);
+  const int st = a ? run_product<E, true, true, true>(g, GatedOut<F32, true>{h, a, b, Ip, I, c.activation, rests}, part, s)
+                   : run_product<E, true, true, true>(g, GatedOut<F32, false>{h, a, b, Ip, I, c.activation, rests}, part, s);
   if (st) return st;
   const Product d{{h, nullptr, Ip, 0, 0}, {f.wd, nullptr, f.ldd, 0, 0}, T, H, f.I};
-  return run_product<E, true, true, false>(d, RowsOut<F32>{y, nullptr, ldy, H, T, T}, part, s);
+  const RowsOut<F32> out{y, nullptr, ldy, H, T, T};
+  if constexpr (!F32) {
+    const bool aligned = aligned16(d.a, E, true, T, f.I) && aligned16(d.b, E, true, H, f.I);
+    if (rests) return launch_skinny<E, false>(d, out, aligned, part, s, WithRests{});
+  }
+  return run_product<E, true, true, false>(d, out, part, s);
 }
 
 template <bool F32>

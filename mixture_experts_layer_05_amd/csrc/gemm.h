@@ -499,12 +499,17 @@ __device__ __forceinline__ Acc16<E> mfma16(const uint4& a, const uint4& b, Acc16
   }
 }
 
-// Where the rows of x come from: as they lie, as operands, or a single row that a functor
-// puts into LDS once the first weights are on their way; it also gives what the epilogue
-// reads of that row.
+// Where the rows of x come from: as they lie, as operands; at most eight, with what their
+// rounding left eight rows further on, which takes the place of the tile's idle rows; or a
+// single row that a functor puts into LDS once the first weights are on their way; it also
+// gives what the epilogue reads of that row.
 struct AsTheyLie {
-  static constexpr bool kStaged = false;
+  static constexpr bool kStaged = false, kRests = false;
 };
+struct WithRests {
+  static constexpr bool kStaged = false, kRests = true;
+};
+constexpr int kRestRows = 8;
 
 template <El E, bool PAIR, bool ANY, int SETS, class Rows, class Epi>
 __global__ void __launch_bounds__(kSkinnyEight * kWave, SETS == 1 ? 6 : 4) product_skinny_kernel(Product g, Rows rows, Epi epi, int parts, float* part) {
@@ -527,8 +532,9 @@ __global__ void __launch_bounds__(kSkinnyEight * kWave, SETS == 1 ? 6 : 4) produ
     woff[h] = static_cast<uint32_t>(min((PAIR ? 0 : 8 * h) + (lane & 7), g.N - 1 - n0)) * static_cast<uint32_t>(g.b.ld) * I::kSize + 16 * lane_piece(lane);
   }
   const uint8_t* xbase = static_cast<const uint8_t*>(g.a.p);
-  const uint32_t xoff = static_cast<uint32_t>(min(r, g.M - 1)) * static_cast<uint32_t>(g.a.ld) * I::kSize + 16 * q;
-  const bool live = r < g.M, tail = g.K % I::kStage != 0;
+  const bool live = (Rows::kRests ? r & 7 : r) < g.M;
+  const uint32_t xoff = static_cast<uint32_t>(live ? r : 0) * static_cast<uint32_t>(g.a.ld) * I::kSize + 16 * q;
+  const bool tail = g.K % I::kStage != 0;
   extern __shared__ __attribute__((aligned(16))) uint8_t staged[];
 
   struct Blk {
@@ -617,7 +623,12 @@ __global__ void __launch_bounds__(kSkinnyEight * kWave, SETS == 1 ? 6 : 4) produ
   constexpr int kQuads = kCols / 4;
   const int m = tid / kQuads, c = 4 * (tid % kQuads), n = n0 + c;
   if (m >= g.M || n >= g.N) return;
-  const f32x4 a = *reinterpret_cast<const f32x4*>(&out[m][c]);
+  f32x4 a = *reinterpret_cast<const f32x4*>(&out[m][c]);
+  if constexpr (Rows::kRests) {
+    const f32x4 b = *reinterpret_cast<const f32x4*>(&out[m + kRestRows][c]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e] += b[e];
+  }
   f32x4 u = {0.f, 0.f, 0.f, 0.f};
   if constexpr (PAIR) u = *reinterpret_cast<const f32x4*>(&out[m][c + 8]);
   if (parts > 1) {

@@ -122,7 +122,7 @@ struct I8Out {
 // than a launch (4 x 5120 x 5120: 19 and 14).
 template <bool F32>
 struct QuantisedRow {
-  static constexpr bool kStaged = true;
+  static constexpr bool kStaged = true, kRests = false;
   const void* x;
   float* scale;
   int ld;                        // bytes of the codes in LDS, whole blocks; the scale behind them

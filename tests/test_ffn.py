@@ -476,3 +476,33 @@ def test_an_infinity_behind_the_end_stays_there(T):
         want = _expect(x[:, :H], w, dy[:, :H], "silu", "bf16")
         y = op(x.cuda()[:, :H])
         _compare(dict(op.backward(x.cuda()[:, :H], dy.cuda()[:, :H]), y=y), want, "padding")
+
+
+# Up to eight rows h keeps what its rounding leaves as a second bf16 number: y's own rounding is
+# the only one.  What remains of h is half a step of a half step: 2^-8 2^-8 |h|, and sums of
+# twice as many products (32 to a pair of matrix instructions).
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,I,pad", [(1, 64, 64, 0), (1, 5120, 2048, 0), (7, 515, 1023, 3), (8, 256, 512, 8), (8, 41, 4097, 0),
+                                       (3, 16, 1, 0), (2, 5120, 17408, 0)])
+@pytest.mark.parametrize("train", [False, True])
+def test_few_rows_round_once(T, H, I, pad, train):
+    print(f"\n[case] ffn rounds once T={T} H={H} I={I} pad={pad} train={train}", flush=True)
+    x, _, w = _inputs(T, H, I, "bf16", T + H + I, pad)
+    x = x[:, :H]
+    op = moe.GatedFFN({n: t.cuda() for n, t in w.items()}, "gelu_tanh", max_rows=T, training=train)
+    op.workspace.fill_(0xFF)
+    y = op(x.cuda()).cpu().double()
+    x, wg, wu, wd = x.double(), w["gate"].double(), w["up"].double(), w["down"].double()
+    cH, cI = _chain(H, "bf16") * U, (2 * I / 16 + 56) * U
+    g, u = x @ wg.t(), x @ wu.t()
+    eg, eu = cH * (x.abs() @ wg.abs().t()), cH * (x.abs() @ wu.abs().t())
+    a, _ = _act64(g, "gelu_tanh")
+    ea = 1.13 * eg + 2.0 ** -21 * (g.abs() + 1)
+    h = a * u
+    eh = a.abs() * eu + ea * (u.abs() + eu) + (4 * U + 2.0 ** -16) * h.abs()
+    want = h @ wd.t()
+    e = eh @ wd.abs().t() + cI * ((h.abs() + eh) @ wd.abs().t())
+    tol = e + 2.0 ** -8 * (want.abs() + e)
+    err = (y - want).abs()
+    print(f"[case] worst error / tolerance {(err / tol).max():.3f}", flush=True)
+    assert (err <= tol).all()
