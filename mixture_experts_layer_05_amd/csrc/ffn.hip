@@ -72,9 +72,7 @@ struct None {};
 // at their ends.  The eight elements that a row of h ends in are written, zeros behind its end.
 template <bool F32, bool KEEP>
 struct GatedOut {
-  // (kBytes without a and b: the tiles, and with them the sums' order and y's bits, are the
-  // same whether they are kept or not.)
-  static constexpr int kAhead = 4, kBytes = F32 ? 4 : 2;
+  static constexpr int kAhead = 4;
   using Cols = None;
   using Ahead = None;
   void* h;
@@ -82,6 +80,9 @@ struct GatedOut {
   int64_t ld;
   int N, act;
   bool rests;
+  // (Without a and b: the tiles, and with them the sums' order and y's bits, are the same
+  // whether they are kept or not.)
+  int bytes() const { return F32 ? 4 : 2; }
   __device__ __forceinline__ None cols(int) const { return {}; }
   __device__ __forceinline__ None ahead(int, int) const { return {}; }
   __device__ __forceinline__ void put(int m, int n, const f32x4& g, const f32x4& u, None, None) const {
@@ -122,7 +123,8 @@ struct GatedOut {
 // dg = dh b and du = dh a, side by side in rows of 2 ld.
 template <bool F32>
 struct SlopesOut {
-  static constexpr int kAhead = 4, kBytes = 8 + (F32 ? 8 : 4);
+  static constexpr int kAhead = 4;
+  int bytes() const { return 8 + (F32 ? 8 : 4); }
   using Cols = None;
   struct Ahead {
     f32x4 a, b;
@@ -162,7 +164,8 @@ struct SlopesOut {
 // of either the first `live`.
 template <bool F32>
 struct RowsOut {
-  static constexpr int kAhead = 4, kBytes = F32 ? 4 : 2;
+  static constexpr int kAhead = 4;
+  int bytes() const { return F32 ? 4 : 2; }
   using Cols = None;
   using Ahead = None;
   void *y, *y2;

@@ -127,7 +127,7 @@ __device__ __forceinline__ uint2 lds_turned(const uint8_t* p) {
 //   Ahead ahead(m, n)             what it reads of row m there, as loaded
 //   put(m, n, s, u, cols, ahead)  the results of the sums s (and u, of a pair)
 //   kAhead                        the rows of a batch in aligned tiles, by its registers
-//   kBytes                        what it reads and writes of a result
+//   bytes()                       what it reads and writes of a result (the host asks)
 // Rows past the end are left out by its caller.
 
 // The rows behind D rows of staged sums, from row R on, and what is read for them.
@@ -1178,7 +1178,7 @@ int run_product(const Product& g, const Epi& epi, float* part, hipStream_t s) {
     // 32-bit offsets of the rows.
     if (g.M <= kSkinnyRows && std::max(g.a.ld, g.b.ld) < (int64_t{1} << 24)) return launch_skinny<E, PAIR>(g, epi, aligned, part, s);
   }
-  const TilePlan t = plan_tiles(E, kPair, Epi::kBytes, by_dma, KA, g.M, g.N, g.K);
+  const TilePlan t = plan_tiles(E, kPair, epi.bytes(), by_dma, KA, g.M, g.N, g.K);
   if constexpr (E != El::F32) {
     if constexpr (KA) {
       if (t.bufs == 2 && t.rows == 64) return launch_aligned<E, KA, KB, PAIR, 64, 128, 2>(g, epi, t, part, s);

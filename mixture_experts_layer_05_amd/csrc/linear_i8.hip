@@ -16,11 +16,13 @@ namespace {
 // A row of x to a workgroup: its largest magnitude, then its codes.  A lane keeps C times
 // eight elements; what is left of a longer row is read again, from the caches.  Zeros
 // behind the row up to `width` codes.  Bound by memory: 8192 x 7168 bf16 takes 31 us, 5.7 TB/s
-// read and written (67 us with every code decided by the exact remainder).
+// read and written (67 us with every code decided by the exact remainder).  Workgroups from
+// M on lay out rows of the product's weights, if those lie odd: a launch less.
 template <bool F32, int C>
-__global__ void __launch_bounds__(1024) quant_i8_kernel(const void* x, int64_t ldx, int K, int8_t* q, int64_t ldq, int width, float* scale) {
+__global__ void __launch_bounds__(1024) quant_i8_kernel(const void* x, int64_t ldx, int K, int8_t* q, int64_t ldq, int width, float* scale, int M, PackItem pack) {
   __shared__ RowLds<uint32_t> lds;
   const int64_t m = blockIdx.x;
+  if (m >= M) return pack_row<uint8_t>(pack, m - M);
   const uint8_t* row = static_cast<const uint8_t*>(x) + m * ldx * (F32 ? 4 : 2);
   const int waves = blockDim.x >> 6, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), step = 8 * blockDim.x;
   const int first = 8 * threadIdx.x;
@@ -55,12 +57,13 @@ __global__ void __launch_bounds__(1024) quant_i8_kernel(const void* x, int64_t l
 // the second: 16 x 5120 3.0 and 4.8, 512 x 7168 4.8 and 5.7, 4096 x 1024 5.1 and 5.8,
 // 1024 x 5120 6.2 and 6.5, 1024 x 7168 8.1 and 7.3, 4096 x 7168 24 and 18.
 constexpr int64_t kFewElements = int64_t{6} << 20;
-int quantise(bool f32, int M, int K, const void* x, int64_t ldx, int8_t* q, int64_t ldq, int width, float* scale, hipStream_t s) {
+int quantise(bool f32, int M, int K, const void* x, int64_t ldx, int8_t* q, int64_t ldq, int width, float* scale, const PackItem& pack, hipStream_t s) {
   const bool few = static_cast<int64_t>(M) * K <= kFewElements;
   const unsigned block = 64u * static_cast<unsigned>(std::min<int64_t>(16, ceil_div(width, few ? 512 : 2048)));
-  const unsigned grid = static_cast<unsigned>(M);
-  if (f32) few ? quant_i8_kernel<true, 1><<<grid, block, 0, s>>>(x, ldx, K, q, ldq, width, scale) : quant_i8_kernel<true, 4><<<grid, block, 0, s>>>(x, ldx, K, q, ldq, width, scale);
-  else few ? quant_i8_kernel<false, 1><<<grid, block, 0, s>>>(x, ldx, K, q, ldq, width, scale) : quant_i8_kernel<false, 4><<<grid, block, 0, s>>>(x, ldx, K, q, ldq, width, scale);
+  const unsigned grid = static_cast<unsigned>(M + pack.dst_rows);
+  const auto launch = [&](auto kernel) { kernel<<<grid, block, 0, s>>>(x, ldx, K, q, ldq, width, scale, M, pack); };
+  if (f32) few ? launch(quant_i8_kernel<true, 1>) : launch(quant_i8_kernel<true, 4>);
+  else few ? launch(quant_i8_kernel<false, 1>) : launch(quant_i8_kernel<false, 4>);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH_FAILED;
 }
 
@@ -68,7 +71,7 @@ int quantise(bool f32, int M, int K, const void* x, int64_t ldx, int8_t* q, int6
 
 template <bool OUT32>
 struct I8Out {
-  static constexpr int kAhead = OUT32 ? 4 : 8, kBytes = OUT32 ? 8 : 4;
+  static constexpr int kAhead = OUT32 ? 4 : 8;
   struct Cols {
     float w[4], b[4];
   };
@@ -82,6 +85,7 @@ struct I8Out {
   int64_t ldr, ldy;
   int N, act;
   bool bias_f32;
+  int bytes() const { return (OUT32 ? 4 : 2) * (residual ? 2 : 1); }
   __device__ __forceinline__ Cols cols(int n) const {
     Cols c;
     const Raw4<true> w = raw4<true>(sw, n, N - n);
@@ -213,7 +217,7 @@ int moe_quant_i8(int32_t dtype, int32_t rows, int32_t columns, const void* x, in
   if (!x || !codes || !scale) return MOE_ERR_NULL_PTR;
   if (ldx < columns || ldc < columns) return MOE_ERR_BAD_SHAPE;
   if (ldx > kFar || ldc > kFar || off(x, size_of(dtype)) || off(scale, 4)) return MOE_ERR_UNSUPPORTED;
-  return quantise(dtype == MOE_DTYPE_F32, rows, columns, x, ldx, codes, ldc, columns, scale, static_cast<hipStream_t>(stream));
+  return quantise(dtype == MOE_DTYPE_F32, rows, columns, x, ldx, codes, ldc, columns, scale, PackItem{}, static_cast<hipStream_t>(stream));
 }
 
 int moe_linear_i8_workspace_size(const moe_linear_i8_config* cfg, int32_t max_rows, size_t* bytes) {
@@ -248,7 +252,6 @@ int moe_linear_i8(const moe_linear_i8_config* cfg, int32_t M, const void* x, int
   int8_t* q = static_cast<int8_t*>(workspace) + part_bytes(false, M, N);
   float* qs = reinterpret_cast<float*>(q + codes_bytes(c, M));
   const int64_t ld = codes_ld(c);
-  PackArgs p{};
   const bool bf = c.bias_dtype == MOE_DTYPE_F32;
   const int row = static_cast<int>(align_up(K, 128));
   if (!codes && M == 1 && N <= kOnTheWayColumns && row <= kOnTheWayBytes && ldw < (int64_t{1} << 24)) {
@@ -260,16 +263,10 @@ int moe_linear_i8(const moe_linear_i8_config* cfg, int32_t M, const void* x, int
     return c.out_dtype == MOE_DTYPE_F32 ? with(I8Out<true>{qs, w_scale, bias, residual, y, ldr, ldy, N, c.activation, bf})
                                         : with(I8Out<false>{qs, w_scale, bias, residual, y, ldr, ldy, N, c.activation, bf});
   }
-  if (!codes) {
-    const int bad = quantise(c.in_dtype == MOE_DTYPE_F32, M, K, x, ldx, q, ld, static_cast<int>(ld), qs, s);
-    if (bad) return bad;
-    g.a.p = q;
-    g.a.ld = ld;
-    sx = qs;
-  }
+  // What lies odd is laid out afresh; with values to quantise, in the quantiser's launch.
+  PackArgs p{};
   if (large(c, M)) {
-    const auto lies_odd = [&](const void* a, int64_t l) { return K % 16 || l % 16 || off(a, 16); };
-    if (codes && lies_odd(x, ldx)) {
+    if (codes && (K % 16 || ldx % 16 || off(x, 16))) {
       p.item[p.n++] = PackItem{x, q, ldx, ld, M, K, M};
       g.a.p = q;
       g.a.ld = ld;
@@ -281,7 +278,15 @@ int moe_linear_i8(const moe_linear_i8_config* cfg, int32_t M, const void* x, int
       g.b.ld = ld;
       g.K = static_cast<int>(align_up(K, 16));
     }
-    if (p.n && !pack_rows<uint8_t>(p, s)) return MOE_ERR_LAUNCH_FAILED;
+  }
+  if (!codes) {
+    const int bad = quantise(c.in_dtype == MOE_DTYPE_F32, M, K, x, ldx, q, ld, static_cast<int>(ld), qs, p.item[0], s);
+    if (bad) return bad;
+    g.a.p = q;
+    g.a.ld = ld;
+    sx = qs;
+  } else if (p.n && !pack_rows<uint8_t>(p, s)) {
+    return MOE_ERR_LAUNCH_FAILED;
   }
   if (c.out_dtype == MOE_DTYPE_F32)
     return run_product<El::I8, true, true, false>(g, I8Out<true>{sx, w_scale, bias, residual, y, ldr, ldy, N, c.activation, bf}, part, s);

@@ -19,17 +19,14 @@ struct PackArgs {
   PackItem item[kPackItems];
   int n;
 };
+// Row `row` of an item, by a workgroup.
 template <class T>
-__global__ void __launch_bounds__(256) pack_rows_kernel(PackArgs a) {
+__device__ __forceinline__ void pack_row(const PackItem& p, int64_t row) {
   constexpr int kPiece = 16 / sizeof(T);
-  int64_t row = blockIdx.x;
-  int k = 0;
-  while (k + 1 < a.n && row >= a.item[k].dst_rows) row -= a.item[k++].dst_rows;
-  const PackItem& p = a.item[k];
   const T* src = static_cast<const T*>(p.src) + row * p.ld;
   const int cols = row < p.rows ? p.cols : 0;
   typedef uint32_t u32x4_t __attribute__((ext_vector_type(4), aligned(1)));
-  for (int i = kPiece * threadIdx.x; i < p.dst_ld; i += kPiece * 256) {
+  for (int i = kPiece * threadIdx.x; i < p.dst_ld; i += kPiece * blockDim.x) {
     uint4 v = {0, 0, 0, 0};
     if (i + kPiece <= cols) {
       const u32x4_t q = *reinterpret_cast<const u32x4_t*>(src + i);
@@ -43,6 +40,13 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(PackArgs a) {
     }
     *reinterpret_cast<uint4*>(static_cast<T*>(p.dst) + row * p.dst_ld + i) = v;
   }
+}
+template <class T>
+__global__ void __launch_bounds__(256) pack_rows_kernel(PackArgs a) {
+  int64_t row = blockIdx.x;
+  int k = 0;
+  while (k + 1 < a.n && row >= a.item[k].dst_rows) row -= a.item[k++].dst_rows;
+  pack_row<T>(a.item[k], row);
 }
 template <class T>
 inline bool pack_rows(const PackArgs& a, hipStream_t s) {
