@@ -1044,7 +1044,7 @@ struct TilePlan {
 // The cheapest tile and split by an estimate in microseconds: what a CU takes in (28 KB a
 // microsecond with two tiles on it, 20 with one), the f32 matrix rate, and the partial sums'
 // way out and back.
-inline TilePlan plan_tiles(El e, bool pair, int out_bytes, bool by_dma, bool rows64, int64_t M, int64_t N, int64_t K) {
+inline TilePlan plan_tiles(El e, bool pair, int out_bytes, bool by_dma, bool strided, int64_t M, int64_t N, int64_t K) {
   const int size = e == El::F32 ? 4 : e == El::BF16 ? 2 : 1;
   const int64_t width = pair ? 2 * N : N, stages = ceil_div(K * size, 128);
   const double room = static_cast<double>(part_bytes(pair, M, N));
@@ -1067,7 +1067,7 @@ inline TilePlan plan_tiles(El e, bool pair, int out_bytes, bool by_dma, bool row
       const double load = (t.rows + t.cols) * 0.128 * deep / (shared > 1 ? 28 : 20);
       const double mult = e == El::F32 ? t.rows * t.cols * 64 * deep / 0.5e6 : 0;
       const double in_turn = e == El::F32 ? static_cast<double>(ceil_div(items, kCus)) : rounds * shared;
-      offer(in_turn * std::max(load, mult) + 2 + 0.5 * rounds + (parts > 1 ? 4 + planes * 2 / 5e6 : 0),
+      offer(in_turn * std::max(load, mult) + 2 + (by_dma && strided ? 4.0 : 0.5) * rounds + (parts > 1 ? 4 + planes * 2 / 5e6 : 0),
             TilePlan{t.rows, t.cols, 0, tiles, 0, parts});
     }
   }
@@ -1077,21 +1077,30 @@ inline TilePlan plan_tiles(El e, bool pair, int out_bytes, bool by_dma, bool row
   // enough where two tiles share a CU or the multiplications take long; elsewhere more keep
   // more loads on their way: 224 x 4096 x 5120 in 64 x 128 tiles takes 47 us with two, 27
   // with four, and in two parts 21 (128 x 128 24, 256 x 256 in eight parts 29).
-  static const struct { int rows, cols, bufs, on; double stage, alone, end; } kDma[] = {
-      {256, 256, 2, 1, 1.55, 1.07, 7}, {256, 128, 3, 1, 0.9, 0.62, 6}, {128, 128, 2, 2, 0.93, 0.55, 5}, {128, 128, 3, 1, 0.5, 0.36, 5},
-      {64, 128, 2, 2, 0.69, 0.5, 4}, {64, 128, 4, 1, 0.36, 0.28, 4}};
+  //
+  // Weight gradients (`strided`) contract over the rows, which may be few: then a tile's begin
+  // and end decide, which two tiles on a CU hide for each other.  5120 x 2048 over 224 rows takes
+  // 21 us in 256 x 256, 23 in 256 x 128, 16 in 128 x 128 by twos and 20 alone; 4096 x 4096 over
+  // 1000 42, 48, 43 and 53; 5120 x 17408 over 64 87, 88, 58 and 97 (75 through registers).
+  static const struct { int rows, cols, bufs, on; double stage, alone, end, strided_end; } kDma[] = {
+      {256, 256, 2, 1, 1.55, 1.07, 7, 13}, {256, 128, 3, 1, 0.9, 0.62, 6, 7.2}, {128, 128, 2, 2, 0.93, 0.55, 5, 4.5},
+      {128, 128, 3, 1, 0.5, 0.36, 5, 4.3}, {64, 128, 2, 2, 0.69, 0.5, 4, 4}, {64, 128, 4, 1, 0.36, 0.28, 4, 4}};
+  // A large tile alone on its CU, with no other row of tiles that would bring its columns into
+  // the L2, waits for memory: 256 x 34816 x 5120 takes 167 us in 136 of them, 133 in
+  // 128 x 128 by twos.
+  const auto pace_alone = [&](const auto& t) { return t.cols == 256 && M <= 256 ? 2.0 : t.alone; };
   // Microseconds of a result's bytes beyond the first two: a CU moves about 15 KB in one.
   const double out = (out_bytes - 2) * (pair ? 0.5 : 1.0) / 15e3;
   for (const auto& t : kDma) {
-    if (t.rows == 64 && !rows64) continue;
+    if (t.rows == 64 && strided) continue;
     // Full rounds of whole tiles; what is left over, which would leave CUs idle, in parts.
     const int64_t slots = int64_t{t.on} * kCus, tiles = ceil_div(M, t.rows) * ceil_div(width, t.cols);
     const int64_t whole = tiles / slots * slots, rest = tiles - whole;
     for (int parts = 1; parts <= kMaxParts; ++parts) {
       const double planes = static_cast<double>(rest) * parts * t.rows * t.cols * 4;
       if (parts > 1 && (rest == 0 || rest * parts > slots || planes > room || stages / parts < 4)) break;
-      const double pace = rest * parts <= kCus ? t.alone : t.stage;
-      const double whole_end = t.end + out * t.rows * t.cols * t.on, rest_end = t.end + (parts > 1 ? 0 : out * t.rows * t.cols);
+      const double pace = rest * parts <= kCus ? pace_alone(t) : t.stage, end = strided ? t.strided_end : t.end;
+      const double whole_end = end + out * t.rows * t.cols * t.on, rest_end = end + (parts > 1 ? 0 : out * t.rows * t.cols);
       offer(whole / slots * (t.stage * stages + whole_end) + (rest ? pace * ceil_div(stages, parts) + rest_end : 0) + 2 +
                 (parts > 1 ? 2 + planes * 0.45e-6 : 0),
             TilePlan{t.rows, t.cols, t.bufs, tiles, whole, parts});
@@ -1178,7 +1187,7 @@ int run_product(const Product& g, const Epi& epi, float* part, hipStream_t s) {
     // 32-bit offsets of the rows.
     if (g.M <= kSkinnyRows && std::max(g.a.ld, g.b.ld) < (int64_t{1} << 24)) return launch_skinny<E, PAIR>(g, epi, aligned, part, s);
   }
-  const TilePlan t = plan_tiles(E, kPair, epi.bytes(), by_dma, KA, g.M, g.N, g.K);
+  const TilePlan t = plan_tiles(E, kPair, epi.bytes(), by_dma, !KA, g.M, g.N, g.K);
   if constexpr (E != El::F32) {
     if constexpr (KA) {
       if (t.bufs == 2 && t.rows == 64) return launch_aligned<E, KA, KB, PAIR, 64, 128, 2>(g, epi, t, part, s);
