@@ -1176,6 +1176,15 @@ int launch_skinny(const Product& g, const Epi& epi, bool aligned, float* part, h
   return MOE_OK;
 }
 
+// Up to 16 rows every workgroup of the streaming kernel reads all rows; where they and the
+// weights are many that weighs more than a tile's idle rows and its parts.  Microseconds of
+// the streaming kernel and of tiles: gated FFN, bf16, 16 x 4096 x 4096 32 and 34, 12 x 5120 x 8192 72
+// and 63, 16 x 5120 x 17408 164 and 111; int8 9 x 5120 x 5120 12 and 14, 16 x 5120 x 5120 14 and 11,
+// 4 x 5120 x 17408 25 and 25, 16 x 5120 x 17408 39 and 26.
+inline bool rows_weigh(El e, int64_t M, int64_t width, int64_t K) {
+  return M >= 4 && M * width * K >= (e == El::I8 ? int64_t{6} << 26 : int64_t{3} << 28);
+}
+
 // Runs a product of M, N, K >= 1; `part` holds part_bytes(pair, M, N).
 template <El E, bool KA, bool KB, bool PAIR, class Epi>
 int run_product(const Product& g, const Epi& epi, float* part, hipStream_t s) {
@@ -1184,8 +1193,9 @@ int run_product(const Product& g, const Epi& epi, float* part, hipStream_t s) {
   bool by_dma = false;
   if constexpr (E != El::F32) by_dma = aligned && fits_dma<E, KB, PAIR>(g);
   if constexpr (KA && KB) {
-    // 32-bit offsets of the rows.
-    if (g.M <= kSkinnyRows && std::max(g.a.ld, g.b.ld) < (int64_t{1} << 24)) return launch_skinny<E, PAIR>(g, epi, aligned, part, s);
+    // (Strides: 32-bit offsets of the rows.)
+    const bool weigh = by_dma && rows_weigh(E, g.M, kPair ? 2 * int64_t{g.N} : g.N, g.K);
+    if (g.M <= kSkinnyRows && !weigh && std::max(g.a.ld, g.b.ld) < (int64_t{1} << 24)) return launch_skinny<E, PAIR>(g, epi, aligned, part, s);
   }
   const TilePlan t = plan_tiles(E, kPair, epi.bytes(), by_dma, !KA, g.M, g.N, g.K);
   if constexpr (E != El::F32) {

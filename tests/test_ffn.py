@@ -506,3 +506,18 @@ def test_few_rows_round_once(T, H, I, pad, train):
     err = (y - want).abs()
     print(f"[case] worst error / tolerance {(err / tol).max():.3f}", flush=True)
     assert (err <= tol).all()
+
+
+# Few rows and many weights, which go through tiles; the functions' and the training form's
+# results are the same bits.
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,I", [(5, 5120, 17408), (12, 5120, 8192), (16, 4096, 16384)])
+def test_few_rows_and_many_weights(T, H, I):
+    print(f"\n[case] ffn T={T} H={H} I={I} many weights", flush=True)
+    x, _, w = _inputs(T, H, I, "bf16", T)
+    wg = {n: t.cuda() for n, t in w.items()}
+    op, train = (moe.GatedFFN(wg, "silu", max_rows=T, training=k) for k in (False, True))
+    op.workspace.fill_(0xFF)
+    y = op(x.cuda())
+    assert torch.equal(y, train(x.cuda()))
+    _compare({"y": y}, _expect(x, w, None, "silu", "bf16"), "many weights")
