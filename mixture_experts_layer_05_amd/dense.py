@@ -359,7 +359,7 @@ class ResidualNorm:
             self.grads = {n: torch.empty_like(p) for n, p in (("weight", weight), ("bias", bias),
                                                               ("post_weight", post_weight), ("post_bias", post_bias))
                           if p is not None}
-            self.dgate = {}                    # by the gate's kind
+            self.dgate = {}                    # by the buffer's shape and type
 
     def _here(self, t: torch.Tensor, T: int) -> torch.Tensor:
         return t if T == self.max_rows else t[:T]
@@ -410,11 +410,13 @@ class ResidualNorm:
         if has_residual:
             got["residual"] = self._here(self.dresidual, T)
         if gate is not None:
-            kind = _gate_kind(gate, T, self.H)
-            buf = self.dgate.get(kind)
-            if buf is None or buf.shape[1:] != gate.shape[1:] or buf.shape[0] < gate.shape[0] or buf.dtype != gate.dtype:
-                rows = gate.shape[0] if kind == GATES["channel"] else self.max_rows
-                buf = self.dgate[kind] = torch.empty(rows, *gate.shape[1:], dtype=gate.dtype, device=gate.device)
+            # A buffer for each shape and type of gate, kept from its first call on: captured
+            # graphs hold its address.
+            rows = gate.shape[0] if _gate_kind(gate, T, self.H) == GATES["channel"] else self.max_rows
+            shape = (rows, *gate.shape[1:])
+            buf = self.dgate.get((shape, gate.dtype))
+            if buf is None:
+                buf = self.dgate[shape, gate.dtype] = torch.empty(*shape, dtype=gate.dtype, device=self.z.device)
             got["gate"] = buf if buf.shape[0] == gate.shape[0] else buf[:gate.shape[0]]
         for n in ("weight", "bias") if dout is not None else ():
             if n in self.grads:

@@ -1,0 +1,68 @@
+"""What the operators around the MoE layer keep between calls: buffers that a captured graph
+may address stay where they are, and what a caller replaces is looked at again.  Stand-ins
+for tensors but for the tests marked gpu."""
+import pytest
+import torch
+
+import mixture_experts_layer_05_amd as moe
+from tests.test_binding_devices import HERE, THERE
+from tests.test_dense_devices import BF16, F32, H, T, _x, calls  # noqa: F401
+
+
+def _gates():
+    return {"vector": _x((H,)), "row": _x((1, H)), "token": _x((T, 1)), "full": _x((T, H)), "row f32": _x((1, H), F32)}
+
+
+def test_gate_gradients_keep_their_buffers(calls):  # noqa: F811
+    """One norm, gates of every shape in turn: a shape's gradient comes in the buffer that it
+    came in first, whatever was called in between."""
+    op = moe.ResidualNorm(H, stream_dtype="bf16", max_rows=T, training=True, device=HERE)
+    a = [_x() for _ in range(4)]
+    first = {}
+    for turn in range(3):
+        for name, gate in _gates().items():
+            got = op.backward(*a, gate)["gate"]
+            assert got.shape == gate.shape and got.dtype == gate.dtype
+            if turn == 0:
+                assert all(got is not t for t in first.values()), name
+                first[name] = got
+            assert got is first[name], name
+    # Of one row a gate of every element is one by channel.
+    one = op.backward(*(_x((1, H)) for _ in range(4)), _x((1, H)))["gate"]
+    assert one is first["row"]
+
+
+def test_a_gate_on_another_gpu_leaves_nothing_behind(calls):  # noqa: F811
+    op = moe.ResidualNorm(H, stream_dtype="bf16", max_rows=T, training=True, device=HERE)
+    a = [_x() for _ in range(4)]
+    with pytest.raises(ValueError, match="GPU"):
+        op.backward(*a, _x((T, 1), device=THERE))
+    assert op.backward(*a, _x((T, 1)))["gate"].device == HERE
+
+
+@pytest.mark.gpu
+def test_a_captured_gate_gradient_lands_where_it_was_captured():
+    """A backward pass captured with a gate [H]; eager ones with [1, H] and by token between
+    the replays; memory that is allocated meanwhile stays as it was."""
+    rows, width = 70, 640
+    g = torch.Generator().manual_seed(21)
+    y, z, dz, dout = (torch.randn(rows, width, generator=g).bfloat16().cuda() for _ in range(4))
+    gate, token = torch.randn(width, generator=g).bfloat16().cuda(), torch.randn(rows, 1, generator=g).bfloat16().cuda()
+    op = moe.ResidualNorm(width, torch.ones(width, dtype=BF16, device="cuda"), max_rows=rows, training=True)
+    want = op.backward(y, z, dz, dout, gate)["gate"].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        at = op.backward(y, z, dz, dout, gate)["gate"].data_ptr()
+    others = []
+    for k in range(4):
+        got = op.backward(y, z, dz, dout, gate[None])["gate"]
+        assert got.shape == (1, width) and torch.equal(got[0], want)
+        op.backward(y, z, dz, dout, token)
+        others += [torch.full((width,), 7.0, dtype=BF16, device="cuda") for _ in range(8)]
+        buf = op.backward(y, z, dz, dout, gate)["gate"]
+        assert buf.data_ptr() == at
+        buf.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(buf, want), k
+        assert all((t == 7.0).all() for t in others), k
