@@ -513,8 +513,8 @@ class LinearI8:
         dev = weight.device
         self.workspace = torch.empty(linear_i8_workspace_size(self.K, self.N, max(max_rows, 1)), dtype=torch.uint8, device=dev)
         self.y = torch.empty(max_rows, self.N, dtype=self.out_t, device=dev)
-        self._c = _LinearI8Config(self.K, self.N, 0, 0 if bias is None else _dtype_code(bias, "bias"), DTYPES[out_dtype],
-                                  _activation(activation))
+        self._c = _LinearI8Config(self.K, self.N, 0, DTYPES["f32"] if bias is None else _dtype_code(bias, "bias"),
+                                  DTYPES[out_dtype], _activation(activation))
 
     def __call__(self, x, residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                  stream=None) -> torch.Tensor:
@@ -529,6 +529,8 @@ class LinearI8:
             raise ValueError(f"out: expected {self.out_t}, got {y.dtype}")
         c = self._c
         c.in_dtype, c.activation = _OUT_TYPES[x.dtype], _activation(self.activation)
+        if self.bias is not None:
+            c.bias_dtype = _dtype_code(self.bias, "bias")
         _linear_i8_call(c, M, self.N, self.K, x, scale, self.weight, self.weight_scale, self.bias, residual, y,
                         self.workspace, stream)
         return y

@@ -5,8 +5,9 @@ import pytest
 import torch
 
 import mixture_experts_layer_05_amd as moe
+from mixture_experts_layer_05_amd import dense
 from tests.test_binding_devices import HERE, THERE
-from tests.test_dense_devices import BF16, F32, H, T, _x, calls  # noqa: F401
+from tests.test_dense_devices import BF16, F32, H, I, I8, T, _x, calls  # noqa: F401
 
 
 def _gates():
@@ -66,3 +67,32 @@ def test_a_captured_gate_gradient_lands_where_it_was_captured():
         torch.cuda.synchronize()
         assert torch.equal(buf, want), k
         assert all((t == 7.0).all() for t in others), k
+
+
+@pytest.mark.parametrize("made", [None, F32, BF16])
+@pytest.mark.parametrize("set_to", [None, F32, BF16])
+def test_a_projection_takes_its_bias_as_it_is(made, set_to, calls, monkeypatch):  # noqa: F811
+    """The bias of an 8-bit projection replaced by one of another type, set, or taken away:
+    the library is told the type of the one that it is given."""
+    seen = []
+
+    def record(config, rows, *args):
+        c = config._obj
+        seen.append((c.bias_dtype, args[6] is not None))
+        return 0
+
+    def bias(t):
+        return None if t is None else _x((I,), t)
+
+    monkeypatch.setattr(dense.lib(), "moe_linear_i8", record)
+    op = moe.LinearI8(_x((I, H), I8), _x((I,), F32), bias(made), max_rows=T)
+    op(_x())
+    op.bias = bias(set_to)
+    op(_x())
+    for (code, there), t in zip(seen, (made, set_to)):
+        assert there == (t is not None)
+        assert t is None or code == moe.DTYPES["f32" if t == F32 else "bf16"]
+    op.bias = _x((I,), torch.float16)
+    with pytest.raises(ValueError, match="bias"):
+        op(_x())
+    assert len(seen) == 2
