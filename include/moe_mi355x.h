@@ -354,9 +354,8 @@ typedef struct moe_ffn_config {
  * in two products: the first computes the gate and the up projection together and
  * writes h = act(gate) * up, the second is the down projection.  Sums and activations
  * are float32; h, a matrix operand, and y are rounded once to dtype (of up to 8 rows only
- * y: h is the sum of two bf16 numbers there; an infinite weight of w_down may then give
- * NaN in place of an infinity).  y and the gradients are bit-reproducible for given sizes
- * and alignments.
+ * y: h is the sum of two bf16 numbers there).  y and the gradients are bit-reproducible for
+ * given sizes and alignments.
  *   x, y           (device) [num_rows, H], rows ldx and ldy elements apart
  *   w_gate, w_up   (device) [I, H];  w_down (device) [H, I]; the expert weights' layout
  *   kept           (device) out, what the backward pass of the same rows needs (h, and

@@ -625,9 +625,11 @@ __global__ void __launch_bounds__(kSkinnyEight * kWave, SETS == 1 ? 6 : 4) produ
   if (m >= g.M || n >= g.N) return;
   f32x4 a = *reinterpret_cast<const f32x4*>(&out[m][c]);
   if constexpr (Rows::kRests) {
+    // Beside an infinity a rest says nothing: a rest of 0 or of the other sign meets an infinite
+    // weight as NaN or as the other infinity.
     const f32x4 b = *reinterpret_cast<const f32x4*>(&out[m + kRestRows][c]);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) a[e] += b[e];
+    for (int e = 0; e < 4; ++e) a[e] = isfinite(a[e]) ? a[e] + b[e] : a[e];
   }
   f32x4 u = {0.f, 0.f, 0.f, 0.f};
   if constexpr (PAIR) u = *reinterpret_cast<const f32x4*>(&out[m][c + 8]);
