@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kSkinnyEight * kWave, SETS == 1 ? 6 : 4) produ
   static_assert(!PAIR || SETS == 2, "a set for either product");
   constexpr int kCols = PAIR ? 8 : 8 * SETS, D = SETS == 1 ? 4 : 5;
   __shared__ f32x4 red[kSkinnyEight][kWave];
-  __shared__ float out[16][20];
+  __shared__ __attribute__((aligned(16))) float out[16][20];      // read by fours
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int n0 = blockIdx.x * kCols, p = blockIdx.y;
