@@ -425,9 +425,10 @@ typedef struct moe_norm_config {
  *   out         (device) out [num_rows, H] or NULL: no norm after the sum; z and out not
  *               both NULL.  I8: codes as moe_quant_i8 chooses them, and out_scale
  *   out_scale   (device) out float32 [num_rows] for I8, else ignored
- * Strides are in elements, at least H (MOE_ERR_BAD_SHAPE otherwise) and at most 2^40;
- * tensors need only be aligned to their element size.  num_rows = 0 returns MOE_OK;
- * num_rows <= MOE_LINEAR_MAX_ROWS.  No output may overlap an input otherwise. */
+ * Strides are in elements, at least H and, in place, the same (MOE_ERR_BAD_SHAPE otherwise),
+ * and at most 2^40; tensors need only be aligned to their element size.  num_rows = 0
+ * returns MOE_OK; num_rows <= MOE_LINEAR_MAX_ROWS.  No output may overlap an input
+ * otherwise. */
 int moe_norm(const moe_norm_config* cfg, int32_t num_rows, const void* y, int64_t ldy, const void* residual,
              int64_t ldr, const void* gate, int64_t ldg, const void* weight, const void* bias,
              const void* post_weight, const void* post_bias, void* z, int64_t ldz, void* out, int64_t ldo,

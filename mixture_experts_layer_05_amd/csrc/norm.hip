@@ -319,6 +319,7 @@ int moe_norm(const moe_norm_config* cfg, int32_t T, const void* y, int64_t ldy, 
                          check_rows(post_bias, H, H, ps), check_rows(z, ldz, H, ss),
                          check_rows(out, ldo, H, type_size(c.out_dtype)), check_rows(out_scale, 1, 1, 4)});
   if (bad) return bad;
+  if (z && z == residual && ldz != ldr) return MOE_ERR_BAD_SHAPE;
   // Few rows: as many lanes as there are, for the latency.  Many: several chunks to a lane,
   // for the loads in flight.  Microseconds of the first and the second (with a post norm):
   // 16 x 5120 4.0 and 4.5, 256 x 7168 5.4 and 5.6, 512 x 7168 8.9 and 8.0, 4096 x 7168 57 and 40.
@@ -371,6 +372,7 @@ int moe_norm_backward(const moe_norm_config* cfg, int32_t T, const void* y, int6
                  check_rows(dout, lddo, H, type_size(c.out_dtype)), check_rows(dy, lddy, H, bs),
                  check_rows(dresidual, lddr, H, ss), check_rows(workspace, 1, 1, 16)});
     if (bad) return bad;
+    if (dz && dz == dresidual && lddz != lddr) return MOE_ERR_BAD_SHAPE;
     if (workspace_bytes < norm_back_bytes(c, T)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   }
   NormBackArgs a{};

@@ -49,3 +49,16 @@ def test_stream_in_place(T, H, stream):
     r = c["r"].clone()
     moe.norm(c["y"], r, r, out2, **args)
     assert torch.equal(r, z) and torch.equal(out2, out)
+
+
+def test_other_strides_in_place_are_refused():
+    """z in the residual's place, or its gradient in dz's, with rows that lie elsewhere would
+    overwrite rows that are still to be read (no GPU: nothing is launched)."""
+    assert N._forward(r=N.FAKE, z=N.FAKE, ldr=64, ldz=72) == N.BAD_SHAPE
+    assert N._forward(r=N.FAKE, z=N.FAKE, ldr=72, ldz=64) == N.BAD_SHAPE
+    assert N._backward(dz=N.FAKE, dr=N.FAKE, lddz=64, lddr=72) == N.BAD_SHAPE
+    assert N._backward(dz=N.FAKE, dr=N.FAKE, lddz=72, lddr=64) == N.BAD_SHAPE
+    # Elsewhere strides differ as they like: the call gets as far as its other arguments.
+    assert N._forward(r=2 * N.FAKE, z=N.FAKE, ldr=64, ldz=72, out=N.FAKE, c=N._cfg(out=4)) == N.NULL_PTR
+    assert N._backward(dz=2 * N.FAKE, dr=N.FAKE, lddz=64, lddr=72, ws_bytes=16) == N.WS_SMALL
+    assert N._backward(dz=None, dr=None, lddz=64, lddr=72, ws_bytes=16) == N.WS_SMALL
