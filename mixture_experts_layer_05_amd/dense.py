@@ -1,10 +1,14 @@
 """Binding of the operators around the MoE layer beside `Linear`: the dense gated FFN
 with its backward pass, the norms before and after a block, and products in 8-bit
 integers.  As in the rest of the binding every step runs in the HIP kernels behind the C
-ABI of include/moe_mi355x.h, on the current stream, and nothing falls back."""
+ABI of include/moe_mi355x.h, on the current stream, and nothing falls back.
+
+autograd does not see these calls: results have no grad_fn, and gradients come from the
+backward passes' own calls (GatedFFN.backward, ResidualNorm.backward)."""
 from __future__ import annotations
 
 import ctypes
+import warnings
 from typing import Dict, Optional
 
 import torch
@@ -28,6 +32,13 @@ def _bytes_of(fn: str, *args) -> int:
     n = ctypes.c_size_t(0)
     _check(getattr(lib(), fn)(*args, ctypes.byref(n)), fn)
     return n.value
+
+
+def _outside_autograd(what: str, gradients: str) -> None:
+    """Warns of an input whose gradient autograd would look for in vain."""
+    if torch.is_grad_enabled():
+        warnings.warn(f"{what}: an input requires gradients, but autograd does not see this call: its results have no "
+                      f"grad_fn ({gradients})", stacklevel=3)
 
 
 # ----------------------------------------------------------------------------- gated FFN
@@ -106,7 +117,8 @@ class GatedFFN:
     `backward(x, dy)` returns {x, gate, up, down}, the gradients for the rows of the last
     call, in the weights' type and in buffers that the next backward overwrites.  The
     buffers serve one call (one forward and its backward) at a time: calls that overlap
-    (other streams, graphs replayed side by side) need a GatedFFN each."""
+    (other streams, graphs replayed side by side) need a GatedFFN each.  autograd does not
+    see the calls; an input that requires gradients is warned of."""
 
     def __init__(self, weights: Dict[str, torch.Tensor], activation: str = "silu", max_rows: int = 1,
                  training: bool = False):
@@ -133,6 +145,8 @@ class GatedFFN:
             raise ValueError("more rows than the block was sized for")
         if x.dtype != self.dtype:
             raise ValueError(f"x: expected {self.dtype}, got {x.dtype}")
+        if getattr(x, "requires_grad", False):
+            _outside_autograd("GatedFFN", "`backward` of a block made with training=True gives the gradients")
         y = out if out is not None else self.y if T == self.max_rows else self.y[:T]
         self.rows = None
         ffn(x, self.weights, y, self.workspace, self.activation, self.kept, stream)
@@ -323,7 +337,8 @@ class ResidualNorm:
 
     With `training=True`, `backward` returns the gradients in buffers that the next
     backward overwrites.  The buffers serve one call at a time: calls that overlap (other
-    streams, graphs replayed side by side) need a ResidualNorm each."""
+    streams, graphs replayed side by side) need a ResidualNorm each.  autograd does not see
+    the calls; an input that requires gradients is warned of."""
 
     def __init__(self, hidden_size: int, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
                  post_weight: Optional[torch.Tensor] = None, post_bias: Optional[torch.Tensor] = None, kind: str = "rms",
@@ -379,6 +394,8 @@ class ResidualNorm:
             raise ValueError("more rows than the norm was sized for")
         if y.dtype != self.block_t:
             raise ValueError(f"y: expected {self.block_t}, got {y.dtype}")
+        if getattr(y, "requires_grad", False) or getattr(residual, "requires_grad", False):
+            _outside_autograd("ResidualNorm", "`backward` of a norm made with training=True gives the gradients")
         c = self._config(T, gate)
         # The rows of the norm's own buffers, and their addresses, of the last call's length.
         mine = self._mine
@@ -524,6 +541,8 @@ class LinearI8:
             raise ValueError("more rows than the projection was sized for")
         if (x.dtype == torch.int8) != (scale is not None) or x.dtype not in _OUT_TYPES:
             raise ValueError(f"x: expected float32, bfloat16 or (int8 codes, scales), got {x.dtype}")
+        if getattr(x, "requires_grad", False):
+            _outside_autograd("LinearI8", "there is no backward pass through 8-bit codes")
         y = out if out is not None else self.y if M == self.max_rows else self.y[:M]
         if y.dtype != self.out_t:
             raise ValueError(f"out: expected {self.out_t}, got {y.dtype}")

@@ -1,6 +1,8 @@
 """What the operators around the MoE layer keep between calls: buffers that a captured graph
 may address stay where they are, and what a caller replaces is looked at again.  Stand-ins
 for tensors but for the tests marked gpu."""
+import warnings
+
 import pytest
 import torch
 
@@ -96,3 +98,27 @@ def test_a_projection_takes_its_bias_as_it_is(made, set_to, calls, monkeypatch):
     with pytest.raises(ValueError, match="bias"):
         op(_x())
     assert len(seen) == 2
+
+
+@pytest.mark.parametrize("where", ["ffn", "y", "residual", "i8"])
+def test_an_input_that_requires_gradients_is_warned_of(where, calls):  # noqa: F811
+    """Results have no grad_fn: a caller in autograd's grad mode is told so."""
+    a = {n: _x() for n in ("ffn", "y", "residual", "gate", "i8")}
+    ffn = moe.GatedFFN({"gate": _x((I, H)), "up": _x((I, H)), "down": _x((H, I))}, max_rows=T, training=True)
+    norm = moe.ResidualNorm(H, stream_dtype="bf16", max_rows=T, training=True, device=HERE)
+    i8 = moe.LinearI8(_x((I, H), I8), _x((I,), F32), max_rows=T)
+
+    def run():
+        ffn(a["ffn"])
+        norm(a["y"], a["residual"], a["gate"])
+        i8(a["i8"])
+
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        run()
+        a[where].requires_grad = True
+        with torch.no_grad():
+            run()
+    with pytest.warns(UserWarning, match="autograd"):
+        run()
+    assert len(calls) == 9
