@@ -124,9 +124,9 @@ __global__ void __launch_bounds__(64 * back_waves(!YF32 && !SF32 && !OF32 && !PF
 #pragma unroll
       for (int c = 0; c < C; ++c) g[c] = rows(std::bool_constant<PF32>{}, a.gate, a.ldg, t, c);
     }
-    // Behind the group's last row that row again: another one's dz may be dresidual's place,
-    // which its own group is writing.
-    load(R, t + a.groups < a.T ? t + a.groups : t);
+    // (Nothing behind the group's last row: another one's dz may be dresidual's place, which its
+    // own group is writing.)
+    if (t + a.groups < a.T) load(R, t + a.groups);
 
     // Statistics of z and y, and z's sums with dn.
     float zmean = 0.0f, ymean = 0.0f;
