@@ -217,8 +217,8 @@ size_t kept_bytes(const moe_ffn_config& c, int64_t T) { return h_bytes(c, T) + 2
 
 // Rows that do not lie in whole 16-byte pieces are laid out afresh, in one launch, for the
 // products of more than 16 rows: loads of odd rows take in less than half as much.  A
-// training step of 1001 x 1537 x 2049 takes 290 us with the rows as they lie, 163 with 2 x 11
-// for laying them out; forward and backward of 256 x 515 x 1023 27 + 45 and 22 + 39, of
+// training step of 1001 x 1537 x 2049 takes 290 us with the rows as they lie, 151 to 172 with
+// 2 x 11 to 12 for laying them out; forward and backward of 256 x 515 x 1023 27 + 45 and 22 + 39, of
 // 64 x 129 x 257 17.9 + 40.3 and 16.2 + 36.4, of 17 x 65 x 129 13.7 + 31.7 and 14.4 + 27.8.  Room
 // for x and dy is always there, room for the weights where their sizes are odd.
 constexpr int64_t kPackFrom = int64_t{1} << 20;      // multiply-adds of a product, forward

@@ -478,8 +478,8 @@ __global__ void __launch_bounds__(256, 2) product_tile_kernel(Product g, Epi epi
 // each.  Of a pair the two sets are eight columns of either product.
 //
 // Bound by memory: one row against the two bf16 matrices of 17408 x 5120 takes 64 us
-// (5.5 TB/s), against the third 39 (4.5 TB/s; 640 workgroups only); 17408 x 5120 int8 21 us
-// (4.2 TB/s).  With 16 rows the rows' own reading, by every workgroup, shows: the three
+// (5.5 TB/s), against the third 39 (4.5 TB/s; 640 workgroups only); 17408 x 5120 int8 21 to
+// 22 us (4.1 TB/s).  With 16 rows the rows' own reading, by every workgroup, shows: the three
 // matrices take 163 us instead of 103.
 constexpr int kSkinnyEight = 8;
 
@@ -658,9 +658,9 @@ __global__ void __launch_bounds__(kSkinnyEight * kWave, SETS == 1 ? 6 : 4) produ
 //
 // Bound by the matrix cores, whose clock falls under full load: they are busy 78 % of the
 // 256 x 256 kernel's time, at 1.8 GHz.  8192 x 17408 x 5120 bf16 with a pair takes 2.36 to 2.48 ms
-// (1.18 to 1.24 PFLOP/s, its results included), one product of these sizes 1.12 to 1.14
-// (1.28 to 1.30; a library product without an epilogue 1.20, or 1.39 with a k-strided side);
-// 8192 x 4096 x 7168 int8 230 to 255 us (1.9 to 2.1 POP/s; a library product 204).
+// (1.18 to 1.24 PFLOP/s, its results included), one product of these sizes 1.11 to 1.14
+// (1.28 to 1.32; a library product without an epilogue 1.20, or 1.39 with a k-strided side);
+// 8192 x 4096 x 7168 int8 221 to 255 us (1.9 to 2.2 POP/s; a library product 204).
 //
 // k-contiguous operands: rows of 128 bytes, 16-byte pieces permuted by (row / 2) mod 8.
 // k-strided: a row for each k, 64-byte pieces permuted by k mod 4, so that the four k of a

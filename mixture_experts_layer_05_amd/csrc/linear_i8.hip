@@ -2,7 +2,7 @@
 //   y = act(sx sw sum_k q[m, k] w[n, k] + bias) + residual
 // The sum is exact in int32, however it is split; everything behind it is float32, rounded
 // once to y's type.  Rows of x in 16 or 32 bits are quantised first (quant_i8_kernel), each by
-// its largest magnitude.  8192 x 4096 x 7168 from bf16 takes 263 to 278 us, of which 31 to 36
+// its largest magnitude.  8192 x 4096 x 7168 from bf16 takes 249 to 278 us, of which 32 to 38
 // are the quantiser's; one row against 17408 x 5120 24 us, 21 from codes.
 #include "gemm.h"
 #include "pack.h"
@@ -15,8 +15,8 @@ namespace {
 
 // A row of x to a workgroup: its largest magnitude, then its codes.  A lane keeps C times
 // eight elements; what is left of a longer row is read again, from the caches.  Zeros
-// behind the row up to `width` codes.  Bound by memory: 8192 x 7168 bf16 takes 31 us, 5.7 TB/s
-// read and written (67 us with every code decided by the exact remainder).  Workgroups from
+// behind the row up to `width` codes.  Bound by memory: 8192 x 7168 bf16 takes 32 to 38 us,
+// 5.3 TB/s read and written at 33 (67 us with every code decided by the exact remainder).  Workgroups from
 // M on lay out rows of the product's weights, if those lie odd: a launch less.
 template <bool F32, int C>
 __global__ void __launch_bounds__(1024) quant_i8_kernel(const void* x, int64_t ldx, int K, int8_t* q, int64_t ldq, int width, float* scale, int M, PackItem pack) {
@@ -189,6 +189,9 @@ int check_i8(const moe_linear_i8_config* c, int32_t rows) {
 // Codes that do not lie in whole 16-byte pieces are laid out afresh, in one launch, where
 // the product is large: 300 x 2049 x 1025 takes 16.0 us with the codes as they lie and 14.5 so,
 // 256 x 1023 x 515 18.5 and 11.7, 64 x 515 x 257 12.4 and 10.4, 64 x 257 x 257 10.7 and 11.1.
+// Weights of whole pieces whose rows alone lie odd are taken as they lie, through registers
+// (the workspace has no room for them): 1 x 4096 x 7168 from bf16 takes 16 us instead of 11,
+// 224 x 4096 x 7168 31 instead of 22, 8192 x 4096 x 7168 384 to 402 instead of 249 to 262.
 constexpr int64_t kPackFrom = int64_t{1} << 23;      // multiply-adds
 bool large(const moe_linear_i8_config& c, int64_t M) { return M > kSkinnyRows && M * c.in_features * c.out_features >= kPackFrom; }
 

@@ -16,9 +16,11 @@
 // that holds a whole row needs no barrier.
 //
 // Bound by memory, or for few rows by one launch: 8192 x 7168 in bf16 with a post norm takes
-// 96 us (4.9 TB/s over four tensors, what a large copy reaches), one row 3 us on the GPU.
-// Backward, six tensors and three sums over rows, 155 (4.5 TB/s), of which 9 are the second
-// launch's.
+// 94 to 100 us (4.9 TB/s over four tensors, what a large copy reaches), one row 3 us on the
+// GPU.  Backward, six tensors and three sums over rows, 150 to 158 (4.6 TB/s), of which 9 are
+// the second launch's.  (Call after call, from the second hundred on; the first hundred after
+// a pause take up to a tenth longer.)  With f32 throughout 176 and 332.  Rows wider than 8192
+// run as fast forward (8192 x 12288 169 us), but not backward: 2.0 ms (norm_back.h).
 #include <algorithm>
 #include <initializer_list>
 
@@ -282,7 +284,10 @@ int launch_norm(const NormArgs& a, int chunks, hipStream_t s) {
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH_FAILED;
 }
 
-// Groups of rows of a backward pass: a workgroup or, for rows of one wave, four to a CU.
+// Groups of rows of a backward pass.  A group is a workgroup, as many to a CU as make 16 waves,
+// or for rows of up to 512 columns one wave, eight to a CU (two workgroups of four).  Of few
+// rows there are fewer groups: as many as rows up to 256, then 256 until a group has eight rows
+// (four where it is one wave), and with those up to the CUs' fill.
 int norm_groups(const moe_norm_config& c, int64_t T) {
   const int waves = static_cast<int>(ceil_div(c.hidden_size, 512));
   const int64_t most = waves == 1 ? 256 * 4 * 2 : 256 * std::max(1, 16 / waves);

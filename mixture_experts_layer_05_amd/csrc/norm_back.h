@@ -40,12 +40,16 @@ struct Columns {
 
 #ifdef MOE_NORM_BACK_KERNELS
 
-// BIAS: with sums for biases.  A workgroup's parameters and sums stay in registers over its
-// rows, and the next row's loads are in flight while a row is worked on.
+// BIAS: with sums for biases.  A workgroup's parameters and sums stay over its rows, and the
+// next row's loads are in flight while a row is worked on: in registers, where they fit.
 //
-// Most waves to a row: with one chunk to a lane everything in bf16 takes 127 registers, the
-// other forms up to 168; two chunks take twice as many.  8192 x 5120 takes 127 us in ten
-// waves of one chunk, 164 in five of two.
+// Most waves to a row: with one chunk to a lane everything in bf16 takes 121 registers, the
+// other forms up to 168, and none uses scratch memory.  Two chunks take 218 to 256; with biases
+// all of these spill (72 to 256 bytes a lane), without them 4 of 16 do (up to 76).  Four
+// chunks, of rows wider than 8192, spill 1256 to 1620 bytes a lane and are bound by that:
+// bf16 8192 x 12288 takes 2.0 ms, 8192 x 16384 2.9, where the rows alone are 0.25 and 0.33.
+// 8192 x 5120 takes 127 us in ten waves of one chunk, 164 in five of two; in bf16 8192 x 7168
+// layer norms with biases, in two chunks, take 262, rms norms without, in one, 153.
 constexpr int back_waves(bool narrow, int chunks) { return chunks > 1 ? 8 : narrow ? 16 : 12; }
 
 template <bool YF32, bool SF32, bool OF32, bool PF32, bool BIAS, int C>
