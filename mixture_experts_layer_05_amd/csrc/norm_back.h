@@ -48,8 +48,9 @@ struct Columns {
 // all of these spill (72 to 256 bytes a lane), without them 4 of 16 do (up to 76).  Four
 // chunks, of rows wider than 8192, spill 1256 to 1620 bytes a lane and are bound by that:
 // bf16 8192 x 12288 takes 2.0 ms, 8192 x 16384 2.9, where the rows alone are 0.25 and 0.33.
-// 8192 x 5120 takes 127 us in ten waves of one chunk, 164 in five of two; in bf16 8192 x 7168
-// layer norms with biases, in two chunks, take 262, rms norms without, in one, 153.
+// 8192 x 5120 took 127 us in ten waves of one chunk and 164 in five of two, measured in turn (117 in
+// ten since); bf16 8192 x 7168 layer norms with biases, in two chunks, take 262, rms norms
+// without, in one, 153.
 constexpr int back_waves(bool narrow, int chunks) { return chunks > 1 ? 8 : narrow ? 16 : 12; }
 
 template <bool YF32, bool SF32, bool OF32, bool PF32, bool BIAS, int C>
